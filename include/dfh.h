@@ -341,6 +341,101 @@ df_status df_encode_device_noalloc(df_kind kind, const void *d_src, uint64_t n, 
                                    uint64_t *d_tile_out, uint8_t *d_sign_mantissa, uint32_t *d_max_tile,
                                    hipStream_t stream);
 
+/* --------------------------------------------- products with uint4 weights */
+
+/* The codes of a uint4 container are weights: a layer of `rows` outputs and
+ * `cols` inputs stores W[n, k] as nibble n * cols + k of df_decompress's
+ * output.  With a scale (and zero point) for each group of group_size
+ * consecutive elements of a row,
+ *     W[n, k] = scales[n, g] * (q[n, k] - zeros[n, g]),   g = k / group_size,
+ * where zeros defaults to 8 (the EntroLLM summary, "Metodologia": unsigned
+ * codes around 8, or asymmetric codes with a shifted zero point).  The calls
+ * below multiply by W without a dequantised copy for few rows.  They enqueue
+ * on the stream and return: no allocation, no synchronisation. */
+
+typedef enum { DF_TYPE_BF16 = 0, DF_TYPE_F16 = 1, DF_TYPE_F32 = 2 } df_type;
+
+typedef struct {
+  uint64_t rows;          /* outputs, 1 .. 2^21                              */
+  uint64_t cols;          /* inputs, a multiple of 8, at most 2^20           */
+  uint32_t group_size;    /* a multiple of 32, or at least cols: one group   */
+  df_type scale_type;
+  uint64_t scale_stride;  /* elements between rows of scales; 0: one row for all */
+  uint64_t zero_stride;
+  const uint8_t *packed;  /* rows * cols / 2 bytes, 4-byte aligned           */
+  const void *scales;     /* rows x ceil(cols / group_size)                  */
+  const uint8_t *zeros;   /* the same, any byte values; NULL: 8              */
+} df_u4_matrix;
+
+/* y[m, n] = sum over k of x[m, k] W[n, k].  x: `rows` rows of w->cols
+ * elements of `type` (BF16 or F16), x_stride elements apart (a multiple of 8,
+ * at most 2^21); y: rows x w->rows of the same type, contiguous.  Both 16-byte
+ * aligned.  Up to 64 rows take no workspace and multiply the integers exactly
+ * (a group's FP32 sum is scaled); more rows expand W to `type` in the
+ * workspace (256-byte aligned), each weight rounded once.  Sums are FP32.
+ * DF_ERR_ARG on a bad pointer, size, alignment or too small a workspace. */
+uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows);
+df_status df_linear_u4(const df_u4_matrix *w, df_type type, const void *x, uint64_t rows, uint64_t x_stride, void *y,
+                       void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* The gradient to x: dx[m, k] = sum over n of dy[m, n] W[n, k], dy with rows
+ * dy_stride elements apart (w->rows a multiple of 8: dy 16-byte aligned and
+ * dy_stride a multiple of 8; any stride otherwise), dx contiguous and 16-byte
+ * aligned.  Always needs its workspace. */
+uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows);
+df_status df_linear_u4_grad(const df_u4_matrix *w, df_type type, const void *dy, uint64_t rows, uint64_t dy_stride,
+                            void *dx, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------- losses over a large vocabulary */
+
+/* Hidden states x [rows, hidden] and head weights [vocab, hidden] (an LM head
+ * that a BF16 container decodes to) give logits z = x head^T, which are never
+ * stored whole.
+ *   Cross entropy (top == 0): loss[m] = log sum_v exp z[m, v] - z[m, labels[m]].
+ *     A row whose label is ignore_index has no loss and no gradient; another
+ *     label outside 0 .. vocab - 1 gives a NaN loss and no gradient.
+ *   Distillation (top > 0) from a teacher's top logits: entries j of row m
+ *     with 0 <= index[m, j] < vocab (others are padding) hold teacher logits
+ *     a; with temperature T, t = softmax(a / T) over the row's entries and
+ *     q = softmax(z / T) over the vocabulary,
+ *       loss[m] = T^2 sum_j t_j (log t_j - log q[index[m, j]]).
+ *     A row without entries has no loss and no gradient; an index that comes
+ *     twice counts as two entries.
+ * Rows without a loss give 0 and may hold anything in x. */
+typedef enum { DF_REDUCE_NONE = 0, DF_REDUCE_SUM = 1, DF_REDUCE_MEAN = 2 } df_reduce;
+
+typedef struct {
+  df_type type;            /* of x and head: BF16 or F16                     */
+  df_reduce reduce;        /* MEAN: over the rows that have a loss, 0 if none */
+  uint64_t rows, vocab, hidden; /* rows and vocab up to 2^21, hidden a multiple of 8 up to 2^17 */
+  uint64_t x_stride, head_stride; /* elements, multiples of 8, at most 2^21  */
+  const void *x, *head;    /* 16-byte aligned                                */
+  const int64_t *labels;   /* [rows], top == 0                               */
+  int64_t ignore_index;
+  const int64_t *index;    /* [rows, top], top > 0                           */
+  const void *teacher;     /* [rows, top]                                    */
+  df_type teacher_type;
+  uint32_t top;            /* at most 1024                                   */
+  uint64_t index_stride, teacher_stride; /* elements                         */
+  float temperature;       /* positive; top == 0: 1                          */
+} df_loss;
+
+/* The loss: float[rows] (DF_REDUCE_NONE) or float[1].  saved
+ * (df_loss_saved_bytes) keeps per row what the gradient needs. */
+uint64_t df_loss_saved_bytes(const df_loss *d);
+uint64_t df_loss_workspace_bytes(const df_loss *d);
+df_status df_vocab_loss(const df_loss *d, float *loss, void *saved, void *workspace, uint64_t workspace_bytes,
+                        hipStream_t stream);
+
+/* Gradients for the loss's own gradient grad_loss (float[rows] or float[1],
+ * on the device): dx [rows, hidden] and, when not NULL, dhead [vocab, hidden],
+ * contiguous, of d->type.  The logits are made again in pieces of the
+ * vocabulary that fit the workspace.  Sums are FP32 in a fixed order: the same
+ * inputs give the same bits. */
+uint64_t df_loss_grad_workspace_bytes(const df_loss *d, int want_dhead);
+df_status df_vocab_loss_grad(const df_loss *d, const void *saved, const float *grad_loss, void *dx, void *dhead,
+                             void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

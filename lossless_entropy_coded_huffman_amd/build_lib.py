@@ -15,6 +15,7 @@ LIB = os.path.join(BUILD, "libdfh.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
+HIP_SOURCES = ("dfh_decode", "dfh_encode", "dfh_linear", "dfh_loss")
 HIP_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
     # keep the compiler from forming packed fp32 instructions
@@ -32,17 +33,22 @@ def build() -> str:
     os.makedirs(BUILD, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROCM, "include")]
     host_o = os.path.join(BUILD, "dfh_host.o")
-    dev_o = os.path.join(BUILD, "dfh_decode.o")
     _run(["g++", "-O3", "-std=c++17", "-fPIC", "-pthread", "-Wall", "-Wextra",
           "-D__HIP_PLATFORM_AMD__"] + inc + ["-c", os.path.join(CSRC, "dfh_host.cpp"), "-o", host_o])
-    _run([os.path.join(ROCM, "bin", "hipcc")] + HIP_FLAGS + inc +
-         ["-c", os.path.join(CSRC, "dfh_decode.hip"), "-o", dev_o])
-    enc_o = os.path.join(BUILD, "dfh_encode.o")
-    _run([os.path.join(ROCM, "bin", "hipcc")] + HIP_FLAGS + inc +
-         ["-c", os.path.join(CSRC, "dfh_encode.hip"), "-o", enc_o])
+    dev_o = []
+    procs = []
+    for name in HIP_SOURCES:   # one compiler each, side by side
+        obj = os.path.join(BUILD, name + ".o")
+        cmd = [os.path.join(ROCM, "bin", "hipcc")] + HIP_FLAGS + inc + ["-c", os.path.join(CSRC, name + ".hip"), "-o", obj]
+        print("+", " ".join(cmd), flush=True)
+        procs.append((cmd, subprocess.Popen(cmd)))
+        dev_o.append(obj)
+    for cmd, p in procs:
+        if p.wait() != 0:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([os.path.join(ROCM, "bin", "hipcc"), "-shared", "-fPIC", "--offload-arch=" + ARCH,
-          host_o, dev_o, enc_o, "-pthread", "-o", tmp])
+          host_o] + dev_o + ["-pthread", "-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 

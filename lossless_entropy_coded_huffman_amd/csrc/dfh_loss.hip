@@ -1,0 +1,618 @@
+// Losses over a large vocabulary without keeping the logits (gfx950).
+//
+//   z = x head^T,  lse[m] = log sum_v exp(z[m, v] / T)
+//   cross entropy: loss = lse - z[label];  distillation: T^2 sum_j t_j (log t_j - z_j / T + lse)
+//   dz[m, v] = T g[m] (exp(z / T - lse) - t[m, v]),  dx = dz head,  dhead = dz^T x
+//
+// with t the row's sparse target (a label is one entry with t = 1, T = 1).
+//
+// Forward: one pass of gemm_nt whose epilogue reduces each wave's columns to a
+// maximum and a sum of exponentials per row; a second kernel joins them.  The
+// few logits that the targets name are dot products of their own.  Backward:
+// for a piece of the vocabulary that fits the workspace the logits are made
+// again, dz goes out in 16 bits, the target entries are put right, and two
+// more products take it.  Exponents are in base 2: c = log2(e) / T.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "dfh.h"
+#include "dfh_gemm.h"
+
+namespace {
+
+using namespace dfh;
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr uint32_t kMaxTop = 1024;
+
+struct Targets {
+  const int64_t *labels;  // top == 0
+  int64_t ignore;
+  const int64_t *index;
+  const void *teacher;
+  uint64_t istride, tstride;
+  int teacher_type;
+  uint32_t top, vocab;
+  float temp;
+};
+
+// What a row keeps: its state, the base-2 log-sum and the target logits.
+enum : uint32_t { kNoLoss = 0, kLoss = 1, kBadLabel = 2 };
+struct Saved {
+  float *lse2;
+  uint32_t *state;
+  float *picked;  // [rows, max(top, 1)]
+};
+
+__device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
+
+__device__ __forceinline__ float teacher_at(const Targets &t, uint32_t m, uint32_t j) {
+  const uint64_t i = m * t.tstride + j;
+  if (t.teacher_type == DF_TYPE_F32) return ((const float *)t.teacher)[i];
+  const uint16_t b = ((const uint16_t *)t.teacher)[i];
+  return t.teacher_type == DF_TYPE_BF16 ? from_bits(BF16{}, b) : from_bits(F16{}, b);
+}
+// Vocabulary entry of a row's target j, or -1.
+__device__ __forceinline__ int32_t target_of(const Targets &t, uint32_t m, uint32_t j) {
+  const int64_t i = t.top ? t.index[m * t.istride + j] : t.labels[m];
+  if (!t.top && i == t.ignore) return -1;
+  return i >= 0 && i < (int64_t)t.vocab ? (int32_t)i : -1;
+}
+
+// ------------------------------------------------------------------ epilogues
+// Per row, over this wave's columns: max of z2 = c z and sum of 2^(z2 - max).
+struct EpiStats {
+  float2 *parts;  // [part][m]
+  float c;
+  template <class T, int NT, int MT>
+  __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
+                                             uint32_t part, uint32_t) const {
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      float mx = -__builtin_huge_valf();
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float v = nb + j * 16 + e < n ? acc[j][i][e] * c : -__builtin_huge_valf();
+          acc[j][i][e] = v;
+          mx = __builtin_fmaxf(mx, v);
+        }
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+      const float ref = mx == -__builtin_huge_valf() ? 0.f : mx;
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) s += exp2_(acc[j][i][e] - ref);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      const uint32_t row = mb + i * 16;
+      if ((threadIdx.x & 48) == 0 && row < m) parts[(uint64_t)part * m + row] = float2{mx, s};
+    }
+  }
+};
+
+// dz / (T g) without the target's part, times `mul`: 2^(c z - lse2), in 16
+// bits; zero in rows without a loss and in the columns that pad a row to ldz.
+// FP16 takes mul = 2^15: probabilities of a large vocabulary lie where FP16
+// has few bits or none; the products' epilogues take the factor out again.
+struct EpiDz {
+  uint16_t *dz;
+  uint32_t ldz;
+  const float *lse2;
+  const uint32_t *state;
+  float c, mul;
+  template <class T, int NT, int MT>
+  __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
+                                             uint32_t, uint32_t) const {
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      const uint32_t row = mb + i * 16;
+      if (row >= m) continue;
+      const bool live = state[row] == kLoss;
+      const float l = lse2[row];
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const uint32_t col = nb + j * 16;
+        if (col >= ldz) continue;
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) p[e] = live && col + e < n ? exp2_(acc[j][i][e] * c - l) * mul : 0.f;
+        *(u32x2 *)(dz + (uint64_t)row * ldz + col) = u32x2{pack2(T{}, p[0], p[1]), pack2(T{}, p[2], p[3])};
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------- kernels
+// picked[m, j] = x[m] . head[target j], one wave each (0 without a target).
+template <class T>
+__global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t rows, const uint16_t *x, uint64_t xs,
+                                                   const uint16_t *head, uint64_t hs, uint32_t k, float *picked) {
+  const uint32_t per = t.top ? t.top : 1, lane = threadIdx.x & 63;
+  const uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e >= (uint64_t)rows * per) return;
+  const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
+  const int32_t v = target_of(t, m, j);
+  float s = 0.f;
+  if (v >= 0) {
+    const u32x4 *px = (const u32x4 *)(x + m * xs), *ph = (const u32x4 *)(head + (uint64_t)v * hs);
+    for (uint32_t c = lane; c < k / 8; c += 64) {
+      const u32x4 a = px[c], b = ph[c];
+#pragma unroll
+      for (int d = 0; d < 4; d++) {
+        s = __builtin_fmaf(from_bits(T{}, (uint16_t)a[d]), from_bits(T{}, (uint16_t)b[d]), s);
+        s = __builtin_fmaf(from_bits(T{}, (uint16_t)(a[d] >> 16)), from_bits(T{}, (uint16_t)(b[d] >> 16)), s);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) picked[e] = s;
+}
+
+// Joins a row's parts and makes its loss.  16 rows a workgroup; thread t takes
+// parts t / 16, t / 16 + 16, ... and targets likewise of row t % 16.
+__global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, uint32_t np,
+                                                   Saved sv, float *loss) {
+  __shared__ float sa[16][17], sb[16][17];
+  const uint32_t r = threadIdx.x & 15, sl = threadIdx.x >> 4, m = blockIdx.x * 16 + r;
+  const bool in = m < rows;
+  auto join_max = [&](float v) {
+    sa[sl][r] = v;
+    __syncthreads();
+    float o = -__builtin_huge_valf();
+    for (int q = 0; q < 16; q++) o = __builtin_fmaxf(o, sa[q][r]);
+    __syncthreads();
+    return o;
+  };
+  auto join_sum = [&](float v) {
+    sb[sl][r] = v;
+    __syncthreads();
+    float o = 0.f;
+    for (int q = 0; q < 16; q++) o += sb[q][r];
+    __syncthreads();
+    return o;
+  };
+  float mx = -__builtin_huge_valf();
+  if (in)
+    for (uint32_t p = sl; p < np; p += 16) mx = __builtin_fmaxf(mx, parts[(uint64_t)p * rows + m].x);
+  mx = join_max(mx);
+  const float ref = mx == -__builtin_huge_valf() ? 0.f : mx;
+  float s = 0.f;
+  if (in)
+    for (uint32_t p = sl; p < np; p += 16) {
+      const float2 v = parts[(uint64_t)p * rows + m];
+      s += v.y * exp2_(v.x - ref);
+    }
+  s = join_sum(s);
+  const float lse2 = ref + __builtin_amdgcn_logf(s);  // base 2
+  const float lse = lse2 * kLn2;
+  const uint32_t per = t.top ? t.top : 1;
+  // the target's softmax over its entries
+  float tm = -__builtin_huge_valf(), any = 0.f;
+  if (in)
+    for (uint32_t j = sl; j < per; j += 16)
+      if (target_of(t, m, j) >= 0) {
+        any = 1.f;
+        if (t.top) tm = __builtin_fmaxf(tm, teacher_at(t, m, j) / t.temp);
+      }
+  any = join_max(any);
+  tm = t.top ? join_max(tm) : 0.f;
+  const float tref = tm == -__builtin_huge_valf() ? 0.f : tm;
+  float ts = 0.f;
+  if (in && t.top)
+    for (uint32_t j = sl; j < per; j += 16)
+      if (target_of(t, m, j) >= 0) ts += expf(teacher_at(t, m, j) / t.temp - tref);
+  ts = t.top ? join_sum(ts) : 1.f;
+  const float lts = logf(ts);
+  float l = 0.f;
+  if (in)
+    for (uint32_t j = sl; j < per; j += 16)
+      if (target_of(t, m, j) >= 0) {
+        const float z = sv.picked[(uint64_t)m * per + j];
+        if (!t.top) {
+          l = lse - z;
+          l = l < 0.f ? 0.f : l;  // z is one of the terms under the logarithm
+        } else {
+          const float d = teacher_at(t, m, j) / t.temp - tref, w = expf(d) / ts;
+          if (!(w == 0.f)) l += w * ((d - lts) - (z / t.temp - lse));
+        }
+      }
+  l = join_sum(l) * (t.top ? t.temp * t.temp : 1.f);
+  if (in && sl == 0) {
+    // a row of entries that all hold -inf has nothing to learn from either
+    uint32_t st = any > 0.f && !(t.top && ts == 0.f) ? kLoss : kNoLoss;
+    if (!t.top && st == kNoLoss && t.labels[m] != t.ignore) st = kBadLabel;
+    sv.lse2[m] = lse2;
+    sv.state[m] = st;
+    loss[m] = st == kLoss ? l : st == kBadLabel ? __builtin_nanf("") : 0.f;
+  }
+}
+
+// One workgroup: sum (mean: over the rows that have a loss) of the rows.
+__global__ __launch_bounds__(1024) void reduce_rows(const float *rows_loss, const uint32_t *state, uint32_t rows,
+                                                    bool mean, float *out) {
+  __shared__ double ss[16];
+  __shared__ uint32_t sc[16];
+  double s = 0.0;
+  uint32_t c = 0;
+  for (uint32_t m = threadIdx.x; m < rows; m += 1024) {
+    s += rows_loss[m];
+    c += state[m] != kNoLoss;
+  }
+  for (int o = 32; o; o >>= 1) {
+    s += __shfl_xor(s, o);
+    c += __shfl_xor(c, o);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    ss[threadIdx.x >> 6] = s;
+    sc[threadIdx.x >> 6] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    c = 0;
+    for (int q = 0; q < 16; q++) {
+      s += ss[q];
+      c += sc[q];
+    }
+    *out = (float)(mean ? (c ? s / c : 0.0) : s);
+  }
+}
+
+// Row factors of the gradient: g[m] = T * grad (mean: / count), 0 without a
+// loss; peak = max |g|; gn[m] = g[m] / peak, which the transposed dz carries
+// (1 in every row for sums and means, so it costs them no rounding).
+__global__ __launch_bounds__(1024) void row_factors(const uint32_t *state, uint32_t rows, const float *grad, int reduce,
+                                                    float temp, float *g, float *gn, float *peak) {
+  __shared__ float sm[16];
+  __shared__ uint32_t sc[16];
+  float mx = 0.f;
+  uint32_t c = 0;
+  for (uint32_t m = threadIdx.x; m < rows; m += 1024) {
+    c += state[m] != kNoLoss;
+    if (state[m] == kLoss) mx = __builtin_fmaxf(mx, __builtin_fabsf(grad[reduce == DF_REDUCE_NONE ? m : 0]));
+  }
+  for (int o = 32; o; o >>= 1) {
+    mx = __builtin_fmaxf(mx, __shfl_xor(mx, o));
+    c += __shfl_xor(c, o);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sm[threadIdx.x >> 6] = mx;
+    sc[threadIdx.x >> 6] = c;
+  }
+  __syncthreads();
+  mx = 0.f;
+  c = 0;
+  for (int q = 0; q < 16; q++) {
+    mx = __builtin_fmaxf(mx, sm[q]);
+    c += sc[q];
+  }
+  const float div = reduce == DF_REDUCE_MEAN && c ? (float)c : 1.f;
+  const float pk = mx > 0.f ? mx : 1.f;
+  for (uint32_t m = threadIdx.x; m < rows; m += 1024) {
+    const float v = state[m] == kLoss ? grad[reduce == DF_REDUCE_NONE ? m : 0] : 0.f;
+    g[m] = v * temp / div;
+    gn[m] = v / pk;
+  }
+  if (threadIdx.x == 0) *peak = pk * temp / div;
+}
+
+// dz at the target entries of vocabulary [v0, v0 + nv): (p - t) * mul with p
+// from the picked logit.  Entries of one row that name the same element each
+// write the same value, p minus the sum of their t.  One wave per row.
+template <class T>
+__global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved sv, uint32_t v0, uint32_t nv, float c,
+                                                  float mul, uint16_t *dz, uint32_t ldz) {
+  __shared__ int32_t ids[kMaxTop];
+  __shared__ float ws[kMaxTop];
+  const uint32_t m = blockIdx.x, lane = threadIdx.x, per = t.top ? t.top : 1;
+  if (sv.state[m] != kLoss) return;
+  float mx = -__builtin_huge_valf();
+  for (uint32_t j = lane; j < per; j += 64) {
+    const int32_t v = target_of(t, m, j);
+    const float a = t.top ? teacher_at(t, m, j) / t.temp : 0.f;
+    ids[j] = v;
+    ws[j] = a;
+    if (v >= 0) mx = __builtin_fmaxf(mx, a);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, o));
+  float s = 0.f;
+  for (uint32_t j = lane; j < per; j += 64) {
+    ws[j] = ids[j] >= 0 ? expf(ws[j] - mx) : 0.f;
+    s += ws[j];
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  __syncthreads();
+  const float l = sv.lse2[m];
+  for (uint32_t j = lane; j < per; j += 64) {
+    const int32_t v = ids[j];
+    if (v < 0 || (uint32_t)v < v0 || (uint32_t)v >= v0 + nv) continue;
+    float w = 0.f;
+    for (uint32_t q = 0; q < per; q++) w += ids[q] == v ? ws[q] : 0.f;
+    const float p = exp2_(sv.picked[(uint64_t)m * per + j] * c - l);
+    dz[(uint64_t)m * ldz + (v - v0)] = to_bits(T{}, (p - w / s) * mul);
+  }
+}
+
+// dst[c, r] = src[r, c] (times gn[r]); rows of another state than kLoss give
+// zeros where a state is given; dst rows hold rp elements, zeros past `rows`.
+template <class T>
+__global__ __launch_bounds__(256) void turn(const uint16_t *src, uint64_t ss, uint32_t rows, uint32_t cols,
+                                            uint16_t *dst, uint32_t rp, const uint32_t *state, const float *gn) {
+  __shared__ uint16_t tile[64][72];  // [c][r]
+  const uint32_t r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
+  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
+    const uint32_t rr = t / 8, c = t % 8, r = r0 + rr;
+    u32x4 v = {0, 0, 0, 0};
+    if (r < rows && c0 + c * 8 < cols && (!state || state[r] == kLoss)) {
+      v = *(const u32x4 *)(src + r * ss + c0 + c * 8);
+      if (gn) {
+        const float f = gn[r];
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+          v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+      tile[c * 8 + 2 * d][rr] = (uint16_t)v[d];
+      tile[c * 8 + 2 * d + 1][rr] = (uint16_t)(v[d] >> 16);
+    }
+  }
+  __syncthreads();
+  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
+    const uint32_t cc = t / 8, r = t % 8;
+    if (c0 + cc < cols && r0 + r * 8 < rp)
+      *(u32x4 *)(dst + (uint64_t)(c0 + cc) * rp + r0 + r * 8) = *(const u32x4 *)&tile[cc][r * 8];
+  }
+}
+
+// dx[m] = g[m] * mul * (sum of the planes), zero in rows without a loss.
+template <class T>
+__global__ __launch_bounds__(256) void finish_dx(const float *planes, uint32_t splits, uint32_t rows, uint32_t k,
+                                                 const uint32_t *state, const float *g, float mul, uint16_t *dx) {
+  const uint32_t m = blockIdx.x;
+  const bool live = state[m] == kLoss;
+  const float f = g[m] * mul;
+  for (uint32_t c = threadIdx.x * 4; c < k; c += 1024) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (live) {
+      for (uint32_t s = 0; s < splits; s++) v += *(const f32x4 *)(planes + ((uint64_t)s * rows + m) * k + c);
+      v *= f;
+    }
+    *(u32x2 *)(dx + (uint64_t)m * k + c) = u32x2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])};
+  }
+}
+
+__global__ __launch_bounds__(256) void fill_words(uint32_t *p, uint64_t n) {
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256) p[i] = 0;
+}
+
+// ---------------------------------------------------------------- host side
+uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
+uint64_t tiles_of(uint64_t m, uint64_t n, uint64_t t) { return up(m, t) / t * (up(n, t) / t); }
+
+// Output tile of a product: the largest that gives most CUs one.
+uint32_t tile_for(uint64_t m, uint64_t n) {
+  return tiles_of(m, n, 256) >= 192 ? 256 : tiles_of(m, n, 128) >= 192 ? 128 : 64;
+}
+uint32_t parts_of(uint64_t m, uint64_t n) {
+  const uint32_t t = tile_for(m, n);
+  return (uint32_t)(up(n, t) / t) * (t == 256 ? 4 : 2);
+}
+template <class T, class Epi>
+hipError_t product(const Gemm &g, const Epi &e, uint32_t tile, uint32_t splits, hipStream_t s) {
+  if (tile == 256) return gemm_launch<T, 256, 256, 2, 4>(g, e, splits, s);
+  if (tile == 128) return gemm_launch<T, 128, 128, 2, 2>(g, e, splits, s);
+  return gemm_launch<T, 64, 64, 2, 2>(g, e, splits, s);
+}
+
+df_status check(const df_loss *d) {
+  if (!d || (d->type != DF_TYPE_BF16 && d->type != DF_TYPE_F16)) return DF_ERR_ARG;
+  if (d->reduce != DF_REDUCE_NONE && d->reduce != DF_REDUCE_SUM && d->reduce != DF_REDUCE_MEAN) return DF_ERR_ARG;
+  if (d->rows > (1u << 21) || d->vocab == 0 || d->vocab > (1u << 21) || d->hidden == 0 || d->hidden % 8 ||
+      d->hidden > (1u << 17))
+    return DF_ERR_ARG;
+  if (d->x_stride < d->hidden || d->x_stride % 8 || d->x_stride > (1u << 21) || d->head_stride < d->hidden ||
+      d->head_stride % 8 || d->head_stride > (1u << 21))
+    return DF_ERR_ARG;
+  if (d->rows && (!d->x || ((uintptr_t)d->x & 15))) return DF_ERR_ARG;
+  if (!d->head || ((uintptr_t)d->head & 15)) return DF_ERR_ARG;
+  if (d->top > kMaxTop || !(d->temperature > 0.f) || !(d->temperature < INFINITY)) return DF_ERR_ARG;
+  if (d->top == 0) {
+    if (d->temperature != 1.f || (d->rows && (!d->labels || ((uintptr_t)d->labels & 7)))) return DF_ERR_ARG;
+  } else {
+    if (d->teacher_type != DF_TYPE_BF16 && d->teacher_type != DF_TYPE_F16 && d->teacher_type != DF_TYPE_F32)
+      return DF_ERR_ARG;
+    if (d->rows && (!d->index || ((uintptr_t)d->index & 7) || !d->teacher ||
+                    ((uintptr_t)d->teacher & (d->teacher_type == DF_TYPE_F32 ? 3 : 1))))
+      return DF_ERR_ARG;
+  }
+  return DF_OK;
+}
+Targets targets_of(const df_loss *d) {
+  return Targets{d->labels,       d->ignore_index,        d->index,         d->teacher,          d->index_stride,
+                 d->teacher_stride, (int)d->teacher_type, d->top,           (uint32_t)d->vocab,  d->temperature};
+}
+uint32_t per_row(const df_loss *d) { return d->top ? d->top : 1; }
+Saved saved_of(const df_loss *d, void *p) {
+  float *f = (float *)p;
+  return Saved{f, (uint32_t *)(f + d->rows), f + 2 * d->rows};
+}
+#define DFH_TRY(e) \
+  do {             \
+    if ((e) != hipSuccess) return DF_ERR_HIP; \
+  } while (0)
+
+template <class T>
+df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws, hipStream_t s) {
+  const uint32_t rows = (uint32_t)d->rows, vocab = (uint32_t)d->vocab, k = (uint32_t)d->hidden;
+  const Targets t = targets_of(d);
+  const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
+  const uint64_t entries = (uint64_t)rows * per_row(d);
+  hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)((entries + 3) / 4)), dim3(256), 0, s, t, rows, x, d->x_stride,
+                     head, d->head_stride, k, sv.picked);
+  DFH_TRY(hipGetLastError());
+  float2 *parts = (float2 *)ws;
+  const uint32_t np = parts_of(rows, vocab);
+  const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0};
+  DFH_TRY((product<T>(g, EpiStats{parts, kLog2e / d->temperature}, tile_for(rows, vocab), 1, s)));
+  float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + up(8ull * np * rows, 256));
+  hipLaunchKernelGGL(finish_rows, dim3((rows + 15) / 16), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv, per);
+  DFH_TRY(hipGetLastError());
+  return DF_OK;
+}
+
+// How a gradient pass is cut: `nv` vocabulary entries a piece (a multiple of
+// 256), so that the piece's dz, its transpose and the turned head rows stay
+// within about the 256 MB that the last-level cache holds; `splits` parts of a
+// piece's sum for dx, whose output is small.
+struct Plan {
+  uint32_t nv, mp, splits, tile_dx;
+  uint64_t dz, dzt, ht, xt, planes, fac, total;
+};
+Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
+  Plan p;
+  const uint64_t rows = d->rows, k = d->hidden, v8 = up(d->vocab, 8);
+  p.mp = (uint32_t)up(rows, 8);
+  const uint64_t per = 2 * rows + (want_dhead ? 2 * p.mp : 0) + (want_dx ? 2 * k : 0);
+  uint64_t nv = (256ull << 20) / per / 256 * 256;
+  if (nv < 2048) nv = 2048;
+  if (nv > v8) nv = v8;
+  p.nv = (uint32_t)nv;
+  p.tile_dx = tile_for(rows, k);
+  const uint64_t tiles = tiles_of(rows, k, p.tile_dx), most = (nv + 511) / 512;
+  const uint64_t want = tiles >= 192 ? 1 : (256 + tiles - 1) / tiles;
+  p.splits = (uint32_t)(want < most ? want : most);
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  p.fac = take(4 * (2 * rows + 1));
+  p.dz = take(2 * rows * nv);
+  p.dzt = take(want_dhead ? 2 * nv * p.mp : 0);
+  p.xt = take(want_dhead ? 2 * k * p.mp : 0);
+  p.ht = take(want_dx ? 2 * k * nv : 0);
+  p.planes = take(want_dx ? 4ull * p.splits * rows * k : 0);
+  p.total = at;
+  return p;
+}
+
+template <class T>
+df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16_t *dx, uint16_t *dhead, uint8_t *ws,
+                    float mul, hipStream_t s) {
+  const Plan p = plan_of(d, dx != nullptr, dhead != nullptr);
+  const uint32_t rows = (uint32_t)d->rows, vocab = (uint32_t)d->vocab, k = (uint32_t)d->hidden;
+  const Targets t = targets_of(d);
+  const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
+  const float c = kLog2e / d->temperature;
+  float *g = (float *)(ws + p.fac), *gn = g + rows, *peak = gn + rows;
+  uint16_t *dz = (uint16_t *)(ws + p.dz), *dzt = (uint16_t *)(ws + p.dzt), *xt = (uint16_t *)(ws + p.xt),
+           *ht = (uint16_t *)(ws + p.ht);
+  float *planes = (float *)(ws + p.planes);
+  hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, (int)d->reduce,
+                     d->temperature, g, gn, peak);
+  if (dhead)
+    hipLaunchKernelGGL((turn<T>), dim3((p.mp + 63) / 64, (k + 63) / 64), dim3(256), 0, s, x, d->x_stride, rows, k, xt,
+                       p.mp, (const uint32_t *)sv.state, (const float *)nullptr);
+  DFH_TRY(hipGetLastError());
+  for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
+    const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);
+    const uint16_t *hp = head + (uint64_t)v0 * d->head_stride;
+    const Gemm gz = {x, hp, d->x_stride, d->head_stride, rows, nv, k, 0, 0, 0};
+    DFH_TRY((product<T>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, tile_for(rows, nv), 1, s)));
+    hipLaunchKernelGGL((fix_targets<T>), dim3(rows), dim3(64), 0, s, t, sv, v0, nv, c, mul, dz, ldz);
+    DFH_TRY(hipGetLastError());
+    if (dhead) {
+      hipLaunchKernelGGL((turn<T>), dim3((p.mp + 63) / 64, (nv + 63) / 64), dim3(256), 0, s, (const uint16_t *)dz,
+                         (uint64_t)ldz, rows, nv, dzt, p.mp, (const uint32_t *)nullptr, (const float *)gn);
+      DFH_TRY(hipGetLastError());
+      const Gemm gw = {dzt, xt, p.mp, p.mp, nv, k, p.mp, 0, 0, 0};
+      DFH_TRY((product<T>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul}, tile_for(nv, k), 1, s)));
+    }
+    if (dx) {
+      hipLaunchKernelGGL((turn<T>), dim3((ldz + 63) / 64, (k + 63) / 64), dim3(256), 0, s, hp, d->head_stride, nv, k,
+                         ht, ldz, (const uint32_t *)nullptr, (const float *)nullptr);
+      DFH_TRY(hipGetLastError());
+      const Gemm gx = {dz, ht, ldz, ldz, rows, k, ldz, 0, 0, 0};
+      DFH_TRY((product<T>(gx, EpiPlane{planes, k, v0 != 0}, p.tile_dx, p.splits, s)));
+    }
+  }
+  if (dx) {
+    hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.splits, rows, k,
+                       (const uint32_t *)sv.state, (const float *)g, 1.f / mul, dx);
+    DFH_TRY(hipGetLastError());
+  }
+  return DF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t df_loss_saved_bytes(const df_loss *d) {
+  return check(d) == DF_OK ? 4 * d->rows * (2 + per_row(d)) : 0;
+}
+
+uint64_t df_loss_workspace_bytes(const df_loss *d) {
+  if (check(d) != DF_OK || d->rows == 0) return 0;
+  return up(8ull * parts_of(d->rows, d->vocab) * d->rows, 256) + up(4 * d->rows, 256);
+}
+
+uint64_t df_loss_grad_workspace_bytes(const df_loss *d, int want_dhead) {
+  if (check(d) != DF_OK || d->rows == 0) return 0;
+  return plan_of(d, true, want_dhead != 0).total;
+}
+
+df_status df_vocab_loss(const df_loss *d, float *loss, void *saved, void *workspace, uint64_t workspace_bytes,
+                        hipStream_t stream) {
+  df_status st = check(d);
+  if (st != DF_OK) return st;
+  if (d->rows == 0) {
+    if (d->reduce == DF_REDUCE_NONE) return DF_OK;
+    if (!loss) return DF_ERR_ARG;
+    hipLaunchKernelGGL(fill_words, dim3(1), dim3(256), 0, stream, (uint32_t *)loss, (uint64_t)1);
+    return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
+  }
+  if (!loss || !saved || ((uintptr_t)saved & 3) || ((uintptr_t)loss & 3) || !workspace ||
+      ((uintptr_t)workspace & 255) || workspace_bytes < df_loss_workspace_bytes(d))
+    return DF_ERR_ARG;
+  const Saved sv = saved_of(d, saved);
+  uint8_t *ws = (uint8_t *)workspace;
+  st = d->type == DF_TYPE_BF16 ? loss_rows<BF16>(d, loss, sv, ws, stream) : loss_rows<F16>(d, loss, sv, ws, stream);
+  if (st != DF_OK || d->reduce == DF_REDUCE_NONE) return st;
+  const float *per = (const float *)(ws + up(8ull * parts_of(d->rows, d->vocab) * d->rows, 256));
+  hipLaunchKernelGGL(reduce_rows, dim3(1), dim3(1024), 0, stream, per, (const uint32_t *)sv.state, (uint32_t)d->rows,
+                     d->reduce == DF_REDUCE_MEAN, loss);
+  return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
+}
+
+df_status df_vocab_loss_grad(const df_loss *d, const void *saved, const float *grad_loss, void *dx, void *dhead,
+                             void *workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  const df_status st = check(d);
+  if (st != DF_OK) return st;
+  if ((!dx && !dhead && d->rows) || ((uintptr_t)dx & 15) || ((uintptr_t)dhead & 15)) return DF_ERR_ARG;
+  if (d->rows == 0) {
+    if (!dhead) return DF_OK;
+    hipLaunchKernelGGL(fill_words, dim3(2048), dim3(256), 0, stream, (uint32_t *)dhead, d->vocab * d->hidden / 2);
+    return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
+  }
+  if (!saved || ((uintptr_t)saved & 3) || !grad_loss || ((uintptr_t)grad_loss & 3) || !workspace ||
+      ((uintptr_t)workspace & 255) || workspace_bytes < plan_of(d, dx != nullptr, dhead != nullptr).total)
+    return DF_ERR_ARG;
+  const Saved sv = saved_of(d, const_cast<void *>(saved));
+  if (d->type == DF_TYPE_BF16)
+    return loss_grad<BF16>(d, sv, grad_loss, (uint16_t *)dx, (uint16_t *)dhead, (uint8_t *)workspace, 1.f, stream);
+  return loss_grad<F16>(d, sv, grad_loss, (uint16_t *)dx, (uint16_t *)dhead, (uint8_t *)workspace, 32768.f, stream);
+}
+
+}  // extern "C"

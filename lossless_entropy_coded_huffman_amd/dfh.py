@@ -53,6 +53,25 @@ class df_device_view(ctypes.Structure):
                 ("lut", ctypes.c_void_p), ("dtab", ctypes.c_void_p)]
 
 
+class df_u4_matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("group_size", ctypes.c_uint32), ("scale_type", ctypes.c_int),
+                ("scale_stride", ctypes.c_uint64), ("zero_stride", ctypes.c_uint64),
+                ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
+class df_loss(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("reduce", ctypes.c_int),
+                ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("hidden", ctypes.c_uint64),
+                ("x_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+                ("x", ctypes.c_void_p), ("head", ctypes.c_void_p),
+                ("labels", ctypes.c_void_p), ("ignore_index", ctypes.c_int64),
+                ("index", ctypes.c_void_p), ("teacher", ctypes.c_void_p),
+                ("teacher_type", ctypes.c_int), ("top", ctypes.c_uint32),
+                ("index_stride", ctypes.c_uint64), ("teacher_stride", ctypes.c_uint64),
+                ("temperature", ctypes.c_float)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -91,6 +110,21 @@ _SIGNATURES = {
     "df_decompress_batch": (ctypes.c_int, [ctypes.POINTER(df_device_view),
                                            ctypes.POINTER(ctypes.c_void_p), ctypes.c_uint32,
                                            ctypes.c_void_p]),
+    "df_linear_u4_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_u4_matrix), ctypes.c_uint64]),
+    "df_linear_u4": (ctypes.c_int, [ctypes.POINTER(df_u4_matrix), ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64,
+                                    ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64,
+                                    ctypes.c_void_p]),
+    "df_linear_u4_grad_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_u4_matrix), ctypes.c_uint64]),
+    "df_linear_u4_grad": (ctypes.c_int, [ctypes.POINTER(df_u4_matrix), ctypes.c_int, ctypes.c_void_p,
+                                         ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_uint64, ctypes.c_void_p]),
+    "df_loss_saved_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
+    "df_loss_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
+    "df_vocab_loss": (ctypes.c_int, [ctypes.POINTER(df_loss), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_uint64, ctypes.c_void_p]),
+    "df_loss_grad_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss), ctypes.c_int]),
+    "df_vocab_loss_grad": (ctypes.c_int, [ctypes.POINTER(df_loss), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
 }
 
 

@@ -1,0 +1,345 @@
+"""Operators on what the codec stores, through the C ABI (include/dfh.h):
+
+* ``linear_u4``: products with uint4 weights and group scales, the packed
+  nibbles that ``df_decompress`` yields for a uint4 container, for one token up
+  to long prompts, with the gradient to the input;
+* ``vocab_loss``: softmax cross entropy of hidden states against an LM head,
+  the logits never stored, with the gradients to both;
+* ``distill_loss``: the divergence from a teacher's top logits over the same
+  head, with the gradients to both.
+
+Everything is enqueued on ``stream`` (default: the current stream of the
+tensors' device) and returns without synchronising.  Outputs and workspaces are
+torch tensors allocated on that stream, so a call can be captured into a HIP
+graph, and two calls never share one.  A call given another stream than the
+current one waits, as every torch consumer does, for nothing by itself: the
+caller orders the streams.  An input that another stream may free while the call
+runs is recorded on the call's stream.
+
+In autograd a call on the current stream records its gradient; a gradient of a
+gradient is refused.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import dfh
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_REDUCE = {"none": 0, "sum": 1, "mean": 2}
+
+
+def _type(t: torch.Tensor, what: str, f32: bool = False) -> int:
+    if t.dtype not in _TYPES or (t.dtype == torch.float32 and not f32):
+        raise TypeError("%s must be bfloat16%s, got %s" % (what, ", float16 or float32" if f32 else " or float16",
+                                                           t.dtype))
+    return _TYPES[t.dtype]
+
+
+def _on(t: torch.Tensor, dev: torch.device, what: str):
+    if not t.is_cuda or t.device != dev:
+        raise ValueError("%s must be a tensor on %s" % (what, dev))
+
+
+def _rows16(t: torch.Tensor) -> torch.Tensor:
+    """t [r, c] with a row stride that is a multiple of 8 elements, unit column
+    stride and a 16-byte aligned base: itself, or a copy."""
+    if t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0:
+        return t
+    c = t.contiguous()
+    return c if c.data_ptr() % 16 == 0 else c.clone()
+
+
+@contextlib.contextmanager
+def _launching(stream, dev, tensors):
+    """The torch stream a call runs on, made current (with its device) when it
+    is not; inputs are then recorded on it."""
+    cur = torch.cuda.current_stream(dev)
+    ts = cur if stream is None else dfh._torch_stream(stream, dev)
+    if ts.cuda_stream == cur.cuda_stream and torch.cuda.current_device() == dev.index:
+        yield ts
+        return
+    with torch.cuda.device(dev), torch.cuda.stream(ts):
+        yield ts
+        if ts.cuda_stream != cur.cuda_stream:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(ts)
+
+
+def _workspace(nbytes: int, dev) -> torch.Tensor:
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------- uint4 products
+class U4Matrix:
+    """A layer's uint4 weights on the device (df_u4_matrix; the tensors are
+    borrowed and kept alive).
+
+    packed: the nibbles, rows * cols / 2 bytes (what ``df_decompress`` writes
+    for a uint4 container of the layer); scales [rows, groups] in bfloat16,
+    float16 or float32, groups = ceil(cols / group_size); zeros: uint8 zero
+    points of the same shape, or None for 8.  group_size (default: cols) is a
+    multiple of 32, or at least cols.  scales and zeros may be broadcast over
+    the rows (stride 0): one scale for a layer is
+    ``scale.reshape(1, 1).expand(rows, 1)``."""
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, *, cols: int,
+                 group_size: int | None = None):
+        cols = int(cols)
+        group_size = cols if group_size is None else int(group_size)
+        if not packed.is_cuda or not packed.is_contiguous() or packed.element_size() != 1:
+            raise ValueError("packed must be a contiguous byte tensor on the device")
+        if cols < 8 or cols % 8 or cols > 1 << 20:
+            raise ValueError("cols must be a multiple of 8 from 8 to 2^20, got %d" % cols)
+        if group_size < 1 or (group_size < cols and group_size % 32):
+            raise ValueError("group_size must be a multiple of 32, or at least cols")
+        if scales.dim() != 2:
+            raise ValueError("scales must be [rows, groups]")
+        rows, groups = int(scales.shape[0]), (cols + group_size - 1) // group_size
+        if rows < 1 or rows > 1 << 21 or scales.shape[1] != groups:
+            raise ValueError("scales must be [rows, %d] with 1 to 2^21 rows, got %s" % (groups, tuple(scales.shape)))
+        if packed.numel() < rows * cols // 2:
+            raise ValueError("packed holds fewer than %d x %d nibbles" % (rows, cols))
+        if packed.data_ptr() % 4:
+            raise ValueError("packed must be 4-byte aligned")
+        _on(scales, packed.device, "scales")
+        self.scale_type = _type(scales, "scales", f32=True)
+        if zeros is not None:
+            _on(zeros, packed.device, "zeros")
+            if zeros.dtype != torch.uint8 or zeros.shape != scales.shape:
+                raise ValueError("zeros must be uint8 of the scales' shape")
+        if scales.requires_grad:
+            raise ValueError("no gradient goes to the scales: detach them")
+        if groups > 1 and scales.stride(1) != 1:
+            scales = scales.contiguous()
+        if zeros is not None and groups > 1 and zeros.stride(1) != 1:
+            zeros = zeros.contiguous()
+        self.packed, self.scales, self.zeros = packed, scales, zeros
+        self.rows, self.cols, self.group_size, self.device = rows, cols, group_size, packed.device
+        self.view = dfh.df_u4_matrix(rows, cols, min(group_size, 0xFFFFFFFF), self.scale_type, scales.stride(0),
+                                     0 if zeros is None else zeros.stride(0), packed.data_ptr(), scales.data_ptr(),
+                                     _p(zeros))
+        self._ref = ctypes.byref(self.view)
+
+    def _tensors(self):
+        return (self.packed, self.scales, self.zeros)
+
+
+def _linear(x: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
+    _on(x, w.device, "x")
+    ty = _type(x, "x")
+    if x.dim() < 1 or x.shape[-1] != w.cols:
+        raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(x.shape)))
+    L = dfh.lib()
+    with _launching(stream, w.device, (x,) + w._tensors()) as ts:
+        x2 = _rows16(x if x.dim() == 2 else x.reshape(-1, w.cols))
+        m = x2.shape[0]
+        y = torch.empty((m, w.rows), dtype=x.dtype, device=w.device)
+        need = L.df_linear_u4_workspace_bytes(w._ref, m)
+        ws = _workspace(need, w.device) if need else None
+        dfh._check(L.df_linear_u4(w._ref, ty, x2.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws), need,
+                                  ts.cuda_stream), "df_linear_u4")
+    return y if x.dim() == 2 else y.view(x.shape[:-1] + (w.rows,))
+
+
+def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
+    """dx[..., k] = sum over n of dy[..., n] W[n, k]: the gradient of linear_u4
+    to its input, in dy's type (bfloat16 or float16)."""
+    _on(dy, w.device, "dy")
+    ty = _type(dy, "dy")
+    if dy.dim() < 1 or dy.shape[-1] != w.rows:
+        raise ValueError("dy must be [..., %d], got %s" % (w.rows, tuple(dy.shape)))
+    L = dfh.lib()
+    with _launching(stream, w.device, (dy,) + w._tensors()) as ts:
+        d2 = dy.reshape(-1, w.rows)
+        if w.rows % 8 == 0:
+            d2 = _rows16(d2)
+        elif d2.stride(1) != 1 or d2.stride(0) < w.rows:
+            d2 = d2.contiguous()
+        m = d2.shape[0]
+        dx = torch.empty((m, w.cols), dtype=dy.dtype, device=w.device)
+        need = L.df_linear_u4_grad_workspace_bytes(w._ref, m)
+        ws = _workspace(need, w.device)
+        dfh._check(L.df_linear_u4_grad(w._ref, ty, d2.data_ptr(), m, d2.stride(0), dx.data_ptr(), ws.data_ptr(), need,
+                                       ts.cuda_stream), "df_linear_u4_grad")
+    return dx.view(dy.shape[:-1] + (w.cols,))
+
+
+class _LinearU4(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, stream):
+        ctx.w, ctx.stream = w, stream
+        return _linear(x, w, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        return linear_u4_grad(dy, ctx.w), None, None
+
+
+def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
+    """y = x W^T for W[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[...]),
+    x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
+    are float32; up to 64 rows multiply the integer weights exactly, more round
+    each weight once to x's type.  Differentiable in x."""
+    if x.requires_grad and torch.is_grad_enabled():
+        return _LinearU4.apply(x, w, stream)
+    return _linear(x, w, stream)
+
+
+# ---------------------------------------------------------------------- losses
+class _Loss:
+    """A call's df_loss and the tensors it points to."""
+
+    def __init__(self, x, head, reduction, labels=None, ignore_index=-100, teacher=None, index=None, temperature=1.0):
+        if reduction not in _REDUCE:
+            raise ValueError("reduction must be 'none', 'sum' or 'mean', got %r" % (reduction,))
+        if not head.is_cuda or head.dim() != 2:
+            raise ValueError("head must be a [vocab, hidden] tensor on the device")
+        vocab, hidden = int(head.shape[0]), int(head.shape[1])
+        dev = head.device
+        _on(x, dev, "x")
+        ty = _type(head, "head")
+        if x.dtype != head.dtype:
+            raise TypeError("x and head must have one type, got %s and %s" % (x.dtype, head.dtype))
+        if x.dim() < 1 or x.shape[-1] != hidden:
+            raise ValueError("x must be [..., %d], got %s" % (hidden, tuple(x.shape)))
+        if hidden < 8 or hidden % 8 or hidden > 1 << 17:
+            raise ValueError("hidden must be a multiple of 8 from 8 to 2^17, got %d" % hidden)
+        if vocab < 1 or vocab > 1 << 21:
+            raise ValueError("vocab must lie in 1 .. 2^21, got %d" % vocab)
+        self.shape = tuple(x.shape[:-1])
+        self.reduction = reduction
+        d = dfh.df_loss()
+        d.type, d.reduce, d.vocab, d.hidden = ty, _REDUCE[reduction], vocab, hidden
+        d.temperature = float(temperature)
+        d.ignore_index = int(ignore_index)
+        if labels is not None:
+            _on(labels, dev, "labels")
+            if labels.dtype != torch.int64 or tuple(labels.shape) != self.shape:
+                raise ValueError("labels must be int64 of shape %s" % (self.shape,))
+        else:
+            if not 0.0 < d.temperature < float("inf"):
+                raise ValueError("temperature must be positive and finite")
+            _on(teacher, dev, "teacher")
+            _on(index, dev, "index")
+            d.teacher_type = _type(teacher, "teacher", f32=True)
+            if index.dtype != torch.int64 or tuple(index.shape[:-1]) != self.shape or index.shape != teacher.shape:
+                raise ValueError("index must be int64 of shape %s + (top,), like teacher" % (self.shape,))
+            d.top = int(index.shape[-1])
+            if not 1 <= d.top <= 1024:
+                raise ValueError("top must lie in 1 .. 1024, got %d" % d.top)
+        self.inputs = (x, head, labels, teacher, index)
+        self.desc, self.dev = d, dev
+
+    def bind(self):
+        """Lays the inputs out and points the descriptor at them (on the call's stream)."""
+        x, head, labels, teacher, index = self.inputs
+        d = self.desc
+        x = _rows16(x.detach().reshape(-1, d.hidden))
+        head = _rows16(head.detach())
+        d.rows = x.shape[0]
+        d.x, d.x_stride, d.head, d.head_stride = x.data_ptr(), x.stride(0), head.data_ptr(), head.stride(0)
+        if labels is not None:
+            labels = labels.reshape(-1).contiguous()
+            d.labels = labels.data_ptr()
+        else:
+            teacher, index = teacher.detach().reshape(-1, d.top), index.reshape(-1, d.top)
+            if teacher.stride(1) != 1:
+                teacher = teacher.contiguous()
+            if index.stride(1) != 1:
+                index = index.contiguous()
+            d.teacher, d.teacher_stride = teacher.data_ptr(), teacher.stride(0)
+            d.index, d.index_stride = index.data_ptr(), index.stride(0)
+        self.held = (x, head, labels, teacher, index)
+
+    def forward(self, stream):
+        L = dfh.lib()
+        with _launching(stream, self.dev, self.inputs) as ts:
+            self.bind()
+            ref = ctypes.byref(self.desc)
+            rows = int(self.desc.rows)
+            none = self.reduction == "none"
+            loss = torch.empty(rows if none else 1, dtype=torch.float32, device=self.dev)
+            saved = torch.empty(max(L.df_loss_saved_bytes(ref) // 4, 1), dtype=torch.float32, device=self.dev)
+            need = L.df_loss_workspace_bytes(ref)
+            ws = _workspace(need, self.dev)
+            dfh._check(L.df_vocab_loss(ref, loss.data_ptr(), saved.data_ptr(), ws.data_ptr(), need, ts.cuda_stream),
+                       "df_vocab_loss")
+        return loss.view(self.shape if none else ()), saved
+
+    def grads(self, saved, gout, want_x, want_head):
+        L = dfh.lib()
+        x, head = self.inputs[0], self.inputs[1]
+        with _launching(None, self.dev, ()) as ts:
+            ref = ctypes.byref(self.desc)
+            g = gout.to(torch.float32).reshape(-1).contiguous()
+            dx = torch.empty((int(self.desc.rows), head.shape[1]), dtype=x.dtype, device=self.dev) if want_x else None
+            dh = torch.empty(head.shape, dtype=head.dtype, device=self.dev) if want_head else None
+            need = L.df_loss_grad_workspace_bytes(ref, int(want_head))
+            ws = _workspace(need, self.dev)
+            dfh._check(L.df_vocab_loss_grad(ref, saved.data_ptr(), g.data_ptr(), _p(dx), _p(dh), ws.data_ptr(), need,
+                                            ts.cuda_stream), "df_vocab_loss_grad")
+        return (None if dx is None else dx.view(x.shape)), dh
+
+
+class _LossFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, head, call, stream):
+        loss, saved = call.forward(stream)
+        # the tensors that the gradient reads again: saved through autograd, so
+        # that a change made to one in between is refused
+        ctx.save_for_backward(*[t for t in call.inputs if t is not None], saved)
+        ctx.call = call
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gout):
+        saved = ctx.saved_tensors[-1]
+        dx, dh = ctx.call.grads(saved, gout, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return dx, dh, None, None
+
+
+def _run_loss(call, stream):
+    x, head = call.inputs[0], call.inputs[1]
+    if torch.is_grad_enabled() and (x.requires_grad or head.requires_grad):
+        return _LossFunction.apply(x, head, call, stream)
+    return call.forward(stream)[0]
+
+
+def vocab_loss(x: torch.Tensor, head: torch.Tensor, labels: torch.Tensor, *, ignore_index: int = -100,
+               reduction: str = "mean", stream=None) -> torch.Tensor:
+    """Softmax cross entropy of the logits x head^T against labels.
+
+    x [..., hidden] and head [vocab, hidden] in bfloat16 or float16 (one type),
+    labels [...] int64.  Rows labelled ignore_index have no loss and no gradient,
+    whatever x holds there; another label outside the vocabulary gives NaN in
+    its row's loss and no gradient.  reduction "mean" is over the rows that have
+    a loss (0 when there are none), "sum", or "none" (the shape of labels).
+    The loss is float32.  Differentiable in x and head."""
+    return _run_loss(_Loss(x, head, reduction, labels=labels, ignore_index=ignore_index), stream)
+
+
+def distill_loss(x: torch.Tensor, head: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor, *,
+                 temperature: float = 1.0, reduction: str = "mean", stream=None) -> torch.Tensor:
+    """Divergence of the student's softmax over the whole vocabulary from the
+    teacher's over its top logits:
+
+        t = softmax(teacher / T),  q = softmax(x head^T / T)
+        loss = T^2 sum_j t_j (log t_j - log q[index_j])
+
+    teacher [..., top] (bfloat16, float16 or float32) and index [..., top]
+    (int64), as torch.topk gives them; entries whose index lies outside the
+    vocabulary (-1) are padding, a row of padding has no loss and no gradient.
+    top is at most 1024.  x, head, reduction and the result as in vocab_loss.
+    Differentiable in x and head; the teacher gets no gradient."""
+    return _run_loss(_Loss(x, head, reduction, teacher=teacher, index=index, temperature=temperature), stream)
