@@ -21,7 +21,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace dfh {
 // Unnamed: every source that includes this has kernels of its own, so that two
@@ -231,6 +233,28 @@ struct EpiPlane {
 };
 
 // ------------------------------------------------------------------- launch
+// Raises a kernel's LDS limit where a launch needs more than 64 KiB, once per
+// kernel and device.
+hipError_t allow_lds(const void *fn, uint32_t bytes) {
+  if (bytes <= 65536) return hipSuccess;
+  static std::mutex mu;
+  static std::map<std::pair<int, const void *>, bool> raised;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    bool &have = raised[{dev, fn}];
+    if (!have) {
+      e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      have = e == hipSuccess;
+    }
+  } catch (...) {  // nothing throws across the C entries
+    e = hipErrorOutOfMemory;
+  }
+  return e;
+}
+
 template <class T, int BM, int BN, int WM, int WN, class Epi>
 hipError_t gemm_launch(Gemm g, const Epi &epi, uint32_t splits, hipStream_t stream) {
   constexpr uint32_t lds = 2 * (BM + BN) * 128;
@@ -238,19 +262,8 @@ hipError_t gemm_launch(Gemm g, const Epi &epi, uint32_t splits, hipStream_t stre
   g.nt = (g.n + BN - 1) / BN;
   const uint32_t nkb = (g.k + kBK - 1) / kBK;
   g.kb_per_split = (nkb + splits - 1) / splits;
-  if (lds > 65536) {  // raise the kernel's LDS limit, once per device
-    static std::atomic<uint64_t> raised{0};
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(raised.load(std::memory_order_acquire) & bit) || !bit) {
-      e = hipFuncSetAttribute((const void *)gemm_nt<T, BM, BN, WM, WN, Epi>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-      raised.fetch_or(bit, std::memory_order_release);
-    }
-  }
+  const hipError_t e = allow_lds((const void *)gemm_nt<T, BM, BN, WM, WN, Epi>, lds);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gemm_nt<T, BM, BN, WM, WN, Epi>), dim3(g.mt * g.nt, splits), dim3(64 * WM * WN), lds, stream, g,
                      epi);
   return hipGetLastError();

@@ -6,8 +6,8 @@
 // The weights are the packed nibbles that a uint4 container decodes to: the
 // element n * cols + k, two per byte, the even one in the low nibble.
 //
-// Few rows (up to 64): u4_rows reads the nibbles once and feeds the matrix
-// cores with the integers themselves; the scale multiplies a group's FP32 sum.
+// Few rows: u4_tokens (up to 4) and u4_tile (up to 256) feed the matrix cores
+// with the integers themselves, and the scale multiplies a group's FP32 sum.
 // More rows: the weights are expanded to 16 bits in the caller's workspace and
 // gemm_nt does the product.
 #include <hip/hip_runtime.h>
@@ -29,6 +29,7 @@ struct U4 {
   uint32_t n, k;
   uint32_t group32;  // group / 32; 0: one group per row
   uint32_t magic;    // floor(2^31 / group32) + 1, or 0
+  uint32_t groups;   // per row
   uint64_t sstride, zstride;
 };
 
@@ -43,16 +44,23 @@ __device__ __forceinline__ float scale_at(const U4 &w, uint32_t n, uint32_t g) {
   const uint16_t b = ((const uint16_t *)w.scales)[i];
   return w.scale_type == DF_TYPE_BF16 ? from_bits(BF16{}, b) : from_bits(F16{}, b);
 }
+// A raw scale of the type that u4_rows was made for.
+__device__ __forceinline__ float scale_of(const U4 &, float s) { return s; }
+__device__ __forceinline__ float scale_of(const U4 &w, uint16_t b) {
+  return w.scale_type == DF_TYPE_BF16 ? from_bits(BF16{}, b) : from_bits(F16{}, b);
+}
 __device__ __forceinline__ float zero_at(const U4 &w, uint32_t n, uint32_t g) {
   return w.zeros ? (float)w.zeros[n * w.zstride + g] : 8.f;
 }
 
-// Eight nibbles -> eight 16-bit floats bias + q, in the order of elements
-// 0,4 1,5 2,6 3,7: the nibble lands in the low mantissa bits of a constant
-// whose unit in the last place is one (BF16 128, FP16 1024), so a pair costs
-// one shift and one and-or.  FP16 then takes 1024 + z off each pair with one
-// packed addition, exactly; there is no such addition for BF16, whose bias
-// (and zero point) come off the group's sum instead.
+// Eight nibbles -> eight 16-bit floats bias + q, in order: the nibble lands in
+// the low mantissa bits of a constant whose unit in the last place is one (BF16
+// 128, FP16 1024), a shift and an and-or for the elements i and i + 4; a byte
+// permute then pairs neighbours (11 operations for 8 weights; left as (i, i + 4)
+// it would be 7, but x would need 4 permutes for every operand of 8 instead).
+// FP16 then takes 1024 + z off each pair with one packed addition, exactly;
+// there is no such addition for BF16, whose bias (and zero point) come off the
+// group's sum instead.
 template <class T>
 struct Bias;
 template <>
@@ -72,7 +80,9 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 template <class T>
 __device__ __forceinline__ u32x4 widen(uint32_t w, uint32_t off) {
   constexpr uint32_t m = 0x000F000Fu, b = Bias<T>::bits;
-  u32x4 v = {(w & m) | b, ((w >> 4) & m) | b, ((w >> 8) & m) | b, ((w >> 12) & m) | b};
+  const uint32_t p = (w & m) | b, q = ((w >> 4) & m) | b, r = ((w >> 8) & m) | b, t = ((w >> 12) & m) | b;
+  u32x4 v = {__builtin_amdgcn_perm(q, p, 0x05040100u), __builtin_amdgcn_perm(t, r, 0x05040100u),
+             __builtin_amdgcn_perm(q, p, 0x07060302u), __builtin_amdgcn_perm(t, r, 0x07060302u)};
   if constexpr (!Bias<T>::in_sum) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -82,12 +92,6 @@ __device__ __forceinline__ u32x4 widen(uint32_t w, uint32_t off) {
   }
   return v;
 }
-// Eight consecutive 16-bit values into the same order.
-__device__ __forceinline__ u32x4 pair_up(u32x4 v) {
-  return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-               __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-}
-
 // One output from the definition, in order; taken where BF16's fast sum is not
 // finite (an infinite or very large x: the bias would turn inf * w into NaN).
 template <class T>
@@ -106,133 +110,383 @@ __device__ float dot_plain(const U4 &w, const uint16_t *xr, uint32_t n) {
   return acc;
 }
 
-// y for up to 16 MT rows.  A workgroup makes 16 NT columns; its waves share
-// the summed index (blocks of 128 go to them in turn) and add up through LDS.
-// Matrix operand A is x (16 rows), B the weights (16 columns n): lane l loads
-// 16 bytes of weight row l % 16, elements 32 (l / 16) .. + 31 of the block, and
-// two exchange steps between the lane groups give every 32-element step of the
-// block to one matrix instruction, so a scale may change every 32 elements.
-// BF16: T = sum x (bias + q) and S = sum x (B operand all ones) give a group's
-// part as s (T - (bias + z) S), in FP32; FP16: T = sum x (q - z) and s T.
-template <class T, int MT, int NT, int W, int U, bool kSub, bool kWide>
-__global__ __launch_bounds__(64 * W) void u4_rows(const U4 w, const uint16_t *x, uint64_t xs, uint32_t m,
-                                                  uint16_t *y) {
-  __shared__ f32x4 part[W][NT * MT][64];
+// A byte 8 where a matrix has no zero points, read like any other.
+__device__ const uint32_t g_eights = 0x08080808u;
+
+// A wave's rows of the weights (16 NT of them, row n0 + 16 j + lane % 16) as
+// the operands below want them.  SUB, the groups that 128 elements hold (1, 2,
+// 4), fixes how scales and zero points are read: a stage's 4 SUB (blocks of 128)
+// in a row where the group size is 128 / SUB, one by one otherwise (SUB = 4: any
+// multiple of 32; 0: a multiple of 128, or one group a row).  Raw values are
+// kept and converted at their use: a conversion at the load would wait for it.
+template <int NT, int BLOCKS, int SUB, class S>
+struct Scales {
+  static constexpr int G = SUB ? SUB : 1, N = BLOCKS * G;
+  const S *ps[NT];
+  const uint8_t *pz[NT];
+  S raw[NT][N];
+  uint32_t zero[NT][(N + 3) / 4];  // four a word
+  __device__ __forceinline__ void rows(const U4 &w, uint32_t n0, uint32_t lr) {
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const uint32_t n = n0 + j * 16 + lr, nn = n < w.n ? n : w.n - 1;
+      ps[j] = (const S *)w.scales + nn * w.sstride;
+      pz[j] = w.zeros ? w.zeros + nn * w.zstride : (const uint8_t *)&g_eights;
+    }
+  }
+  // those of the blocks at element 32 * b32 on
+  __device__ __forceinline__ void request(const U4 &w, uint32_t b32) {
+    const uint32_t zon = w.zeros ? 1 : 0;
+    const uint32_t g0 = b32 / 4 * G;
+    if (SUB && w.group32 * SUB == 4 && g0 + N <= w.groups) {
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        __builtin_memcpy(&raw[j], ps[j] + g0, sizeof raw[j]);
+        if (zon) {
+          if constexpr (N % 4 == 0) {
+            __builtin_memcpy(&zero[j], pz[j] + g0, N);
+          } else {
+            uint16_t h;
+            if constexpr (N == 2) __builtin_memcpy(&h, pz[j] + g0, 2);
+            if constexpr (N == 1) h = pz[j][g0];
+            zero[j][0] = h;
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < (N + 3) / 4; g++) zero[j][g] = 0x08080808u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+#pragma unroll
+        for (int g = 0; g < N; g++) {
+          uint32_t gi = group_of(w, b32 + g * (4 / G));
+          gi = gi < w.groups ? gi : w.groups - 1;
+          raw[j][g] = ps[j][gi];
+          const uint32_t zb = pz[j][gi * zon];
+          zero[j][g / 4] = (g & 3 ? zero[j][g / 4] : 0) | zb << (8 * (g & 3));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float scale(const U4 &w, int j, int g) const { return scale_of(w, raw[j][g]); }
+  __device__ __forceinline__ float zero_point(int j, int g) const {
+    return (float)((zero[j][g / 4] >> (8 * (g & 3))) & 255u);
+  }
+};
+
+// The four dwords of 16 bytes that the lane groups hold (group kg: elements
+// 32 kg .. + 31 of a block), exchanged so that dword d of group kg holds
+// elements 32 d + 8 kg .. + 7: a 4 x 4 transposition over the groups.
+__device__ __forceinline__ u32x4 by_step(u32x4 q) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false));
+  const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false));
+  const u32x2 d = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false));
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ void to_lds(const void *src, uint8_t *dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t minus_pair(float v) {
+  return (uint32_t)to_bits(T{}, -v) * 0x10001u;
+}
+
+// acc += s (T - (bias + z) S), or s T where the operand had the bias taken off.
+template <class T>
+__device__ __forceinline__ float scaled(float acc, float s, float z, float t, float sx) {
+  return __builtin_fmaf(s, Bias<T>::in_sum ? __builtin_fmaf(-(Bias<T>::value + z), sx, t) : t, acc);
+}
+
+// The last k % 32 elements of the rows, one matrix step from guarded dwords:
+// adds to acc[j][i][0 .. J).  px: this lane's rows of x.
+template <class T, int J, int MT, int NT, class Acc>
+__device__ __forceinline__ void row_ends(const U4 &w, uint32_t n0, const uint16_t *const (&px)[MT], Acc &acc) {
+  const uint32_t lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
+  const uint32_t k32 = w.k & ~31u, k = k32 + kg * 8;
+  const uint32_t one = (uint32_t)to_bits(T{}, 1.f) * 0x10001u;
+  const uint32_t g = group_of(w, k32 / 32);
+  u32x4 xp[MT];
+  f32x4 sx[MT];
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    xp[i] = u32x4{0, 0, 0, 0};
+    if (k < w.k) xp[i] = *(const u32x4 *)(px[i] + k);
+    sx[i] = mfma(T{}, xp[i], u32x4{one, one, one, one}, f32x4{0.f, 0.f, 0.f, 0.f});
+  }
+#pragma unroll
+  for (int j = 0; j < NT; j++) {
+    const uint32_t n = n0 + j * 16 + lr, nn = n < w.n ? n : w.n - 1;
+    uint32_t q = 0;
+    if (k < w.k) q = *(const uint32_t *)(w.packed + ((uint64_t)nn * w.k + k) / 2);
+    const float s = scale_at(w, nn, g), z = zero_at(w, nn, g);
+    const u32x4 f = widen<T>(q, minus_pair<T>(Bias<T>::value + z));
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      const f32x4 t = mfma(T{}, xp[i], f, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int r = 0; r < J; r++) acc[j][i][r] = scaled<T>(acc[j][i][r], s, z, t[r], sx[i][r]);
+    }
+  }
+}
+
+// y for up to four rows (tokens).  A workgroup makes 16 NT columns; each wave
+// has a part of the summed index, in stages of 512 elements, and the waves add
+// up through LDS.  Matrix operand A is x, B the weights (16 columns n): lane l
+// holds 16 bytes of weight row l % 16.  BF16: T = sum x (bias + q) and
+// S = sum x (operand B all ones) give a group's part as s (T - (bias + z) S),
+// in FP32; FP16: T = sum x (q - z) and s T.  A result's row is 4 (l / 16) + r:
+// row m of x is put at 4 m (the rows between hold copies), so the scales cost
+// one multiplication a lane, not four.
+//
+// The loads go to LDS: an operand wants 16 rows side by side, of which a
+// register load would fetch 64 bytes each, while here a load takes 256
+// contiguous bytes of 4 rows (and x's 512 elements of a row), and what is in
+// flight needs no registers.  A wave's two buffers are its own, so the waves
+// do not meet before the sum; a stage is requested while the one before is
+// used.  LDS rows hold their 16-byte chunks at position chunk ^ row, exchanged
+// in the source address.
+template <class T, int NT, int W, int SUB, class S>
+__global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *x, uint64_t xs, uint32_t m,
+                                                    uint16_t *y) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  typedef Scales<NT, 4, SUB, S> Sc;
+  constexpr int G = Sc::G;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lr = lane & 15, kg = lane >> 4;
   const uint32_t n0 = blockIdx.x * (16 * NT);
-  const uint32_t nkb = (w.k + 127) / 128;
-  constexpr int G = kSub ? 4 : 1;
+  const uint32_t k32 = w.k & ~31u;
+  const uint32_t stages = (k32 + 511) / 512, per = (stages + W - 1) / W;
+  const uint32_t s0 = wave * per, s1 = s0 + per < stages ? s0 + per : stages;
+  const uint32_t bytes = NT * 4096 + m * 1024;  // a buffer
+  const uint32_t step = per > 1 ? bytes : 0;    // one buffer is enough for one stage
+  uint8_t *buf = lds + wave * (bytes + step);
   const uint32_t one = (uint32_t)to_bits(T{}, 1.f) * 0x10001u;
   const u32x4 ones = {one, one, one, one};
-  const uint8_t *prow[NT];
-  uint32_t nn[NT];
+  const uint32_t xr = lr >> 2 < m ? lr >> 2 : m - 1;  // the row of x in this lane's operand row
+  Sc next, now;
+  next.rows(w, n0, lr);
+  auto request = [&](uint32_t st, uint8_t *dst) {
 #pragma unroll
-  for (int j = 0; j < NT; j++) {
-    const uint32_t n = n0 + j * 16 + lr;
-    nn[j] = n < w.n ? n : w.n - 1;
-    prow[j] = w.packed + (uint64_t)nn[j] * (w.k / 2) + kg * 16;
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint32_t r = i * 4 + (lane >> 4), c = (lane & 15) ^ r, n = n0 + j * 16 + r;
+        const uint8_t *src = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2);
+        src = st * 512 + c * 32 < k32 ? src + st * 256 + c * 16 : (const uint8_t *)&g_zero16;
+        to_lds(src, dst + j * 4096 + i * 1024);
+      }
+    for (uint32_t r = 0; r < m; r++) {
+      const uint32_t k = st * 512 + (lane ^ r) * 8;
+      to_lds(k < k32 ? (const void *)(x + r * xs + k) : (const void *)&g_zero16, dst + NT * 4096 + r * 1024);
+    }
+    next.request(w, st * 16);
+  };
+  float acc[NT][1][1] = {};
+  if (s0 < s1) request(s0, buf);
+  if (k32 < w.k && wave == W - 1) {
+    const uint16_t *px[1] = {x + xr * xs};
+    row_ends<T, 1, 1, NT>(w, n0, px, acc);
   }
-  const uint16_t *px[MT];
+  for (uint32_t st = s0; st < s1; st++) {
+    uint8_t *p = buf + ((st - s0) & 1) * step;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    now = next;
+    if (st + 1 < s1) request(st + 1, buf + ((st + 1 - s0) & 1) * step);
+    const uint8_t *px = p + NT * 4096 + xr * 1024;
 #pragma unroll
-  for (int i = 0; i < MT; i++) px[i] = x + (uint64_t)(i * 16 + lr) * xs + kg * 8;
-
-  f32x4 acc[NT][MT] = {};
-  for (uint32_t kb = wave; kb < nkb; kb += W * U) {
-    u32x4 qw[U][NT], xv[U][MT][4];
-    float sc[U][NT][G], ze[U][NT][G];
+    for (int b = 0; b < 4; b++) {
+      if (st * 512 + b * 128 >= k32) break;  // uniform
+      u32x4 xp[4];
+      f32x4 sx[G] = {};
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const uint32_t b = kb + u * W;
-      const uint32_t k0 = b * 128;
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        qw[u][j] = u32x4{0, 0, 0, 0};
-        if (kWide) {
-          if (k0 + kg * 32 < w.k) qw[u][j] = __builtin_nontemporal_load((const u32x4 *)(prow[j] + (uint64_t)b * 64));
-        } else {
-#pragma unroll
-          for (int d = 0; d < 4; d++)
-            if (k0 + kg * 32 + d * 8 < w.k) qw[u][j][d] = *(const uint32_t *)(prow[j] + (uint64_t)b * 64 + d * 4);
-        }
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-          sc[u][j][g] = 0.f;
-          ze[u][j][g] = 0.f;
-          if (k0 + g * 32 < w.k) {
-            const uint32_t gi = group_of(w, b * 4 + g);
-            sc[u][j][g] = scale_at(w, nn[j], gi);
-            ze[u][j][g] = zero_at(w, nn[j], gi);
-          }
-        }
+      for (int d = 0; d < 4; d++) {
+        const uint32_t c = b * 16 + (SUB > 1 ? d * 4 + kg : kg * 4 + d);
+        xp[d] = *(const u32x4 *)(px + (c ^ xr) * 16);
+        if constexpr (Bias<T>::in_sum) sx[d * G / 4] = mfma(T{}, xp[d], ones, sx[d * G / 4]);
       }
 #pragma unroll
-      for (int i = 0; i < MT; i++)
-#pragma unroll
-        for (int d = 0; d < 4; d++) {
-          xv[u][i][d] = u32x4{0, 0, 0, 0};
-          if (i * 16 + lr < m && k0 + d * 32 + kg * 8 < w.k) xv[u][i][d] = *(const u32x4 *)(px[i] + k0 + d * 32);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (kb + u * W >= nkb) break;  // uniform
-      u32x4 xp[MT][4];
-      f32x4 sx[MT][G] = {};
-#pragma unroll
-      for (int i = 0; i < MT; i++)
-#pragma unroll
-        for (int d = 0; d < 4; d++) {
-          xp[i][d] = pair_up(xv[u][i][d]);
-          if constexpr (Bias<T>::in_sum) sx[i][kSub ? d : 0] = mfma(T{}, xp[i][d], ones, sx[i][kSub ? d : 0]);
-        }
-#pragma unroll
       for (int j = 0; j < NT; j++) {
-        const u32x4 q = qw[u][j];
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false));
-        const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false));
-        const u32x2 e = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false));
-        const uint32_t step[4] = {c[0], c[1], e[0], e[1]};
-        f32x4 t[MT][G] = {};
+        u32x4 q = *(const u32x4 *)(p + j * 4096 + lr * 256 + (((b * 4 + kg) ^ lr) * 16));
+        if (SUB > 1) q = by_step(q);
+        f32x4 t[G] = {};
 #pragma unroll
-        for (int d = 0; d < 4; d++) {
-          uint32_t off = 0;
-          if constexpr (!Bias<T>::in_sum) off = to_bits(T{}, -(Bias<T>::value + ze[u][j][kSub ? d : 0])) * 0x10001u;
-          const u32x4 f = widen<T>(step[d], off);
+        for (int d = 0; d < 4; d++)
+          t[d * G / 4] = mfma(T{}, xp[d], widen<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(j, b * G + d * G / 4))),
+                              t[d * G / 4]);
 #pragma unroll
-          for (int i = 0; i < MT; i++) t[i][kSub ? d : 0] = mfma(T{}, xp[i][d], f, t[i][kSub ? d : 0]);
-        }
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-          const float s = sc[u][j][g], z = Bias<T>::value + ze[u][j][g];
-#pragma unroll
-          for (int i = 0; i < MT; i++)
-#pragma unroll
-            for (int e4 = 0; e4 < 4; e4++)
-              acc[j][i][e4] = __builtin_fmaf(
-                  s, Bias<T>::in_sum ? __builtin_fmaf(-z, sx[i][g][e4], t[i][g][e4]) : t[i][g][e4], acc[j][i][e4]);
-        }
+        for (int g = 0; g < G; g++)
+          acc[j][0][0] = scaled<T>(acc[j][0][0], now.scale(w, j, b * G + g), now.zero_point(j, b * G + g), t[g][0], sx[g][0]);
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < NT; j++)
-#pragma unroll
-    for (int i = 0; i < MT; i++) part[wave][j * MT + i][lane] = acc[j][i];
+  // every wave has its last buffer behind it; the sums take its place
   __syncthreads();
-  for (uint32_t t = threadIdx.x; t < NT * MT * 256; t += 64 * W) {
-    const uint32_t tile = t / 256, row = (t / 16) & 15, col = t & 15;  // row of x, column n
-    const uint32_t src = (row / 4) * 16 + col;                         // the lane that holds it
+  float *part = (float *)lds;  // [W][NT][64]
+#pragma unroll
+  for (int j = 0; j < NT; j++) part[(wave * NT + j) * 64 + lane] = acc[j][0][0];
+  __syncthreads();
+  for (uint32_t t = threadIdx.x; t < NT * 64; t += 64 * W) {
+    const uint32_t j = t / 64, mm = (t % 64) / 16, n = n0 + j * 16 + (t & 15);
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < W; q++) v += ((const float *)&part[q][tile][src])[row & 3];
-    const uint32_t mm = (tile % MT) * 16 + row, n = n0 + (tile / MT) * 16 + col;
+    for (int q = 0; q < W; q++) v += part[q * NT * 64 + t];
     if (mm < m && n < w.n) {
-      if (Bias<T>::in_sum && !(__builtin_fabsf(v) < __builtin_huge_valf())) v = dot_plain<T>(w, x + (uint64_t)mm * xs, n);
+      if (Bias<T>::in_sum && !(__builtin_fabsf(v) < __builtin_huge_valf())) v = dot_plain<T>(w, x + mm * xs, n);
       y[(uint64_t)mm * w.n + n] = to_bits(T{}, v);
     }
   }
+}
+
+// y for a tile of 16 MT rows of x and 64 NT weight rows, for row counts between
+// tokens and prompts.  Eight waves: wave w takes weight rows 16 NT (w % 4) .. and
+// the block w / 4 of a stage's two blocks of 128 elements; all share the stage's
+// x in LDS.  Arithmetic as in u4_tokens, all four result rows of a lane used.
+// blockIdx.y: split of the summed index; a split's sums go to its FP32 plane
+// (one split: straight to y).
+template <class T, int MT, int NT, int SUB, class S>
+__global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, uint64_t xs, uint32_t m, uint32_t mt,
+                                               uint32_t per, uint16_t *y, float *planes, uint32_t ld) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  typedef Scales<NT, 1, SUB, S> Sc;
+  constexpr int G = Sc::G, BN = 64 * NT, BM = 16 * MT;
+  constexpr uint32_t kBuf = BN * 128 + BM * 512;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lr = lane & 15, kg = lane >> 4, wn = wave & 3, wk = wave >> 2;
+  const uint32_t m0 = blockIdx.x % mt * BM, nb = blockIdx.x / mt * BN, n0 = nb + wn * 16 * NT;
+  const uint32_t rows = m - m0 < BM ? m - m0 : BM;
+  const uint32_t k32 = w.k & ~31u, stages = (k32 + 255) / 256;
+  const uint32_t s0 = blockIdx.y * per, s1 = s0 + per < stages ? s0 + per : stages;
+  const uint32_t one = (uint32_t)to_bits(T{}, 1.f) * 0x10001u;
+  const u32x4 ones = {one, one, one, one};
+  Sc next, now;
+  next.rows(w, n0, lr);
+  auto request = [&](uint32_t st, uint8_t *dst) {
+#pragma unroll
+    for (int i = 0; i < BN / 64; i++) {  // 8 weight rows of 128 bytes a load
+      const uint32_t r = (i * 8 + wave) * 8 + lane / 8, c = (lane & 7) ^ swz(r), n = nb + r;
+      const uint8_t *src = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2);
+      src = st * 256 + c * 32 < k32 ? src + st * 128 + c * 16 : (const uint8_t *)&g_zero16;
+      to_lds(src, dst + (i * 8 + wave) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; i++) {  // 2 rows of x a load
+      const uint32_t pair = i * 8 + wave;
+      if (pair * 2 >= rows) continue;  // uniform
+      const uint32_t r = pair * 2 + lane / 32, k = st * 256 + ((lane & 31) ^ (r & 15)) * 8;
+      const uint16_t *src = x + (uint64_t)(m0 + (r < rows ? r : rows - 1)) * xs + k;
+      to_lds(k < k32 ? (const void *)src : (const void *)&g_zero16, dst + BN * 128 + pair * 1024);
+    }
+    next.request(w, st * 8 + wk * 4);
+  };
+  f32x4 acc[NT][MT] = {};
+  if (s0 < s1) request(s0, lds);
+  if (k32 < w.k && blockIdx.y == 0 && wk == 1) {
+    const uint16_t *px[MT];
+#pragma unroll
+    for (int i = 0; i < MT; i++) px[i] = x + (uint64_t)(m0 + (i * 16 + lr < rows ? i * 16 + lr : rows - 1)) * xs;
+    row_ends<T, 4, MT, NT>(w, n0, px, acc);
+  }
+  for (uint32_t st = s0; st < s1; st++) {
+    const uint8_t *p = lds + ((st - s0) & 1) * kBuf;
+    wait_loads();
+    __syncthreads();
+    now = next;
+    if (st + 1 < s1) request(st + 1, lds + ((st + 1 - s0) & 1) * kBuf);
+    if (st * 256 + wk * 128 < k32) {
+      const uint8_t *px = p + BN * 128 + lr * 512, *pw = p + (wn * 16 * NT + lr) * 128 + (((wk * 4 + kg) ^ swz(lr)) * 16);
+      u32x4 q[NT];
+      f32x4 t[G][NT][MT] = {}, sx[G][MT] = {};
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        q[j] = *(const u32x4 *)(pw + j * 2048);
+        if (SUB > 1) q[j] = by_step(q[j]);
+      }
+#pragma unroll
+      for (int d = 0; d < 4; d++) {
+        constexpr int step = 4 / G;
+        const uint32_t c = wk * 16 + (SUB > 1 ? d * 4 + kg : kg * 4 + d);
+        u32x4 xp[MT];
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+          xp[i] = *(const u32x4 *)(px + i * 8192 + ((c ^ lr) * 16));
+          if constexpr (Bias<T>::in_sum) sx[d / step][i] = mfma(T{}, xp[i], ones, sx[d / step][i]);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          const u32x4 f = widen<T>(q[j][d], minus_pair<T>(Bias<T>::value + now.zero_point(j, d / step)));
+#pragma unroll
+          for (int i = 0; i < MT; i++) t[d / step][j][i] = mfma(T{}, xp[i], f, t[d / step][j][i]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; g++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+          const float s = now.scale(w, j, g), z = now.zero_point(j, g);
+#pragma unroll
+          for (int i = 0; i < MT; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) acc[j][i][r] = scaled<T>(acc[j][i][r], s, z, t[g][j][i][r], sx[g][i][r]);
+        }
+    }
+  }
+  // the second block's waves hand their sums to the first block's
+  __syncthreads();
+  f32x4 *part = (f32x4 *)lds;
+  if (wk == 1)
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int i = 0; i < MT; i++) part[((j * MT + i) * 4 + wn) * 64 + lane] = acc[j][i];
+  __syncthreads();
+  if (wk == 1) return;
+#pragma unroll
+  for (int j = 0; j < NT; j++) {
+    const uint32_t n = n0 + j * 16 + lr;
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      const f32x4 v = acc[j][i] + part[((j * MT + i) * 4 + wn) * 64 + lane];
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const uint32_t row = m0 + i * 16 + kg * 4 + r;
+        if (row >= m || n >= w.n) continue;
+        if (planes) {
+          planes[((uint64_t)blockIdx.y * m + row) * ld + n] = v[r];
+        } else {
+          float o = v[r];
+          if (Bias<T>::in_sum && !(__builtin_fabsf(o) < __builtin_huge_valf())) o = dot_plain<T>(w, x + (uint64_t)row * xs, n);
+          y[(uint64_t)row * w.n + n] = to_bits(T{}, o);
+        }
+      }
+    }
+  }
+}
+
+// The planes of u4_tile's splits added up.
+template <class T>
+__global__ __launch_bounds__(256) void join_tiles(const U4 w, const uint16_t *x, uint64_t xs, const float *planes,
+                                                  uint32_t splits, uint32_t m, uint32_t ld, uint16_t *y) {
+  const uint32_t row = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 2;
+  if (n >= w.n) return;
+  float v0 = 0.f, v1 = 0.f;
+  for (uint32_t s = 0; s < splits; s++) {
+    const float2 p = *(const float2 *)(planes + ((uint64_t)s * m + row) * ld + n);
+    v0 += p.x;
+    v1 += p.y;
+  }
+  if (Bias<T>::in_sum) {
+    if (!(__builtin_fabsf(v0) < __builtin_huge_valf())) v0 = dot_plain<T>(w, x + row * xs, n);
+    if (n + 1 < w.n && !(__builtin_fabsf(v1) < __builtin_huge_valf())) v1 = dot_plain<T>(w, x + row * xs, n + 1);
+  }
+  uint16_t *p = y + (uint64_t)row * w.n + n;
+  p[0] = to_bits(T{}, v0);
+  if (n + 1 < w.n) p[1] = to_bits(T{}, v1);
 }
 
 // The weights as 16-bit floats, [n, k].  Each is rounded once from FP32
@@ -301,7 +555,7 @@ __global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss
   for (uint32_t c = threadIdx.x; c < np; c += 256) dst[r * np + c] = c < n ? src[r * ss + c] : (uint16_t)0;
 }
 
-constexpr uint32_t kFewRows = 64;
+constexpr uint32_t kFewRows = 256;
 
 uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 
@@ -334,6 +588,7 @@ df_status matrix_of(const df_u4_matrix *m, U4 *w) {
   w->zstride = m->zero_stride;
   w->group32 = (uint32_t)(m->group_size < m->cols ? m->group_size / 32 : 0);
   w->magic = w->group32 ? (1u << 31) / w->group32 + 1 : 0;
+  w->groups = w->group32 ? (uint32_t)((m->cols + m->group_size - 1) / m->group_size) : 1;
   return DF_OK;
 }
 
@@ -356,24 +611,92 @@ df_status many_rows(const Gemm &g, uint16_t *out, float *planes, hipStream_t s) 
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
 
-template <class T, int MT, int NT, int W, int U>
-hipError_t rows_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, hipStream_t s) {
-  const bool sub = w.group32 % 4 != 0, wide = w.k % 32 == 0 && ((uintptr_t)w.packed & 15) == 0;
-  auto *fn = sub ? (wide ? u4_rows<T, MT, NT, W, U, true, true> : u4_rows<T, MT, NT, W, U, true, false>)
-                 : (wide ? u4_rows<T, MT, NT, W, U, false, true> : u4_rows<T, MT, NT, W, U, false, false>);
-  hipLaunchKernelGGL(fn, dim3((w.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), 0, s, w, x, xs, m, y);
+int sub_of(const U4 &w) { return w.group32 == 4 ? 1 : w.group32 == 2 ? 2 : w.group32 % 4 == 0 ? 0 : 4; }
+
+template <class T, int NT, int W, class S>
+hipError_t tokens_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, hipStream_t s) {
+  const int sub = sub_of(w);
+  auto *fn = sub == 0   ? u4_tokens<T, NT, W, 0, S>
+             : sub == 1 ? u4_tokens<T, NT, W, 1, S>
+             : sub == 2 ? u4_tokens<T, NT, W, 2, S>
+                        : u4_tokens<T, NT, W, 4, S>;
+  const uint32_t buffers = (w.k / 32 * 32 + 511) / 512 > W ? 2 : 1;
+  const uint32_t lds = W * buffers * (NT * 4096 + m * 1024);
+  const hipError_t e = allow_lds((const void *)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3((w.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), lds, s, w, x, xs, m, y);
   return hipGetLastError();
 }
+template <class T, int NT, int W>
+hipError_t tokens_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, hipStream_t s) {
+  return w.scale_type == DF_TYPE_F32 ? tokens_of<T, NT, W, float>(w, x, xs, m, y, s)
+                                     : tokens_of<T, NT, W, uint16_t>(w, x, xs, m, y, s);
+}
+
+// How u4_tile cuts a product: splits of the summed index so that about two
+// workgroups come to a CU, of four stages of 256 elements at least.
+struct TilePlan {
+  uint32_t mtile, ntile, mt, splits, per, ld;
+};
+TilePlan tile_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t mtile, uint32_t ntile) {
+  TilePlan p;
+  p.mtile = mtile;
+  p.ntile = ntile;
+  p.mt = (m + 16 * p.mtile - 1) / (16 * p.mtile);
+  const uint32_t tiles = p.mt * ((n + 64 * p.ntile - 1) / (64 * p.ntile)), stages = (k / 32 * 32 + 255) / 256;
+  uint32_t want = tiles >= 384 ? 1 : (512 + tiles - 1) / tiles;
+  const uint32_t most = stages / 4 < 1 ? 1 : stages / 4;
+  want = want < most ? want : most;
+  p.per = (stages + want - 1) / want;
+  if (p.per == 0) p.per = 1;
+  p.splits = stages ? (stages + p.per - 1) / p.per : 1;
+  p.ld = (uint32_t)up(n, 4);
+  return p;
+}
+
+template <class T, int MT, int NT, class S>
+hipError_t tile_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, float *planes,
+                   const TilePlan &p, hipStream_t s) {
+  const int sub = sub_of(w);
+  auto *fn = sub == 0   ? u4_tile<T, MT, NT, 0, S>
+             : sub == 1 ? u4_tile<T, MT, NT, 1, S>
+             : sub == 2 ? u4_tile<T, MT, NT, 2, S>
+                        : u4_tile<T, MT, NT, 4, S>;
+  constexpr uint32_t lds = 2 * (64 * NT * 128 + 16 * MT * 512);
+  hipError_t e = allow_lds((const void *)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(p.mt * ((w.n + 64 * NT - 1) / (64 * NT)), p.splits), dim3(512), lds, s, w, x, xs, m, p.mt,
+                     p.per, y, p.splits > 1 ? planes : (float *)nullptr, p.ld);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL((join_tiles<T>), dim3((w.n + 511) / 512, m), dim3(256), 0, s, w, x, xs, (const float *)planes,
+                     p.splits, m, p.ld, y);
+  return hipGetLastError();
+}
+template <class T, int MT, int NT>
+hipError_t tile_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, float *planes,
+                       const TilePlan &p, hipStream_t s) {
+  return w.scale_type == DF_TYPE_F32 ? tile_of<T, MT, NT, float>(w, x, xs, m, y, planes, p, s)
+                                     : tile_of<T, MT, NT, uint16_t>(w, x, xs, m, y, planes, p, s);
+}
+
+constexpr uint32_t kTokens = 4;
+TilePlan few_plan(uint32_t m, uint32_t n, uint32_t k) { return tile_plan(m, n, k, m <= 16 ? 1 : m <= 32 ? 2 : 4, 1); }
 
 template <class T>
 df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16_t *y, uint8_t *ws, hipStream_t s) {
   hipError_t e;
-  if (m <= 16) {
-    e = rows_launch<T, 1, 1, 8, 4>(w, x, xs, m, y, s);
-  } else if (m <= 32) {
-    e = rows_launch<T, 2, 2, 8, 2>(w, x, xs, m, y, s);
+  if (m <= kTokens) {
+    // waves a workgroup: 4 where the columns alone fill the chip, 16 where they
+    // give one workgroup a CU or less and the rows are long
+    e = w.n >= 32768                    ? tokens_launch<T, 1, 4>(w, x, xs, m, y, s)
+        : m == 1 && w.n <= 4096 && w.k > 8192 ? tokens_launch<T, 1, 16>(w, x, xs, m, y, s)
+                                        : tokens_launch<T, 1, 8>(w, x, xs, m, y, s);
   } else if (m <= kFewRows) {
-    e = rows_launch<T, 4, 2, 4, 1>(w, x, xs, m, y, s);
+    const TilePlan p = few_plan(m, w.n, w.k);
+    e = p.mtile == 1   ? tile_launch<T, 1, 1>(w, x, xs, m, y, (float *)ws, p, s)
+        : p.mtile == 2 ? tile_launch<T, 2, 1>(w, x, xs, m, y, (float *)ws, p, s)
+                       : tile_launch<T, 4, 1>(w, x, xs, m, y, (float *)ws, p, s);
   } else {
     hipLaunchKernelGGL((u4_expand<T>), dim3(w.n), dim3(256), 0, s, w, (uint16_t *)ws);
     Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0};
@@ -408,12 +731,18 @@ uint64_t plane_bytes(uint32_t m, uint32_t n, uint32_t k) {
 extern "C" {
 
 uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
-  if (!w || rows <= kFewRows || rows > (1u << 24)) return 0;
+  U4 u;
+  if (matrix_of(w, &u) != DF_OK || rows <= kTokens || rows > (1u << 24)) return 0;
+  if (rows <= kFewRows) {
+    const TilePlan p = few_plan((uint32_t)rows, u.n, u.k);
+    return p.splits > 1 ? 4ull * p.splits * rows * p.ld : 0;
+  }
   return up(w->rows * w->cols * 2, 256) + plane_bytes((uint32_t)rows, (uint32_t)w->rows, (uint32_t)w->cols);
 }
 
 uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
-  if (!w || rows == 0 || rows > (1u << 24)) return 0;
+  U4 u;
+  if (matrix_of(w, &u) != DF_OK || rows == 0 || rows > (1u << 24)) return 0;
   const uint64_t np = up(w->rows, 8);
   return up(np * w->cols * 2, 256) + (np != w->rows ? up(rows * np * 2, 256) : 0) + plane_bytes((uint32_t)rows, (uint32_t)w->cols, (uint32_t)np);
 }

@@ -188,7 +188,7 @@ class _LinearU4(torch.autograd.Function):
 def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """y = x W^T for W[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[...]),
     x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
-    are float32; up to 64 rows multiply the integer weights exactly, more round
+    are float32; up to 256 rows multiply the integer weights exactly, more round
     each weight once to x's type.  Differentiable in x."""
     if x.requires_grad and torch.is_grad_enabled():
         return _LinearU4.apply(x, w, stream)

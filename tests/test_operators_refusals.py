@@ -33,7 +33,7 @@ def test_bad_matrix(kw):
 
 @pytest.mark.parametrize("kw", [dict(ty=2), dict(ty=7), dict(x=None), dict(x=P + 8), dict(xs=56), dict(xs=68),
                                 dict(xs=(1 << 21) + 8), dict(y=None), dict(y=P + 8), dict(rows=(1 << 24) + 1),
-                                dict(rows=65, ws=None), dict(rows=65, nbytes=100), dict(rows=65, ws=P + 16)])
+                                dict(rows=257, ws=None), dict(rows=257, nbytes=100), dict(rows=257, ws=P + 16)])
 def test_bad_linear_call(kw):
     assert linear(matrix(), **kw) == ARG
 
@@ -96,7 +96,7 @@ def test_sizes():
     L = dfh.lib()
     w = matrix(rows=4096, cols=14336, group_size=128)
     assert L.df_linear_u4_workspace_bytes(ctypes.byref(w), 1) == 0
-    assert L.df_linear_u4_workspace_bytes(ctypes.byref(w), 64) == 0
+    assert 0 < L.df_linear_u4_workspace_bytes(ctypes.byref(w), 64) < 64 * 4096 * 4 * 64
     assert L.df_linear_u4_workspace_bytes(ctypes.byref(w), 2048) >= 0
     # the logits of a training step are never whole in the workspace
     d = loss(rows=4096, vocab=128256, hidden=4096, x_stride=4096, head_stride=4096)
