@@ -3,18 +3,19 @@
 //
 //   C[m, n] = sum_k A[m, k] B[n, k]
 //
-// Both operands are row major with the summed index contiguous, in BF16 or
-// FP16; sums are FP32.  Products that sum over another index get a transposed
-// copy of the operand (made in the caller's workspace), so one kernel serves
-// every direction.
+// in BF16 or FP16 with FP32 sums.  Either operand may be stored with the summed
+// index contiguous ([rows, k]) or across ([k, rows]), so every direction of a
+// product reads its operands as they lie.
 //
-// gemm_nt: one workgroup makes a BM x BN tile.  Each step takes 64 summed
-// elements (128 bytes) of BM + BN rows from global memory straight into LDS
-// (16 bytes a lane, no registers in between) into one of two buffers, while
-// the waves run v_mfma_f32_16x16x32 from the other.  A row's eight 16-byte
-// chunks are stored at position chunk ^ swz(row): the load writes LDS linearly,
-// so the exchange is made in the source address, and the 16 rows that a
-// fragment read touches at one chunk fall into different banks.
+// gemm: one workgroup makes a BM x BN tile.  Each step takes 64 summed elements
+// of BM + BN rows from global memory straight into LDS (16 bytes a lane, no
+// registers in between) into one of two buffers, while the waves run
+// v_mfma_f32_16x16x32 from the other (the step loop is described at the kernel).  An operand of 16 rows wants 8 summed
+// elements of one row in a lane: 16 bytes in a [rows, k] tile, and two
+// transposing reads (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 elements and
+// get a column of 4 each) in a [k, rows] tile.  The 16-byte chunks of an LDS row
+// are stored at chunk ^ f(row), so that what one read touches lies in different
+// banks; a load writes LDS linearly, so the exchange is in its source address.
 #ifndef DFH_GEMM_H
 #define DFH_GEMM_H
 
@@ -58,24 +59,58 @@ __device__ __forceinline__ uint32_t pack2(T t, float lo, float hi) {
   return (uint32_t)to_bits(t, lo) | ((uint32_t)to_bits(t, hi) << 16);
 }
 
-// Wait until every load of this wave (to LDS too) has landed: vmcnt(0).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// Wait until all but the N youngest loads of this wave (to LDS too) have landed:
+// vmcnt(N), N < 64.
+template <int N>
+__device__ __forceinline__ void wait_but() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+// A barrier without the waits of __syncthreads; nothing that reads or writes
+// memory is moved across it.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Wait until this wave's LDS reads have returned: lgkmcnt(0).
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ void to_lds(const void *src, uint8_t *dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4 *)(__attribute__((address_space(3))) void *)p);
+  return __builtin_bit_cast(u32x2, v);
+}
 
 // What a lane past the end of the summed index loads instead.
 __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 
 struct Gemm {
-  const uint16_t *a, *b;      // A [m, k], B [n, k]
+  const uint16_t *a, *b;      // A [m, k] or [k, m], B [n, k] or [k, n]
   uint64_t lda, ldb;          // row strides in elements, multiples of 8
-  uint32_t m, n, k;           // k a multiple of 8
+  uint32_t m, n, k;           // [rows, k]: k a multiple of 8; [k, rows]: rows padded to 8
   uint32_t mt, nt;            // tiles
   uint32_t kb_per_split;      // 64-element steps per split of the summed index
 };
 
 constexpr int kBK = 64;
 
-// Chunk exchange of an LDS row.
+// Chunk exchange of an LDS row of 64 summed elements (128 bytes): 16 rows read
+// at one chunk fall into 16 different places of two rows' span.
 __device__ __forceinline__ uint32_t swz(uint32_t row) { return (row >> 1) & 7u; }
+// Chunk exchange of an LDS row of R elements at summed index k: a transposing
+// read takes 32 bytes (two chunks, so the low bit stays) of rows 8 i + 0..3.
+template <int R>
+__device__ __forceinline__ uint32_t swz_across(uint32_t k) {
+  return R == 32 ? (k >> 2) & 2u : R == 64 ? (k & 2u) | ((k >> 1) & 4u) : ((k & 3u) << 1) | (k & 8u);
+}
 
 // Tile of a workgroup.  Workgroups go to the eight XCDs in turn, so workgroup
 // id works on tile (id % 8) * ceil(tiles / 8) + id / 8: an XCD gets a contiguous
@@ -85,13 +120,100 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t id, uint32_t tiles) {
   return x * per + (x < rem ? x : rem) + l;
 }
 
-template <class T, int BM, int BN, int WM, int WN, class Epi>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_nt(const Gemm g, const Epi epi) {
+// One operand of a workgroup's tile: R rows from r0 on.  ACROSS: stored [k, rows].
+template <class T, int R, int kWaves, bool ACROSS>
+struct Operand {
+  static constexpr int kLoads = R / 8 / kWaves;      // of 1 KiB, per wave and step
+  static constexpr int kPer = ACROSS ? 512 / R : 8;  // LDS rows a load fills
+  const uint8_t *base;
+  uint64_t step;  // bytes from one 64-element step to the next
+  uint32_t off[kLoads];
+
+  __device__ __forceinline__ void init(const uint16_t *p, uint64_t ld, uint32_t r0, uint32_t total, uint32_t wave,
+                                       uint32_t lane) {
+    const uint32_t last = total - 1 - r0;  // rows past the end read the last ones, their results are dropped
+    base = (const uint8_t *)(ACROSS ? p + r0 : p + r0 * ld);
+    step = ACROSS ? ld * (2 * kBK) : 2 * kBK;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      if (ACROSS) {
+        const uint32_t k = (i * kWaves + wave) * kPer + lane / (R / 8), c = (lane % (R / 8)) ^ swz_across<R>(k);
+        off[i] = k * (uint32_t)ld * 2 + (c < last / 8 ? c : last / 8) * 16;
+      } else {
+        const uint32_t r = (i * kWaves + wave) * 8 + lane / 8;
+        off[i] = (r < last ? r : last) * (uint32_t)ld * 2 + ((lane & 7) ^ swz(r)) * 16;
+      }
+    }
+  }
+  // left: summed elements from this step on
+  __device__ __forceinline__ void load(uint32_t kb, uint32_t left, uint8_t *dst, uint32_t wave, uint32_t lane) const {
+    const uint8_t *src = base + kb * step;
+    if (left >= kBK) {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) to_lds(src + off[i], dst + (i * kWaves + wave) * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) {
+        const uint32_t row = (i * kWaves + wave) * kPer;
+        const uint32_t k = ACROSS ? row + lane / (R / 8) : ((lane & 7) ^ swz(row + lane / 8)) * 8;
+        to_lds(k < left ? src + off[i] : (const uint8_t *)&g_zero16, dst + (i * kWaves + wave) * 1024);
+      }
+    }
+  }
+};
+
+// A wave's fragments of an operand: COUNT times 16 rows from LDS row r on.
+template <class T, int R, int COUNT, bool ACROSS>
+struct Fragments {
+  uint32_t at[ACROSS ? COUNT : 2];
+  __device__ __forceinline__ void init(uint32_t r, uint32_t lane) {
+    const uint32_t lr = lane & 15, kg = lane >> 4;
+    if constexpr (ACROSS) {
+      const uint32_t k = kg * 8 + lr / 4, f = swz_across<R>(k);
+#pragma unroll
+      for (int i = 0; i < COUNT; i++)
+        at[i] = k * (R * 2) + (((r / 8 + 2 * i) ^ f) + ((lr >> 1) & 1)) * 16 + (lr & 1) * 8;
+    } else {
+      at[0] = (r + lr) * 128 + (kg ^ swz(lr)) * 16;
+      at[1] = (r + lr) * 128 + ((4 + kg) ^ swz(lr)) * 16;
+    }
+  }
+  // fragment i of the step's first or second 32 elements
+  __device__ __forceinline__ u32x4 get(const uint8_t *p, int ks, int i) const {
+    if constexpr (ACROSS) {
+      // rows k .. k + 3 and k + 4 .. k + 7 of this lane's 8; f(k + 4) = f(k), f(k + 32) = f(k)
+      const u32x2 lo = read_turned(p + at[i] + ks * (R * 64)), hi = read_turned(p + at[i] + ks * (R * 64) + R * 8);
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+      return *(const u32x4 *)(p + at[ks] + i * 2048);
+    }
+  }
+};
+
+// The step loop keeps the two waves that share a SIMD in opposite phases: half
+// of the waves run one barrier late, so one's fragment reads and load requests
+// lie under the other's matrix instructions (which go first, s_setprio).  A step
+// has two phases, the upper and the lower half of a wave's rows against all its
+// columns; each is: read the phase's fragments, request loads, wait for the
+// reads, barrier, multiply, barrier.  Requested are, in the first phase of step
+// kb, A of step kb + 1 (A of step kb - 1 was last read in the phase before) and,
+// in the second, B of step kb + 2 (B of step kb was last read in the first); then
+// the wave waits for all but the latter, so step kb + 1 is whole in LDS.  An
+// early wave's phase begins after the barrier by which the late waves' reads of
+// the phase before have returned, and the other way round, so no request
+// overwrites what is still read.
+// 2048 x 128256 x 4096: 1614 us (1333 TFLOP/s) against 1787 us with both halves
+// in step and one barrier a step; 2048 x 4096 x 14336 in two splits 175 against
+// 211 us; with B stored across 218 against 288 us (16384 long).  Four phases a
+// step (a quarter of the tile each) 1708 us; 32-element steps in four or five
+// buffers 1910 to 2000 us; four waves of 128 x 128 each 2300 us.
+template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, class Epi>
+__global__ __launch_bounds__(64 * WM * WN) void gemm(const Gemm g, const Epi epi) {
   constexpr int kWaves = WM * WN;
-  constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int kRows = BM + BN;
-  constexpr int kLoads = kRows / 8 / kWaves, kLoadsA = BM / 8 / kWaves;
-  static_assert(kRows % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole loads per wave");
+  constexpr int MT = BM / WM / 16, NT = BN / WN / 16, MH = MT / 2;
+  constexpr uint32_t kBuf = (BM + BN) * 128;
+  typedef Operand<T, BM, kWaves, KA> OA;
+  typedef Operand<T, BN, kWaves, KB> OB;
   extern __shared__ __align__(1024) uint8_t lds[];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = xcd_tile(blockIdx.x, g.mt * g.nt);
@@ -101,77 +223,78 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_nt(const Gemm g, const Epi 
   const uint32_t kb0 = blockIdx.y * g.kb_per_split;
   const uint32_t kb1 = kb0 + g.kb_per_split < nkb ? kb0 + g.kb_per_split : nkb;
 
-  // source of this lane's chunks: the tile's first row (uniform) plus a 32-bit
-  // byte offset; rows past the end read the last row (their results are dropped)
-  const uint8_t *pa = (const uint8_t *)(g.a + (uint64_t)m0 * g.lda);
-  const uint8_t *pb = (const uint8_t *)(g.b + (uint64_t)n0 * g.ldb);
-  uint32_t off[kLoads];
-#pragma unroll
-  for (int i = 0; i < kLoads; i++) {
-    const bool isa = i < kLoadsA;
-    const uint32_t r = ((isa ? i : i - kLoadsA) * kWaves + wave) * 8 + lane / 8;
-    const uint32_t last = isa ? g.m - 1 - m0 : g.n - 1 - n0;
-    const uint32_t rr = r < last ? r : last;
-    off[i] = rr * (uint32_t)(isa ? g.lda : g.ldb) * 2 + ((lane & 7) ^ swz(r)) * 16;
-  }
-  auto load = [&](uint32_t kb, uint32_t buf) {
-    uint8_t *dst = lds + buf * (kRows * 128);
-    const uint64_t kbyte = (uint64_t)kb * (kBK * 2);
-    const uint32_t left = g.k - kb * kBK;  // summed elements from here on
-    if (left >= kBK) {
-#pragma unroll
-      for (int i = 0; i < kLoads; i++) {
-        const uint8_t *src = (i < kLoadsA ? pa : pb) + kbyte + off[i];
-        const uint32_t row = i < kLoadsA ? (i * kWaves + wave) * 8 : BM + ((i - kLoadsA) * kWaves + wave) * 8;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                         (__attribute__((address_space(3))) void *)(dst + row * 128), 16, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; i++) {
-        const uint32_t row = i < kLoadsA ? (i * kWaves + wave) * 8 : BM + ((i - kLoadsA) * kWaves + wave) * 8;
-        const uint32_t rl = row - (i < kLoadsA ? 0 : BM) + lane / 8;
-        const uint32_t c = (lane & 7) ^ swz(rl);
-        const uint8_t *src = (i < kLoadsA ? pa : pb) + kbyte + off[i];
-        src = c * 8 < left ? src : (const uint8_t *)&g_zero16;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                         (__attribute__((address_space(3))) void *)(dst + row * 128), 16, 0, 0);
-      }
-    }
-  };
-
+  OA oa;
+  OB ob;
+  oa.init(g.a, g.lda, m0, g.m, wave, lane);
+  ob.init(g.b, g.ldb, n0, g.n, wave, lane);
+  auto buffer = [&](uint32_t kb) { return lds + ((kb - kb0) & 1) * kBuf; };
+  auto load_a = [&](uint32_t kb) { oa.load(kb, g.k - kb * kBK, buffer(kb), wave, lane); };
+  auto load_b = [&](uint32_t kb) { ob.load(kb, g.k - kb * kBK, buffer(kb) + BM * 128, wave, lane); };
   const uint32_t wm = wave % WM, wn = wave / WM;
-  const uint32_t lr = lane & 15, kg = lane >> 4;
-  // byte offset of this lane's fragment chunks (first and second 32 elements)
-  const uint32_t c0 = (kg ^ swz(lr)) * 16, c1 = ((4 + kg) ^ swz(lr)) * 16;
-  const uint32_t ra = (wm * (BM / WM) + lr) * 128, rb = (BM + wn * (BN / WN) + lr) * 128;
+  Fragments<T, BM, MT, KA> la;
+  Fragments<T, BN, NT, KB> lb;
+  la.init(wm * (BM / WM), lane);
+  lb.init(wn * (BN / WN), lane);
   f32x4 acc[NT][MT] = {};
-  if (kb0 < kb1) load(kb0, 0);
-  wait_loads();
-  __syncthreads();
-  for (uint32_t kb = kb0; kb < kb1; kb++) {
-    const uint32_t buf = (kb - kb0) & 1;
-    if (kb + 1 < kb1) load(kb + 1, buf ^ 1);
-    const uint8_t *p = lds + buf * (kRows * 128);
+  u32x4 fa[2][MH], fb[2][NT];  // by 32 elements of the step
+  auto fetch_a = [&](const uint8_t *p, int h) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-      const uint32_t c = ks ? c1 : c0;
-      u32x4 fa[MT], fb[NT];
+    for (int ks = 0; ks < 2; ks++)
 #pragma unroll
-      for (int i = 0; i < MT; i++) fa[i] = *(const u32x4 *)(p + ra + i * 2048 + c);
+      for (int i = 0; i < MH; i++) fa[ks][i] = la.get(p, ks, h * MH + i);
+  };
+  auto multiply = [&](int h) {
+    wait_reads();
+    meet();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int j = 0; j < NT; j++) fb[j] = *(const u32x4 *)(p + rb + j * 2048 + c);
+    for (int ks = 0; ks < 2; ks++)
 #pragma unroll
       for (int j = 0; j < NT; j++)
 #pragma unroll
-        for (int i = 0; i < MT; i++) acc[j][i] = mfma(T{}, fb[j], fa[i], acc[j][i]);
+        for (int i = 0; i < MH; i++)
+          acc[j][h * MH + i] = mfma(T{}, fb[ks][j], fa[ks][i], acc[j][h * MH + i]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    meet();
+  };
+  if (kb0 < kb1) {
+    load_a(kb0);
+    load_b(kb0);
+    if (kb0 + 1 < kb1) {
+      load_a(kb0 + 1);
+      load_b(kb0 + 1);
+      wait_but<OA::kLoads + OB::kLoads>();
+    } else {
+      wait_but<0>();
     }
-    wait_loads();  // this wave's part of the next buffer is in LDS
-    __syncthreads();
+    meet();
+    const bool late = wave >= kWaves / 2;
+    if (late) meet();
+    for (uint32_t kb = kb0; kb < kb1; kb++) {
+      const uint8_t *p = buffer(kb);
+      fetch_a(p, 0);
+#pragma unroll
+      for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) fb[ks][j] = lb.get(p + BM * 128, ks, j);
+      if (kb > kb0 && kb + 1 < kb1) load_a(kb + 1);
+      multiply(0);
+      fetch_a(p, 1);
+      if (kb + 2 < kb1) {
+        load_b(kb + 2);
+        wait_but<OB::kLoads>();
+      } else {
+        wait_but<0>();
+      }
+      multiply(1);
+    }
+    if (!late) meet();
   }
-  // lane: rows m = .. + i*16 + lr, columns n = .. + j*16 + kg*4 + 0..3
-  epi.template operator()<T, NT, MT>(acc, m0 + wm * (BM / WM) + lr, n0 + wn * (BN / WN) + kg * 4, g.m, g.n,
-                                     bn * WN + wn, blockIdx.y);
+  // lane: rows m = .. + i*16 + lane % 16, columns n = .. + j*16 + lane / 16 * 4 + 0..3
+  epi.template operator()<T, NT, MT>(acc, m0 + wm * (BM / WM) + (lane & 15), n0 + wn * (BN / WN) + (lane >> 4) * 4, g.m,
+                                     g.n, bn * WN + wn, blockIdx.y);
 }
 
 // ----------------------------------------------------------------- epilogues
@@ -255,18 +378,66 @@ hipError_t allow_lds(const void *fn, uint32_t bytes) {
   return e;
 }
 
-template <class T, int BM, int BN, int WM, int WN, class Epi>
+template <class T, int BM, int BN, int WM, int WN, bool KA, bool KB, class Epi>
 hipError_t gemm_launch(Gemm g, const Epi &epi, uint32_t splits, hipStream_t stream) {
   constexpr uint32_t lds = 2 * (BM + BN) * 128;
   g.mt = (g.m + BM - 1) / BM;
   g.nt = (g.n + BN - 1) / BN;
   const uint32_t nkb = (g.k + kBK - 1) / kBK;
   g.kb_per_split = (nkb + splits - 1) / splits;
-  const hipError_t e = allow_lds((const void *)gemm_nt<T, BM, BN, WM, WN, Epi>, lds);
+  const hipError_t e = allow_lds((const void *)gemm<T, BM, BN, WM, WN, KA, KB, Epi>, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((gemm_nt<T, BM, BN, WM, WN, Epi>), dim3(g.mt * g.nt, splits), dim3(64 * WM * WN), lds, stream, g,
-                     epi);
+  hipLaunchKernelGGL((gemm<T, BM, BN, WM, WN, KA, KB, Epi>), dim3(g.mt * g.nt, splits), dim3(64 * WM * WN), lds, stream,
+                     g, epi);
   return hipGetLastError();
+}
+
+// The tiles a product is cut into.
+struct Shape {
+  uint32_t bm, bn, waves_n, slots;  // slots: workgroups that the chip holds at once
+  double step;                      // us a step of 64 summed elements takes with all slots busy
+};
+constexpr Shape kShapes[5] = {{256, 256, 4, 256, 1.7}, {128, 128, 2, 512, 1.2}, {64, 64, 2, 1024, 1.2},
+                              {64, 128, 4, 768, 1.3}, {32, 128, 4, 1024, 1.2}};
+template <class T, bool KA, bool KB, class Epi>
+hipError_t product(const Gemm &g, const Epi &e, uint32_t shape, uint32_t splits, hipStream_t s) {
+  switch (shape) {
+    case 0: return gemm_launch<T, 256, 256, 2, 4, KA, KB>(g, e, splits, s);
+    case 1: return gemm_launch<T, 128, 128, 2, 2, KA, KB>(g, e, splits, s);
+    case 2: return gemm_launch<T, 64, 64, 2, 2, KA, KB>(g, e, splits, s);
+    case 3: return gemm_launch<T, 64, 128, 1, 4, KA, KB>(g, e, splits, s);
+    default: return gemm_launch<T, 32, 128, 1, 4, KA, KB>(g, e, splits, s);
+  }
+}
+
+uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
+
+// Shape and splits of the summed index for a product, by what its workgroups
+// take: rounds of `slots` of them, each its steps plus 4 us to start and end, and
+// 4 us plus the planes' traffic at 4 TB/s to join splits.  A split keeps at least
+// eight steps.  Few rows take a flat tile: they are bound by reading B, which
+// 128 rows a workgroup ask for in longer runs and with less of A beside it.
+struct Cut {
+  uint32_t shape, splits;
+};
+Cut cut_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
+  const uint64_t steps = up(k, kBK) / kBK;
+  Cut best = {2, 1};
+  double least = 1e30;
+  const int from = m <= 32 ? 4 : m <= 64 ? 3 : 0, to = m <= 32 ? 4 : m <= 64 ? 3 : 2;
+  for (int i = from; i <= to; i++) {
+    const Shape &sh = kShapes[i];
+    const uint64_t tiles = up(m, sh.bm) / sh.bm * (up(n, sh.bn) / sh.bn);
+    for (uint32_t s = 1; s <= (may_split ? 32u : 1u) && (s == 1 || steps / s >= 8); s *= 2) {
+      double t = (double)up(tiles * s, sh.slots) / sh.slots * ((double)((steps + s - 1) / s) * sh.step + 4.0);
+      if (s > 1) t += 4.0 + 8e-6 * (double)(m * n * s) / 4.0;
+      if (t < least) {
+        least = t;
+        best = Cut{(uint32_t)i, s};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace

@@ -12,9 +12,6 @@
 // gemm_nt does the product.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
-#include <cstring>
-
 #include "dfh.h"
 #include "dfh_gemm.h"
 
@@ -394,7 +391,7 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
   }
   for (uint32_t st = s0; st < s1; st++) {
     const uint8_t *p = lds + ((st - s0) & 1) * kBuf;
-    wait_loads();
+    wait_but<0>();
     __syncthreads();
     now = next;
     if (st + 1 < s1) request(st + 1, lds + ((st + 1 - s0) & 1) * kBuf);
@@ -507,33 +504,6 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out) {
   }
 }
 
-// The same, transposed: [k, np] with np = n rounded up to 8 (zeros past n).
-// 64 x 64 tiles through LDS, whose rows are padded by two elements so that the
-// column writes spread over the banks.
-template <class T>
-__global__ __launch_bounds__(256) void u4_expand_t(const U4 w, uint16_t *out, uint32_t np) {
-  __shared__ uint16_t tile[64][72];  // [k][n]
-  const uint32_t n0 = blockIdx.x * 64, k0 = blockIdx.y * 64;
-  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
-    const uint32_t r = t / 8, c = t % 8, n = n0 + r, k = k0 + c * 8;
-    uint32_t q = 0;
-    float s = 0.f, z = 0.f;
-    if (n < w.n && k < w.k) {
-      q = *(const uint32_t *)(w.packed + ((uint64_t)n * w.k + k) / 2);
-      const uint32_t g = group_of(w, k / 32);
-      s = scale_at(w, n, g);
-      z = zero_at(w, n, g);
-    }
-#pragma unroll
-    for (int d = 0; d < 8; d++) tile[c * 8 + d][r] = to_bits(T{}, ((float)((q >> (4 * d)) & 15u) - z) * s);
-  }
-  __syncthreads();
-  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
-    const uint32_t kk = t / 8, c = t % 8, k = k0 + kk, n = n0 + c * 8;
-    if (k < w.k && n < np) *(u32x4 *)(out + (uint64_t)k * np + n) = *(const u32x4 *)&tile[kk][c * 8];
-  }
-}
-
 // Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n].
 template <class T>
 __global__ __launch_bounds__(256) void join_planes(const float *p, uint32_t splits, uint32_t m, uint32_t n,
@@ -556,18 +526,6 @@ __global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss
 }
 
 constexpr uint32_t kFewRows = 256;
-
-uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
-
-// Splits of the summed index for an output of m x n: enough workgroups of
-// 64 x 64 tiles for two per CU, with four 64-element steps each at least.
-uint32_t splits_for(uint32_t m, uint32_t n, uint32_t k) {
-  const uint64_t tiles = up(m, 64) / 64 * (up(n, 64) / 64);
-  if (tiles >= 256) return 1;
-  const uint64_t most = up(k, 256) / 256;
-  const uint64_t want = (512 + tiles - 1) / tiles;
-  return (uint32_t)(want < most ? want : most < 1 ? 1 : most);
-}
 
 bool type_ok(df_type t) { return t == DF_TYPE_BF16 || t == DF_TYPE_F16; }
 
@@ -592,22 +550,15 @@ df_status matrix_of(const df_u4_matrix *m, U4 *w) {
   return DF_OK;
 }
 
-template <class T, class Epi>
-hipError_t product(const Gemm &g, const Epi &e, uint32_t splits, hipStream_t s) {
-  if (splits > 1) return gemm_launch<T, 64, 64, 2, 2>(g, e, splits, s);
-  if ((uint64_t)(up(g.m, 256) / 256) * (up(g.n, 256) / 256) >= 192) return gemm_launch<T, 256, 256, 2, 4>(g, e, 1, s);
-  if ((uint64_t)(up(g.m, 128) / 128) * (up(g.n, 128) / 128) >= 192) return gemm_launch<T, 128, 128, 2, 2>(g, e, 1, s);
-  return gemm_launch<T, 64, 64, 2, 2>(g, e, 1, s);
-}
-
-template <class T>
+// y or dx from 16-bit operands; planes: cut_for's splits.
+template <class T, bool KB>
 df_status many_rows(const Gemm &g, uint16_t *out, float *planes, hipStream_t s) {
-  const uint32_t splits = splits_for(g.m, g.n, g.k);
-  if (splits <= 1)
-    return product<T>(g, EpiStore{out, g.n, nullptr, 1.f}, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
+  const Cut c = cut_for(g.m, g.n, g.k, true);
+  if (c.splits <= 1)
+    return product<T, false, KB>(g, EpiStore{out, g.n, nullptr, 1.f}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
   const uint32_t ld = (uint32_t)up(g.n, 4);
-  if (product<T>(g, EpiPlane{planes, ld, false}, splits, s) != hipSuccess) return DF_ERR_HIP;
-  hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, splits, g.m, g.n, ld, out);
+  if (product<T, false, KB>(g, EpiPlane{planes, ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
+  hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld, out);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
 
@@ -700,7 +651,7 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
   } else {
     hipLaunchKernelGGL((u4_expand<T>), dim3(w.n), dim3(256), 0, s, w, (uint16_t *)ws);
     Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0};
-    return many_rows<T>(g, y, (float *)(ws + up((uint64_t)w.n * w.k * 2, 256)), s);
+    return many_rows<T, false>(g, y, (float *)(ws + up((uint64_t)w.n * w.k * 2, 256)), s);
   }
   return e == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
@@ -708,22 +659,22 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
 template <class T>
 df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, uint16_t *dx, uint8_t *ws,
                       hipStream_t s) {
+  hipLaunchKernelGGL((u4_expand<T>), dim3(w.n), dim3(256), 0, s, w, (uint16_t *)ws);
+  uint8_t *next = ws + up((uint64_t)w.n * w.k * 2, 256);
   const uint32_t np = (uint32_t)up(w.n, 8);
-  hipLaunchKernelGGL((u4_expand_t<T>), dim3((np + 63) / 64, (w.k + 63) / 64), dim3(256), 0, s, w, (uint16_t *)ws, np);
-  uint8_t *next = ws + up((uint64_t)np * w.k * 2, 256);
   if (np != w.n) {  // the summed index in whole 16-byte chunks
     hipLaunchKernelGGL(pad_rows, dim3(m), dim3(256), 0, s, dy, ds, w.n, np, (uint16_t *)next);
     dy = (const uint16_t *)next;
     ds = np;
     next += up((uint64_t)m * np * 2, 256);
   }
-  Gemm g = {dy, (const uint16_t *)ws, ds, np, m, w.k, np, 0, 0, 0};
-  return many_rows<T>(g, dx, (float *)next, s);
+  Gemm g = {dy, (const uint16_t *)ws, ds, w.k, m, w.k, w.n, 0, 0, 0};
+  return many_rows<T, true>(g, dx, (float *)next, s);
 }
 
-uint64_t plane_bytes(uint32_t m, uint32_t n, uint32_t k) {
-  const uint32_t splits = splits_for(m, n, k);
-  return splits > 1 ? 4ull * splits * m * up(n, 4) : 0;
+uint64_t plane_bytes(uint64_t m, uint64_t n, uint64_t k) {
+  const Cut c = cut_for(m, n, k, true);
+  return c.splits > 1 ? 4ull * c.splits * m * up(n, 4) : 0;
 }
 
 }  // namespace
@@ -737,14 +688,15 @@ uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
     const TilePlan p = few_plan((uint32_t)rows, u.n, u.k);
     return p.splits > 1 ? 4ull * p.splits * rows * p.ld : 0;
   }
-  return up(w->rows * w->cols * 2, 256) + plane_bytes((uint32_t)rows, (uint32_t)w->rows, (uint32_t)w->cols);
+  return up(w->rows * w->cols * 2, 256) + plane_bytes(rows, w->rows, w->cols);
 }
 
 uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
   U4 u;
   if (matrix_of(w, &u) != DF_OK || rows == 0 || rows > (1u << 24)) return 0;
   const uint64_t np = up(w->rows, 8);
-  return up(np * w->cols * 2, 256) + (np != w->rows ? up(rows * np * 2, 256) : 0) + plane_bytes((uint32_t)rows, (uint32_t)w->cols, (uint32_t)np);
+  return up(w->rows * w->cols * 2, 256) + (np != w->rows ? up(rows * np * 2, 256) : 0) +
+         plane_bytes(rows, w->cols, w->rows);
 }
 
 df_status df_linear_u4(const df_u4_matrix *w, df_type type, const void *x, uint64_t rows, uint64_t x_stride, void *y,

@@ -6,7 +6,7 @@
 //
 // with t the row's sparse target (a label is one entry with t = 1, T = 1).
 //
-// Forward: one pass of gemm_nt whose epilogue reduces each wave's columns to a
+// Forward: one pass of gemm whose epilogue reduces each wave's columns to a
 // maximum and a sum of exponentials per row; a second kernel joins them.  The
 // few logits that the targets name are dot products of their own.  Backward:
 // for a piece of the vocabulary that fits the workspace the logits are made
@@ -154,75 +154,84 @@ __global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t row
   if (lane == 0) picked[e] = s;
 }
 
-// Joins a row's parts and makes its loss.  16 rows a workgroup; thread t takes
-// parts t / 16, t / 16 + 16, ... and targets likewise of row t % 16.
+// Joins a row's parts and makes its loss.  R rows a workgroup of 256; thread t
+// takes parts t / R, t / R + 256 / R, ... (four loads in flight) and targets
+// likewise of row t % R.  R = 8 reads 64 bytes of a part at once; few rows take
+// R = 1, so that 256 threads share a row's parts (7 rows of 2004 parts: 64 us with
+// 16 rows a workgroup and one load in flight).
+template <int R>
 __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, uint32_t np,
                                                    Saved sv, float *loss) {
-  __shared__ float sa[16][17], sb[16][17];
-  const uint32_t r = threadIdx.x & 15, sl = threadIdx.x >> 4, m = blockIdx.x * 16 + r;
+  constexpr uint32_t S = 256 / R;
+  __shared__ float sa[S][R];
+  const uint32_t r = threadIdx.x % R, sl = threadIdx.x / R, m = blockIdx.x * R + r;
   const bool in = m < rows;
-  auto join_max = [&](float v) {
+  // over a row's S threads, in a fixed order
+  auto join = [&](float v, auto op) {
     sa[sl][r] = v;
     __syncthreads();
-    float o = -__builtin_huge_valf();
-    for (int q = 0; q < 16; q++) o = __builtin_fmaxf(o, sa[q][r]);
-    __syncthreads();
-    return o;
-  };
-  auto join_sum = [&](float v) {
-    sb[sl][r] = v;
-    __syncthreads();
-    float o = 0.f;
-    for (int q = 0; q < 16; q++) o += sb[q][r];
-    __syncthreads();
-    return o;
-  };
-  float mx = -__builtin_huge_valf();
-  if (in)
-    for (uint32_t p = sl; p < np; p += 16) mx = __builtin_fmaxf(mx, parts[(uint64_t)p * rows + m].x);
-  mx = join_max(mx);
-  const float ref = mx == -__builtin_huge_valf() ? 0.f : mx;
-  float s = 0.f;
-  if (in)
-    for (uint32_t p = sl; p < np; p += 16) {
-      const float2 v = parts[(uint64_t)p * rows + m];
-      s += v.y * exp2_(v.x - ref);
+#pragma unroll
+    for (uint32_t h = S / 2; h; h >>= 1) {
+      if (sl < h) sa[sl][r] = op(sa[sl][r], sa[sl + h][r]);
+      __syncthreads();
     }
-  s = join_sum(s);
+    v = sa[0][r];
+    __syncthreads();
+    return v;
+  };
+  auto most = [](float a, float b) { return __builtin_fmaxf(a, b); };
+  auto add = [](float a, float b) { return a + b; };
+  const float none = -__builtin_huge_valf();
+  float mx = none, s = 0.f;
+  for (uint32_t p = sl; in && p < np; p += 4 * S) {
+    float2 v[4];
+    float top = mx;
+#pragma unroll
+    for (uint32_t q = 0; q < 4; q++) {
+      v[q] = float2{none, 0.f};
+      if (p + q * S < np) v[q] = parts[(uint64_t)(p + q * S) * rows + m];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) top = most(top, v[q].x);
+    const float ref = top == none ? 0.f : top;
+    s *= exp2_(mx - ref);
+#pragma unroll
+    for (int q = 0; q < 4; q++) s += v[q].y * exp2_(v[q].x - ref);
+    mx = top;
+  }
+  const float all = join(mx, most), ref = all == none ? 0.f : all;
+  s = join(s * exp2_(mx - ref), add);
   const float lse2 = ref + __builtin_amdgcn_logf(s);  // base 2
   const float lse = lse2 * kLn2;
   const uint32_t per = t.top ? t.top : 1;
   // the target's softmax over its entries
-  float tm = -__builtin_huge_valf(), any = 0.f;
-  if (in)
-    for (uint32_t j = sl; j < per; j += 16)
-      if (target_of(t, m, j) >= 0) {
-        any = 1.f;
-        if (t.top) tm = __builtin_fmaxf(tm, teacher_at(t, m, j) / t.temp);
-      }
-  any = join_max(any);
-  tm = t.top ? join_max(tm) : 0.f;
-  const float tref = tm == -__builtin_huge_valf() ? 0.f : tm;
+  float tm = none, any = 0.f;
+  for (uint32_t j = sl; in && j < per; j += S)
+    if (target_of(t, m, j) >= 0) {
+      any = 1.f;
+      if (t.top) tm = most(tm, teacher_at(t, m, j) / t.temp);
+    }
+  any = join(any, most);
+  tm = t.top ? join(tm, most) : 0.f;
+  const float tref = tm == none ? 0.f : tm;
   float ts = 0.f;
-  if (in && t.top)
-    for (uint32_t j = sl; j < per; j += 16)
-      if (target_of(t, m, j) >= 0) ts += expf(teacher_at(t, m, j) / t.temp - tref);
-  ts = t.top ? join_sum(ts) : 1.f;
+  for (uint32_t j = sl; in && t.top && j < per; j += S)
+    if (target_of(t, m, j) >= 0) ts += expf(teacher_at(t, m, j) / t.temp - tref);
+  ts = t.top ? join(ts, add) : 1.f;
   const float lts = logf(ts);
   float l = 0.f;
-  if (in)
-    for (uint32_t j = sl; j < per; j += 16)
-      if (target_of(t, m, j) >= 0) {
-        const float z = sv.picked[(uint64_t)m * per + j];
-        if (!t.top) {
-          l = lse - z;
-          l = l < 0.f ? 0.f : l;  // z is one of the terms under the logarithm
-        } else {
-          const float d = teacher_at(t, m, j) / t.temp - tref, w = expf(d) / ts;
-          if (!(w == 0.f)) l += w * ((d - lts) - (z / t.temp - lse));
-        }
+  for (uint32_t j = sl; in && j < per; j += S)
+    if (target_of(t, m, j) >= 0) {
+      const float z = sv.picked[(uint64_t)m * per + j];
+      if (!t.top) {
+        l = lse - z;
+        l = l < 0.f ? 0.f : l;  // z is one of the terms under the logarithm
+      } else {
+        const float d = teacher_at(t, m, j) / t.temp - tref, w = expf(d) / ts;
+        if (!(w == 0.f)) l += w * ((d - lts) - (z / t.temp - lse));
       }
-  l = join_sum(l) * (t.top ? t.temp * t.temp : 1.f);
+    }
+  l = join(l, add) * (t.top ? t.temp * t.temp : 1.f);
   if (in && sl == 0) {
     // a row of entries that all hold -inf has nothing to learn from either
     uint32_t st = any > 0.f && !(t.top && ts == 0.f) ? kLoss : kNoLoss;
@@ -265,8 +274,8 @@ __global__ __launch_bounds__(1024) void reduce_rows(const float *rows_loss, cons
 }
 
 // Row factors of the gradient: g[m] = T * grad (mean: / count), 0 without a
-// loss; peak = max |g|; gn[m] = g[m] / peak, which the transposed dz carries
-// (1 in every row for sums and means, so it costs them no rounding).
+// loss; peak = max |g|; gn[m] = g[m] / peak, which weigh_rows puts on x (1 in
+// every row for sums and means, so it costs them no rounding).
 __global__ __launch_bounds__(1024) void row_factors(const uint32_t *state, uint32_t rows, const float *grad, int reduce,
                                                     float temp, float *g, float *gn, float *peak) {
   __shared__ float sm[16];
@@ -341,36 +350,23 @@ __global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved s
   }
 }
 
-// dst[c, r] = src[r, c] (times gn[r]); rows of another state than kLoss give
-// zeros where a state is given; dst rows hold rp elements, zeros past `rows`.
+// out[m] = gn[m] x[m], zeros in rows without a loss (whatever x holds there):
+// what dhead's sum over the rows takes for x, so dz needs no row factor.
 template <class T>
-__global__ __launch_bounds__(256) void turn(const uint16_t *src, uint64_t ss, uint32_t rows, uint32_t cols,
-                                            uint16_t *dst, uint32_t rp, const uint32_t *state, const float *gn) {
-  __shared__ uint16_t tile[64][72];  // [c][r]
-  const uint32_t r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
-    const uint32_t rr = t / 8, c = t % 8, r = r0 + rr;
+__global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs, uint32_t k, const uint32_t *state,
+                                                  const float *gn, uint16_t *out) {
+  const uint32_t m = blockIdx.x;
+  const bool live = state[m] == kLoss;
+  const float f = gn[m];
+  for (uint32_t c = threadIdx.x; c < k / 8; c += 256) {
     u32x4 v = {0, 0, 0, 0};
-    if (r < rows && c0 + c * 8 < cols && (!state || state[r] == kLoss)) {
-      v = *(const u32x4 *)(src + r * ss + c0 + c * 8);
-      if (gn) {
-        const float f = gn[r];
+    if (live) {
+      v = *(const u32x4 *)(x + m * xs + c * 8);
 #pragma unroll
-        for (int d = 0; d < 4; d++)
-          v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
-      }
+      for (int d = 0; d < 4; d++)
+        v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
     }
-#pragma unroll
-    for (int d = 0; d < 4; d++) {
-      tile[c * 8 + 2 * d][rr] = (uint16_t)v[d];
-      tile[c * 8 + 2 * d + 1][rr] = (uint16_t)(v[d] >> 16);
-    }
-  }
-  __syncthreads();
-  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
-    const uint32_t cc = t / 8, r = t % 8;
-    if (c0 + cc < cols && r0 + r * 8 < rp)
-      *(u32x4 *)(dst + (uint64_t)(c0 + cc) * rp + r0 + r * 8) = *(const u32x4 *)&tile[cc][r * 8];
+    *(u32x4 *)(out + (uint64_t)m * k + c * 8) = v;
   }
 }
 
@@ -396,22 +392,9 @@ __global__ __launch_bounds__(256) void fill_words(uint32_t *p, uint64_t n) {
 }
 
 // ---------------------------------------------------------------- host side
-uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
-uint64_t tiles_of(uint64_t m, uint64_t n, uint64_t t) { return up(m, t) / t * (up(n, t) / t); }
-
-// Output tile of a product: the largest that gives most CUs one.
-uint32_t tile_for(uint64_t m, uint64_t n) {
-  return tiles_of(m, n, 256) >= 192 ? 256 : tiles_of(m, n, 128) >= 192 ? 128 : 64;
-}
-uint32_t parts_of(uint64_t m, uint64_t n) {
-  const uint32_t t = tile_for(m, n);
-  return (uint32_t)(up(n, t) / t) * (t == 256 ? 4 : 2);
-}
-template <class T, class Epi>
-hipError_t product(const Gemm &g, const Epi &e, uint32_t tile, uint32_t splits, hipStream_t s) {
-  if (tile == 256) return gemm_launch<T, 256, 256, 2, 4>(g, e, splits, s);
-  if (tile == 128) return gemm_launch<T, 128, 128, 2, 2>(g, e, splits, s);
-  return gemm_launch<T, 64, 64, 2, 2>(g, e, splits, s);
+uint32_t parts_of(uint64_t m, uint64_t n, uint64_t k) {
+  const Shape &sh = kShapes[cut_for(m, n, k, false).shape];
+  return (uint32_t)(up(n, sh.bn) / sh.bn) * sh.waves_n;
 }
 
 df_status check(const df_loss *d) {
@@ -461,36 +444,37 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
                      head, d->head_stride, k, sv.picked);
   DFH_TRY(hipGetLastError());
   float2 *parts = (float2 *)ws;
-  const uint32_t np = parts_of(rows, vocab);
+  const uint32_t np = parts_of(rows, vocab, k);
   const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0};
-  DFH_TRY((product<T>(g, EpiStats{parts, kLog2e / d->temperature}, tile_for(rows, vocab), 1, s)));
+  DFH_TRY((product<T, false, false>(g, EpiStats{parts, kLog2e / d->temperature}, cut_for(rows, vocab, k, false).shape,
+                                    1, s)));
   float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + up(8ull * np * rows, 256));
-  hipLaunchKernelGGL(finish_rows, dim3((rows + 15) / 16), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv, per);
+  if (rows <= 256)
+    hipLaunchKernelGGL((finish_rows<1>), dim3(rows), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv, per);
+  else
+    hipLaunchKernelGGL((finish_rows<8>), dim3((rows + 7) / 8), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv,
+                       per);
   DFH_TRY(hipGetLastError());
   return DF_OK;
 }
 
 // How a gradient pass is cut: `nv` vocabulary entries a piece (a multiple of
-// 256), so that the piece's dz, its transpose and the turned head rows stay
-// within about the 256 MB that the last-level cache holds; `splits` parts of a
-// piece's sum for dx, whose output is small.
+// 256), so that the piece's dz stays within the last-level cache (256 MB; half of
+// it, beside the head's rows); dx is cut into `splits` parts of a piece's sum,
+// whose planes take the pieces one after the other.
 struct Plan {
-  uint32_t nv, mp, splits, tile_dx;
-  uint64_t dz, dzt, ht, xt, planes, fac, total;
+  uint32_t nv;
+  Cut dx;
+  uint64_t dz, xm, planes, fac, total;
 };
 Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
   Plan p;
   const uint64_t rows = d->rows, k = d->hidden, v8 = up(d->vocab, 8);
-  p.mp = (uint32_t)up(rows, 8);
-  const uint64_t per = 2 * rows + (want_dhead ? 2 * p.mp : 0) + (want_dx ? 2 * k : 0);
-  uint64_t nv = (256ull << 20) / per / 256 * 256;
+  uint64_t nv = (128ull << 20) / (2 * rows) / 256 * 256;
   if (nv < 2048) nv = 2048;
   if (nv > v8) nv = v8;
   p.nv = (uint32_t)nv;
-  p.tile_dx = tile_for(rows, k);
-  const uint64_t tiles = tiles_of(rows, k, p.tile_dx), most = (nv + 511) / 512;
-  const uint64_t want = tiles >= 192 ? 1 : (256 + tiles - 1) / tiles;
-  p.splits = (uint32_t)(want < most ? want : most);
+  p.dx = cut_for(rows, k, nv, true);
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t o = at;
@@ -499,10 +483,8 @@ Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
   };
   p.fac = take(4 * (2 * rows + 1));
   p.dz = take(2 * rows * nv);
-  p.dzt = take(want_dhead ? 2 * nv * p.mp : 0);
-  p.xt = take(want_dhead ? 2 * k * p.mp : 0);
-  p.ht = take(want_dx ? 2 * k * nv : 0);
-  p.planes = take(want_dx ? 4ull * p.splits * rows * k : 0);
+  p.xm = take(want_dhead ? 2 * rows * k : 0);
+  p.planes = take(want_dx ? 4ull * p.dx.splits * rows * k : 0);
   p.total = at;
   return p;
 }
@@ -516,39 +498,34 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
   const float c = kLog2e / d->temperature;
   float *g = (float *)(ws + p.fac), *gn = g + rows, *peak = gn + rows;
-  uint16_t *dz = (uint16_t *)(ws + p.dz), *dzt = (uint16_t *)(ws + p.dzt), *xt = (uint16_t *)(ws + p.xt),
-           *ht = (uint16_t *)(ws + p.ht);
+  uint16_t *dz = (uint16_t *)(ws + p.dz), *xm = (uint16_t *)(ws + p.xm);
   float *planes = (float *)(ws + p.planes);
   hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, (int)d->reduce,
                      d->temperature, g, gn, peak);
   if (dhead)
-    hipLaunchKernelGGL((turn<T>), dim3((p.mp + 63) / 64, (k + 63) / 64), dim3(256), 0, s, x, d->x_stride, rows, k, xt,
-                       p.mp, (const uint32_t *)sv.state, (const float *)nullptr);
+    hipLaunchKernelGGL((weigh_rows<T>), dim3(rows), dim3(256), 0, s, x, d->x_stride, k, (const uint32_t *)sv.state,
+                       (const float *)gn, xm);
   DFH_TRY(hipGetLastError());
   for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
     const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);
     const uint16_t *hp = head + (uint64_t)v0 * d->head_stride;
     const Gemm gz = {x, hp, d->x_stride, d->head_stride, rows, nv, k, 0, 0, 0};
-    DFH_TRY((product<T>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, tile_for(rows, nv), 1, s)));
+    DFH_TRY((product<T, false, false>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, cut_for(rows, nv, k, false).shape,
+                                      1, s)));
     hipLaunchKernelGGL((fix_targets<T>), dim3(rows), dim3(64), 0, s, t, sv, v0, nv, c, mul, dz, ldz);
     DFH_TRY(hipGetLastError());
     if (dhead) {
-      hipLaunchKernelGGL((turn<T>), dim3((p.mp + 63) / 64, (nv + 63) / 64), dim3(256), 0, s, (const uint16_t *)dz,
-                         (uint64_t)ldz, rows, nv, dzt, p.mp, (const uint32_t *)nullptr, (const float *)gn);
-      DFH_TRY(hipGetLastError());
-      const Gemm gw = {dzt, xt, p.mp, p.mp, nv, k, p.mp, 0, 0, 0};
-      DFH_TRY((product<T>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul}, tile_for(nv, k), 1, s)));
+      const Gemm gw = {dz, xm, ldz, k, nv, k, rows, 0, 0, 0};
+      DFH_TRY((product<T, true, true>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul},
+                                      cut_for(nv, k, rows, false).shape, 1, s)));
     }
     if (dx) {
-      hipLaunchKernelGGL((turn<T>), dim3((ldz + 63) / 64, (k + 63) / 64), dim3(256), 0, s, hp, d->head_stride, nv, k,
-                         ht, ldz, (const uint32_t *)nullptr, (const float *)nullptr);
-      DFH_TRY(hipGetLastError());
-      const Gemm gx = {dz, ht, ldz, ldz, rows, k, ldz, 0, 0, 0};
-      DFH_TRY((product<T>(gx, EpiPlane{planes, k, v0 != 0}, p.tile_dx, p.splits, s)));
+      const Gemm gx = {dz, hp, ldz, d->head_stride, rows, k, nv, 0, 0, 0};
+      DFH_TRY((product<T, false, true>(gx, EpiPlane{planes, k, v0 != 0}, p.dx.shape, p.dx.splits, s)));
     }
   }
   if (dx) {
-    hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.splits, rows, k,
+    hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.dx.splits, rows, k,
                        (const uint32_t *)sv.state, (const float *)g, 1.f / mul, dx);
     DFH_TRY(hipGetLastError());
   }
@@ -565,7 +542,7 @@ uint64_t df_loss_saved_bytes(const df_loss *d) {
 
 uint64_t df_loss_workspace_bytes(const df_loss *d) {
   if (check(d) != DF_OK || d->rows == 0) return 0;
-  return up(8ull * parts_of(d->rows, d->vocab) * d->rows, 256) + up(4 * d->rows, 256);
+  return up(8ull * parts_of(d->rows, d->vocab, d->hidden) * d->rows, 256) + up(4 * d->rows, 256);
 }
 
 uint64_t df_loss_grad_workspace_bytes(const df_loss *d, int want_dhead) {
@@ -590,7 +567,7 @@ df_status df_vocab_loss(const df_loss *d, float *loss, void *saved, void *worksp
   uint8_t *ws = (uint8_t *)workspace;
   st = d->type == DF_TYPE_BF16 ? loss_rows<BF16>(d, loss, sv, ws, stream) : loss_rows<F16>(d, loss, sv, ws, stream);
   if (st != DF_OK || d->reduce == DF_REDUCE_NONE) return st;
-  const float *per = (const float *)(ws + up(8ull * parts_of(d->rows, d->vocab) * d->rows, 256));
+  const float *per = (const float *)(ws + up(8ull * parts_of(d->rows, d->vocab, d->hidden) * d->rows, 256));
   hipLaunchKernelGGL(reduce_rows, dim3(1), dim3(1024), 0, stream, per, (const uint32_t *)sv.state, (uint32_t)d->rows,
                      d->reduce == DF_REDUCE_MEAN, loss);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
