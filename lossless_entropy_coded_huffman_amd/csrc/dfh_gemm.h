@@ -298,7 +298,27 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const Gemm g, const Epi epi
 }
 
 // ----------------------------------------------------------------- epilogues
-// 16-bit output, times *scale * mul.
+// A lane has 4 consecutive columns of a 16-column block (8 bytes in 16 bits).  Two
+// neighbouring blocks' words exchanged between lane groups 2 i and 2 i + 1 give
+// each lane 8 consecutive columns of one block: block j (even group) or j + 1
+// (odd group), columns 8 (group / 2) .. + 7.  Half as many stores, of 16 bytes.
+__device__ __forceinline__ u32x4 pair_blocks(u32x2 a, u32x2 b) {
+  const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false));
+  const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false));
+  return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
+// Eight 16-bit columns from `col` on into a row of n that starts at p.
+__device__ __forceinline__ void store8(uint16_t *p, uint32_t col, uint32_t n, bool aligned, u32x4 v) {
+  if (aligned && col + 8 <= n) {
+    *(u32x4 *)(p + col) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (col + e < n) p[col + e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+// 16-bit output (base 16-byte aligned), times *scale * mul.
 struct EpiStore {
   uint16_t *c;
   uint64_t ldc;
@@ -307,39 +327,36 @@ struct EpiStore {
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t) const {
+    static_assert(NT % 2 == 0, "blocks in pairs");
     const float s = (scale ? *scale : 1.f) * mul;
+    const bool aligned = (ldc & 7) == 0;
+    const uint32_t kg = (threadIdx.x >> 4) & 3, first = nb - 4 * kg + (kg & 1) * 16 + (kg >> 1) * 8;
 #pragma unroll
     for (int i = 0; i < MT; i++) {
       const uint32_t row = mb + i * 16;
-      if (row >= m) continue;
-      uint16_t *p = c + (uint64_t)row * ldc;
-      const bool al = ((ldc & 3) == 0);
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const uint32_t col = nb + j * 16;
-        const f32x4 v = acc[j][i] * s;
-        if (al && col + 4 <= n) {
-          *(u32x2 *)(p + col) = u32x2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (col + e < n) p[col + e] = to_bits(T{}, v[e]);
-        }
+      for (int j = 0; j < NT; j += 2) {
+        const f32x4 v = acc[j][i] * s, w = acc[j + 1][i] * s;
+        const u32x4 o = pair_blocks(u32x2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])},
+                                    u32x2{pack2(T{}, w[0], w[1]), pack2(T{}, w[2], w[3])});
+        if (row < m) store8(c + (uint64_t)row * ldc, first + j * 16, n, aligned, o);
       }
     }
   }
 };
 
-// FP32 partial planes [split][m][ld], stored or added to; ld is n rounded up
-// to a multiple of 4.
+// FP32 partial planes [split][..][ld], `stride` elements each, stored or added
+// to; ld is n rounded up to a multiple of 4.
 struct EpiPlane {
   float *c;
   uint32_t ld;
+  uint64_t stride;
   bool add;
+  EpiPlane from_row(uint32_t r) const { return EpiPlane{c + (uint64_t)r * ld, ld, stride, add}; }
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t split) const {
-    float *plane = c + (uint64_t)split * m * ld;
+    float *plane = c + split * stride;
 #pragma unroll
     for (int i = 0; i < MT; i++) {
       const uint32_t row = mb + i * 16;
@@ -414,30 +431,58 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 
 // Shape and splits of the summed index for a product, by what its workgroups
 // take: rounds of `slots` of them, each its steps plus 4 us to start and end, and
-// 4 us plus the planes' traffic at 4 TB/s to join splits.  A split keeps at least
-// eight steps.  Few rows take a flat tile: they are bound by reading B, which
-// 128 rows a workgroup ask for in longer runs and with less of A beside it.
+// 4 us plus the planes' traffic at 4 TB/s to join splits; B is read at 5 TB/s at
+// most.  A split keeps at least eight steps.  Few rows take a flat tile: they are
+// bound by reading B, which 128 rows a workgroup ask for in longer runs and with
+// less of A beside it.
 struct Cut {
   uint32_t shape, splits;
+  double us;
 };
 Cut cut_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
   const uint64_t steps = up(k, kBK) / kBK;
-  Cut best = {2, 1};
-  double least = 1e30;
+  Cut best = {2, 1, 1e30};
   const int from = m <= 32 ? 4 : m <= 64 ? 3 : 0, to = m <= 32 ? 4 : m <= 64 ? 3 : 2;
   for (int i = from; i <= to; i++) {
     const Shape &sh = kShapes[i];
     const uint64_t tiles = up(m, sh.bm) / sh.bm * (up(n, sh.bn) / sh.bn);
     for (uint32_t s = 1; s <= (may_split ? 32u : 1u) && (s == 1 || steps / s >= 8); s *= 2) {
       double t = (double)up(tiles * s, sh.slots) / sh.slots * ((double)((steps + s - 1) / s) * sh.step + 4.0);
+      const double read = 2.0 * (double)n * (double)k / 5e6 + 4.0;
+      if (t < read) t = read;
       if (s > 1) t += 4.0 + 8e-6 * (double)(m * n * s) / 4.0;
-      if (t < least) {
-        least = t;
-        best = Cut{(uint32_t)i, s};
-      }
+      if (t < best.us) best = Cut{(uint32_t)i, s, t};
     }
   }
   return best;
+}
+
+// The same for a product whose rows may go in two launches: whole tiles of 256
+// rows, and up to 64 rows behind them in flat tiles, where that takes less (517
+// x 32003 x 2056: a third row of tiles for 5 rows costs a second round, 111 us
+// against 57 + 25).  rest.us is 0 where there is one launch.
+struct RowCut {
+  uint32_t rows;  // in the first launch
+  Cut main, rest;
+};
+RowCut rows_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
+  RowCut c = {(uint32_t)m, cut_for(m, n, k, may_split), {0, 0, 0.0}};
+  const uint32_t r = (uint32_t)(m % 256);
+  if (m > 256 && r && r <= 64) {
+    const Cut a = cut_for(m - r, n, k, may_split), b = cut_for(r, n, k, may_split);
+    if (a.us + b.us < c.main.us) c = RowCut{(uint32_t)m - r, a, b};
+  }
+  return c;
+}
+template <class T, bool KB, class Epi>
+hipError_t product_rows(const Gemm &g, const Epi &e, const RowCut &c, hipStream_t s) {
+  Gemm f = g;
+  f.m = c.rows;
+  const hipError_t st = product<T, false, KB>(f, e, c.main.shape, c.main.splits, s);
+  if (st != hipSuccess || c.rest.us == 0.0) return st;
+  f.m = g.m - c.rows;
+  f.a = g.a + (uint64_t)c.rows * g.lda;
+  return product<T, false, KB>(f, e.from_row(c.rows), c.rest.shape, c.rest.splits, s);
 }
 
 }  // namespace

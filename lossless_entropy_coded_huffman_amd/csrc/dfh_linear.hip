@@ -6,7 +6,7 @@
 // The weights are the packed nibbles that a uint4 container decodes to: the
 // element n * cols + k, two per byte, the even one in the low nibble.
 //
-// Few rows: u4_tokens (up to 4) and u4_tile (up to 256) feed the matrix cores
+// Few rows: u4_tokens (up to 4) and u4_tile (few_rows) feed the matrix cores
 // with the integers themselves, and the scale multiplies a group's FP32 sum.
 // More rows: the weights are expanded to 16 bits in the caller's workspace and
 // gemm_nt does the product.
@@ -488,20 +488,41 @@ __global__ __launch_bounds__(256) void join_tiles(const U4 w, const uint16_t *x,
 
 // The weights as 16-bit floats, [n, k].  Each is rounded once from FP32
 // (relative 2^-8 / 2^-11 at most); the sums over them are FP32.
-template <class T>
+// A workgroup takes 1024 chunks of 8 weights of a row, four a thread, all loaded
+// (scales unconverted) before the first is used.
+template <class T, class S>
 __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out) {
-  const uint32_t n = blockIdx.x;
-  for (uint32_t c = threadIdx.x; c < w.k / 8; c += 256) {
-    const uint64_t at = (uint64_t)n * (w.k / 8) + c;
-    const uint32_t q = ((const uint32_t *)w.packed)[at];
-    const uint32_t g = group_of(w, c / 4);
-    const float s = scale_at(w, n, g), z = zero_at(w, n, g);
-    u32x4 o;
+  const uint32_t n = blockIdx.x, chunks = w.k / 8, c0 = blockIdx.y * 1024 + threadIdx.x;
+  const uint64_t row = (uint64_t)n * chunks;
+  const S *ps = (const S *)w.scales + n * w.sstride;
+  const uint8_t *pz = w.zeros ? w.zeros + n * w.zstride : (const uint8_t *)&g_eights;
+  const uint32_t zon = w.zeros ? 1 : 0;
+  uint32_t q[4];
+  S s[4];
+  uint8_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t c = c0 + i * 256 < chunks ? c0 + i * 256 : chunks - 1, g = group_of(w, c / 4);
+    q[i] = ((const uint32_t *)w.packed)[row + c];
+    s[i] = ps[g];
+    z[i] = pz[g * zon];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t c = c0 + i * 256;
+    if (c >= chunks) break;
+    const float f = scale_of(w, s[i]), o = (float)z[i];
+    u32x4 v;
 #pragma unroll
     for (int d = 0; d < 4; d++)
-      o[d] = pack2(T{}, ((float)((q >> (8 * d)) & 15u) - z) * s, ((float)((q >> (8 * d + 4)) & 15u) - z) * s);
-    ((u32x4 *)out)[at] = o;
+      v[d] = pack2(T{}, ((float)((q[i] >> (8 * d)) & 15u) - o) * f, ((float)((q[i] >> (8 * d + 4)) & 15u) - o) * f);
+    ((u32x4 *)out)[row + c] = v;
   }
+}
+template <class T>
+void expand(const U4 &w, uint16_t *out, hipStream_t s) {
+  auto *fn = w.scale_type == DF_TYPE_F32 ? u4_expand<T, float> : u4_expand<T, uint16_t>;
+  hipLaunchKernelGGL(fn, dim3(w.n, (w.k + 8191) / 8192), dim3(256), 0, s, w, out);
 }
 
 // Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n].
@@ -525,7 +546,12 @@ __global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss
   for (uint32_t c = threadIdx.x; c < np; c += 256) dst[r * np + c] = c < n ? src[r * ss + c] : (uint16_t)0;
 }
 
-constexpr uint32_t kFewRows = 256;
+// Rows that u4_tile takes rather than an expansion: the expansion costs a fixed
+// time per weight (0.6 us a million), the tile kernel a time per weight and 64
+// rows (0.34 us a million once the chip is full, less before).
+// 256 x 14336 x 4096: 79 us against 83; 512 x 14336 x 4096: 140 against 95;
+// 512 x 4096 x 4096: 41 against 49; 333 x 2047 x 1416: 17 against 23.
+bool few_rows(uint64_t m, uint64_t n, uint64_t k) { return m <= 256 || (m <= 512 && n * k <= 1u << 24); }
 
 bool type_ok(df_type t) { return t == DF_TYPE_BF16 || t == DF_TYPE_F16; }
 
@@ -557,7 +583,7 @@ df_status many_rows(const Gemm &g, uint16_t *out, float *planes, hipStream_t s) 
   if (c.splits <= 1)
     return product<T, false, KB>(g, EpiStore{out, g.n, nullptr, 1.f}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
   const uint32_t ld = (uint32_t)up(g.n, 4);
-  if (product<T, false, KB>(g, EpiPlane{planes, ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
+  if (product<T, false, KB>(g, EpiPlane{planes, ld, (uint64_t)g.m * ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
   hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld, out);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
@@ -643,13 +669,13 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
     e = w.n >= 32768                    ? tokens_launch<T, 1, 4>(w, x, xs, m, y, s)
         : m == 1 && w.n <= 4096 && w.k > 8192 ? tokens_launch<T, 1, 16>(w, x, xs, m, y, s)
                                         : tokens_launch<T, 1, 8>(w, x, xs, m, y, s);
-  } else if (m <= kFewRows) {
+  } else if (few_rows(m, w.n, w.k)) {
     const TilePlan p = few_plan(m, w.n, w.k);
     e = p.mtile == 1   ? tile_launch<T, 1, 1>(w, x, xs, m, y, (float *)ws, p, s)
         : p.mtile == 2 ? tile_launch<T, 2, 1>(w, x, xs, m, y, (float *)ws, p, s)
                        : tile_launch<T, 4, 1>(w, x, xs, m, y, (float *)ws, p, s);
   } else {
-    hipLaunchKernelGGL((u4_expand<T>), dim3(w.n), dim3(256), 0, s, w, (uint16_t *)ws);
+    expand<T>(w, (uint16_t *)ws, s);
     Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0};
     return many_rows<T, false>(g, y, (float *)(ws + up((uint64_t)w.n * w.k * 2, 256)), s);
   }
@@ -659,7 +685,7 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
 template <class T>
 df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, uint16_t *dx, uint8_t *ws,
                       hipStream_t s) {
-  hipLaunchKernelGGL((u4_expand<T>), dim3(w.n), dim3(256), 0, s, w, (uint16_t *)ws);
+  expand<T>(w, (uint16_t *)ws, s);
   uint8_t *next = ws + up((uint64_t)w.n * w.k * 2, 256);
   const uint32_t np = (uint32_t)up(w.n, 8);
   if (np != w.n) {  // the summed index in whole 16-byte chunks
@@ -684,7 +710,7 @@ extern "C" {
 uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
   U4 u;
   if (matrix_of(w, &u) != DF_OK || rows <= kTokens || rows > (1u << 24)) return 0;
-  if (rows <= kFewRows) {
+  if (few_rows(rows, u.n, u.k)) {
     const TilePlan p = few_plan((uint32_t)rows, u.n, u.k);
     return p.splits > 1 ? 4ull * p.splits * rows * p.ld : 0;
   }

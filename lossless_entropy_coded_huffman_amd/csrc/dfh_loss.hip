@@ -63,8 +63,10 @@ __device__ __forceinline__ int32_t target_of(const Targets &t, uint32_t m, uint3
 // ------------------------------------------------------------------ epilogues
 // Per row, over this wave's columns: max of z2 = c z and sum of 2^(z2 - max).
 struct EpiStats {
-  float2 *parts;  // [part][m]
+  float2 *parts;  // [part][rows]
+  uint32_t rows;
   float c;
+  EpiStats from_row(uint32_t r) const { return EpiStats{parts + r, rows, c}; }
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t part, uint32_t) const {
@@ -90,7 +92,7 @@ struct EpiStats {
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
       const uint32_t row = mb + i * 16;
-      if ((threadIdx.x & 48) == 0 && row < m) parts[(uint64_t)part * m + row] = float2{mx, s};
+      if ((threadIdx.x & 48) == 0 && row < m) parts[(uint64_t)part * rows + row] = float2{mx, s};
     }
   }
 };
@@ -105,23 +107,31 @@ struct EpiDz {
   const float *lse2;
   const uint32_t *state;
   float c, mul;
+  EpiDz from_row(uint32_t r) const { return EpiDz{dz + (uint64_t)r * ldz, ldz, lse2 + r, state + r, c, mul}; }
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t) const {
+    static_assert(NT % 2 == 0, "blocks in pairs");
+    const uint32_t kg = (threadIdx.x >> 4) & 3, first = nb - 4 * kg + (kg & 1) * 16 + (kg >> 1) * 8;
 #pragma unroll
     for (int i = 0; i < MT; i++) {
-      const uint32_t row = mb + i * 16;
-      if (row >= m) continue;
-      const bool live = state[row] == kLoss;
-      const float l = lse2[row];
+      const uint32_t row = mb + i * 16, r = row < m ? row : m - 1;
+      const bool live = state[r] == kLoss;
+      const float l = lse2[r];
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const uint32_t col = nb + j * 16;
-        if (col >= ldz) continue;
-        float p[4];
+      for (int j = 0; j < NT; j += 2) {
+        u32x2 o[2];
 #pragma unroll
-        for (int e = 0; e < 4; e++) p[e] = live && col + e < n ? exp2_(acc[j][i][e] * c - l) * mul : 0.f;
-        *(u32x2 *)(dz + (uint64_t)row * ldz + col) = u32x2{pack2(T{}, p[0], p[1]), pack2(T{}, p[2], p[3])};
+        for (int h = 0; h < 2; h++) {
+          const uint32_t col = nb + (j + h) * 16;
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) p[e] = live && col + e < n ? exp2_(acc[j + h][i][e] * c - l) * mul : 0.f;
+          o[h] = u32x2{pack2(T{}, p[0], p[1]), pack2(T{}, p[2], p[3])};
+        }
+        const u32x4 v = pair_blocks(o[0], o[1]);
+        const uint32_t col = first + j * 16;
+        if (row < m && col < ldz) *(u32x4 *)(dz + (uint64_t)row * ldz + col) = v;
       }
     }
   }
@@ -154,13 +164,19 @@ __global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t row
   if (lane == 0) picked[e] = s;
 }
 
+// Parts of a row: `main` in the first `rows` rows, `rest` in those behind them.
+struct Parts {
+  uint32_t rows, main, rest;
+  uint32_t most() const { return main > rest ? main : rest; }
+};
+
 // Joins a row's parts and makes its loss.  R rows a workgroup of 256; thread t
 // takes parts t / R, t / R + 256 / R, ... (four loads in flight) and targets
 // likewise of row t % R.  R = 8 reads 64 bytes of a part at once; few rows take
 // R = 1, so that 256 threads share a row's parts (7 rows of 2004 parts: 64 us with
 // 16 rows a workgroup and one load in flight).
 template <int R>
-__global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, uint32_t np,
+__global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, Parts np,
                                                    Saved sv, float *loss) {
   constexpr uint32_t S = 256 / R;
   __shared__ float sa[S][R];
@@ -183,13 +199,14 @@ __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t row
   auto add = [](float a, float b) { return a + b; };
   const float none = -__builtin_huge_valf();
   float mx = none, s = 0.f;
-  for (uint32_t p = sl; in && p < np; p += 4 * S) {
+  const uint32_t mine = m < np.rows ? np.main : np.rest;
+  for (uint32_t p = sl; in && p < mine; p += 4 * S) {
     float2 v[4];
     float top = mx;
 #pragma unroll
     for (uint32_t q = 0; q < 4; q++) {
       v[q] = float2{none, 0.f};
-      if (p + q * S < np) v[q] = parts[(uint64_t)(p + q * S) * rows + m];
+      if (p + q * S < mine) v[q] = parts[(uint64_t)(p + q * S) * rows + m];
     }
 #pragma unroll
     for (int q = 0; q < 4; q++) top = most(top, v[q].x);
@@ -350,33 +367,48 @@ __global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved s
   }
 }
 
-// out[m] = gn[m] x[m], zeros in rows without a loss (whatever x holds there):
-// what dhead's sum over the rows takes for x, so dz needs no row factor.
+// out[c, m] = gn[m] x[m, c], zeros in rows without a loss (whatever x holds
+// there) and in the columns that pad a row to mp: what dhead's sum over the rows
+// takes for x, so dz needs no row factor; turned, so that only dz is read across
+// there.  64 x 64 tiles through LDS, padded rows spread the column writes.
 template <class T>
-__global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs, uint32_t k, const uint32_t *state,
-                                                  const float *gn, uint16_t *out) {
-  const uint32_t m = blockIdx.x;
-  const bool live = state[m] == kLoss;
-  const float f = gn[m];
-  for (uint32_t c = threadIdx.x; c < k / 8; c += 256) {
+__global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs, uint32_t rows, uint32_t k,
+                                                  const uint32_t *state, const float *gn, uint16_t *out, uint32_t mp) {
+  __shared__ uint16_t tile[64][72];  // [c][m]
+  const uint32_t m0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
+#pragma unroll
+  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
+    const uint32_t r = t / 8, c = t % 8, m = m0 + r;
     u32x4 v = {0, 0, 0, 0};
-    if (live) {
-      v = *(const u32x4 *)(x + m * xs + c * 8);
+    if (m < rows && c0 + c * 8 < k && state[m] == kLoss) {
+      const float f = gn[m];
+      v = *(const u32x4 *)(x + m * xs + c0 + c * 8);
 #pragma unroll
       for (int d = 0; d < 4; d++)
         v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
     }
-    *(u32x4 *)(out + (uint64_t)m * k + c * 8) = v;
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+      tile[c * 8 + 2 * d][r] = (uint16_t)v[d];
+      tile[c * 8 + 2 * d + 1][r] = (uint16_t)(v[d] >> 16);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t t = threadIdx.x; t < 512; t += 256) {
+    const uint32_t c = t / 8, m = m0 + t % 8 * 8;
+    if (c0 + c < k && m < mp) *(u32x4 *)(out + (uint64_t)(c0 + c) * mp + m) = *(const u32x4 *)&tile[c][t % 8 * 8];
   }
 }
 
 // dx[m] = g[m] * mul * (sum of the planes), zero in rows without a loss.
 template <class T>
-__global__ __launch_bounds__(256) void finish_dx(const float *planes, uint32_t splits, uint32_t rows, uint32_t k,
+__global__ __launch_bounds__(256) void finish_dx(const float *planes, Parts parts, uint32_t rows, uint32_t k,
                                                  const uint32_t *state, const float *g, float mul, uint16_t *dx) {
   const uint32_t m = blockIdx.x;
   const bool live = state[m] == kLoss;
   const float f = g[m] * mul;
+  const uint32_t splits = m < parts.rows ? parts.main : parts.rest;
   for (uint32_t c = threadIdx.x * 4; c < k; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (live) {
@@ -392,9 +424,15 @@ __global__ __launch_bounds__(256) void fill_words(uint32_t *p, uint64_t n) {
 }
 
 // ---------------------------------------------------------------- host side
-uint32_t parts_of(uint64_t m, uint64_t n, uint64_t k) {
-  const Shape &sh = kShapes[cut_for(m, n, k, false).shape];
-  return (uint32_t)(up(n, sh.bn) / sh.bn) * sh.waves_n;
+Parts parts_of(const RowCut &c, uint64_t n) {
+  auto of = [&](const Cut &q) {
+    const Shape &sh = kShapes[q.shape];
+    return (uint32_t)(up(n, sh.bn) / sh.bn) * sh.waves_n;
+  };
+  return Parts{c.rows, of(c.main), c.rest.us == 0.0 ? 0 : of(c.rest)};
+}
+uint64_t parts_bytes(const df_loss *d) {
+  return up(8ull * parts_of(rows_for(d->rows, d->vocab, d->hidden, false), d->vocab).most() * d->rows, 256);
 }
 
 df_status check(const df_loss *d) {
@@ -444,11 +482,11 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
                      head, d->head_stride, k, sv.picked);
   DFH_TRY(hipGetLastError());
   float2 *parts = (float2 *)ws;
-  const uint32_t np = parts_of(rows, vocab, k);
+  const RowCut cut = rows_for(rows, vocab, k, false);
+  const Parts np = parts_of(cut, vocab);
   const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0};
-  DFH_TRY((product<T, false, false>(g, EpiStats{parts, kLog2e / d->temperature}, cut_for(rows, vocab, k, false).shape,
-                                    1, s)));
-  float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + up(8ull * np * rows, 256));
+  DFH_TRY((product_rows<T, false>(g, EpiStats{parts, rows, kLog2e / d->temperature}, cut, s)));
+  float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + parts_bytes(d));
   if (rows <= 256)
     hipLaunchKernelGGL((finish_rows<1>), dim3(rows), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv, per);
   else
@@ -464,8 +502,9 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
 // whose planes take the pieces one after the other.
 struct Plan {
   uint32_t nv;
-  Cut dx;
+  RowCut dx;
   uint64_t dz, xm, planes, fac, total;
+  Parts splits() const { return Parts{dx.rows, dx.main.splits, dx.rest.splits}; }
 };
 Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
   Plan p;
@@ -474,7 +513,7 @@ Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
   if (nv < 2048) nv = 2048;
   if (nv > v8) nv = v8;
   p.nv = (uint32_t)nv;
-  p.dx = cut_for(rows, k, nv, true);
+  p.dx = rows_for(rows, k, nv, true);
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t o = at;
@@ -483,8 +522,8 @@ Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
   };
   p.fac = take(4 * (2 * rows + 1));
   p.dz = take(2 * rows * nv);
-  p.xm = take(want_dhead ? 2 * rows * k : 0);
-  p.planes = take(want_dx ? 4ull * p.dx.splits * rows * k : 0);
+  p.xm = take(want_dhead ? 2 * up(rows, 8) * k : 0);
+  p.planes = take(want_dx ? 4ull * p.splits().most() * rows * k : 0);
   p.total = at;
   return p;
 }
@@ -494,6 +533,7 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
                     float mul, hipStream_t s) {
   const Plan p = plan_of(d, dx != nullptr, dhead != nullptr);
   const uint32_t rows = (uint32_t)d->rows, vocab = (uint32_t)d->vocab, k = (uint32_t)d->hidden;
+  const uint32_t mp = (uint32_t)up(rows, 8);
   const Targets t = targets_of(d);
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
   const float c = kLog2e / d->temperature;
@@ -503,29 +543,28 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, (int)d->reduce,
                      d->temperature, g, gn, peak);
   if (dhead)
-    hipLaunchKernelGGL((weigh_rows<T>), dim3(rows), dim3(256), 0, s, x, d->x_stride, k, (const uint32_t *)sv.state,
-                       (const float *)gn, xm);
+    hipLaunchKernelGGL((weigh_rows<T>), dim3((mp + 63) / 64, (k + 63) / 64), dim3(256), 0, s, x, d->x_stride, rows, k,
+                       (const uint32_t *)sv.state, (const float *)gn, xm, mp);
   DFH_TRY(hipGetLastError());
   for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
     const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);
     const uint16_t *hp = head + (uint64_t)v0 * d->head_stride;
     const Gemm gz = {x, hp, d->x_stride, d->head_stride, rows, nv, k, 0, 0, 0};
-    DFH_TRY((product<T, false, false>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, cut_for(rows, nv, k, false).shape,
-                                      1, s)));
+    DFH_TRY((product_rows<T, false>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, rows_for(rows, nv, k, false), s)));
     hipLaunchKernelGGL((fix_targets<T>), dim3(rows), dim3(64), 0, s, t, sv, v0, nv, c, mul, dz, ldz);
     DFH_TRY(hipGetLastError());
     if (dhead) {
-      const Gemm gw = {dz, xm, ldz, k, nv, k, rows, 0, 0, 0};
-      DFH_TRY((product<T, true, true>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul},
+      const Gemm gw = {dz, xm, ldz, mp, nv, k, rows, 0, 0, 0};
+      DFH_TRY((product<T, true, false>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul},
                                       cut_for(nv, k, rows, false).shape, 1, s)));
     }
     if (dx) {
       const Gemm gx = {dz, hp, ldz, d->head_stride, rows, k, nv, 0, 0, 0};
-      DFH_TRY((product<T, false, true>(gx, EpiPlane{planes, k, v0 != 0}, p.dx.shape, p.dx.splits, s)));
+      DFH_TRY((product_rows<T, true>(gx, EpiPlane{planes, k, (uint64_t)rows * k, v0 != 0}, p.dx, s)));
     }
   }
   if (dx) {
-    hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.dx.splits, rows, k,
+    hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.splits(), rows, k,
                        (const uint32_t *)sv.state, (const float *)g, 1.f / mul, dx);
     DFH_TRY(hipGetLastError());
   }
@@ -542,7 +581,7 @@ uint64_t df_loss_saved_bytes(const df_loss *d) {
 
 uint64_t df_loss_workspace_bytes(const df_loss *d) {
   if (check(d) != DF_OK || d->rows == 0) return 0;
-  return up(8ull * parts_of(d->rows, d->vocab, d->hidden) * d->rows, 256) + up(4 * d->rows, 256);
+  return parts_bytes(d) + up(4 * d->rows, 256);
 }
 
 uint64_t df_loss_grad_workspace_bytes(const df_loss *d, int want_dhead) {
@@ -567,7 +606,7 @@ df_status df_vocab_loss(const df_loss *d, float *loss, void *saved, void *worksp
   uint8_t *ws = (uint8_t *)workspace;
   st = d->type == DF_TYPE_BF16 ? loss_rows<BF16>(d, loss, sv, ws, stream) : loss_rows<F16>(d, loss, sv, ws, stream);
   if (st != DF_OK || d->reduce == DF_REDUCE_NONE) return st;
-  const float *per = (const float *)(ws + up(8ull * parts_of(d->rows, d->vocab, d->hidden) * d->rows, 256));
+  const float *per = (const float *)(ws + parts_bytes(d));
   hipLaunchKernelGGL(reduce_rows, dim3(1), dim3(1024), 0, stream, per, (const uint32_t *)sv.state, (uint32_t)d->rows,
                      d->reduce == DF_REDUCE_MEAN, loss);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;

@@ -21,7 +21,6 @@ gradient is refused.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -53,21 +52,25 @@ def _rows16(t: torch.Tensor) -> torch.Tensor:
     return c if c.data_ptr() % 16 == 0 else c.clone()
 
 
-@contextlib.contextmanager
-def _launching(stream, dev, tensors):
-    """The torch stream a call runs on, made current (with its device) when it
-    is not; inputs are then recorded on it."""
+# the raw handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(stream, dev, tensors, call):
+    """call(stream handle) with the stream it runs on current (and its device);
+    inputs are recorded on a stream that was not."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return call(_raw_stream(dev.index))
     cur = torch.cuda.current_stream(dev)
     ts = cur if stream is None else dfh._torch_stream(stream, dev)
-    if ts.cuda_stream == cur.cuda_stream and torch.cuda.current_device() == dev.index:
-        yield ts
-        return
     with torch.cuda.device(dev), torch.cuda.stream(ts):
-        yield ts
+        out = call(ts.cuda_stream)
         if ts.cuda_stream != cur.cuda_stream:
             for t in tensors:
                 if t is not None:
                     t.record_stream(ts)
+    return out
 
 
 def _workspace(nbytes: int, dev) -> torch.Tensor:
@@ -128,68 +131,94 @@ class U4Matrix:
                                      0 if zeros is None else zeros.stride(0), packed.data_ptr(), scales.data_ptr(),
                                      _p(zeros))
         self._ref = ctypes.byref(self.view)
+        self._need, self._need_grad = {}, {}   # workspace bytes by row count
 
     def _tensors(self):
         return (self.packed, self.scales, self.zeros)
 
 
 def _linear(x: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
-    _on(x, w.device, "x")
+    dev = w.device
+    if x.device != dev:
+        _on(x, dev, "x")
     ty = _type(x, "x")
+    flat = x.dim() == 2
     if x.dim() < 1 or x.shape[-1] != w.cols:
         raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(x.shape)))
     L = dfh.lib()
-    with _launching(stream, w.device, (x,) + w._tensors()) as ts:
-        x2 = _rows16(x if x.dim() == 2 else x.reshape(-1, w.cols))
+
+    def call(handle):
+        x2 = _rows16(x if flat else x.reshape(-1, w.cols))
         m = x2.shape[0]
-        y = torch.empty((m, w.rows), dtype=x.dtype, device=w.device)
-        need = L.df_linear_u4_workspace_bytes(w._ref, m)
-        ws = _workspace(need, w.device) if need else None
-        dfh._check(L.df_linear_u4(w._ref, ty, x2.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws), need,
-                                  ts.cuda_stream), "df_linear_u4")
-    return y if x.dim() == 2 else y.view(x.shape[:-1] + (w.rows,))
+        y = torch.empty((m, w.rows), dtype=x.dtype, device=dev)
+        need = w._need.get(m)
+        if need is None:
+            need = w._need[m] = L.df_linear_u4_workspace_bytes(w._ref, m)
+        ws = _workspace(need, dev) if need else None
+        st = L.df_linear_u4(w._ref, ty, x2.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws), need, handle)
+        if st:
+            dfh._check(st, "df_linear_u4")
+        return y
+
+    y = _launch(stream, dev, (x,) + w._tensors(), call)
+    return y if flat else y.view(x.shape[:-1] + (w.rows,))
 
 
 def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """dx[..., k] = sum over n of dy[..., n] W[n, k]: the gradient of linear_u4
     to its input, in dy's type (bfloat16 or float16)."""
-    _on(dy, w.device, "dy")
+    dev = w.device
+    if dy.device != dev:
+        _on(dy, dev, "dy")
     ty = _type(dy, "dy")
     if dy.dim() < 1 or dy.shape[-1] != w.rows:
         raise ValueError("dy must be [..., %d], got %s" % (w.rows, tuple(dy.shape)))
     L = dfh.lib()
-    with _launching(stream, w.device, (dy,) + w._tensors()) as ts:
-        d2 = dy.reshape(-1, w.rows)
+
+    def call(handle):
+        d2 = dy if dy.dim() == 2 else dy.reshape(-1, w.rows)
         if w.rows % 8 == 0:
             d2 = _rows16(d2)
         elif d2.stride(1) != 1 or d2.stride(0) < w.rows:
             d2 = d2.contiguous()
         m = d2.shape[0]
-        dx = torch.empty((m, w.cols), dtype=dy.dtype, device=w.device)
-        need = L.df_linear_u4_grad_workspace_bytes(w._ref, m)
-        ws = _workspace(need, w.device)
-        dfh._check(L.df_linear_u4_grad(w._ref, ty, d2.data_ptr(), m, d2.stride(0), dx.data_ptr(), ws.data_ptr(), need,
-                                       ts.cuda_stream), "df_linear_u4_grad")
-    return dx.view(dy.shape[:-1] + (w.cols,))
+        dx = torch.empty((m, w.cols), dtype=dy.dtype, device=dev)
+        need = w._need_grad.get(m)
+        if need is None:
+            need = w._need_grad[m] = L.df_linear_u4_grad_workspace_bytes(w._ref, m)
+        ws = _workspace(need, dev)
+        st = L.df_linear_u4_grad(w._ref, ty, d2.data_ptr(), m, d2.stride(0), dx.data_ptr(), ws.data_ptr(), need, handle)
+        if st:
+            dfh._check(st, "df_linear_u4_grad")
+        return dx
+
+    dx = _launch(stream, dev, (dy,) + w._tensors(), call)
+    return dx if dy.dim() == 2 else dx.view(dy.shape[:-1] + (w.cols,))
 
 
 class _LinearU4(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stream):
-        ctx.w, ctx.stream = w, stream
+        ctx.w = w
         return _linear(x, w, stream)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        if torch.is_grad_enabled():   # under create_graph: a graph that refuses to be differentiated
+            return _LinearU4._once(ctx, dy)
+        return linear_u4_grad(dy, ctx.w), None, None
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def _once(ctx, dy):
         return linear_u4_grad(dy, ctx.w), None, None
 
 
 def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """y = x W^T for W[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[...]),
     x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
-    are float32; up to 256 rows multiply the integer weights exactly, more round
-    each weight once to x's type.  Differentiable in x."""
+    are float32; up to 256 rows (512 for at most 2^24 weights) multiply the integer
+    weights exactly, more round each weight once to x's type.  Differentiable in x."""
     if x.requires_grad and torch.is_grad_enabled():
         return _LinearU4.apply(x, w, stream)
     return _linear(x, w, stream)
@@ -262,32 +291,41 @@ class _Loss:
         self.held = (x, head, labels, teacher, index)
 
     def forward(self, stream):
-        L = dfh.lib()
-        with _launching(stream, self.dev, self.inputs) as ts:
+        L, dev = dfh.lib(), self.dev
+        none = self.reduction == "none"
+
+        def call(handle):
             self.bind()
             ref = ctypes.byref(self.desc)
-            rows = int(self.desc.rows)
-            none = self.reduction == "none"
-            loss = torch.empty(rows if none else 1, dtype=torch.float32, device=self.dev)
-            saved = torch.empty(max(L.df_loss_saved_bytes(ref) // 4, 1), dtype=torch.float32, device=self.dev)
+            loss = torch.empty(int(self.desc.rows) if none else 1, dtype=torch.float32, device=dev)
+            saved = torch.empty(max(L.df_loss_saved_bytes(ref) // 4, 1), dtype=torch.float32, device=dev)
             need = L.df_loss_workspace_bytes(ref)
-            ws = _workspace(need, self.dev)
-            dfh._check(L.df_vocab_loss(ref, loss.data_ptr(), saved.data_ptr(), ws.data_ptr(), need, ts.cuda_stream),
-                       "df_vocab_loss")
+            ws = _workspace(need, dev)
+            st = L.df_vocab_loss(ref, loss.data_ptr(), saved.data_ptr(), ws.data_ptr(), need, handle)
+            if st:
+                dfh._check(st, "df_vocab_loss")
+            return loss, saved
+
+        loss, saved = _launch(stream, dev, self.inputs, call)
         return loss.view(self.shape if none else ()), saved
 
     def grads(self, saved, gout, want_x, want_head):
-        L = dfh.lib()
+        L, dev = dfh.lib(), self.dev
         x, head = self.inputs[0], self.inputs[1]
-        with _launching(None, self.dev, ()) as ts:
+
+        def call(handle):
             ref = ctypes.byref(self.desc)
             g = gout.to(torch.float32).reshape(-1).contiguous()
-            dx = torch.empty((int(self.desc.rows), head.shape[1]), dtype=x.dtype, device=self.dev) if want_x else None
-            dh = torch.empty(head.shape, dtype=head.dtype, device=self.dev) if want_head else None
+            dx = torch.empty((int(self.desc.rows), head.shape[1]), dtype=x.dtype, device=dev) if want_x else None
+            dh = torch.empty(head.shape, dtype=head.dtype, device=dev) if want_head else None
             need = L.df_loss_grad_workspace_bytes(ref, int(want_head))
-            ws = _workspace(need, self.dev)
-            dfh._check(L.df_vocab_loss_grad(ref, saved.data_ptr(), g.data_ptr(), _p(dx), _p(dh), ws.data_ptr(), need,
-                                            ts.cuda_stream), "df_vocab_loss_grad")
+            ws = _workspace(need, dev)
+            st = L.df_vocab_loss_grad(ref, saved.data_ptr(), g.data_ptr(), _p(dx), _p(dh), ws.data_ptr(), need, handle)
+            if st:
+                dfh._check(st, "df_vocab_loss_grad")
+            return dx, dh
+
+        dx, dh = _launch(None, dev, (), call)
         return (None if dx is None else dx.view(x.shape)), dh
 
 
@@ -302,11 +340,21 @@ class _LossFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, gout):
+        if torch.is_grad_enabled():   # under create_graph: a graph that refuses to be differentiated
+            return _LossFunction._once(ctx, gout)
+        return _LossFunction._grads(ctx, gout)
+
+    @staticmethod
+    def _grads(ctx, gout):
         saved = ctx.saved_tensors[-1]
         dx, dh = ctx.call.grads(saved, gout, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
         return dx, dh, None, None
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def _once(ctx, gout):
+        return _LossFunction._grads(ctx, gout)
 
 
 def _run_loss(call, stream):

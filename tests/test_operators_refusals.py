@@ -33,7 +33,7 @@ def test_bad_matrix(kw):
 
 @pytest.mark.parametrize("kw", [dict(ty=2), dict(ty=7), dict(x=None), dict(x=P + 8), dict(xs=56), dict(xs=68),
                                 dict(xs=(1 << 21) + 8), dict(y=None), dict(y=P + 8), dict(rows=(1 << 24) + 1),
-                                dict(rows=257, ws=None), dict(rows=257, nbytes=100), dict(rows=257, ws=P + 16)])
+                                dict(rows=513, ws=None), dict(rows=513, nbytes=100), dict(rows=513, ws=P + 16)])
 def test_bad_linear_call(kw):
     assert linear(matrix(), **kw) == ARG
 
