@@ -50,11 +50,12 @@ __device__ __forceinline__ float zero_at(const U4 &w, uint32_t n, uint32_t g) {
   return w.zeros ? (float)w.zeros[n * w.zstride + g] : 8.f;
 }
 
-// Eight nibbles -> eight 16-bit floats bias + q, in order: the nibble lands in
-// the low mantissa bits of a constant whose unit in the last place is one (BF16
-// 128, FP16 1024), a shift and an and-or for the elements i and i + 4; a byte
-// permute then pairs neighbours (11 operations for 8 weights; left as (i, i + 4)
-// it would be 7, but x would need 4 permutes for every operand of 8 instead).
+// Eight nibbles -> eight 16-bit floats bias + q: a nibble lands in the low
+// mantissa bits of a constant whose unit in the last place is one (BF16 128, FP16
+// 1024), a shift and an and-or for the elements i and i + 4.  widen_pairs leaves
+// them so, in the order 0,4 1,5 2,6 3,7 (7 operations for 8 weights), for an x
+// whose elements are exchanged likewise; widen pairs neighbours with four byte
+// permutes more.
 // FP16 then takes 1024 + z off each pair with one packed addition, exactly;
 // there is no such addition for BF16, whose bias (and zero point) come off the
 // group's sum instead.
@@ -73,22 +74,35 @@ struct Bias<F16> {
   static constexpr bool in_sum = false;
 };
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+// (w & mask) | bits in one instruction (truth table 0xEA); left to itself the
+// compiler makes two, each with a literal.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  return __builtin_amdgcn_bitop3_b32(w, mask, bits, 0xEA);
+}
 // off: the pair of -(1024 + z), FP16 only
 template <class T>
-__device__ __forceinline__ u32x4 widen(uint32_t w, uint32_t off) {
-  constexpr uint32_t m = 0x000F000Fu, b = Bias<T>::bits;
-  const uint32_t p = (w & m) | b, q = ((w >> 4) & m) | b, r = ((w >> 8) & m) | b, t = ((w >> 12) & m) | b;
-  u32x4 v = {__builtin_amdgcn_perm(q, p, 0x05040100u), __builtin_amdgcn_perm(t, r, 0x05040100u),
-             __builtin_amdgcn_perm(q, p, 0x07060302u), __builtin_amdgcn_perm(t, r, 0x07060302u)};
-  if constexpr (!Bias<T>::in_sum) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t e = v[i];
-      v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, e) + __builtin_bit_cast(f16x2, off));
-    }
-  }
-  return v;
+__device__ __forceinline__ uint32_t unbias(uint32_t v, uint32_t off) {
+  if constexpr (Bias<T>::in_sum) return v;
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) + __builtin_bit_cast(f16x2, off));
 }
+template <class T>
+__device__ __forceinline__ u32x4 widen_pairs(uint32_t w, uint32_t off) {
+  constexpr uint32_t m = 0x000F000Fu, b = Bias<T>::bits;
+  return u32x4{unbias<T>(and_or(w, m, b), off), unbias<T>(and_or(w >> 4, m, b), off),
+               unbias<T>(and_or(w >> 8, m, b), off), unbias<T>(and_or(w >> 12, m, b), off)};
+}
+template <class T>
+__device__ __forceinline__ u32x4 widen(uint32_t w, uint32_t off) {
+  const u32x4 p = widen_pairs<T>(w, off);
+  return u32x4{__builtin_amdgcn_perm(p[1], p[0], 0x05040100u), __builtin_amdgcn_perm(p[3], p[2], 0x05040100u),
+               __builtin_amdgcn_perm(p[1], p[0], 0x07060302u), __builtin_amdgcn_perm(p[3], p[2], 0x07060302u)};
+}
+// Eight 16-bit values in order into widen_pairs' order.
+__device__ __forceinline__ u32x4 pair_up(u32x4 v) {
+  return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+               __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+}
+
 // One output from the definition, in order; taken where BF16's fast sum is not
 // finite (an infinite or very large x: the bias would turn inf * w into NaN).
 template <class T>
@@ -268,15 +282,24 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
   const uint32_t xr = lr >> 2 < m ? lr >> 2 : m - 1;  // the row of x in this lane's operand row
   Sc next, now;
   next.rows(w, n0, lr);
+  // this lane's 16 bytes of four weight rows a load
+  const uint8_t *src[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; j++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t r = i * 4 + (lane >> 4), n = n0 + j * 16 + r;
+      src[j][i] = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2) + ((lane & 15) ^ r) * 16;
+    }
   auto request = [&](uint32_t st, uint8_t *dst) {
+    const bool whole = st * 512 + 512 <= k32;  // uniform
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const uint32_t r = i * 4 + (lane >> 4), c = (lane & 15) ^ r, n = n0 + j * 16 + r;
-        const uint8_t *src = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2);
-        src = st * 512 + c * 32 < k32 ? src + st * 256 + c * 16 : (const uint8_t *)&g_zero16;
-        to_lds(src, dst + j * 4096 + i * 1024);
+        const uint8_t *p = src[j][i] + st * 256;
+        if (!whole && st * 512 + ((lane & 15) ^ (i * 4 + (lane >> 4))) * 32 >= k32) p = (const uint8_t *)&g_zero16;
+        to_lds(p, dst + j * 4096 + i * 1024);
       }
     for (uint32_t r = 0; r < m; r++) {
       const uint32_t k = st * 512 + (lane ^ r) * 8;
@@ -295,6 +318,12 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     now = next;
     if (st + 1 < s1) request(st + 1, buf + ((st + 1 - s0) & 1) * step);
+    // x into widen_pairs' order where it lies: once a stage, 16 bytes a lane
+    for (uint32_t r = 0; r < m; r++) {
+      u32x4 *c = (u32x4 *)(p + NT * 4096 + r * 1024) + lane;
+      *c = pair_up(*c);
+    }
+    asm volatile("" ::: "memory");
     const uint8_t *px = p + NT * 4096 + xr * 1024;
 #pragma unroll
     for (int b = 0; b < 4; b++) {
@@ -314,8 +343,10 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
         f32x4 t[G] = {};
 #pragma unroll
         for (int d = 0; d < 4; d++)
-          t[d * G / 4] = mfma(T{}, xp[d], widen<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(j, b * G + d * G / 4))),
-                              t[d * G / 4]);
+          t[d * G / 4] =
+              mfma(T{}, xp[d],
+                   widen_pairs<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(j, b * G + d * G / 4))),
+                   t[d * G / 4]);
 #pragma unroll
         for (int g = 0; g < G; g++)
           acc[j][0][0] = scaled<T>(acc[j][0][0], now.scale(w, j, b * G + g), now.zero_point(j, b * G + g), t[g][0], sx[g][0]);
@@ -363,21 +394,33 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
   const u32x4 ones = {one, one, one, one};
   Sc next, now;
   next.rows(w, n0, lr);
-  auto request = [&](uint32_t st, uint8_t *dst) {
+  const uint8_t *wsrc[NT];  // 8 weight rows of 128 bytes a load
 #pragma unroll
-    for (int i = 0; i < BN / 64; i++) {  // 8 weight rows of 128 bytes a load
-      const uint32_t r = (i * 8 + wave) * 8 + lane / 8, c = (lane & 7) ^ swz(r), n = nb + r;
-      const uint8_t *src = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2);
-      src = st * 256 + c * 32 < k32 ? src + st * 128 + c * 16 : (const uint8_t *)&g_zero16;
-      to_lds(src, dst + (i * 8 + wave) * 1024);
+  for (int i = 0; i < NT; i++) {
+    const uint32_t r = (i * 8 + wave) * 8 + lane / 8, n = nb + r;
+    wsrc[i] = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2) + ((lane & 7) ^ swz(r)) * 16;
+  }
+  const uint16_t *xsrc[MT];  // 2 rows of x a load
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    const uint32_t r = (i * 8 + wave) * 2 + lane / 32;
+    xsrc[i] = x + (uint64_t)(m0 + (r < rows ? r : rows - 1)) * xs + ((lane & 31) ^ (r & 15)) * 8;
+  }
+  auto request = [&](uint32_t st, uint8_t *dst) {
+    const bool whole = st * 256 + 256 <= k32;  // uniform
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+      const uint8_t *p = wsrc[i] + st * 128;
+      if (!whole && st * 256 + ((lane & 7) ^ swz((i * 8 + wave) * 8 + lane / 8)) * 32 >= k32) p = (const uint8_t *)&g_zero16;
+      to_lds(p, dst + (i * 8 + wave) * 1024);
     }
 #pragma unroll
-    for (int i = 0; i < MT; i++) {  // 2 rows of x a load
+    for (int i = 0; i < MT; i++) {
       const uint32_t pair = i * 8 + wave;
       if (pair * 2 >= rows) continue;  // uniform
-      const uint32_t r = pair * 2 + lane / 32, k = st * 256 + ((lane & 31) ^ (r & 15)) * 8;
-      const uint16_t *src = x + (uint64_t)(m0 + (r < rows ? r : rows - 1)) * xs + k;
-      to_lds(k < k32 ? (const void *)src : (const void *)&g_zero16, dst + BN * 128 + pair * 1024);
+      const uint16_t *p = xsrc[i] + st * 256;
+      if (!whole && st * 256 + ((lane & 31) ^ ((pair * 2 + lane / 32) & 15)) * 8 >= k32) p = (const uint16_t *)&g_zero16;
+      to_lds(p, dst + BN * 128 + pair * 1024);
     }
     next.request(w, st * 8 + wk * 4);
   };
@@ -610,8 +653,11 @@ hipError_t tokens_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m
                                      : tokens_of<T, NT, W, uint16_t>(w, x, xs, m, y, s);
 }
 
-// How u4_tile cuts a product: splits of the summed index so that about two
-// workgroups come to a CU, of four stages of 256 elements at least.
+// How u4_tile cuts a product: splits of the summed index so that up to two
+// workgroups come to a CU, of four stages of 256 elements at least (16 x 14336 x
+// 4096, 224 tiles: one split 17.8 us, two 15.8, three 16.8, eight 18.2; 23 x 4096 x
+// 14336, 64 tiles: one 50, four 18.5, eight 17.7).  A third and fourth buffer a
+// workgroup measured the same.
 struct TilePlan {
   uint32_t mtile, ntile, mt, splits, per, ld;
 };
@@ -621,7 +667,7 @@ TilePlan tile_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t mtile, uint32_t 
   p.ntile = ntile;
   p.mt = (m + 16 * p.mtile - 1) / (16 * p.mtile);
   const uint32_t tiles = p.mt * ((n + 64 * p.ntile - 1) / (64 * p.ntile)), stages = (k / 32 * 32 + 255) / 256;
-  uint32_t want = tiles >= 384 ? 1 : (512 + tiles - 1) / tiles;
+  uint32_t want = tiles >= 512 ? 1 : 512 / tiles;
   const uint32_t most = stages / 4 < 1 ? 1 : stages / 4;
   want = want < most ? want : most;
   p.per = (stages + want - 1) / want;
@@ -664,9 +710,11 @@ template <class T>
 df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16_t *y, uint8_t *ws, hipStream_t s) {
   hipError_t e;
   if (m <= kTokens) {
-    // waves a workgroup: 4 where the columns alone fill the chip, 16 where they
-    // give one workgroup a CU or less and the rows are long
-    e = w.n >= 32768                    ? tokens_launch<T, 1, 4>(w, x, xs, m, y, s)
+    // waves a workgroup: 4 where the columns alone fill the chip (14336 x 4096:
+    // 10.5 us, with 8 11.8), 16 where they give one workgroup a CU or less and the
+    // rows are long (4096 x 14336: 10.5 us, with 8 12.0), else 8 (4096 x 4096: 5.3
+    // us, with 4 6.0); 16 have LDS for one row of x
+    e = w.n >= 8192                     ? tokens_launch<T, 1, 4>(w, x, xs, m, y, s)
         : m == 1 && w.n <= 4096 && w.k > 8192 ? tokens_launch<T, 1, 16>(w, x, xs, m, y, s)
                                         : tokens_launch<T, 1, 8>(w, x, xs, m, y, s);
   } else if (few_rows(m, w.n, w.k)) {

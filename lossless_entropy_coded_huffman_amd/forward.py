@@ -12,6 +12,14 @@ last read it, compute waits for its decode).
 The block itself is plain PyTorch in BF16 (RMSNorm, grouped-query attention
 with rotary embeddings, SwiGLU MLP), weights random, norms at one.  Every
 batched product takes contiguous operands.
+
+The EntroLLM summary ("Metodologia") stores quantised weights instead.
+``QuantizedBlocks`` runs the same blocks from uint4 containers: a block's seven
+layers are decoded in one batch to packed nibbles and multiplied as they are
+(``linear_u4``), so no dequantised copy is kept; gradients to the activations
+decode a block again.  ``CompressedHead`` holds an LM head as one BF16 container
+and scores hidden states against it (``vocab_loss``, ``distill_loss``): what the
+quantised model loses against the lossless one, and the gradient to mend it.
 """
 from __future__ import annotations
 
@@ -21,6 +29,7 @@ import numpy as np
 import torch
 
 from . import dfh
+from .ops import U4Matrix, distill_loss, linear_u4, vocab_loss
 
 
 @dataclass(frozen=True)
@@ -74,29 +83,47 @@ def _rope(x: torch.Tensor, theta: float) -> torch.Tensor:
     return torch.cat([a * cos - b * sin, a * sin + b * cos], dim=-1).to(x.dtype)
 
 
-def block_forward(x: torch.Tensor, w: dict, shape: BlockShape) -> torch.Tensor:
-    """One Llama block on activations x [T, hidden] (BF16), causal attention."""
+class _Bmm(torch.autograd.Function):
+    """torch.bmm of contiguous operands whose gradients take contiguous operands
+    too (torch's own hands transposed views on)."""
+
+    @staticmethod
+    def forward(ctx, a, b):
+        ctx.save_for_backward(a, b)
+        return torch.bmm(a, b)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        a, b = ctx.saved_tensors
+        dy = dy.contiguous()
+        return (torch.bmm(dy, b.transpose(1, 2).contiguous()), torch.bmm(a.transpose(1, 2).contiguous(), dy))
+
+
+def block_forward(x: torch.Tensor, w: dict, shape: BlockShape, linear=torch.nn.functional.linear) -> torch.Tensor:
+    """One Llama block on activations x [T, hidden] (BF16), causal attention.
+    linear(x, w[name]) multiplies by a layer's weights."""
     t = x.shape[0]
     hd, nh, nkv = shape.head_dim, shape.heads, shape.kv_heads
     h = _rms_norm(x)
-    q = torch.nn.functional.linear(h, w["q"]).view(t, nh, hd).transpose(0, 1).contiguous()
-    k = torch.nn.functional.linear(h, w["k"]).view(t, nkv, hd).transpose(0, 1).contiguous()
-    v = torch.nn.functional.linear(h, w["v"]).view(t, nkv, hd).transpose(0, 1).contiguous()
+    q = linear(h, w["q"]).view(t, nh, hd).transpose(0, 1).contiguous()
+    k = linear(h, w["k"]).view(t, nkv, hd).transpose(0, 1).contiguous()
+    v = linear(h, w["v"]).view(t, nkv, hd).transpose(0, 1).contiguous()
     q, k = _rope(q, shape.rope_theta), _rope(k, shape.rope_theta)
     rep = nh // nkv
     k = k.repeat_interleave(rep, dim=0)
     v = v.repeat_interleave(rep, dim=0).contiguous()
     kt = k.transpose(1, 2).contiguous()                       # [heads, hd, T]
-    scores = torch.bmm(q, kt).float() * (hd ** -0.5)           # [heads, T, T]
+    scores = _Bmm.apply(q, kt).float() * (hd ** -0.5)           # [heads, T, T]
     mask = torch.ones(t, t, device=x.device, dtype=torch.bool).triu(1)
     scores.masked_fill_(mask, float("-inf"))
     probs = torch.softmax(scores, dim=-1).to(x.dtype).contiguous()
-    att = torch.bmm(probs, v).transpose(0, 1).reshape(t, nh * hd)
-    x = x + torch.nn.functional.linear(att, w["o"])
+    att = _Bmm.apply(probs, v).transpose(0, 1).reshape(t, nh * hd)
+    x = x + linear(att, w["o"])
     h2 = _rms_norm(x)
-    g = torch.nn.functional.linear(h2, w["gate"])
-    u = torch.nn.functional.linear(h2, w["up"])
-    return x + torch.nn.functional.linear(torch.nn.functional.silu(g) * u, w["down"])
+    g = linear(h2, w["gate"])
+    u = linear(h2, w["up"])
+    return x + linear(torch.nn.functional.silu(g) * u, w["down"])
 
 
 class CompressedBlocks:
@@ -150,6 +177,96 @@ class CompressedBlocks:
         return x
 
 
+class QuantizedBlocks:
+    """Blocks held as uint4 containers with group scales, decoded to packed
+    nibbles right before they run.
+
+    layers: per block a list of (container, scales, zeros) in
+    BlockShape.matrices() order, as quantize_block makes them; scales [rows,
+    groups] in float32 (kept in scale_dtype), zeros uint8 of that shape or None.
+    One scratch buffer of a block's nibbles is allocated up front."""
+
+    def __init__(self, layers, shape: BlockShape, device, group_size: int, scale_dtype=torch.bfloat16):
+        self.shape = shape
+        self.device = torch.device(device)
+        mats = shape.matrices()
+        self.scratch = [torch.empty(r * c // 2, dtype=torch.uint8, device=self.device) for _, r, c in mats]
+        self.blocks, self.weights = [], []
+        for block in layers:
+            if len(block) != len(mats):
+                raise ValueError("a block needs %d layers" % len(mats))
+            dcs, ws = [], {}
+            for (name, r, c), packed, (con, scales, zeros) in zip(mats, self.scratch, block):
+                inf = con.info()
+                if int(inf["n"]) != r * c or int(inf["kind"]) != dfh.KIND_U4:
+                    raise ValueError("container does not hold the uint4 codes of layer %r" % name)
+                dcs.append(dfh.to_device(con, self.device))
+                s = torch.as_tensor(scales).to(self.device, scale_dtype)
+                z = None if zeros is None else torch.as_tensor(zeros).to(self.device)
+                ws[name] = U4Matrix(packed, s, z, cols=c, group_size=group_size)
+            self.blocks.append(dcs)
+            self.weights.append(ws)
+
+    def _run(self, i: int, x: torch.Tensor) -> torch.Tensor:
+        dfh.df_decompress_batch(self.blocks[i], self.scratch, torch.cuda.current_stream(self.device))
+        return block_forward(x, self.weights[i], self.shape, linear_u4)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        """All blocks in order on the current stream.  Differentiable in x: a
+        block keeps its input and is decoded and run again for its gradient."""
+        for i in range(len(self.blocks)):
+            if x.requires_grad and torch.is_grad_enabled():
+                x = _QuantizedBlock.apply(x, self, i)
+            else:
+                with torch.no_grad():
+                    x = self._run(i, x)
+        return x
+
+
+class _QuantizedBlock(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, blocks, i):
+        ctx.save_for_backward(x)
+        ctx.blocks, ctx.i = blocks, i
+        return blocks._run(i, x)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, = ctx.saved_tensors
+        with torch.enable_grad():
+            leaf = x.detach().requires_grad_()
+            y = ctx.blocks._run(ctx.i, leaf)
+        return torch.autograd.grad(y, leaf, dy)[0], None, None
+
+
+class CompressedHead:
+    """An LM head [vocab, hidden] held as one BF16 container (the DF11 digest
+    compresses embedding and LM head on their own), decoded into one scratch
+    buffer before each use."""
+
+    def __init__(self, container, vocab: int, hidden: int, device):
+        inf = container.info()
+        if int(inf["n"]) != vocab * hidden or int(inf["kind"]) != dfh.KIND_BF16:
+            raise ValueError("container does not hold a BF16 head of this shape")
+        self.device = torch.device(device)
+        self.head = dfh.to_device(container, self.device)
+        self.scratch = torch.empty((vocab, hidden), dtype=torch.bfloat16, device=self.device)
+
+    def weight(self) -> torch.Tensor:
+        """The decoded head (on the current stream; the same bits every time)."""
+        dfh.df_decompress(self.head, self.scratch, torch.cuda.current_stream(self.device))
+        return self.scratch
+
+    def loss(self, x: torch.Tensor, labels: torch.Tensor, **kw) -> torch.Tensor:
+        """Cross entropy of hidden states x against labels (vocab_loss)."""
+        return vocab_loss(x, self.weight(), labels, **kw)
+
+    def distill(self, x: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor, **kw) -> torch.Tensor:
+        """Divergence from a teacher's top logits (distill_loss)."""
+        return distill_loss(x, self.weight(), teacher, index, **kw)
+
+
 def resident_forward(x: torch.Tensor, weights, shape: BlockShape) -> torch.Tensor:
     """The same blocks with every weight buffer resident (the reference)."""
     for flat in weights:
@@ -163,6 +280,19 @@ def random_blocks(n_blocks: int, shape: BlockShape, seed: int = 0):
     from . import synth
     return [synth.bf16_block(seed, config=synth.CONFIG_FORWARD, block=b, shapes=shape.matrices())[0]
             for b in range(n_blocks)]
+
+
+def quantize_block(host: np.ndarray, shape: BlockShape, group_size: int, asymmetric: bool = True):
+    """One block's host BF16 weights -> QuantizedBlocks' layers: per matrix the
+    uint4 container of its codes, its group scales and zero points."""
+    from . import synth
+    out, off = [], 0
+    for _, r, c in shape.matrices():
+        w = synth.bf16_to_f32(host[off: off + r * c]).reshape(r, c)
+        codes, scales, zeros = synth.quantize_u4_groups(w, group_size, asymmetric)
+        out.append((dfh.compress(dfh.KIND_U4, synth.pack_u4(codes), n=r * c), scales, zeros))
+        off += r * c
+    return out
 
 
 def to_torch(host: np.ndarray, device) -> torch.Tensor:

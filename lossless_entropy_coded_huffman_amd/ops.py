@@ -200,17 +200,21 @@ class _LinearU4(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stream):
         ctx.w = w
+        # read again by the gradient: a change that torch sees in between is refused
+        ctx.save_for_backward(*[t for t in w._tensors() if t is not None])
         return _linear(x, w, stream)
 
     @staticmethod
     def backward(ctx, dy):
         if torch.is_grad_enabled():   # under create_graph: a graph that refuses to be differentiated
             return _LinearU4._once(ctx, dy)
+        ctx.saved_tensors
         return linear_u4_grad(dy, ctx.w), None, None
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def _once(ctx, dy):
+        ctx.saved_tensors
         return linear_u4_grad(dy, ctx.w), None, None
 
 
@@ -218,7 +222,9 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """y = x W^T for W[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[...]),
     x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
     are float32; up to 256 rows (512 for at most 2^24 weights) multiply the integer
-    weights exactly, more round each weight once to x's type.  Differentiable in x."""
+    weights exactly, more round each weight once to x's type.  Differentiable in x;
+    the nibbles must stay as they are until the gradient has run (df_decompress
+    into the same buffer is not seen by autograd)."""
     if x.requires_grad and torch.is_grad_enabled():
         return _LinearU4.apply(x, w, stream)
     return _linear(x, w, stream)

@@ -182,6 +182,40 @@ def quantize_u4(x: np.ndarray, asymmetric: bool) -> np.ndarray:
     return np.clip(q, 0, 15).astype(np.uint8)
 
 
+def quantize_u4_groups(x: np.ndarray, group_size: int, asymmetric: bool):
+    """quantize_u4 for each group of group_size consecutive elements of a row
+    of x [rows, cols] (the last group of a row may be shorter).  Returns (codes
+    [rows, cols], scales float32 [rows, groups], zeros uint8 [rows, groups]):
+    x ~ scales * (codes - zeros)."""
+    x = np.ascontiguousarray(x, np.float32)
+    rows, cols = x.shape
+    groups = -(-cols // group_size)
+    codes = np.empty((rows, cols), np.uint8)
+    scales = np.empty((rows, groups), np.float32)
+    zeros = np.full((rows, groups), 8, np.uint8)
+    for g in range(groups):
+        part = x[:, g * group_size: (g + 1) * group_size]
+        if asymmetric:
+            lo, hi = part.min(axis=1), part.max(axis=1)
+            s = ((hi - lo) / np.float32(15)).astype(np.float32)
+            s[s <= 0] = 1
+            z = np.clip(np.rint(-lo / s), 0, 15)
+            zeros[:, g] = z.astype(np.uint8)
+        else:
+            s = (np.abs(part).max(axis=1) / np.float32(7)).astype(np.float32)
+            s[s <= 0] = 1
+            z = np.full(rows, 8, np.float32)
+        scales[:, g] = s
+        codes[:, g * group_size: (g + 1) * group_size] = \
+            np.clip(np.rint(part / s[:, None]) + z[:, None], 0, 15).astype(np.uint8)
+    return codes, scales, zeros
+
+
+def bf16_to_f32(bits: np.ndarray) -> np.ndarray:
+    """BF16 bit patterns -> float32."""
+    return (np.asarray(bits, np.uint16).astype(np.uint32) << np.uint32(16)).view(np.float32)
+
+
 def pack_u4(q: np.ndarray) -> np.ndarray:
     """Values 0..15 -> packed bytes, element 2j in the low nibble of byte j
     (input layout of the uint4 kind)."""
