@@ -318,17 +318,17 @@ __device__ __forceinline__ void store8(uint16_t *p, uint32_t col, uint32_t n, bo
   }
 }
 
-// 16-bit output (base 16-byte aligned), times *scale * mul.
+// 16-bit output (base 16-byte aligned), times *scale (null: 1) * *scale2 * mul.
 struct EpiStore {
   uint16_t *c;
   uint64_t ldc;
-  const float *scale;  // null: 1
+  const float *scale, *scale2;
   float mul;
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t) const {
     static_assert(NT % 2 == 0, "blocks in pairs");
-    const float s = (scale ? *scale : 1.f) * mul;
+    const float s = (scale ? *scale * *scale2 : 1.f) * mul;
     const bool aligned = (ldc & 7) == 0;
     const uint32_t kg = (threadIdx.x >> 4) & 3, first = nb - 4 * kg + (kg & 1) * 16 + (kg >> 1) * 8;
 #pragma unroll
@@ -371,6 +371,21 @@ struct EpiPlane {
     }
   }
 };
+
+// Four columns of `count` planes added up, eight loads in flight.
+__device__ __forceinline__ f32x4 add_planes(const float *p, uint64_t stride, uint32_t count) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  uint32_t s = 0;
+  for (; s + 8 <= count; s += 8) {
+    f32x4 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) t[i] = *(const f32x4 *)(p + (s + i) * stride);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v += t[i];
+  }
+  for (; s < count; s++) v += *(const f32x4 *)(p + s * stride);
+  return v;
+}
 
 // ------------------------------------------------------------------- launch
 // Raises a kernel's LDS limit where a launch needs more than 64 KiB, once per

@@ -512,21 +512,16 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
 template <class T>
 __global__ __launch_bounds__(256) void join_tiles(const U4 w, const uint16_t *x, uint64_t xs, const float *planes,
                                                   uint32_t splits, uint32_t m, uint32_t ld, uint16_t *y) {
-  const uint32_t row = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 2;
+  const uint32_t row = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (n >= w.n) return;
-  float v0 = 0.f, v1 = 0.f;
-  for (uint32_t s = 0; s < splits; s++) {
-    const float2 p = *(const float2 *)(planes + ((uint64_t)s * m + row) * ld + n);
-    v0 += p.x;
-    v1 += p.y;
+  const f32x4 v = add_planes(planes + (uint64_t)row * ld + n, (uint64_t)m * ld, splits);
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    if (n + e >= w.n) break;
+    float o = v[e];
+    if (Bias<T>::in_sum && !(__builtin_fabsf(o) < __builtin_huge_valf())) o = dot_plain<T>(w, x + row * xs, n + e);
+    y[(uint64_t)row * w.n + n + e] = to_bits(T{}, o);
   }
-  if (Bias<T>::in_sum) {
-    if (!(__builtin_fabsf(v0) < __builtin_huge_valf())) v0 = dot_plain<T>(w, x + row * xs, n);
-    if (n + 1 < w.n && !(__builtin_fabsf(v1) < __builtin_huge_valf())) v1 = dot_plain<T>(w, x + row * xs, n + 1);
-  }
-  uint16_t *p = y + (uint64_t)row * w.n + n;
-  p[0] = to_bits(T{}, v0);
-  if (n + 1 < w.n) p[1] = to_bits(T{}, v1);
 }
 
 // The weights as 16-bit floats, [n, k].  Each is rounded once from FP32
@@ -574,8 +569,7 @@ __global__ __launch_bounds__(256) void join_planes(const float *p, uint32_t spli
                                                    uint32_t ld, uint16_t *out) {
   const uint32_t row = blockIdx.x;
   for (uint32_t c = threadIdx.x * 4; c < n; c += 1024) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s = 0; s < splits; s++) v += *(const f32x4 *)(p + ((uint64_t)s * m + row) * ld + c);
+    const f32x4 v = add_planes(p + (uint64_t)row * ld + c, (uint64_t)m * ld, splits);
 #pragma unroll
     for (int e = 0; e < 4; e++)
       if (c + e < n) out[(uint64_t)row * n + c + e] = to_bits(T{}, v[e]);
@@ -624,7 +618,7 @@ template <class T, bool KB>
 df_status many_rows(const Gemm &g, uint16_t *out, float *planes, hipStream_t s) {
   const Cut c = cut_for(g.m, g.n, g.k, true);
   if (c.splits <= 1)
-    return product<T, false, KB>(g, EpiStore{out, g.n, nullptr, 1.f}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
+    return product<T, false, KB>(g, EpiStore{out, g.n, nullptr, nullptr, 1.f}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
   const uint32_t ld = (uint32_t)up(g.n, 4);
   if (product<T, false, KB>(g, EpiPlane{planes, ld, (uint64_t)g.m * ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
   hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld, out);
@@ -692,7 +686,7 @@ hipError_t tile_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint
                      p.per, y, p.splits > 1 ? planes : (float *)nullptr, p.ld);
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL((join_tiles<T>), dim3((w.n + 511) / 512, m), dim3(256), 0, s, w, x, xs, (const float *)planes,
+  hipLaunchKernelGGL((join_tiles<T>), dim3((w.n + 1023) / 1024, m), dim3(256), 0, s, w, x, xs, (const float *)planes,
                      p.splits, m, p.ld, y);
   return hipGetLastError();
 }

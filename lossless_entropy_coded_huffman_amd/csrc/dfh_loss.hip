@@ -40,6 +40,7 @@ struct Targets {
 // What a row keeps: its state, the base-2 log-sum and the target logits.
 enum : uint32_t { kNoLoss = 0, kLoss = 1, kBadLabel = 2 };
 struct Saved {
+  float *share;  // [1]: 1 / the rows that a mean is over, 1 for a sum
   float *lse2;
   uint32_t *state;
   float *picked;  // [rows, max(top, 1)]
@@ -138,19 +139,18 @@ struct EpiDz {
 };
 
 // ------------------------------------------------------------------- kernels
-// picked[m, j] = x[m] . head[target j], one wave each (0 without a target).
+struct Head {
+  const uint16_t *x, *head;
+  uint64_t xs, hs;
+  uint32_t k;
+};
+// x[m] . head[v] by a wave (0 for v < 0), in every lane.
 template <class T>
-__global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t rows, const uint16_t *x, uint64_t xs,
-                                                   const uint16_t *head, uint64_t hs, uint32_t k, float *picked) {
-  const uint32_t per = t.top ? t.top : 1, lane = threadIdx.x & 63;
-  const uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (e >= (uint64_t)rows * per) return;
-  const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
-  const int32_t v = target_of(t, m, j);
+__device__ __forceinline__ float dot_row(const Head &h, uint32_t m, int32_t v) {
   float s = 0.f;
   if (v >= 0) {
-    const u32x4 *px = (const u32x4 *)(x + m * xs), *ph = (const u32x4 *)(head + (uint64_t)v * hs);
-    for (uint32_t c = lane; c < k / 8; c += 64) {
+    const u32x4 *px = (const u32x4 *)(h.x + m * h.xs), *ph = (const u32x4 *)(h.head + (uint64_t)v * h.hs);
+    for (uint32_t c = threadIdx.x & 63; c < h.k / 8; c += 64) {
       const u32x4 a = px[c], b = ph[c];
 #pragma unroll
       for (int d = 0; d < 4; d++) {
@@ -161,7 +161,18 @@ __global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t row
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  if (lane == 0) picked[e] = s;
+  return s;
+}
+
+// picked[m, j] = x[m] . head[target j], one wave each (0 without a target).
+template <class T>
+__global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t rows, const Head h, float *picked) {
+  const uint32_t per = t.top ? t.top : 1;
+  const uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e >= (uint64_t)rows * per) return;
+  const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
+  const float s = dot_row<T>(h, m, target_of(t, m, j));
+  if ((threadIdx.x & 63) == 0) picked[e] = s;
 }
 
 // Parts of a row: `main` in the first `rows` rows, `rest` in those behind them.
@@ -174,14 +185,22 @@ struct Parts {
 // takes parts t / R, t / R + 256 / R, ... (four loads in flight) and targets
 // likewise of row t % R.  R = 8 reads 64 bytes of a part at once; few rows take
 // R = 1, so that 256 threads share a row's parts (7 rows of 2004 parts: 64 us with
-// 16 rows a workgroup and one load in flight).
-template <int R>
+// 16 rows a workgroup and one load in flight).  PICK (with R = 1, where a row has
+// few targets): the four waves make the picked logits themselves.
+template <class T, int R, bool PICK>
 __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, Parts np,
-                                                   Saved sv, float *loss) {
+                                                   const Head h, Saved sv, float *loss) {
   constexpr uint32_t S = 256 / R;
   __shared__ float sa[S][R];
   const uint32_t r = threadIdx.x % R, sl = threadIdx.x / R, m = blockIdx.x * R + r;
   const bool in = m < rows;
+  if (PICK) {  // written here, read below after several barriers
+    const uint32_t per = t.top ? t.top : 1;
+    for (uint32_t j = threadIdx.x >> 6; j < per; j += 4) {
+      const float z = dot_row<T>(h, m, target_of(t, m, j));
+      if ((threadIdx.x & 63) == 0) sv.picked[(uint64_t)m * per + j] = z;
+    }
+  }
   // over a row's S threads, in a fixed order
   auto join = [&](float v, auto op) {
     sa[sl][r] = v;
@@ -261,7 +280,7 @@ __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t row
 
 // One workgroup: sum (mean: over the rows that have a loss) of the rows.
 __global__ __launch_bounds__(1024) void reduce_rows(const float *rows_loss, const uint32_t *state, uint32_t rows,
-                                                    bool mean, float *out) {
+                                                    bool mean, float *out, float *share) {
   __shared__ double ss[16];
   __shared__ uint32_t sc[16];
   double s = 0.0;
@@ -287,45 +306,31 @@ __global__ __launch_bounds__(1024) void reduce_rows(const float *rows_loss, cons
       c += sc[q];
     }
     *out = (float)(mean ? (c ? s / c : 0.0) : s);
+    *share = mean && c ? 1.f / (float)c : 1.f;
   }
 }
 
-// Row factors of the gradient: g[m] = T * grad (mean: / count), 0 without a
-// loss; peak = max |g|; gn[m] = g[m] / peak, which weigh_rows puts on x (1 in
-// every row for sums and means, so it costs them no rounding).
-__global__ __launch_bounds__(1024) void row_factors(const uint32_t *state, uint32_t rows, const float *grad, int reduce,
-                                                    float temp, float *g, float *gn, float *peak) {
+// Rows with gradients of their own (DF_REDUCE_NONE): peak = max |grad| of the rows
+// that have a loss, and gn[m] = grad[m] / peak, which weigh_rows puts on x.  (A
+// sum or mean has one gradient, which the products' epilogues take: no row
+// factor, no rounding.)
+__global__ __launch_bounds__(1024) void row_factors(const uint32_t *state, uint32_t rows, const float *grad, float *gn,
+                                                    float *peak) {
   __shared__ float sm[16];
-  __shared__ uint32_t sc[16];
   float mx = 0.f;
-  uint32_t c = 0;
-  for (uint32_t m = threadIdx.x; m < rows; m += 1024) {
-    c += state[m] != kNoLoss;
-    if (state[m] == kLoss) mx = __builtin_fmaxf(mx, __builtin_fabsf(grad[reduce == DF_REDUCE_NONE ? m : 0]));
-  }
-  for (int o = 32; o; o >>= 1) {
-    mx = __builtin_fmaxf(mx, __shfl_xor(mx, o));
-    c += __shfl_xor(c, o);
-  }
-  if ((threadIdx.x & 63) == 0) {
-    sm[threadIdx.x >> 6] = mx;
-    sc[threadIdx.x >> 6] = c;
-  }
+  for (uint32_t m = threadIdx.x; m < rows; m += 1024)
+    if (state[m] == kLoss) mx = __builtin_fmaxf(mx, __builtin_fabsf(grad[m]));
+  for (int o = 32; o; o >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, o));
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = mx;
   __syncthreads();
   mx = 0.f;
-  c = 0;
-  for (int q = 0; q < 16; q++) {
-    mx = __builtin_fmaxf(mx, sm[q]);
-    c += sc[q];
-  }
-  const float div = reduce == DF_REDUCE_MEAN && c ? (float)c : 1.f;
+  for (int q = 0; q < 16; q++) mx = __builtin_fmaxf(mx, sm[q]);
   const float pk = mx > 0.f ? mx : 1.f;
-  for (uint32_t m = threadIdx.x; m < rows; m += 1024) {
-    const float v = state[m] == kLoss ? grad[reduce == DF_REDUCE_NONE ? m : 0] : 0.f;
-    g[m] = v * temp / div;
-    gn[m] = v / pk;
+  for (uint32_t m = threadIdx.x; m < rows; m += 1024) gn[m] = state[m] == kLoss ? grad[m] / pk : 0.f;
+  if (threadIdx.x == 0) {
+    peak[0] = pk;
+    peak[1] = 1.f;
   }
-  if (threadIdx.x == 0) *peak = pk * temp / div;
 }
 
 // dz at the target entries of vocabulary [v0, v0 + nv): (p - t) * mul with p
@@ -367,7 +372,7 @@ __global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved s
   }
 }
 
-// out[c, m] = gn[m] x[m, c], zeros in rows without a loss (whatever x holds
+// out[c, m] = gn[m] x[m, c] (gn null: x), zeros in rows without a loss (whatever x holds
 // there) and in the columns that pad a row to mp: what dhead's sum over the rows
 // takes for x, so dz needs no row factor; turned, so that only dz is read across
 // there.  64 x 64 tiles through LDS, padded rows spread the column writes.
@@ -381,10 +386,10 @@ __global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs
     const uint32_t r = t / 8, c = t % 8, m = m0 + r;
     u32x4 v = {0, 0, 0, 0};
     if (m < rows && c0 + c * 8 < k && state[m] == kLoss) {
-      const float f = gn[m];
       v = *(const u32x4 *)(x + m * xs + c0 + c * 8);
+      const float f = gn ? gn[m] : 1.f;
 #pragma unroll
-      for (int d = 0; d < 4; d++)
+      for (int d = 0; gn && d < 4; d++)
         v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
     }
 #pragma unroll
@@ -401,20 +406,18 @@ __global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs
   }
 }
 
-// dx[m] = g[m] * mul * (sum of the planes), zero in rows without a loss.
+// dx[m] = mul * grad * share * (sum of the planes), zero in rows without a loss.
 template <class T>
 __global__ __launch_bounds__(256) void finish_dx(const float *planes, Parts parts, uint32_t rows, uint32_t k,
-                                                 const uint32_t *state, const float *g, float mul, uint16_t *dx) {
+                                                 const uint32_t *state, const float *grad, const float *share, float mul,
+                                                 uint16_t *dx) {
   const uint32_t m = blockIdx.x;
   const bool live = state[m] == kLoss;
-  const float f = g[m] * mul;
+  const float f = (share ? grad[0] * *share : grad[m]) * mul;
   const uint32_t splits = m < parts.rows ? parts.main : parts.rest;
   for (uint32_t c = threadIdx.x * 4; c < k; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-      for (uint32_t s = 0; s < splits; s++) v += *(const f32x4 *)(planes + ((uint64_t)s * rows + m) * k + c);
-      v *= f;
-    }
+    if (live) v = add_planes(planes + (uint64_t)m * k + c, (uint64_t)rows * k, splits) * f;
     *(u32x2 *)(dx + (uint64_t)m * k + c) = u32x2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])};
   }
 }
@@ -465,7 +468,7 @@ Targets targets_of(const df_loss *d) {
 uint32_t per_row(const df_loss *d) { return d->top ? d->top : 1; }
 Saved saved_of(const df_loss *d, void *p) {
   float *f = (float *)p;
-  return Saved{f, (uint32_t *)(f + d->rows), f + 2 * d->rows};
+  return Saved{f, f + 4, (uint32_t *)(f + 4 + d->rows), f + 4 + 2 * d->rows};
 }
 #define DFH_TRY(e) \
   do {             \
@@ -477,21 +480,24 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
   const uint32_t rows = (uint32_t)d->rows, vocab = (uint32_t)d->vocab, k = (uint32_t)d->hidden;
   const Targets t = targets_of(d);
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
-  const uint64_t entries = (uint64_t)rows * per_row(d);
-  hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)((entries + 3) / 4)), dim3(256), 0, s, t, rows, x, d->x_stride,
-                     head, d->head_stride, k, sv.picked);
-  DFH_TRY(hipGetLastError());
+  const Head h = {x, head, d->x_stride, d->head_stride, k};
+  // few rows with few targets: 96 rows of 16 x 1024, one launch less of 4.5 us; 64
+  // x 4096 in four waves would take longer than the launch
+  const bool pick = rows <= 256 && (uint64_t)per_row(d) * k <= 32768;
+  if (!pick) {
+    const uint64_t entries = (uint64_t)rows * per_row(d);
+    hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)((entries + 3) / 4)), dim3(256), 0, s, t, rows, h, sv.picked);
+    DFH_TRY(hipGetLastError());
+  }
   float2 *parts = (float2 *)ws;
   const RowCut cut = rows_for(rows, vocab, k, false);
   const Parts np = parts_of(cut, vocab);
   const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0};
   DFH_TRY((product_rows<T, false>(g, EpiStats{parts, rows, kLog2e / d->temperature}, cut, s)));
   float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + parts_bytes(d));
-  if (rows <= 256)
-    hipLaunchKernelGGL((finish_rows<1>), dim3(rows), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv, per);
-  else
-    hipLaunchKernelGGL((finish_rows<8>), dim3((rows + 7) / 8), dim3(256), 0, s, t, rows, (const float2 *)parts, np, sv,
-                       per);
+  auto *fn = pick ? finish_rows<T, 1, true> : rows <= 256 ? finish_rows<T, 1, false> : finish_rows<T, 8, false>;
+  hipLaunchKernelGGL(fn, dim3(rows <= 256 ? rows : (rows + 7) / 8), dim3(256), 0, s, t, rows, (const float2 *)parts, np,
+                     h, sv, per);
   DFH_TRY(hipGetLastError());
   return DF_OK;
 }
@@ -520,7 +526,7 @@ Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
     at += up(bytes, 256);
     return o;
   };
-  p.fac = take(4 * (2 * rows + 1));
+  p.fac = take(4 * (rows + 2));
   p.dz = take(2 * rows * nv);
   p.xm = take(want_dhead ? 2 * up(rows, 8) * k : 0);
   p.planes = take(want_dx ? 4ull * p.splits().most() * rows * k : 0);
@@ -537,14 +543,15 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   const Targets t = targets_of(d);
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
   const float c = kLog2e / d->temperature;
-  float *g = (float *)(ws + p.fac), *gn = g + rows, *peak = gn + rows;
+  float *peak = (float *)(ws + p.fac), *gn = peak + 2;
   uint16_t *dz = (uint16_t *)(ws + p.dz), *xm = (uint16_t *)(ws + p.xm);
   float *planes = (float *)(ws + p.planes);
-  hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, (int)d->reduce,
-                     d->temperature, g, gn, peak);
+  const bool own = d->reduce == DF_REDUCE_NONE;  // every row has its own gradient
+  if (own && dhead)
+    hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, gn, peak);
   if (dhead)
     hipLaunchKernelGGL((weigh_rows<T>), dim3((mp + 63) / 64, (k + 63) / 64), dim3(256), 0, s, x, d->x_stride, rows, k,
-                       (const uint32_t *)sv.state, (const float *)gn, xm, mp);
+                       (const uint32_t *)sv.state, own ? (const float *)gn : (const float *)nullptr, xm, mp);
   DFH_TRY(hipGetLastError());
   for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
     const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);
@@ -555,7 +562,7 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
     DFH_TRY(hipGetLastError());
     if (dhead) {
       const Gemm gw = {dz, xm, ldz, mp, nv, k, rows, 0, 0, 0};
-      DFH_TRY((product<T, true, false>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, peak, 1.f / mul},
+      DFH_TRY((product<T, true, false>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, own ? peak : grad, own ? peak + 1 : sv.share, d->temperature / mul},
                                       cut_for(nv, k, rows, false).shape, 1, s)));
     }
     if (dx) {
@@ -565,7 +572,8 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   }
   if (dx) {
     hipLaunchKernelGGL((finish_dx<T>), dim3(rows), dim3(256), 0, s, (const float *)planes, p.splits(), rows, k,
-                       (const uint32_t *)sv.state, (const float *)g, 1.f / mul, dx);
+                       (const uint32_t *)sv.state, grad, own ? (const float *)nullptr : (const float *)sv.share,
+                       d->temperature / mul, dx);
     DFH_TRY(hipGetLastError());
   }
   return DF_OK;
@@ -576,7 +584,7 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
 extern "C" {
 
 uint64_t df_loss_saved_bytes(const df_loss *d) {
-  return check(d) == DF_OK ? 4 * d->rows * (2 + per_row(d)) : 0;
+  return check(d) == DF_OK ? 16 + 4 * d->rows * (2 + per_row(d)) : 0;
 }
 
 uint64_t df_loss_workspace_bytes(const df_loss *d) {
@@ -608,7 +616,7 @@ df_status df_vocab_loss(const df_loss *d, float *loss, void *saved, void *worksp
   if (st != DF_OK || d->reduce == DF_REDUCE_NONE) return st;
   const float *per = (const float *)(ws + parts_bytes(d));
   hipLaunchKernelGGL(reduce_rows, dim3(1), dim3(1024), 0, stream, per, (const uint32_t *)sv.state, (uint32_t)d->rows,
-                     d->reduce == DF_REDUCE_MEAN, loss);
+                     d->reduce == DF_REDUCE_MEAN, loss, sv.share);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
 

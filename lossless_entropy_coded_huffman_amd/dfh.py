@@ -131,6 +131,8 @@ _SIGNATURES = {
 def lib():
     """The loaded libdfh.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -46,13 +46,16 @@ def _on(t: torch.Tensor, dev: torch.device, what: str):
 def _rows16(t: torch.Tensor) -> torch.Tensor:
     """t [r, c] with a row stride that is a multiple of 8 elements, unit column
     stride and a 16-byte aligned base: itself, or a copy."""
-    if t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0:
+    step, one = t.stride()
+    if one == 1 and step % 8 == 0 and step >= t.shape[1] and t.data_ptr() % 16 == 0:
         return t
     c = t.contiguous()
     return c if c.data_ptr() % 16 == 0 else c.clone()
 
 
-# the raw handle of a device's current stream, without a Stream object around it
+# the current device, and the raw handle of a device's current stream, without
+# the objects that torch.cuda makes around them (a token's product is short)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -60,7 +63,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _launch(stream, dev, tensors, call):
     """call(stream handle) with the stream it runs on current (and its device);
     inputs are recorded on a stream that was not."""
-    if stream is None and torch.cuda.current_device() == dev.index:
+    if stream is None and _current_device() == dev.index:
         return call(_raw_stream(dev.index))
     cur = torch.cuda.current_stream(dev)
     ts = cur if stream is None else dfh._torch_stream(stream, dev)
@@ -137,31 +140,35 @@ class U4Matrix:
         return (self.packed, self.scales, self.zeros)
 
 
+def _linear_on(x: torch.Tensor, w: U4Matrix, ty: int, handle: int) -> torch.Tensor:
+    """y for x [m, cols] on a stream."""
+    x = _rows16(x)
+    m = x.shape[0]
+    y = x.new_empty((m, w.rows))
+    L = dfh.lib()
+    need = w._need.get(m)
+    if need is None:
+        need = w._need[m] = L.df_linear_u4_workspace_bytes(w._ref, m)
+    ws = _workspace(need, w.device) if need else None
+    st = L.df_linear_u4(w._ref, ty, x.data_ptr(), m, x.stride(0), y.data_ptr(), _p(ws), need, handle)
+    if st:
+        dfh._check(st, "df_linear_u4")
+    return y
+
+
 def _linear(x: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
-    dev = w.device
+    dev, shape = w.device, x.shape
     if x.device != dev:
         _on(x, dev, "x")
     ty = _type(x, "x")
-    flat = x.dim() == 2
-    if x.dim() < 1 or x.shape[-1] != w.cols:
-        raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(x.shape)))
-    L = dfh.lib()
-
-    def call(handle):
-        x2 = _rows16(x if flat else x.reshape(-1, w.cols))
-        m = x2.shape[0]
-        y = torch.empty((m, w.rows), dtype=x.dtype, device=dev)
-        need = w._need.get(m)
-        if need is None:
-            need = w._need[m] = L.df_linear_u4_workspace_bytes(w._ref, m)
-        ws = _workspace(need, dev) if need else None
-        st = L.df_linear_u4(w._ref, ty, x2.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws), need, handle)
-        if st:
-            dfh._check(st, "df_linear_u4")
-        return y
-
-    y = _launch(stream, dev, (x,) + w._tensors(), call)
-    return y if flat else y.view(x.shape[:-1] + (w.rows,))
+    if not shape or shape[-1] != w.cols:
+        raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(shape)))
+    x2 = x if len(shape) == 2 else x.reshape(-1, w.cols)
+    if stream is None and _current_device() == dev.index:
+        y = _linear_on(x2, w, ty, _raw_stream(dev.index))
+    else:
+        y = _launch(stream, dev, (x,) + w._tensors(), lambda handle: _linear_on(x2, w, ty, handle))
+    return y if len(shape) == 2 else y.view(shape[:-1] + (w.rows,))
 
 
 def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:

@@ -102,9 +102,9 @@ def test_sizes():
     d = loss(rows=4096, vocab=128256, hidden=4096, x_stride=4096, head_stride=4096)
     assert 0 < L.df_loss_workspace_bytes(ctypes.byref(d)) < 4096 * 128256 * 2 // 8
     assert 0 < L.df_loss_grad_workspace_bytes(ctypes.byref(d), 1) < 4096 * 128256 * 2
-    assert L.df_loss_saved_bytes(ctypes.byref(d)) == 4096 * 3 * 4
+    assert L.df_loss_saved_bytes(ctypes.byref(d)) == 16 + 4096 * 3 * 4
     d = loss(**dict(DISTILL, rows=10))
-    assert L.df_loss_saved_bytes(ctypes.byref(d)) == 10 * 6 * 4
+    assert L.df_loss_saved_bytes(ctypes.byref(d)) == 16 + 10 * 6 * 4
 
 
 def test_host_tensors_are_refused():
