@@ -78,9 +78,11 @@ __device__ __forceinline__ void meet() {
 // Wait until this wave's LDS reads have returned: lgkmcnt(0).
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// 16 bytes a lane from src to dst + 16 lane.  ONCE: non-temporal.
+template <bool ONCE = false>
 __device__ __forceinline__ void to_lds(const void *src, uint8_t *dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void *)dst, 16, 0, ONCE ? 2 : 0);
 }
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
@@ -461,7 +463,11 @@ Cut cut_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
   for (int i = from; i <= to; i++) {
     const Shape &sh = kShapes[i];
     const uint64_t tiles = up(m, sh.bm) / sh.bm * (up(n, sh.bn) / sh.bn);
-    for (uint32_t s = 1; s <= (may_split ? 32u : 1u) && (s == 1 || steps / s >= 8); s *= 2) {
+    // one split, powers of two, and as many as fill one round or two
+    const uint32_t full = (uint32_t)(sh.slots / tiles), twice = (uint32_t)(2 * sh.slots / tiles);
+    for (uint32_t q = 0; q < 8; q++) {
+      const uint32_t s = q < 6 ? 1u << q : q == 6 ? full : twice;
+      if (s < 1 || s > 32 || (s > 1 && (!may_split || steps / s < 8))) continue;
       double t = (double)up(tiles * s, sh.slots) / sh.slots * ((double)((steps + s - 1) / s) * sh.step + 4.0);
       const double read = 2.0 * (double)n * (double)k / 5e6 + 4.0;
       if (t < read) t = read;
