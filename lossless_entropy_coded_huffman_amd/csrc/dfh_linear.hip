@@ -199,11 +199,6 @@ __device__ __forceinline__ u32x4 by_step(u32x4 q) {
   return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ void to_lds(const void *src, uint8_t *dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-}
-
 template <class T>
 __device__ __forceinline__ uint32_t minus_pair(float v) {
   return (uint32_t)to_bits(T{}, -v) * 0x10001u;
