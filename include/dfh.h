@@ -417,7 +417,7 @@ typedef struct {
   df_type teacher_type;
   uint32_t top;            /* at most 1024                                   */
   uint64_t index_stride, teacher_stride; /* elements                         */
-  float temperature;       /* positive; top == 0: 1                          */
+  float temperature;       /* 0.001 .. 1000; top == 0: 1                     */
 } df_loss;
 
 /* The loss: float[rows] (DF_REDUCE_NONE) or float[1].  saved

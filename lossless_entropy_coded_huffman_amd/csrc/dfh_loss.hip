@@ -14,8 +14,6 @@
 // more products take it.  Exponents are in base 2: c = log2(e) / T.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
-
 #include "dfh.h"
 #include "dfh_gemm.h"
 
@@ -449,7 +447,7 @@ df_status check(const df_loss *d) {
     return DF_ERR_ARG;
   if (d->rows && (!d->x || ((uintptr_t)d->x & 15))) return DF_ERR_ARG;
   if (!d->head || ((uintptr_t)d->head & 15)) return DF_ERR_ARG;
-  if (d->top > kMaxTop || !(d->temperature > 0.f) || !(d->temperature < INFINITY)) return DF_ERR_ARG;
+  if (d->top > kMaxTop || !(d->temperature >= 1e-3f) || !(d->temperature <= 1e3f)) return DF_ERR_ARG;
   if (d->top == 0) {
     if (d->temperature != 1.f || (d->rows && (!d->labels || ((uintptr_t)d->labels & 7)))) return DF_ERR_ARG;
   } else {

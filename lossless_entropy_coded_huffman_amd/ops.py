@@ -16,8 +16,10 @@ current one waits, as every torch consumer does, for nothing by itself: the
 caller orders the streams.  An input that another stream may free while the call
 runs is recorded on the call's stream.
 
-In autograd a call on the current stream records its gradient; a gradient of a
-gradient is refused.
+In autograd a gradient runs on the stream that was current in the forward call;
+a gradient of a gradient is refused.  To capture a training step into a HIP graph,
+make its leaves inside the capture (``x.detach().requires_grad_()``): a leaf that
+an eager graph still holds ties the captured backward to that graph's stream.
 """
 from __future__ import annotations
 
@@ -269,8 +271,8 @@ class _Loss:
             if labels.dtype != torch.int64 or tuple(labels.shape) != self.shape:
                 raise ValueError("labels must be int64 of shape %s" % (self.shape,))
         else:
-            if not 0.0 < d.temperature < float("inf"):
-                raise ValueError("temperature must be positive and finite")
+            if not 1e-3 <= float(temperature) <= 1e3:
+                raise ValueError("temperature must lie in 0.001 .. 1000, got %r" % (temperature,))
             _on(teacher, dev, "teacher")
             _on(index, dev, "index")
             d.teacher_type = _type(teacher, "teacher", f32=True)
@@ -401,6 +403,6 @@ def distill_loss(x: torch.Tensor, head: torch.Tensor, teacher: torch.Tensor, ind
     teacher [..., top] (bfloat16, float16 or float32) and index [..., top]
     (int64), as torch.topk gives them; entries whose index lies outside the
     vocabulary (-1) are padding, a row of padding has no loss and no gradient.
-    top is at most 1024.  x, head, reduction and the result as in vocab_loss.
+    top is at most 1024, T lies in 0.001 .. 1000.  x, head, reduction and the result as in vocab_loss.
     Differentiable in x and head; the teacher gets no gradient."""
     return _run_loss(_Loss(x, head, reduction, teacher=teacher, index=index, temperature=temperature), stream)

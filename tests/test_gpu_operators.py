@@ -204,6 +204,31 @@ def test_linear_u4_infinities_and_nan(torch, m):
     assert ((got - ref).abs() <= 2.02 * 2.0 ** -8 * ref.abs()).all()
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_linear_u4_any_zero_point(torch, dtype):
+    # zero points are bytes: 0 to 255, not only those of the quantiser
+    dt, D = getattr(torch, dtype), dev(torch)
+    g = torch.Generator().manual_seed(3)
+    n, k, grp = 70, 200, 32
+    q = torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 256, (n, 7), generator=g, dtype=torch.uint8)
+    z[0], z[1] = 0, 255
+    s = torch.rand(n, 7, generator=g) * 0.01 + 0.01
+    w = dfh.U4Matrix((q[:, 0::2] | (q[:, 1::2] << 4)).reshape(-1).to(D), s.to(D), z.to(D), cols=k, group_size=grp)
+    idx = torch.arange(k) // grp
+    w64, s64 = (q.double() - z.double()[:, idx]) * s.double()[:, idx], s.double()[:, idx]
+    for m in (2, 30, 600):
+        x = torch.randn(m, k, generator=g).to(dt)
+        few = m <= 512
+        # the sums are of x (128 + q) and (128 + z) x in BF16, of x (q - z) in FP16
+        mag = x.double().abs() @ (s64 * 526).t()
+        u = half_ulp(torch, dt)
+        ref = x.double() @ w64.t()
+        bound = (128 + k / 128 + 16) * E * mag * (1 + u) + u * ref.abs() + tiny(torch, dt) if few else \
+            (u * 1.01 + (k + 16) * E) * (x.double().abs() @ w64.abs().t()) * (1 + u) + u * ref.abs() + tiny(torch, dt)
+        within(dfh.linear_u4(x.to(D), w), ref, bound)
+
+
 def test_linear_u4_rows_behind_the_last_are_left(torch):
     # columns and rows past the end of y in a larger buffer keep their bytes
     D = dev(torch)
@@ -297,7 +322,7 @@ def check_loss(torch, loss, dx, dhead, x, head, valid, t, idx, temp, reduction, 
         within(dhead, ref, bound * (1 + u) + (u + 8 * E) * ref.abs() + tiny(torch, dt))
 
 
-LOSS_SHAPES = [(1, 5, 8), (3, 64, 72), (17, 1000, 128), (64, 257, 264), (65, 2049, 64), (130, 517, 520),
+LOSS_SHAPES = [(1, 5, 8), (4, 1, 16), (2, 2, 8), (3, 64, 72), (17, 1000, 128), (64, 257, 264), (65, 2049, 64), (130, 517, 520),
                (300, 4100, 136), (1100, 3001, 64), (261, 60003, 72), (513, 33000, 64)]
 
 
@@ -571,7 +596,75 @@ def test_refusals_on_the_device(torch):
     with pytest.raises(ValueError):
         dfh.vocab_loss(x, head, lab, reduction="average")
     t, i = torch.zeros(2, 4, device=D), torch.zeros(2, 4, dtype=torch.int64, device=D)
-    for a, b, temp in ((t, i[:, :3], 1.0), (t, i.int(), 1.0), (t, i, 0.0), (t, i, float("inf")), (t, i, float("nan")),
+    for a, b, temp in ((t, i[:, :3], 1.0), (t, i.int(), 1.0), (t, i, 0.0), (t, i, 1e-4), (t, i, 1e4), (t, i, float("inf")), (t, i, float("nan")),
                        (t.double(), i, 1.0), (t[:, :0], i[:, :0], 1.0)):
         with pytest.raises((ValueError, TypeError)):
             dfh.distill_loss(x, head, a, b, temperature=temp)
+
+
+def test_gradients_of_gradients_are_refused(torch):
+    # first order under create_graph works, the second raises
+    D = dev(torch)
+    w, _, _ = matrix(torch, 24, 64, 32, "fp32", seed=1)
+    x, head = head_and_x(torch, 5, 40, 24, torch.bfloat16, 1)
+    a = torch.randn(5, 64).to(torch.bfloat16).to(D).requires_grad_()
+    h = dfh.linear_u4(a, w)
+    loss = dfh.vocab_loss(h, head.to(D), torch.zeros(5, dtype=torch.int64, device=D))
+    plain, = torch.autograd.grad(loss, a, retain_graph=True)
+    g, = torch.autograd.grad(loss, a, create_graph=True)
+    assert torch.equal(g, plain)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.float().sum(), a)
+
+
+def test_strided_targets(torch):
+    # columns of wider tensors, rows expanded over the batch, labels with a stride
+    D = dev(torch)
+    x, head = head_and_x(torch, 10, 90, 64, torch.float16, 6)
+    x, head = x.to(D), head.to(D)
+    g = torch.Generator().manual_seed(4)
+    t, i = (torch.randn(10, 90, generator=g) * 2).topk(6, dim=1)
+    t, i = t.to(D), i.to(D)
+    want = dfh.distill_loss(x, head, t, i, reduction="none")
+    tw, iw = torch.zeros(10, 20, device=D), torch.zeros(10, 13, dtype=torch.int64, device=D)
+    tw[:, 3:9], iw[:, 5:11] = t, i
+    assert torch.equal(dfh.distill_loss(x, head, tw[:, 3:9], iw[:, 5:11], reduction="none"), want)
+    assert torch.equal(dfh.distill_loss(x, head, t.t().contiguous().t(), i.t().contiguous().t(), reduction="none"), want)
+    e = dfh.distill_loss(x, head, t[:1].expand(10, 6), i[:1].expand(10, 6), reduction="none")
+    assert torch.equal(e, dfh.distill_loss(x, head, t[:1].repeat(10, 1), i[:1].repeat(10, 1), reduction="none"))
+    lab = torch.randint(0, 90, (10, 3), generator=g).to(D)
+    assert torch.equal(dfh.vocab_loss(x, head, lab[:, 1], reduction="none"),
+                       dfh.vocab_loss(x, head, lab[:, 1].contiguous(), reduction="none"))
+
+
+def test_loss_in_pieces_of_the_vocabulary(torch):
+    # a vocabulary of several pieces (16384 rows: 4096 entries each), the target in
+    # each piece, against one call per half of the rows (pieces twice as long)
+    D = dev(torch)
+    m, v, h = 16384, 9000, 64
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(m, h, generator=g).to(torch.bfloat16).to(D)
+    head = (torch.randn(v, h, generator=g) * 0.3).to(torch.bfloat16).to(D).requires_grad_()
+    labels = torch.randint(0, v, (m,), generator=g).to(D)
+    xs = x.clone().requires_grad_()
+    loss = dfh.vocab_loss(xs, head, labels, reduction="sum")
+    dx, dh = torch.autograd.grad(loss, (xs, head))
+    parts = []
+    for lo in (0, m // 2):
+        xp = x[lo: lo + m // 2].clone().requires_grad_()
+        lp = dfh.vocab_loss(xp, head, labels[lo: lo + m // 2], reduction="sum")
+        parts.append((lp.detach(),) + torch.autograd.grad(lp, (xp, head)))
+    # a float64 run of the whole on the GPU
+    z = x.double() @ head.detach().double().t()
+    p = torch.softmax(z, 1)
+    ref = torch.nn.functional.cross_entropy(z, labels, reduction="sum")
+    p[torch.arange(m, device=D), labels] -= 1
+    assert abs(float(loss.detach()) - float(ref)) <= float(ref) * 64 * E * 8
+    u = 2.0 ** -8
+    a = p.abs()
+    bx = ((u + 1e-4) * a @ head.detach().double().abs()) + u * 1.1 * (p @ head.detach().double()).abs()
+    bh = ((u + 1e-4) * a.t() @ x.double().abs()) + u * 1.1 * (p.t() @ x.double()).abs()
+    assert bool(((dx.double() - p @ head.detach().double()).abs() <= bx).all())
+    assert bool(((dh.double() - p.t() @ x.double()).abs() <= bh).all())
+    assert abs(float(parts[0][0] + parts[1][0]) - float(ref)) <= float(ref) * 64 * E * 8
+    assert bool(((torch.cat([parts[0][1], parts[1][1]]).double() - p @ head.detach().double()).abs() <= bx).all())

@@ -66,7 +66,7 @@ BAD_LOSS = [dict(type=2), dict(reduce=3), dict(rows=1 << 24), dict(vocab=0), dic
             dict(x=P + 8), dict(head=None), dict(head=P + 2), dict(labels=None), dict(labels=P + 4),
             dict(temperature=2.0), dict(DISTILL, top=1025), dict(DISTILL, index=None), dict(DISTILL, index=P + 4),
             dict(DISTILL, teacher=None), dict(DISTILL, teacher_type=2, teacher=P + 2), dict(DISTILL, teacher_type=4),
-            dict(DISTILL, temperature=0.0), dict(DISTILL, temperature=-1.0), dict(DISTILL, temperature=float("inf")),
+            dict(DISTILL, temperature=0.0), dict(DISTILL, temperature=-1.0), dict(DISTILL, temperature=float("inf")), dict(DISTILL, temperature=5e-4), dict(DISTILL, temperature=2000.0),
             dict(DISTILL, temperature=float("nan"))]
 
 
