@@ -370,8 +370,8 @@ typedef struct {
 /* y[m, n] = sum over k of x[m, k] W[n, k].  x: `rows` rows of w->cols
  * elements of `type` (BF16 or F16), x_stride elements apart (a multiple of 8,
  * at most 2^21); y: rows x w->rows of the same type, contiguous.  Both 16-byte
- * aligned.  Up to 256 rows (512 where W has at most 2^24 elements) multiply the
- * integers exactly (a group's FP32 sum is scaled); more rows expand W to `type` in the workspace (256-byte aligned),
+ * aligned.  Few rows (up to 192; 384 where W has at most 2^24 elements, 512 at most
+ * 2^22) multiply the integers exactly (a group's FP32 sum is scaled); more expand W to `type` in the workspace (256-byte aligned),
  * each weight rounded once.  Sums are FP32.  Up to 4 rows need no workspace.
  * DF_ERR_ARG on a bad pointer, size, alignment or too small a workspace. */
 uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows);

@@ -588,12 +588,13 @@ __global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss
 }
 
 // Rows that u4_tile takes rather than an expansion: the expansion costs a fixed
-// time per weight (0.6 us a million), the tile kernel a time per weight and 64
-// rows (0.34 us a million once the chip is full, less before).
-// 256 x 14336 x 4096: 79 us against 83; 512 x 14336 x 4096: 140 against 95;
-// 512 x 4096 x 4096: 41 against 49; 333 x 2047 x 1416: 17 against 23.
-bool few_rows(uint64_t m, uint64_t n, uint64_t k) { return m <= 256 || (m <= 512 && n * k <= 1u << 24); }
-
+// time per weight (0.45 us a million), the tile kernel a time per weight and 64
+// rows (0.34 us a million once the chip is full, less before).  Tile against
+// expansion, us: 200 x 4096 x 4096 28 : 32, 512 rows of it 44 : 41; 64 x 14336 x
+// 4096 30 : 65, 256 rows of it 80 : 74; 333 x 2047 x 1416 17 : 22.
+bool few_rows(uint64_t m, uint64_t n, uint64_t k) {
+  return m <= 192 || (m <= 384 && n * k <= 1u << 24) || (m <= 512 && n * k <= 1u << 22);
+}
 bool type_ok(df_type t) { return t == DF_TYPE_BF16 || t == DF_TYPE_F16; }
 
 df_status matrix_of(const df_u4_matrix *m, U4 *w) {

@@ -69,9 +69,14 @@ def matrix(torch, n, k, group, scale="bf16", zeros=True, seed=0, broadcast=False
     return w, ((q.double() - zz.expand(n, ng)[:, idx]) * s.double().expand(n, ng)[:, idx]), s.double().abs().expand(n, ng)[:, idx]
 
 
+def few_rows(m, n, k):
+    """Rows whose products take the integers as they are (include/dfh.h)."""
+    return m <= 192 or (m <= 384 and n * k <= 1 << 24) or (m <= 512 and n * k <= 1 << 22)
+
+
 def linear_bound(torch, dt, x, w64, s64, few):
-    """Bound on |y - ref|: few rows (up to 256; 512 of a small matrix) scale the sums of integers, more
-    round every weight."""
+    """Bound on |y - ref|: few rows scale the sums of integers, more round every
+    weight."""
     u, k = half_ulp(torch, dt), x.shape[1]
     xa = x.double().abs()
     mag = xa @ w64.abs().t()
@@ -87,8 +92,8 @@ def linear_bound(torch, dt, x, w64, s64, few):
 
 
 FEW = [(1, 16, 64, 32), (4, 4100, 8712, 96), (1, 70, 9000, 128), (3, 33000, 520, 32), (1, 37, 16384, 160), (6, 2048, 2048, 64), (48, 1000, 3080, 32), (1, 17, 4096, 128), (1, 300, 1416, 1416), (2, 1024, 256, 64), (16, 33, 8, 32), (16, 130, 520, 96),
-       (17, 64, 1024, 128), (128, 260, 1032, 128), (200, 129, 640, 64), (256, 65, 2080, 416), (32, 47, 136, 32), (33, 200, 2048, 256), (64, 31, 4104, 128), (5, 1, 24, 64)]
-MANY = [(65, 64, 64, 32), (100, 130, 520, 96), (257, 64, 72, 72), (513, 70, 136, 32), (300, 4200, 4104, 128), (333, 257, 1416, 32), (256, 512, 256, 128), (129, 1, 8, 32),
+       (17, 64, 1024, 128), (128, 260, 1032, 128), (200, 129, 640, 64), (256, 65, 2080, 416), (300, 2304, 2048, 64), (32, 47, 136, 32), (33, 200, 2048, 256), (64, 31, 4104, 128), (5, 1, 24, 64)]
+MANY = [(65, 64, 64, 32), (100, 130, 520, 96), (257, 64, 72, 72), (513, 70, 136, 32), (193, 4200, 4104, 128), (400, 2304, 2048, 64), (333, 257, 1416, 32), (256, 512, 256, 128), (129, 1, 8, 32),
         (640, 1031, 72, 72), (1500, 2304, 192, 64), (2049, 6400, 64, 64)]
 
 
@@ -101,7 +106,7 @@ def test_linear_u4(torch, m, n, k, group, dtype):
     x = torch.randn(m, k, generator=torch.Generator().manual_seed(k)).to(dt)
     y = dfh.linear_u4(x.to(dev(torch)), w)
     assert y.dtype == dt and y.shape == (m, n)
-    within(y, x.double() @ w64.t(), linear_bound(torch, dt, x, w64, s64, m <= 256 or (m <= 512 and n * k <= 1 << 24)))
+    within(y, x.double() @ w64.t(), linear_bound(torch, dt, x, w64, s64, few_rows(m, n, k)))
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
