@@ -9,7 +9,7 @@
 // Few rows: u4_tokens (up to 4) and u4_tile (few_rows) feed the matrix cores
 // with the integers themselves, and the scale multiplies a group's FP32 sum.
 // More rows: the weights are expanded to 16 bits in the caller's workspace and
-// gemm_nt does the product.
+// the tiled product of dfh_gemm.h takes them.
 #include <hip/hip_runtime.h>
 
 #include "dfh.h"
@@ -42,7 +42,7 @@ __device__ __forceinline__ float scale_at(const U4 &w, uint32_t n, uint32_t g) {
   const uint16_t b = ((const uint16_t *)w.scales)[i];
   return w.scale_type == DF_TYPE_BF16 ? from_bits(BF16{}, b) : from_bits(F16{}, b);
 }
-// A raw scale of the type that u4_rows was made for.
+// A raw scale of the type that a kernel was made for.
 __device__ __forceinline__ float scale_of(const U4 &, float s) { return s; }
 __device__ __forceinline__ float scale_of(const U4 &w, uint16_t b) {
   return w.scale_type == DF_TYPE_BF16 ? from_bits(BF16{}, b) : from_bits(F16{}, b);

@@ -186,7 +186,9 @@ def quantize_u4_groups(x: np.ndarray, group_size: int, asymmetric: bool):
     """quantize_u4 for each group of group_size consecutive elements of a row
     of x [rows, cols] (the last group of a row may be shorter).  Returns (codes
     [rows, cols], scales float32 [rows, groups], zeros uint8 [rows, groups]):
-    x ~ scales * (codes - zeros)."""
+    x ~ scales * (codes - zeros).  As in quantize_u4 the zero point is a code, so
+    an asymmetric group whose values all lie on one side of zero is clipped at 15
+    steps from zero."""
     x = np.ascontiguousarray(x, np.float32)
     rows, cols = x.shape
     groups = -(-cols // group_size)
