@@ -45,14 +45,22 @@ def _on(t: torch.Tensor, dev: torch.device, what: str):
         raise ValueError("%s must be a tensor on %s" % (what, dev))
 
 
+_MAX_STRIDE = 1 << 21   # the kernels' largest row stride
+
+
+def _copied(t: torch.Tensor) -> torch.Tensor:
+    """A copy with a contiguous tensor's strides (contiguous() may return t itself,
+    with any stride in a dimension of one element)."""
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _rows16(t: torch.Tensor) -> torch.Tensor:
-    """t [r, c] with a row stride that is a multiple of 8 elements, unit column
-    stride and a 16-byte aligned base: itself, or a copy."""
+    """t [r, c] with a row stride that is a multiple of 8 elements and at most 2^21,
+    unit column stride and a 16-byte aligned base: itself, or a copy."""
     step, one = t.stride()
-    if one == 1 and step % 8 == 0 and step >= t.shape[1] and t.data_ptr() % 16 == 0:
+    if one == 1 and step % 8 == 0 and t.shape[1] <= step <= _MAX_STRIDE and t.data_ptr() % 16 == 0:
         return t
-    c = t.contiguous()
-    return c if c.data_ptr() % 16 == 0 else c.clone()
+    return _copied(t)
 
 
 # the current device, and the raw handle of a device's current stream, without
@@ -188,8 +196,8 @@ def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
         d2 = dy if dy.dim() == 2 else dy.reshape(-1, w.rows)
         if w.rows % 8 == 0:
             d2 = _rows16(d2)
-        elif d2.stride(1) != 1 or d2.stride(0) < w.rows:
-            d2 = d2.contiguous()
+        elif d2.stride(1) != 1 or not w.rows <= d2.stride(0) <= _MAX_STRIDE:
+            d2 = _copied(d2)
         m = d2.shape[0]
         dx = torch.empty((m, w.cols), dtype=dy.dtype, device=dev)
         need = w._need_grad.get(m)
