@@ -12,12 +12,13 @@ Everything is enqueued on ``stream`` (default: the current stream of the
 tensors' device) and returns without synchronising.  Outputs and workspaces are
 torch tensors allocated on that stream, so a call can be captured into a HIP
 graph, and two calls never share one.  A call given another stream than the
-current one waits, as every torch consumer does, for nothing by itself: the
-caller orders the streams.  An input that another stream may free while the call
-runs is recorded on the call's stream.
+current one does not wait for the current one: the caller orders the streams.  An
+input that another stream may free while the call runs is recorded on the call's
+stream.
 
-In autograd a gradient runs on the stream that was current in the forward call;
-a gradient of a gradient is refused.  To capture a training step into a HIP graph,
+In autograd a gradient runs on the stream that was current in the forward call,
+after a forward call that was given another one; a gradient of a gradient is
+refused.  To capture a training step into a HIP graph,
 make its leaves inside the capture (``x.detach().requires_grad_()``): a leaf that
 an eager graph still holds ties the captured backward to that graph's stream.
 """
@@ -292,6 +293,7 @@ class _Loss:
                 raise ValueError("top must lie in 1 .. 1024, got %d" % d.top)
         self.inputs = (x, head, labels, teacher, index)
         self.desc, self.dev = d, dev
+        self.done = None   # an event behind the forward call, where that ran on another stream
 
     def bind(self):
         """Lays the inputs out and points the descriptor at them (on the call's stream)."""
@@ -317,6 +319,7 @@ class _Loss:
     def forward(self, stream):
         L, dev = dfh.lib(), self.dev
         none = self.reduction == "none"
+        current = _raw_stream(dev.index)
 
         def call(handle):
             self.bind()
@@ -328,6 +331,9 @@ class _Loss:
             st = L.df_vocab_loss(ref, loss.data_ptr(), saved.data_ptr(), ws.data_ptr(), need, handle)
             if st:
                 dfh._check(st, "df_vocab_loss")
+            if handle != current:
+                self.done = torch.cuda.Event()
+                self.done.record()   # on the call's stream
             return loss, saved
 
         loss, saved = _launch(stream, dev, self.inputs, call)
@@ -338,6 +344,13 @@ class _Loss:
         x, head = self.inputs[0], self.inputs[1]
 
         def call(handle):
+            if self.done is not None:
+                # what the forward call keeps is written, and was allocated, on its stream
+                here = torch.cuda.current_stream(dev)
+                here.wait_event(self.done)
+                for t in self.held + (saved,):
+                    if t is not None:
+                        t.record_stream(here)
             ref = ctypes.byref(self.desc)
             g = gout.to(torch.float32).reshape(-1).contiguous()
             dx = torch.empty((int(self.desc.rows), head.shape[1]), dtype=x.dtype, device=dev) if want_x else None

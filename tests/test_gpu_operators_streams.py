@@ -1,0 +1,38 @@
+"""The gradient of a loss whose forward call was given a stream: the one that a call
+on the current stream gives."""
+import pytest
+
+import lossless_entropy_coded_huffman_amd as dfh
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch
+
+
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_gradient_of_a_loss_on_another_stream(torch, reduction):
+    # the forward call runs on s and keeps its statistics there, and a copy of x
+    # (which is not laid out for the kernels); its gradient runs on the current one
+    g = torch.Generator().manual_seed(3)
+    m, v, h = 300, 9001, 512
+    head = (torch.randn(v, h, generator=g) * 0.1).to(torch.bfloat16).cuda().requires_grad_()
+    x = torch.randn(h, m, generator=g).to(torch.bfloat16).cuda().requires_grad_()
+    labels = torch.randint(0, v, (m,), generator=g).cuda()
+    gout = torch.rand(m, generator=g).cuda() + 0.5 if reduction == "none" else torch.ones((), device="cuda")
+    want = torch.autograd.grad(dfh.vocab_loss(x.t(), head, labels, reduction=reduction), (x, head), gout)
+    s = torch.cuda.Stream()
+    for _ in range(6):
+        s.wait_stream(torch.cuda.current_stream())
+        loss = dfh.vocab_loss(x.t(), head, labels, reduction=reduction, stream=s)
+        got = torch.autograd.grad(loss, (x, head), gout)
+        del loss
+        with torch.cuda.stream(s):   # takes what the call's stream has to give
+            torch.full((m * h,), 7.0, dtype=torch.bfloat16, device="cuda")
+            torch.full((4 * m,), 7.0, device="cuda")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
