@@ -23,6 +23,8 @@ quantised model loses against the lossless one, and the gradient to mend it.
 """
 from __future__ import annotations
 
+import contextlib
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -184,7 +186,10 @@ class QuantizedBlocks:
     layers: per block a list of (container, scales, zeros) in
     BlockShape.matrices() order, as quantize_block makes them; scales [rows,
     groups] in float32 (kept in scale_dtype), zeros uint8 of that shape or None.
-    One scratch buffer of a block's nibbles is allocated up front."""
+    One scratch buffer of a block's nibbles is allocated up front.  Calls take turns
+    with it, from any thread and on any stream (each waits for the one before); a
+    captured call's replays are for the caller to order with what else uses these
+    blocks."""
 
     def __init__(self, layers, shape: BlockShape, device, group_size: int, scale_dtype=torch.bfloat16):
         self.shape = shape
@@ -206,6 +211,23 @@ class QuantizedBlocks:
                 ws[name] = U4Matrix(packed, s, z, cols=c, group_size=group_size)
             self.blocks.append(dcs)
             self.weights.append(ws)
+        self._lock = threading.RLock()
+        self._stream, self._used = None, torch.cuda.Event()  # the last turn's stream, and its end
+
+    @contextlib.contextmanager
+    def _turn(self):
+        """A block's use of the scratch buffer, from its decode to its last reader."""
+        with self._lock, torch.cuda.device(self.device):
+            stream = torch.cuda.current_stream(self.device)
+            capturing = torch.cuda.is_current_stream_capturing()
+            if not capturing and self._stream is not None and self._stream != stream:
+                stream.wait_event(self._used)
+            try:
+                yield
+            finally:
+                if not capturing:
+                    self._used.record(stream)
+                    self._stream = stream
 
     def _run(self, i: int, x: torch.Tensor) -> torch.Tensor:
         dfh.df_decompress_batch(self.blocks[i], self.scratch, torch.cuda.current_stream(self.device))
@@ -218,7 +240,7 @@ class QuantizedBlocks:
             if x.requires_grad and torch.is_grad_enabled():
                 x = _QuantizedBlock.apply(x, self, i)
             else:
-                with torch.no_grad():
+                with torch.no_grad(), self._turn():
                     x = self._run(i, x)
         return x
 
@@ -228,22 +250,24 @@ class _QuantizedBlock(torch.autograd.Function):
     def forward(ctx, x, blocks, i):
         ctx.save_for_backward(x)
         ctx.blocks, ctx.i = blocks, i
-        return blocks._run(i, x)
+        with blocks._turn():
+            return blocks._run(i, x)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, = ctx.saved_tensors
-        with torch.enable_grad():
-            leaf = x.detach().requires_grad_()
-            y = ctx.blocks._run(ctx.i, leaf)
-        return torch.autograd.grad(y, leaf, dy)[0], None, None
+        with ctx.blocks._turn():
+            with torch.enable_grad():
+                leaf = x.detach().requires_grad_()
+                y = ctx.blocks._run(ctx.i, leaf)
+            return torch.autograd.grad(y, leaf, dy)[0], None, None
 
 
 class CompressedHead:
     """An LM head [vocab, hidden] held as one BF16 container (the DF11 digest
     compresses embedding and LM head on their own), decoded into one scratch
-    buffer before each use."""
+    buffer before each use.  The caller orders uses on several streams."""
 
     def __init__(self, container, vocab: int, hidden: int, device):
         inf = container.info()
