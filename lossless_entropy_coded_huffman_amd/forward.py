@@ -86,20 +86,32 @@ def _rope(x: torch.Tensor, theta: float) -> torch.Tensor:
 
 
 class _Bmm(torch.autograd.Function):
-    """torch.bmm of contiguous operands whose gradients take contiguous operands
-    too (torch's own hands transposed views on)."""
+    """torch.bmm of contiguous operands whose derivatives take contiguous operands
+    too (torch's own hands transposed views on).  They are made of the same
+    product, so they can be differentiated and transformed (torch.func) again."""
+    generate_vmap_rule = True
 
     @staticmethod
-    def forward(ctx, a, b):
-        ctx.save_for_backward(a, b)
+    def forward(a, b):
         return torch.bmm(a, b)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    def setup_context(ctx, inputs, output):
+        ctx.save_for_backward(*inputs)
+        ctx.save_for_forward(*inputs)
+
+    @staticmethod
     def backward(ctx, dy):
         a, b = ctx.saved_tensors
         dy = dy.contiguous()
-        return (torch.bmm(dy, b.transpose(1, 2).contiguous()), torch.bmm(a.transpose(1, 2).contiguous(), dy))
+        da = _Bmm.apply(dy, b.transpose(1, 2).contiguous()) if ctx.needs_input_grad[0] else None
+        db = _Bmm.apply(a.transpose(1, 2).contiguous(), dy) if ctx.needs_input_grad[1] else None
+        return da, db
+
+    @staticmethod
+    def jvp(ctx, da, db):
+        a, b = ctx.saved_tensors
+        return _Bmm.apply(da.contiguous(), b) + _Bmm.apply(a, db.contiguous())
 
 
 def block_forward(x: torch.Tensor, w: dict, shape: BlockShape, linear=torch.nn.functional.linear) -> torch.Tensor:
