@@ -17,8 +17,8 @@ input that another stream may free while the call runs is recorded on the call's
 stream.
 
 In autograd a gradient runs on the stream that was current in the forward call,
-after a forward call that was given another one; a gradient of a gradient is
-refused.  To capture a training step into a HIP graph,
+after a forward call that was given another one.  linear_u4 can be differentiated
+again, a gradient of a loss's gradient is refused.  To capture a training step into a HIP graph,
 make its leaves inside the capture (``x.detach().requires_grad_()``): a leaf that
 an eager graph still holds ties the captured backward to that graph's stream.
 """
@@ -182,9 +182,7 @@ def _linear(x: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
     return y if len(shape) == 2 else y.view(shape[:-1] + (w.rows,))
 
 
-def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
-    """dx[..., k] = sum over n of dy[..., n] W[n, k]: the gradient of linear_u4
-    to its input, in dy's type (bfloat16 or float16)."""
+def _linear_grad(dy: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
     dev = w.device
     if dy.device != dev:
         _on(dy, dev, "dy")
@@ -214,26 +212,44 @@ def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     return dx if dy.dim() == 2 else dx.view(dy.shape[:-1] + (w.cols,))
 
 
+def _keep_weights(ctx, w: U4Matrix):
+    """The derivative reads them again: a change that torch sees in between is refused."""
+    ctx.w = w
+    ctx.save_for_backward(*[t for t in w._tensors() if t is not None])
+
+
 class _LinearU4(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stream):
-        ctx.w = w
-        # read again by the gradient: a change that torch sees in between is refused
-        ctx.save_for_backward(*[t for t in w._tensors() if t is not None])
+        _keep_weights(ctx, w)
         return _linear(x, w, stream)
 
     @staticmethod
     def backward(ctx, dy):
-        if torch.is_grad_enabled():   # under create_graph: a graph that refuses to be differentiated
-            return _LinearU4._once(ctx, dy)
         ctx.saved_tensors
         return linear_u4_grad(dy, ctx.w), None, None
 
+
+class _LinearU4Grad(torch.autograd.Function):
+    """dx is linear in dy, and its derivative the product itself."""
+
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def _once(ctx, dy):
+    def forward(ctx, dy, w, stream):
+        _keep_weights(ctx, w)
+        return _linear_grad(dy, w, stream)
+
+    @staticmethod
+    def backward(ctx, ddx):
         ctx.saved_tensors
-        return linear_u4_grad(dy, ctx.w), None, None
+        return linear_u4(ddx, ctx.w), None, None
+
+
+def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
+    """dx[..., k] = sum over n of dy[..., n] W[n, k]: the gradient of linear_u4
+    to its input, in dy's type (bfloat16 or float16).  Differentiable in dy."""
+    if dy.requires_grad and torch.is_grad_enabled():
+        return _LinearU4Grad.apply(dy, w, stream)
+    return _linear_grad(dy, w, stream)
 
 
 def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:

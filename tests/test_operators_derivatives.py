@@ -1,0 +1,60 @@
+"""What the operators' derivatives do with a second differentiation and with
+forward mode: the autograd functions over plain stand-ins for the kernels, so no
+GPU is needed.  In every second derivative x is reached by another path too, as a
+residual connection does: a node that autograd prunes cannot refuse."""
+import pytest
+import torch
+
+from lossless_entropy_coded_huffman_amd import ops
+
+
+class Dense:
+    """A weight matrix in place of a U4Matrix."""
+
+    def __init__(self, weight):
+        self.weight = weight
+
+    def _tensors(self):
+        return (self.weight, None)
+
+
+@pytest.fixture
+def dense(monkeypatch):
+    g = torch.Generator().manual_seed(0)
+    w = Dense(torch.randn(7, 5, generator=g, dtype=torch.float64))
+    monkeypatch.setattr(ops, "_linear", lambda x, w, stream: x @ w.weight.t())
+    monkeypatch.setattr(ops, "_linear_grad", lambda dy, w, stream: dy @ w.weight, raising=False)
+    return w
+
+
+def second(f, x0, v):
+    x = x0.clone().requires_grad_()
+    g, = torch.autograd.grad(f(x), x, create_graph=True)
+    return torch.autograd.grad((g * v).sum(), x)[0]
+
+
+def test_second_gradient_of_linear_u4(dense):
+    g = torch.Generator().manual_seed(1)
+    x, v = (torch.randn(3, 5, generator=g, dtype=torch.float64) for _ in range(2))
+    got = second(lambda x: (x * x).sum() + ops.linear_u4(x, dense).pow(3).sum(), x, v)
+    want = second(lambda x: (x * x).sum() + (x @ dense.weight.t()).pow(3).sum(), x, v)
+    # a dozen float64 roundings of a sum of 35 terms
+    assert float((got - want).abs().max()) <= 2.0 ** -40 * float(want.abs().max())
+    y = x.clone().requires_grad_()
+    assert torch.autograd.gradcheck(lambda x: ops.linear_u4(x, dense), y)
+    assert torch.autograd.gradgradcheck(lambda x: ops.linear_u4(x, dense), y)
+
+
+def test_linear_u4_grad_is_differentiable(dense):
+    g = torch.Generator().manual_seed(2)
+    dy = torch.randn(3, 7, generator=g, dtype=torch.float64).requires_grad_()
+    assert torch.autograd.gradcheck(lambda d: ops.linear_u4_grad(d, dense), dy)
+    assert not ops.linear_u4_grad(dy.detach(), dense).requires_grad
+
+
+def test_changed_weights_are_refused_by_a_second_gradient(dense):
+    x = torch.ones(2, 5, dtype=torch.float64, requires_grad=True)
+    g, = torch.autograd.grad(ops.linear_u4(x, dense).pow(2).sum(), x, create_graph=True)
+    dense.weight.mul_(2.0)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), x)
