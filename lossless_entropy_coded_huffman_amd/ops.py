@@ -394,20 +394,25 @@ class _LossFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gout):
-        if torch.is_grad_enabled():   # under create_graph: a graph that refuses to be differentiated
-            return _LossFunction._once(ctx, gout)
-        return _LossFunction._grads(ctx, gout)
-
-    @staticmethod
-    def _grads(ctx, gout):
-        saved = ctx.saved_tensors[-1]
-        dx, dh = ctx.call.grads(saved, gout, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        call, saved, want = ctx.call, ctx.saved_tensors[-1], ctx.needs_input_grad[:2]
+        if torch.is_grad_enabled():   # under create_graph
+            dx, dh = _LossGrad.apply(gout, *call.inputs[:2], call, saved, want)
+        else:
+            dx, dh = call.grads(saved, gout, *want)
         return dx, dh, None, None
 
+
+class _LossGrad(torch.autograd.Function):
+    """The gradients as a function of all they depend on: a second derivative is
+    refused on whatever path it comes."""
+
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def _once(ctx, gout):
-        return _LossFunction._grads(ctx, gout)
+    def forward(ctx, gout, x, head, call, saved, want):
+        return call.grads(saved, gout, *want)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("vocab_loss and distill_loss have no second gradient")
 
 
 def _run_loss(call, stream):

@@ -58,3 +58,38 @@ def test_changed_weights_are_refused_by_a_second_gradient(dense):
     dense.weight.mul_(2.0)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(g.sum(), x)
+
+
+class Squares:
+    """A loss call over [rows, hidden] states and a head: sum of (x head^T)^2, in
+    place of a _Loss."""
+
+    def __init__(self, x, head):
+        self.inputs = (x, head, None, None, None)
+
+    def forward(self, stream):
+        x, head = self.inputs[:2]
+        return (x @ head.t()).pow(2).sum(), torch.zeros(1)
+
+    def grads(self, saved, gout, want_x, want_head):
+        x, head = (t.detach() for t in self.inputs[:2])
+        z = 2 * gout * (x @ head.t())
+        return z @ head if want_x else None, z.t() @ x if want_head else None
+
+
+@pytest.mark.parametrize("leaf", ["x", "head"])
+def test_second_gradients_of_losses_are_refused(leaf):
+    g = torch.Generator().manual_seed(3)
+    x, head = (torch.randn(s, 5, generator=g, dtype=torch.float64) for s in (3, 7))
+    x, head = x.requires_grad_(leaf == "x"), head.requires_grad_(leaf == "head")
+    t = x if leaf == "x" else head
+    loss = ops._run_loss(Squares(x, head), None)
+    plain, = torch.autograd.grad((t * t).sum() + loss, t, retain_graph=True)
+    # the first gradient stays what it is under create_graph
+    first, = torch.autograd.grad((t * t).sum() + loss, t, create_graph=True)
+    assert torch.equal(first, plain)
+    want = (x @ head.t()) * 2
+    want = (want @ head if leaf == "x" else want.t() @ x) + 2 * t
+    assert float((first - want).abs().max()) <= 2.0 ** -44 * float(want.abs().max())
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(first.sum(), t)
