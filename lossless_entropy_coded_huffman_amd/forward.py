@@ -246,7 +246,7 @@ class QuantizedBlocks:
         return block_forward(x, self.weights[i], self.shape, linear_u4)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """All blocks in order on the current stream.  Differentiable in x: a
+        """All blocks in order on the current stream.  Differentiable in x, once: a
         block keeps its input and is decoded and run again for its gradient."""
         for i in range(len(self.blocks)):
             if x.requires_grad and torch.is_grad_enabled():
@@ -266,14 +266,23 @@ class _QuantizedBlock(torch.autograd.Function):
             return blocks._run(i, x)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, = ctx.saved_tensors
-        with ctx.blocks._turn():
-            with torch.enable_grad():
-                leaf = x.detach().requires_grad_()
-                y = ctx.blocks._run(ctx.i, leaf)
-            return torch.autograd.grad(y, leaf, dy)[0], None, None
+        return _QuantizedBlockGrad.apply(dy, *ctx.saved_tensors, ctx.blocks, ctx.i), None, None
+
+
+class _QuantizedBlockGrad(torch.autograd.Function):
+    """A block's gradient as a function of all it depends on: a second derivative
+    is refused on whatever path it comes."""
+
+    @staticmethod
+    def forward(ctx, dy, x, blocks, i):
+        with blocks._turn(), torch.enable_grad():
+            leaf = x.detach().requires_grad_()
+            return torch.autograd.grad(blocks._run(i, leaf), leaf, dy)[0]
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("QuantizedBlocks have no second gradient")
 
 
 class CompressedHead:

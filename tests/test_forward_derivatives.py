@@ -1,6 +1,8 @@
 """Derivatives of a resident block beyond the first gradient: a gradient of a
 gradient, forward mode and torch.func's transforms give what the block of plain
 batched products gives.  No GPU needed."""
+import contextlib
+
 import pytest
 import torch
 
@@ -97,3 +99,28 @@ def test_transforms(monkeypatch, transform):
          "grad of vmap": lambda: torch.func.grad(lambda a: torch.func.vmap(one)(a).pow(2).sum())(xs)}[transform]
     got, want = both(monkeypatch, f)
     close(got, want)
+
+
+class Cubes:
+    """Blocks of x^3 in place of a QuantizedBlocks."""
+
+    def _turn(self):
+        return contextlib.nullcontext()
+
+    def _run(self, i, x):
+        return x.pow(3)
+
+
+def test_second_gradient_of_quantised_blocks_is_refused():
+    # x goes round the block too, as in a residual connection: a node that autograd
+    # prunes cannot refuse
+    x = torch.arange(1.0, 5.0).requires_grad_()
+
+    def f():
+        return (x * x).sum() + fw._QuantizedBlock.apply(x, Cubes(), 0).sum()
+
+    plain, = torch.autograd.grad(f(), x)
+    first, = torch.autograd.grad(f(), x, create_graph=True)
+    assert torch.equal(first, plain) and torch.equal(plain, (2 * x + 3 * x * x).detach())
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(first.sum(), x)
