@@ -18,7 +18,7 @@ stream.
 
 In autograd a gradient runs on the stream that was current in the forward call,
 after a forward call that was given another one.  linear_u4 can be differentiated
-again, a gradient of a loss's gradient is refused.  To capture a training step into a HIP graph,
+again, a gradient of a loss's gradient is refused, and so is forward mode.  To capture a training step into a HIP graph,
 make its leaves inside the capture (``x.detach().requires_grad_()``): a leaf that
 an eager graph still holds ties the captured backward to that graph's stream.
 """
@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import dfh
 
@@ -44,6 +45,15 @@ def _type(t: torch.Tensor, what: str, f32: bool = False) -> int:
 def _on(t: torch.Tensor, dev: torch.device, what: str):
     if not t.is_cuda or t.device != dev:
         raise ValueError("%s must be a tensor on %s" % (what, dev))
+
+
+def _no_tangent(*tensors):
+    """Refuses forward mode, whose tangents the kernels would drop (they are there
+    only inside a dual level, and without gradients enabled too)."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("no forward-mode derivative is offered")
 
 
 _MAX_STRIDE = 1 << 21   # the kernels' largest row stride
@@ -135,6 +145,7 @@ class U4Matrix:
                 raise ValueError("zeros must be uint8 of the scales' shape")
         if scales.requires_grad:
             raise ValueError("no gradient goes to the scales: detach them")
+        _no_tangent(scales)
         if groups > 1 and scales.stride(1) != 1:
             scales = scales.contiguous()
         if zeros is not None and groups > 1 and zeros.stride(1) != 1:
@@ -247,6 +258,7 @@ class _LinearU4Grad(torch.autograd.Function):
 def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """dx[..., k] = sum over n of dy[..., n] W[n, k]: the gradient of linear_u4
     to its input, in dy's type (bfloat16 or float16).  Differentiable in dy."""
+    _no_tangent(dy)
     if dy.requires_grad and torch.is_grad_enabled():
         return _LinearU4Grad.apply(dy, w, stream)
     return _linear_grad(dy, w, stream)
@@ -260,6 +272,7 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     type.  Differentiable in x;
     the nibbles must stay as they are until the gradient has run (df_decompress
     into the same buffer is not seen by autograd)."""
+    _no_tangent(x)
     if x.requires_grad and torch.is_grad_enabled():
         return _LinearU4.apply(x, w, stream)
     return _linear(x, w, stream)
@@ -394,6 +407,7 @@ class _LossFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gout):
+        _no_tangent(gout)
         call, saved, want = ctx.call, ctx.saved_tensors[-1], ctx.needs_input_grad[:2]
         if torch.is_grad_enabled():   # under create_graph
             dx, dh = _LossGrad.apply(gout, *call.inputs[:2], call, saved, want)
@@ -417,6 +431,7 @@ class _LossGrad(torch.autograd.Function):
 
 def _run_loss(call, stream):
     x, head = call.inputs[0], call.inputs[1]
+    _no_tangent(x, head)
     if torch.is_grad_enabled() and (x.requires_grad or head.requires_grad):
         return _LossFunction.apply(x, head, call, stream)
     return call.forward(stream)[0]

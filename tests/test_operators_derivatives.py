@@ -4,6 +4,7 @@ GPU is needed.  In every second derivative x is reached by another path too, as 
 residual connection does: a node that autograd prunes cannot refuse."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from lossless_entropy_coded_huffman_amd import ops
 
@@ -93,3 +94,31 @@ def test_second_gradients_of_losses_are_refused(leaf):
     assert float((first - want).abs().max()) <= 2.0 ** -44 * float(want.abs().max())
     with pytest.raises(RuntimeError):
         torch.autograd.grad(first.sum(), t)
+
+
+def test_forward_mode_is_refused(dense):
+    # a tangent that no operator would carry on is not dropped
+    x, dy, t = (torch.ones(3, n, dtype=torch.float64) for n in (5, 7, 5))
+    head = torch.ones(7, 5, dtype=torch.float64)
+    calls = [(lambda a: ops.linear_u4(a, dense), x, t), (lambda a: ops.linear_u4_grad(a, dense), dy, torch.ones_like(dy)),
+             (lambda a: ops._run_loss(Squares(a, head), None), x, t),
+             (lambda a: ops._run_loss(Squares(x, a), None), head, torch.ones_like(head))]
+    for f, primal, tangent in calls:
+        with forward_ad.dual_level():
+            dual = forward_ad.make_dual(primal, tangent)
+            for a in (dual, dual.detach().requires_grad_() * 1 + dual * 0):
+                with pytest.raises(NotImplementedError):
+                    f(a)
+            f(primal)   # no tangent: as ever
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                f(dual)
+        with pytest.raises(NotImplementedError):
+            torch.func.jvp(f, (primal,), (tangent,))
+    # forward over reverse, where only the gradient that comes in has a tangent
+    for f in (lambda a: ops.linear_u4(a, dense), lambda a: ops._run_loss(Squares(a, head), None)):
+        a = x.clone().requires_grad_()
+        y = f(a)
+        with forward_ad.dual_level():
+            dual = forward_ad.make_dual(torch.ones_like(y).detach(), torch.ones_like(y).detach())
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(y, a, dual)
