@@ -163,8 +163,8 @@ class U4Matrix:
 
 
 def _linear_on(x: torch.Tensor, w: U4Matrix, ty: int, handle: int) -> torch.Tensor:
-    """y for x [m, cols] on a stream."""
-    x = _rows16(x)
+    """y [m, rows] for x [..., cols] on a stream, which a copy of x is made on too."""
+    x = _rows16(x if x.dim() == 2 else x.reshape(-1, w.cols))
     m = x.shape[0]
     y = x.new_empty((m, w.rows))
     L = dfh.lib()
@@ -185,11 +185,10 @@ def _linear(x: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
     ty = _type(x, "x")
     if not shape or shape[-1] != w.cols:
         raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(shape)))
-    x2 = x if len(shape) == 2 else x.reshape(-1, w.cols)
     if stream is None and _current_device() == dev.index:
-        y = _linear_on(x2, w, ty, _raw_stream(dev.index))
+        y = _linear_on(x, w, ty, _raw_stream(dev.index))
     else:
-        y = _launch(stream, dev, (x,) + w._tensors(), lambda handle: _linear_on(x2, w, ty, handle))
+        y = _launch(stream, dev, (x,) + w._tensors(), lambda handle: _linear_on(x, w, ty, handle))
     return y if len(shape) == 2 else y.view(shape[:-1] + (w.rows,))
 
 

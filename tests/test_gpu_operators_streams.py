@@ -36,3 +36,27 @@ def test_gradient_of_a_loss_on_another_stream(torch, reduction):
             torch.full((m * h,), 7.0, dtype=torch.bfloat16, device="cuda")
             torch.full((4 * m,), 7.0, device="cuda")
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("m", [3, 40, 700])
+def test_product_of_a_transposed_batch_on_another_stream(torch, m):
+    # x is ready on s and no view of rows, and the current stream is busy: the copy
+    # that the call makes belongs to s
+    g = torch.Generator().manual_seed(m)
+    n, k = 96, 128
+    packed = torch.randint(0, 256, (n * k // 2,), generator=g, dtype=torch.uint8).cuda()
+    w = dfh.U4Matrix(packed, (torch.rand(n, 4, generator=g) + 0.5).cuda(), None, cols=k, group_size=32)
+    x = torch.randn(2, m, k, generator=g).to(torch.bfloat16).cuda()
+    dy = torch.randn(2, m, n, generator=g).to(torch.bfloat16).cuda()
+    want = dfh.linear_u4(x.transpose(0, 1).contiguous(), w), dfh.linear_u4_grad(dy.transpose(0, 1).contiguous(), w)
+    bx, bdy = torch.zeros_like(x), torch.zeros_like(dy)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)
+    with torch.cuda.stream(s):
+        bx.copy_(x)
+        bdy.copy_(dy)
+    got = dfh.linear_u4(bx.transpose(0, 1), w, stream=s), dfh.linear_u4_grad(bdy.transpose(0, 1), w, stream=s)
+    s.synchronize()
+    torch.cuda.current_stream().synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

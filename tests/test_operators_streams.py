@@ -1,0 +1,58 @@
+"""Where a call that is given a stream does its work: everything that it enqueues
+lies inside the launch on that stream.  Plain stand-ins for the kernels, no GPU
+needed."""
+import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
+
+from lossless_entropy_coded_huffman_amd import ops
+
+
+class Launches(TorchDispatchMode):
+    """Notes the copies made outside a launch."""
+
+    def __init__(self):
+        super().__init__()
+        self.inside, self.early = False, []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        if not self.inside and func in (torch.ops.aten.clone.default, torch.ops.aten.copy_.default):
+            self.early.append(func)
+        return func(*args, **(kwargs or {}))
+
+
+class Dense:
+    def __init__(self, weight):
+        self.weight, self.device = weight, weight.device
+        self.rows, self.cols = weight.shape
+
+    def _tensors(self):
+        return (self.weight, None)
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    mode = Launches()
+
+    def launch(stream, dev, tensors, call):
+        mode.inside = True
+        try:
+            return call(0)
+        finally:
+            mode.inside = False
+
+    monkeypatch.setattr(ops, "_launch", launch)
+    return mode
+
+
+@pytest.mark.parametrize("shape", [(3, 4, 16), (2, 3, 5, 16)])
+def test_linear_u4_lays_x_out_on_its_stream(launches, monkeypatch, shape):
+    # leading dimensions that are no view of rows: reshape copies
+    w = Dense(torch.randn(8, 16, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16))
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).transpose(0, -2)
+    monkeypatch.setattr(ops, "_linear_on", lambda x, w, ty, handle: x @ w.weight.t())
+    want = x.reshape(-1, 16) @ w.weight.t()
+    with launches:
+        y = ops._linear(x, w, object())
+    assert not launches.early
+    assert y.shape == x.shape[:-1] + (8,) and torch.equal(y.reshape(-1, 8), want)
