@@ -52,7 +52,7 @@ def test_product_of_a_transposed_batch_on_another_stream(torch, m):
     bx, bdy = torch.zeros_like(x), torch.zeros_like(dy)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    torch.cuda._sleep(100_000_000)
+    torch.cuda._sleep(20_000_000)
     with torch.cuda.stream(s):
         bx.copy_(x)
         bdy.copy_(dy)
