@@ -298,18 +298,21 @@ class CompressedHead:
         self.head = dfh.to_device(container, self.device)
         self.scratch = torch.empty((vocab, hidden), dtype=torch.bfloat16, device=self.device)
 
-    def weight(self) -> torch.Tensor:
-        """The decoded head (on the current stream; the same bits every time)."""
-        dfh.df_decompress(self.head, self.scratch, torch.cuda.current_stream(self.device))
+    def weight(self, stream=None) -> torch.Tensor:
+        """The decoded head, on a stream (default: the current one; the same bits
+        every time)."""
+        with torch.cuda.device_of(self.scratch):
+            dfh.df_decompress(self.head, self.scratch, stream)
         return self.scratch
 
-    def loss(self, x: torch.Tensor, labels: torch.Tensor, **kw) -> torch.Tensor:
-        """Cross entropy of hidden states x against labels (vocab_loss)."""
-        return vocab_loss(x, self.weight(), labels, **kw)
+    def loss(self, x: torch.Tensor, labels: torch.Tensor, *, stream=None, **kw) -> torch.Tensor:
+        """Cross entropy of hidden states x against labels (vocab_loss); the head is
+        decoded on the loss's stream."""
+        return vocab_loss(x, self.weight(stream), labels, stream=stream, **kw)
 
-    def distill(self, x: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor, **kw) -> torch.Tensor:
-        """Divergence from a teacher's top logits (distill_loss)."""
-        return distill_loss(x, self.weight(), teacher, index, **kw)
+    def distill(self, x: torch.Tensor, teacher: torch.Tensor, index: torch.Tensor, *, stream=None, **kw) -> torch.Tensor:
+        """Divergence from a teacher's top logits (distill_loss), likewise."""
+        return distill_loss(x, self.weight(stream), teacher, index, stream=stream, **kw)
 
 
 def resident_forward(x: torch.Tensor, weights, shape: BlockShape) -> torch.Tensor:

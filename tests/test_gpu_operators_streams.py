@@ -1,8 +1,11 @@
 """The gradient of a loss whose forward call was given a stream: the one that a call
 on the current stream gives."""
+import numpy as np
 import pytest
 
 import lossless_entropy_coded_huffman_amd as dfh
+from lossless_entropy_coded_huffman_amd import forward as fw
+from lossless_entropy_coded_huffman_amd import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +63,33 @@ def test_product_of_a_transposed_batch_on_another_stream(torch, m):
     s.synchronize()
     torch.cuda.current_stream().synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("call", ["loss", "distill"])
+def test_first_use_of_a_compressed_head_on_a_given_stream(torch, call):
+    # the current stream is busy when a fresh head is used on s, and its gradient
+    # follows without a wait of the caller's
+    g = torch.Generator().manual_seed(5)
+    m, v, h = 40, 3001, 256
+    bits = synth.bf16_rne(np.random.default_rng(1).normal(0, 0.15, v * h).astype(np.float32))
+    con = dfh.compress(dfh.KIND_BF16, bits)
+    x = torch.randn(m, h, generator=g).to(torch.bfloat16).cuda()
+    if call == "loss":
+        args = (torch.randint(0, v, (m,), generator=g).cuda(),)
+    else:
+        args = tuple(t.cuda() for t in torch.randn(m, v, generator=g).topk(8, dim=1))
+
+    def step(stream):
+        head = fw.CompressedHead(con, v, h, torch.device("cuda:0"))
+        head.scratch.fill_(float("nan"))
+        leaf = x.clone().requires_grad_()
+        torch.cuda.synchronize()
+        if stream is not None:
+            torch.cuda._sleep(20_000_000)
+        loss = getattr(head, call)(leaf, *args, stream=stream)
+        grad, = torch.autograd.grad(loss, leaf)
+        torch.cuda.synchronize()
+        return loss.detach(), grad
+
+    want, got = step(None), step(torch.cuda.Stream())
+    assert torch.isfinite(want[0]) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -5,7 +5,8 @@ import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
-from lossless_entropy_coded_huffman_amd import ops
+from lossless_entropy_coded_huffman_amd import dfh, ops
+from lossless_entropy_coded_huffman_amd import forward as fw
 
 
 class Launches(TorchDispatchMode):
@@ -56,3 +57,21 @@ def test_linear_u4_lays_x_out_on_its_stream(launches, monkeypatch, shape):
         y = ops._linear(x, w, object())
     assert not launches.early
     assert y.shape == x.shape[:-1] + (8,) and torch.equal(y.reshape(-1, 8), want)
+
+
+@pytest.mark.parametrize("call", ["loss", "distill"])
+def test_compressed_head_decodes_on_the_losses_stream(monkeypatch, call):
+    where = []
+    monkeypatch.setattr(dfh, "df_decompress", lambda dc, dst, stream=None: where.append(("decode", stream)))
+    for fn in ("vocab_loss", "distill_loss"):
+        monkeypatch.setattr(fw, fn, lambda *a, stream=None, **kw: where.append(("loss", stream)))
+    head = fw.CompressedHead.__new__(fw.CompressedHead)
+    head.device, head.head, head.scratch = torch.device("cpu"), None, torch.zeros(4, 8)
+    args = (None,) * (2 if call == "loss" else 3)
+    getattr(head, call)(*args, stream=77, reduction="sum")
+    assert where == [("decode", 77), ("loss", 77)]
+    # and without one, both on the one that is current
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    del where[:]
+    getattr(head, call)(*args)
+    assert where == [("decode", None), ("loss", None)]
