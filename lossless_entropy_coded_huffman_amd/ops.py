@@ -222,22 +222,33 @@ def _linear_grad(dy: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
     return dx if dy.dim() == 2 else dx.view(dy.shape[:-1] + (w.cols,))
 
 
-def _keep_weights(ctx, w: U4Matrix):
-    """The derivative reads them again: a change that torch sees in between is refused."""
-    ctx.w = w
+def _keep_weights(ctx, w: U4Matrix, stream):
+    """For a derivative, which reads the weights again: a change that torch sees in
+    between is refused, and a call that was given a stream is waited for."""
+    ctx.w, ctx.done = w, None
     ctx.save_for_backward(*[t for t in w._tensors() if t is not None])
+    if stream is not None:
+        ctx.done = torch.cuda.Event()
+        ctx.done.record(dfh._torch_stream(stream, w.device))
+
+
+def _kept_weights(ctx) -> U4Matrix:
+    ctx.saved_tensors
+    if ctx.done is not None:
+        torch.cuda.current_stream(ctx.w.device).wait_event(ctx.done)
+    return ctx.w
 
 
 class _LinearU4(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stream):
-        _keep_weights(ctx, w)
-        return _linear(x, w, stream)
+        y = _linear(x, w, stream)
+        _keep_weights(ctx, w, stream)
+        return y
 
     @staticmethod
     def backward(ctx, dy):
-        ctx.saved_tensors
-        return linear_u4_grad(dy, ctx.w), None, None
+        return linear_u4_grad(dy, _kept_weights(ctx)), None, None
 
 
 class _LinearU4Grad(torch.autograd.Function):
@@ -245,13 +256,13 @@ class _LinearU4Grad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, dy, w, stream):
-        _keep_weights(ctx, w)
-        return _linear_grad(dy, w, stream)
+        dx = _linear_grad(dy, w, stream)
+        _keep_weights(ctx, w, stream)
+        return dx
 
     @staticmethod
     def backward(ctx, ddx):
-        ctx.saved_tensors
-        return linear_u4(ddx, ctx.w), None, None
+        return linear_u4(ddx, _kept_weights(ctx)), None, None
 
 
 def linear_u4_grad(dy: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:

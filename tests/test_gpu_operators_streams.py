@@ -93,3 +93,26 @@ def test_first_use_of_a_compressed_head_on_a_given_stream(torch, call):
 
     want, got = step(None), step(torch.cuda.Stream())
     assert torch.isfinite(want[0]) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("m", [3, 300])
+def test_gradient_of_a_product_on_another_stream(torch, m):
+    # the weights come late on s; the gradient on the current stream is ordered behind
+    # the call on s, which read them
+    g = torch.Generator().manual_seed(m)
+    n, k = 96, 128
+    packed = torch.randint(0, 256, (n * k // 2,), generator=g, dtype=torch.uint8).cuda()
+    late = torch.zeros_like(packed)
+    w = dfh.U4Matrix(late, (torch.rand(n, 4, generator=g) + 0.5).cuda(), None, cols=k, group_size=32)
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16).cuda().requires_grad_()
+    dy = torch.randn(m, n, generator=g).to(torch.bfloat16).cuda()
+    want = dfh.linear_u4_grad(dy, dfh.U4Matrix(packed, w.scales, None, cols=k, group_size=32))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(packed)
+    y = dfh.linear_u4(x, w, stream=s)
+    got, = torch.autograd.grad(y, x, dy)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

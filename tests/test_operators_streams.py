@@ -75,3 +75,28 @@ def test_compressed_head_decodes_on_the_losses_stream(monkeypatch, call):
     del where[:]
     getattr(head, call)(*args)
     assert where == [("decode", None), ("loss", None)]
+
+
+def test_gradient_of_a_product_waits_for_the_stream_of_its_forward_call(monkeypatch):
+    log = []
+
+    class Event:
+        def record(self, stream):
+            log.append(("record", stream))
+
+    class Current:
+        def wait_event(self, event):
+            log.append("wait")
+
+    w = Dense(torch.ones(8, 16))
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Current())
+    monkeypatch.setattr(dfh, "_torch_stream", lambda stream, device: stream)
+    monkeypatch.setattr(ops, "_linear", lambda x, w, stream: log.append(("product", stream)) or x @ w.weight.t())
+    monkeypatch.setattr(ops, "_linear_grad", lambda dy, w, stream: log.append(("gradient", stream)) or dy @ w.weight)
+    x = torch.ones(3, 16, requires_grad=True)
+    ops.linear_u4(x, w, stream=5).sum().backward()
+    assert log == [("product", 5), ("record", 5), "wait", ("gradient", None)]
+    del log[:]
+    ops.linear_u4(x, w).sum().backward()
+    assert log == [("product", None), ("gradient", None)]
