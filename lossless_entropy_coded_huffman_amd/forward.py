@@ -191,6 +191,32 @@ class CompressedBlocks:
         return x
 
 
+class _Made:
+    """Device tensors that an object made on the stream then current, and uses on
+    others: the first use on another stream waits until they are there, and keeps
+    their memory until that stream has passed.  A captured use does neither; its
+    capture and replays are ordered by the caller."""
+
+    def __init__(self, device, tensors):
+        self.device, self.tensors = device, tensors
+        stream = torch.cuda.current_stream(device)
+        self.seen = {stream.cuda_stream}
+        self.event = torch.cuda.Event()
+        self.event.record(stream)
+
+    def use(self, stream=None):
+        ts = dfh._torch_stream(stream, self.device)
+        if ts.cuda_stream in self.seen:
+            return
+        with torch.cuda.stream(ts):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        ts.wait_event(self.event)
+        for t in self.tensors:
+            t.record_stream(ts)
+        self.seen.add(ts.cuda_stream)
+
+
 class QuantizedBlocks:
     """Blocks held as uint4 containers with group scales, decoded to packed
     nibbles right before they run.
@@ -223,6 +249,9 @@ class QuantizedBlocks:
                 ws[name] = U4Matrix(packed, s, z, cols=c, group_size=group_size)
             self.blocks.append(dcs)
             self.weights.append(ws)
+        self._made = _Made(self.device, self.scratch
+                           + [t for dcs in self.blocks for dc in dcs for t in dc.sections.values()]
+                           + [t for ws in self.weights for w in ws.values() for t in w._tensors()[1:] if t is not None])
         self._lock = threading.RLock()
         self._stream, self._used = None, torch.cuda.Event()  # the last turn's stream, and its end
 
@@ -232,6 +261,7 @@ class QuantizedBlocks:
         with self._lock, torch.cuda.device(self.device):
             stream = torch.cuda.current_stream(self.device)
             capturing = torch.cuda.is_current_stream_capturing()
+            self._made.use(stream)
             if not capturing and self._stream is not None and self._stream != stream:
                 stream.wait_event(self._used)
             try:
@@ -297,11 +327,13 @@ class CompressedHead:
         self.device = torch.device(device)
         self.head = dfh.to_device(container, self.device)
         self.scratch = torch.empty((vocab, hidden), dtype=torch.bfloat16, device=self.device)
+        self._made = _Made(self.device, [self.scratch, *self.head.sections.values()])
 
     def weight(self, stream=None) -> torch.Tensor:
         """The decoded head, on a stream (default: the current one; the same bits
         every time)."""
         with torch.cuda.device_of(self.scratch):
+            self._made.use(stream)
             dfh.df_decompress(self.head, self.scratch, stream)
         return self.scratch
 

@@ -104,3 +104,28 @@ def test_blocks_gradient_captured_and_replayed(torch, blocks):
         got = out.clone()
         assert torch.equal(got, step())
         torch.cuda.synchronize()
+
+
+def test_first_use_on_a_stream_other_than_the_one_that_made_them(torch, monkeypatch):
+    # the scales are tensors of the device, converted behind a busy spell of the
+    # stream that makes the blocks; the first call, on another stream, waits for them
+    host = fw.random_blocks(1, SHAPE, 5)
+    layers = [[(con, torch.from_numpy(s).cuda(), torch.from_numpy(z).cuda()) for con, s, z in
+               fw.quantize_block(h, SHAPE, GROUP)] for h in host]
+    x = acts(torch, 5, 1)
+    want = fw.QuantizedBlocks(layers, SHAPE, torch.device("cuda:0"), GROUP).forward(x)
+    upload = fw.dfh.to_device
+
+    def late(con, device):
+        out = upload(con, device)   # returns when the copy is done
+        torch.cuda._sleep(5_000_000)
+        return out
+
+    monkeypatch.setattr(fw.dfh, "to_device", late)
+    torch.cuda.synchronize()
+    made = fw.QuantizedBlocks(layers, SHAPE, torch.device("cuda:0"), GROUP)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = made.forward(x)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

@@ -1,6 +1,8 @@
 """Where a call that is given a stream does its work: everything that it enqueues
 lies inside the launch on that stream.  Plain stand-ins for the kernels, no GPU
 needed."""
+import contextlib
+
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
@@ -59,6 +61,11 @@ def test_linear_u4_lays_x_out_on_its_stream(launches, monkeypatch, shape):
     assert y.shape == x.shape[:-1] + (8,) and torch.equal(y.reshape(-1, 8), want)
 
 
+class Made:
+    def use(self, stream=None):
+        pass
+
+
 @pytest.mark.parametrize("call", ["loss", "distill"])
 def test_compressed_head_decodes_on_the_losses_stream(monkeypatch, call):
     where = []
@@ -67,6 +74,7 @@ def test_compressed_head_decodes_on_the_losses_stream(monkeypatch, call):
         monkeypatch.setattr(fw, fn, lambda *a, stream=None, **kw: where.append(("loss", stream)))
     head = fw.CompressedHead.__new__(fw.CompressedHead)
     head.device, head.head, head.scratch = torch.device("cpu"), None, torch.zeros(4, 8)
+    head._made = Made()
     args = (None,) * (2 if call == "loss" else 3)
     getattr(head, call)(*args, stream=77, reduction="sum")
     assert where == [("decode", 77), ("loss", 77)]
@@ -100,3 +108,39 @@ def test_gradient_of_a_product_waits_for_the_stream_of_its_forward_call(monkeypa
     del log[:]
     ops.linear_u4(x, w).sum().backward()
     assert log == [("product", None), ("gradient", None)]
+
+
+def test_what_an_object_made_is_waited_for_once_on_each_other_stream(monkeypatch):
+    log, capturing = [], [False]
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+        def wait_event(self, event):
+            log.append(("wait", self.cuda_stream))
+
+    class Event:
+        def record(self, stream):
+            log.append(("made", stream.cuda_stream))
+
+    class Tensor:
+        def record_stream(self, stream):
+            log.append(("keep", stream.cuda_stream))
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(1))
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(dfh, "_torch_stream", lambda stream, device: Stream(1) if stream is None else Stream(stream))
+    made = fw._Made("cuda", [Tensor(), Tensor()])
+    assert log == [("made", 1)]
+    made.use()
+    capturing[0] = True
+    made.use(2)
+    assert log == [("made", 1)]
+    capturing[0] = False
+    made.use(2)
+    made.use(2)
+    made.use(3)
+    assert log == [("made", 1)] + [(what, s) for s in (2, 3) for what in ("wait", "keep", "keep")]
