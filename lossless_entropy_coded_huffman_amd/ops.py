@@ -290,7 +290,7 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
 
 # ---------------------------------------------------------------------- losses
 class _Loss:
-    """A call's df_loss and the tensors it points to."""
+    """A call's df_loss and, until autograd has them, the tensors it points to."""
 
     def __init__(self, x, head, reduction, labels=None, ignore_index=-100, teacher=None, index=None, temperature=1.0):
         if reduction not in _REDUCE:
@@ -334,10 +334,10 @@ class _Loss:
         self.desc, self.dev = d, dev
         self.done = None   # an event behind the forward call, where that ran on another stream
 
-    def bind(self):
-        """Lays the inputs out and points the descriptor at them (on the call's stream)."""
-        x, head, labels, teacher, index = self.inputs
-        d = self.desc
+    @staticmethod
+    def bind(d, x, head, labels, teacher, index):
+        """Lays the inputs out and points the descriptor d at them (on the call's
+        stream).  Returns them as they lie, in the same order."""
         x = _rows16(x.detach().reshape(-1, d.hidden))
         head = _rows16(head.detach())
         d.rows = x.shape[0]
@@ -353,7 +353,7 @@ class _Loss:
                 index = index.contiguous()
             d.teacher, d.teacher_stride = teacher.data_ptr(), teacher.stride(0)
             d.index, d.index_stride = index.data_ptr(), index.stride(0)
-        self.held = (x, head, labels, teacher, index)
+        return x, head, labels, teacher, index
 
     def forward(self, stream):
         L, dev = dfh.lib(), self.dev
@@ -361,7 +361,10 @@ class _Loss:
         current = _raw_stream(dev.index)
 
         def call(handle):
-            self.bind()
+            laid = self.bind(self.desc, *self.inputs)
+            # what was copied goes on to the gradient beside the inputs
+            self.copies = tuple(c if c is not None and c.data_ptr() != t.data_ptr() else None
+                                for t, c in zip(self.inputs, laid))
             ref = ctypes.byref(self.desc)
             loss = torch.empty(int(self.desc.rows) if none else 1, dtype=torch.float32, device=dev)
             saved = torch.empty(max(L.df_loss_saved_bytes(ref) // 4, 1), dtype=torch.float32, device=dev)
@@ -378,27 +381,30 @@ class _Loss:
         loss, saved = _launch(stream, dev, self.inputs, call)
         return loss.view(self.shape if none else ()), saved
 
-    def grads(self, saved, gout, want_x, want_head):
+    def grads(self, inputs, copies, saved, gout, want_x, want_head):
         L, dev = dfh.lib(), self.dev
-        x, head = self.inputs[0], self.inputs[1]
+        x, head = inputs[:2]
+        desc = dfh.df_loss.from_buffer_copy(self.desc)
 
         def call(handle):
             if self.done is not None:
                 # what the forward call keeps is written, and was allocated, on its stream
                 here = torch.cuda.current_stream(dev)
                 here.wait_event(self.done)
-                for t in self.held + (saved,):
+                for t in (*inputs, *copies, saved):
                     if t is not None:
                         t.record_stream(here)
-            ref = ctypes.byref(self.desc)
+            laid = self.bind(desc, *(t if c is None else c for t, c in zip(inputs, copies)))
+            ref = ctypes.byref(desc)
             g = gout.to(torch.float32).reshape(-1).contiguous()
-            dx = torch.empty((int(self.desc.rows), head.shape[1]), dtype=x.dtype, device=dev) if want_x else None
+            dx = torch.empty((int(desc.rows), head.shape[1]), dtype=x.dtype, device=dev) if want_x else None
             dh = torch.empty(head.shape, dtype=head.dtype, device=dev) if want_head else None
             need = L.df_loss_grad_workspace_bytes(ref, int(want_head))
             ws = _workspace(need, dev)
             st = L.df_vocab_loss_grad(ref, saved.data_ptr(), g.data_ptr(), _p(dx), _p(dh), ws.data_ptr(), need, handle)
             if st:
                 dfh._check(st, "df_vocab_loss_grad")
+            del laid   # enqueued: the copies' memory follows in the stream's order
             return dx, dh
 
         dx, dh = _launch(None, dev, (), call)
@@ -409,20 +415,22 @@ class _LossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, head, call, stream):
         loss, saved = call.forward(stream)
-        # the tensors that the gradient reads again: saved through autograd, so
-        # that a change made to one in between is refused
-        ctx.save_for_backward(*[t for t in call.inputs if t is not None], saved)
+        # the tensors that the gradient reads again: kept by autograd alone, so that
+        # a change made to one in between is refused and saved-tensor hooks see all
+        ctx.save_for_backward(*call.inputs, *call.copies, saved)
+        call.inputs = call.copies = None
         ctx.call = call
         return loss
 
     @staticmethod
     def backward(ctx, gout):
         _no_tangent(gout)
-        call, saved, want = ctx.call, ctx.saved_tensors[-1], ctx.needs_input_grad[:2]
+        call, (*kept, saved), want = ctx.call, ctx.saved_tensors, ctx.needs_input_grad[:2]
+        inputs, copies = kept[:5], kept[5:]
         if torch.is_grad_enabled():   # under create_graph
-            dx, dh = _LossGrad.apply(gout, *call.inputs[:2], call, saved, want)
+            dx, dh = _LossGrad.apply(gout, *inputs[:2], call, (inputs, copies, saved), want)
         else:
-            dx, dh = call.grads(saved, gout, *want)
+            dx, dh = call.grads(inputs, copies, saved, gout, *want)
         return dx, dh, None, None
 
 
@@ -431,8 +439,8 @@ class _LossGrad(torch.autograd.Function):
     refused on whatever path it comes."""
 
     @staticmethod
-    def forward(ctx, gout, x, head, call, saved, want):
-        return call.grads(saved, gout, *want)
+    def forward(ctx, gout, x, head, call, kept, want):
+        return call.grads(*kept, gout, *want)
 
     @staticmethod
     def backward(ctx, *_):

@@ -2,6 +2,9 @@
 forward mode: the autograd functions over plain stand-ins for the kernels, so no
 GPU is needed.  In every second derivative x is reached by another path too, as a
 residual connection does: a node that autograd prunes cannot refuse."""
+import gc
+import weakref
+
 import pytest
 import torch
 from torch.autograd import forward_ad
@@ -66,14 +69,14 @@ class Squares:
     place of a _Loss."""
 
     def __init__(self, x, head):
-        self.inputs = (x, head, None, None, None)
+        self.inputs, self.copies = (x, head, None, None, None), (None,) * 5
 
     def forward(self, stream):
         x, head = self.inputs[:2]
         return (x @ head.t()).pow(2).sum(), torch.zeros(1)
 
-    def grads(self, saved, gout, want_x, want_head):
-        x, head = (t.detach() for t in self.inputs[:2])
+    def grads(self, inputs, copies, saved, gout, want_x, want_head):
+        x, head = (t.detach() for t in inputs[:2])
         z = 2 * gout * (x @ head.t())
         return z @ head if want_x else None, z.t() @ x if want_head else None
 
@@ -122,3 +125,19 @@ def test_forward_mode_is_refused(dense):
             dual = forward_ad.make_dual(torch.ones_like(y).detach(), torch.ones_like(y).detach())
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(y, a, dual)
+
+
+def test_a_loss_leaves_its_inputs_to_autograd():
+    # with hooks that put what is saved elsewhere, nothing else holds the inputs
+    g = torch.Generator().manual_seed(4)
+    base, head = (torch.randn(s, 5, generator=g, dtype=torch.float64) for s in (3, 7))
+    leaf = base.clone().requires_grad_()
+    x = leaf * 2
+    ref = weakref.ref(x)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.numpy(force=True).copy(), torch.from_numpy):
+        loss = ops._run_loss(Squares(x, head), None)
+    del x
+    gc.collect()
+    assert ref() is None
+    got, = torch.autograd.grad(loss, leaf)
+    assert torch.equal(got, 2 * ((2 * (2 * base @ head.t())) @ head))
