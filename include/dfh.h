@@ -372,7 +372,8 @@ typedef struct {
  * at most 2^21); y: rows x w->rows of the same type, contiguous.  Both 16-byte
  * aligned.  Few rows (up to 192; 384 where W has at most 2^24 elements, 512 at most
  * 2^22) multiply the integers exactly (a group's FP32 sum is scaled); more expand W to `type` in the workspace (256-byte aligned),
- * each weight rounded once.  Sums are FP32.  Up to 4 rows need no workspace.
+ * each weight rounded once: to 2^-8 (BF16) or 2^-11 (FP16) of itself, in FP16 to 2^-31 of its row's largest scale
+ * where that is more (a power of two a row keeps any scales within range).  Sums are FP32.  Up to 4 rows need no workspace.
  * DF_ERR_ARG on a bad pointer, size, alignment or too small a workspace. */
 uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows);
 df_status df_linear_u4(const df_u4_matrix *w, df_type type, const void *x, uint64_t rows, uint64_t x_stride, void *y,
@@ -381,7 +382,8 @@ df_status df_linear_u4(const df_u4_matrix *w, df_type type, const void *x, uint6
 /* The gradient to x: dx[m, k] = sum over n of dy[m, n] W[n, k], dy with rows
  * dy_stride elements apart (w->rows a multiple of 8: dy 16-byte aligned and
  * dy_stride a multiple of 8; any stride otherwise), dx contiguous and 16-byte
- * aligned.  Always needs its workspace. */
+ * aligned.  W is expanded as above, in FP16 with the matrix's largest scale in
+ * place of the row's.  Always needs its workspace. */
 uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows);
 df_status df_linear_u4_grad(const df_u4_matrix *w, df_type type, const void *dy, uint64_t rows, uint64_t dy_stride,
                             void *dx, void *workspace, uint64_t workspace_bytes, hipStream_t stream);

@@ -320,12 +320,15 @@ __device__ __forceinline__ void store8(uint16_t *p, uint32_t col, uint32_t n, bo
   }
 }
 
-// 16-bit output (base 16-byte aligned), times *scale (null: 1) * *scale2 * mul.
+// 16-bit output (base 16-byte aligned), times *scale (null: 1) * *scale2 * mul,
+// and column n times columns[n] where COLUMNS.
+template <bool COLUMNS = false>
 struct EpiStore {
   uint16_t *c;
   uint64_t ldc;
   const float *scale, *scale2;
   float mul;
+  const float *columns;
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t) const {
@@ -333,12 +336,26 @@ struct EpiStore {
     const float s = (scale ? *scale * *scale2 : 1.f) * mul;
     const bool aligned = (ldc & 7) == 0;
     const uint32_t kg = (threadIdx.x >> 4) & 3, first = nb - 4 * kg + (kg & 1) * 16 + (kg >> 1) * 8;
+    f32x4 f[NT];
+    if constexpr (COLUMNS) {
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) f[j][e] = nb + j * 16 + e < n ? columns[nb + j * 16 + e] * s : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < MT; i++) {
       const uint32_t row = mb + i * 16;
 #pragma unroll
       for (int j = 0; j < NT; j += 2) {
-        const f32x4 v = acc[j][i] * s, w = acc[j + 1][i] * s;
+        f32x4 v, w;
+        if constexpr (COLUMNS) {
+          v = acc[j][i] * f[j];
+          w = acc[j + 1][i] * f[j + 1];
+        } else {
+          v = acc[j][i] * s;
+          w = acc[j + 1][i] * s;
+        }
         const u32x4 o = pair_blocks(u32x2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])},
                                     u32x2{pack2(T{}, w[0], w[1]), pack2(T{}, w[2], w[3])});
         if (row < m) store8(c + (uint64_t)row * ldc, first + j * 16, n, aligned, o);

@@ -533,12 +533,57 @@ __global__ __launch_bounds__(256) void join_tiles(const U4 w, const uint16_t *x,
   }
 }
 
+// FP16 keeps neither small nor large weights, so its copies are lifted: a power
+// of two per row (for the gradient, which sums over the rows, one for the matrix)
+// brings the largest scale to 2^6 .. 2^7, with any q - z within FP16, and comes off
+// the FP32 sums.  A weight then keeps FP16's 11 bits, or 2^-31 of the largest scale
+// where that is more.  BF16 has FP32's range and needs none.
+struct Lift {
+  const float *peaks;  // gradient: the matrix's largest scale in 256 parts
+  float *back;         // what comes off: one a row; gradient: one, and a 1
+};
+template <class S>
+__device__ __forceinline__ float size_at(const U4 &w, const S *p) {
+  const float v = __builtin_fabsf(scale_of(w, *p));
+  return v < __builtin_huge_valf() ? v : 0.f;  // where not finite, all results are as they are
+}
+__device__ __forceinline__ float most_of_256(float v) {
+  __shared__ float top[4];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
+  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return __builtin_fmaxf(__builtin_fmaxf(top[0], top[1]), __builtin_fmaxf(top[2], top[3]));
+}
+__device__ __forceinline__ int lift_bits(float peak) {
+  if (peak == 0.f) return 0;
+  const int f = 6 - ((int)(__float_as_uint(peak) >> 23) - 127);
+  return f < -112 ? -112 : f > 112 ? 112 : f;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The largest finite scale of the matrix in 256 parts.
+template <class S>
+__global__ __launch_bounds__(256) void scale_peaks(const U4 w, float *peaks) {
+  const uint64_t all = w.sstride ? (uint64_t)w.n * w.groups : w.groups;
+  float v = 0.f;
+#pragma unroll 4
+  for (uint64_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += 65536) {
+    uint64_t at = i;
+    if (w.sstride != w.groups) at = i / w.groups * w.sstride + i % w.groups;
+    v = __builtin_fmaxf(v, size_at(w, (const S *)w.scales + at));
+  }
+  v = most_of_256(v);
+  if (threadIdx.x == 0) peaks[blockIdx.x] = v;
+}
+
 // The weights as 16-bit floats, [n, k].  Each is rounded once from FP32
-// (relative 2^-8 / 2^-11 at most); the sums over them are FP32.
+// (relative 2^-8 / 2^-11 at most, but for what is said above); the sums over them
+// are FP32.
 // A workgroup takes 1024 chunks of 8 weights of a row, four a thread, all loaded
 // (scales unconverted) before the first is used.
 template <class T, class S>
-__global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out) {
+__global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out, const Lift lift) {
   const uint32_t n = blockIdx.x, chunks = w.k / 8, c0 = blockIdx.y * 1024 + threadIdx.x;
   const uint64_t row = (uint64_t)n * chunks;
   const S *ps = (const S *)w.scales + n * w.sstride;
@@ -554,11 +599,30 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out) {
     s[i] = ps[g];
     z[i] = pz[g * zon];
   }
+  float up = 1.f;
+  if constexpr (!Bias<T>::in_sum) {
+    float v = 0.f;
+    if (lift.peaks) {
+      v = lift.peaks[threadIdx.x];
+    } else {
+      for (uint32_t g = threadIdx.x; g < w.groups; g += 256) v = __builtin_fmaxf(v, size_at(w, ps + g));
+    }
+    const int bits = lift_bits(most_of_256(v));
+    up = power_of_two(bits);
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+      if (!lift.peaks) {
+        lift.back[n] = power_of_two(-bits);
+      } else if (n == 0) {
+        lift.back[0] = power_of_two(-bits);
+        lift.back[1] = 1.f;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const uint32_t c = c0 + i * 256;
     if (c >= chunks) break;
-    const float f = scale_of(w, s[i]), o = (float)z[i];
+    const float f = scale_of(w, s[i]) * up, o = (float)z[i];
     u32x4 v;
 #pragma unroll
     for (int d = 0; d < 4; d++)
@@ -566,22 +630,39 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out) {
     ((u32x4 *)out)[row + c] = v;
   }
 }
+// The copy and the lift's part of a workspace, in bytes.
+uint64_t copy_bytes(uint64_t n, uint64_t k) { return up(n * k * 2, 256); }
+uint64_t lift_bytes(uint64_t n, bool gradient) { return gradient ? 1280 : up(n * 4, 256); }
+// Expands into a workspace; what comes off the sums: back, null where nothing does.
 template <class T>
-void expand(const U4 &w, uint16_t *out, hipStream_t s) {
+const float *expand(const U4 &w, uint8_t *ws, bool gradient, hipStream_t s) {
+  Lift lift = {nullptr, nullptr};
+  if (!Bias<T>::in_sum) {
+    float *f = (float *)(ws + copy_bytes(w.n, w.k));
+    lift.back = f;
+    if (gradient) {
+      lift.peaks = f + 64;
+      hipLaunchKernelGGL((w.scale_type == DF_TYPE_F32 ? scale_peaks<float> : scale_peaks<uint16_t>), dim3(256), dim3(256),
+                         0, s, w, f + 64);
+    }
+  }
   auto *fn = w.scale_type == DF_TYPE_F32 ? u4_expand<T, float> : u4_expand<T, uint16_t>;
-  hipLaunchKernelGGL(fn, dim3(w.n, (w.k + 8191) / 8192), dim3(256), 0, s, w, out);
+  hipLaunchKernelGGL(fn, dim3(w.n, (w.k + 8191) / 8192), dim3(256), 0, s, w, (uint16_t *)ws, lift);
+  return lift.back;
 }
 
-// Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n].
+// Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n], times columns[n] and *all
+// (null: 1).
 template <class T>
 __global__ __launch_bounds__(256) void join_planes(const float *p, uint32_t splits, uint32_t m, uint32_t n,
-                                                   uint32_t ld, uint16_t *out) {
+                                                   uint32_t ld, const float *columns, const float *all, uint16_t *out) {
   const uint32_t row = blockIdx.x;
+  const float f = all ? *all : 1.f;
   for (uint32_t c = threadIdx.x * 4; c < n; c += 1024) {
     const f32x4 v = add_planes(p + (uint64_t)row * ld + c, (uint64_t)m * ld, splits);
 #pragma unroll
     for (int e = 0; e < 4; e++)
-      if (c + e < n) out[(uint64_t)row * n + c + e] = to_bits(T{}, v[e]);
+      if (c + e < n) out[(uint64_t)row * n + c + e] = to_bits(T{}, v[e] * (columns ? columns[c + e] : f));
   }
 }
 
@@ -626,15 +707,20 @@ df_status matrix_of(const df_u4_matrix *m, U4 *w) {
   return DF_OK;
 }
 
-// y or dx from 16-bit operands; planes: cut_for's splits.
-template <class T, bool KB>
-df_status many_rows(const Gemm &g, uint16_t *out, float *planes, hipStream_t s) {
+// y or dx from 16-bit operands, times back; planes: cut_for's splits.
+template <class T, bool GRAD>
+df_status many_rows(const Gemm &g, uint16_t *out, const float *back, float *planes, hipStream_t s) {
+  constexpr bool kColumns = !GRAD && !Bias<T>::in_sum;  // a factor for every column
   const Cut c = cut_for(g.m, g.n, g.k, true);
-  if (c.splits <= 1)
-    return product<T, false, KB>(g, EpiStore{out, g.n, nullptr, nullptr, 1.f}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
+  if (c.splits <= 1) {
+    const EpiStore<kColumns> e = {out,    g.n, GRAD ? back : nullptr, GRAD && back ? back + 1 : nullptr, 1.f,
+                                  kColumns ? back : nullptr};
+    return product<T, false, GRAD>(g, e, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
+  }
   const uint32_t ld = (uint32_t)up(g.n, 4);
-  if (product<T, false, KB>(g, EpiPlane{planes, ld, (uint64_t)g.m * ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
-  hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld, out);
+  if (product<T, false, GRAD>(g, EpiPlane{planes, ld, (uint64_t)g.m * ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
+  hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld,
+                     kColumns ? back : nullptr, GRAD ? back : nullptr, out);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
 
@@ -730,9 +816,9 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
         : p.mtile == 2 ? tile_launch<T, 2, 1>(w, x, xs, m, y, (float *)ws, p, s)
                        : tile_launch<T, 4, 1>(w, x, xs, m, y, (float *)ws, p, s);
   } else {
-    expand<T>(w, (uint16_t *)ws, s);
+    const float *back = expand<T>(w, ws, false, s);
     Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0};
-    return many_rows<T, false>(g, y, (float *)(ws + up((uint64_t)w.n * w.k * 2, 256)), s);
+    return many_rows<T, false>(g, y, back, (float *)(ws + copy_bytes(w.n, w.k) + lift_bytes(w.n, false)), s);
   }
   return e == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
@@ -740,8 +826,8 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
 template <class T>
 df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, uint16_t *dx, uint8_t *ws,
                       hipStream_t s) {
-  expand<T>(w, (uint16_t *)ws, s);
-  uint8_t *next = ws + up((uint64_t)w.n * w.k * 2, 256);
+  const float *back = expand<T>(w, ws, true, s);
+  uint8_t *next = ws + copy_bytes(w.n, w.k) + lift_bytes(w.n, true);
   const uint32_t np = (uint32_t)up(w.n, 8);
   if (np != w.n) {  // the summed index in whole 16-byte chunks
     hipLaunchKernelGGL(pad_rows, dim3(m), dim3(256), 0, s, dy, ds, w.n, np, (uint16_t *)next);
@@ -750,7 +836,7 @@ df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, 
     next += up((uint64_t)m * np * 2, 256);
   }
   Gemm g = {dy, (const uint16_t *)ws, ds, w.k, m, w.k, w.n, 0, 0, 0};
-  return many_rows<T, true>(g, dx, (float *)next, s);
+  return many_rows<T, true>(g, dx, back, (float *)next, s);
 }
 
 uint64_t plane_bytes(uint64_t m, uint64_t n, uint64_t k) {
@@ -769,14 +855,14 @@ uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
     const TilePlan p = few_plan((uint32_t)rows, u.n, u.k);
     return p.splits > 1 ? 4ull * p.splits * rows * p.ld : 0;
   }
-  return up(w->rows * w->cols * 2, 256) + plane_bytes(rows, w->rows, w->cols);
+  return copy_bytes(w->rows, w->cols) + lift_bytes(w->rows, false) + plane_bytes(rows, w->rows, w->cols);
 }
 
 uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows) {
   U4 u;
   if (matrix_of(w, &u) != DF_OK || rows == 0 || rows > (1u << 24)) return 0;
   const uint64_t np = up(w->rows, 8);
-  return up(w->rows * w->cols * 2, 256) + (np != w->rows ? up(rows * np * 2, 256) : 0) +
+  return copy_bytes(w->rows, w->cols) + lift_bytes(w->rows, true) + (np != w->rows ? up(rows * np * 2, 256) : 0) +
          plane_bytes(rows, w->cols, w->rows);
 }
 

@@ -560,7 +560,7 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
     DFH_TRY(hipGetLastError());
     if (dhead) {
       const Gemm gw = {dz, xm, ldz, mp, nv, k, rows, 0, 0, 0};
-      DFH_TRY((product<T, true, false>(gw, EpiStore{dhead + (uint64_t)v0 * k, k, own ? peak : grad, own ? peak + 1 : sv.share, d->temperature / mul},
+      DFH_TRY((product<T, true, false>(gw, EpiStore<>{dhead + (uint64_t)v0 * k, k, own ? peak : grad, own ? peak + 1 : sv.share, d->temperature / mul, nullptr},
                                       cut_for(nv, k, rows, false).shape, 1, s)));
     }
     if (dx) {

@@ -1,0 +1,95 @@
+"""Scales of any size that float32 holds: products with FP16 operands on both sides
+of the row counts where the kernel changes, and their gradients, against float64.
+The bounds are those of test_gpu_operators, where a weight that is held in 16 bits is
+off by 2^-31 of the largest scale (of its row; in a gradient of the matrix) if that
+is more than half a step of its own."""
+import pytest
+
+import lossless_entropy_coded_huffman_amd as dfh
+from test_gpu_operators import E, dev, few_rows, half_ulp, linear_bound, tiny, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch
+
+
+def weights(torch, n, k, group, s, zeros, seed):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 16, s.shape, generator=g, dtype=torch.uint8) if zeros else None
+    d = dev(torch)
+    w = dfh.U4Matrix((q[:, 0::2] | (q[:, 1::2] << 4)).reshape(-1).to(d), s.to(d).expand(n, -1),
+                     None if z is None else z.to(d).expand(n, -1), cols=k, group_size=group)
+    idx = torch.arange(k) // group
+    s64 = s.double().expand(n, -1)[:, idx]
+    z64 = z.double().expand(n, -1)[:, idx] if zeros else 8.0
+    return w, (q.double() - z64) * s64, s64.abs()
+
+
+SIZES = [(3, 70, 200, 32), (70, 70, 200, 32), (530, 70, 200, 32), (530, 259, 4104, 128), (193, 4200, 4104, 4104),
+         (530, 70, 40, 32)]
+
+
+@pytest.mark.parametrize("size,act", [(1e-9, 6e4), (1e-7, 1e4), (1e-6, 1e3), (1e4, 2.0 ** -8), (3e6, 2.0 ** -16)])
+@pytest.mark.parametrize("m,n,k,group", SIZES)
+def test_scales_out_of_fp16s_range(torch, m, n, k, group, size, act):
+    dt, D = torch.float16, dev(torch)
+    g = torch.Generator().manual_seed(m + n)
+    s = (torch.rand(n if n % 2 == 0 else 1, (k + group - 1) // group, generator=g) + 0.5) * size
+    w, w64, s64 = weights(torch, n, k, group, s, n % 2 == 1, m)
+    x = (torch.randn(m, k, generator=g) * act / k ** 0.5).to(dt)
+    few = few_rows(m, n, k)
+    peak = s64.amax(1)[None, :] * (0 if few else 2.0 ** -31)
+    bound = linear_bound(torch, dt, x, w64, s64, few) + x.double().abs().sum(1, keepdim=True) * peak * 1.01
+    y = dfh.linear_u4(x.to(D), w)
+    ref = x.double() @ w64.t()
+    assert float(ref.abs().max()) < 6e4 and float(ref.abs().max()) > 2.0 ** -20
+    within(y, ref, bound)
+    dy = (torch.randn(m, n, generator=g) * act / n ** 0.5).to(dt)
+    ref, u = dy.double() @ w64, half_ulp(torch, dt)
+    bound = (u * 1.01 + (n + 16) * E) * (dy.double().abs() @ w64.abs()) * (1 + u) + u * ref.abs() + tiny(torch, dt)
+    within(dfh.linear_u4_grad(dy.to(D), w), ref,
+           bound + dy.double().abs().sum(1, keepdim=True) * s64.max() * 2.0 ** -31 * 1.01)
+
+
+@pytest.mark.parametrize("m,n,k,group", [(3, 70, 200, 32), (530, 70, 200, 32), (193, 4200, 4104, 128)])
+def test_scales_of_all_sizes_in_one_matrix(torch, m, n, k, group):
+    # a row's results depend on that row's scales alone, however large another's are
+    dt, D = torch.float16, dev(torch)
+    g = torch.Generator().manual_seed(n)
+    s = 10.0 ** (torch.rand(n, 1, generator=g) * 10 - 9) * (torch.rand(n, (k + group - 1) // group, generator=g) + 0.5)
+    s[5] = 0.0
+    w, w64, s64 = weights(torch, n, k, group, s, True, m)
+    x = torch.randn(m, k, generator=g).to(dt)
+    few = few_rows(m, n, k)
+    peak = s64.amax(1)[None, :] * (0 if few else 2.0 ** -31)
+    bound = linear_bound(torch, dt, x, w64, s64, few) + x.double().abs().sum(1, keepdim=True) * peak * 1.01
+    within(dfh.linear_u4(x.to(D), w), x.double() @ w64.t(), bound)
+    dy = torch.randn(m, n, generator=g).to(dt)
+    ref, u = dy.double() @ w64, half_ulp(torch, dt)
+    bound = (u * 1.01 + (n + 16) * E) * (dy.double().abs() @ w64.abs()) * (1 + u) + u * ref.abs() + tiny(torch, dt)
+    within(dfh.linear_u4_grad(dy.to(D), w), ref,
+           bound + dy.double().abs().sum(1, keepdim=True) * s64.max() * 2.0 ** -31 * 1.01)
+
+
+def test_one_infinite_scale(torch):
+    # the group it stands for is infinite (NaN where q = z); other rows are as ever
+    D = dev(torch)
+    for m in (3, 530):
+        n, k = 40, 64
+        s = torch.full((n, 2), 0.01)
+        s[7, 1] = float("inf")
+        w, w64, _ = weights(torch, n, k, 32, s, False, 1)
+        x = torch.ones(m, k, dtype=torch.float16)
+        y = dfh.linear_u4(x.to(D), w).double().cpu()
+        assert not torch.isfinite(y[:, 7]).any()
+        s[7, 1] = 0.01
+        w2, _, _ = weights(torch, n, k, 32, s, False, 1)
+        keep = [i for i in range(n) if i != 7]
+        assert torch.equal(y[:, keep], dfh.linear_u4(x.to(D), w2).double().cpu()[:, keep])
