@@ -74,6 +74,11 @@ def _rows16(t: torch.Tensor) -> torch.Tensor:
     return _copied(t)
 
 
+def _flat(t: torch.Tensor) -> torch.Tensor:
+    """t [..., c] as rows."""
+    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+
+
 # the current device, and the raw handle of a device's current stream, without
 # the objects that torch.cuda makes around them (a token's product is short)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -164,7 +169,7 @@ class U4Matrix:
 
 def _linear_on(x: torch.Tensor, w: U4Matrix, ty: int, handle: int) -> torch.Tensor:
     """y [m, rows] for x [..., cols] on a stream, which a copy of x is made on too."""
-    x = _rows16(x if x.dim() == 2 else x.reshape(-1, w.cols))
+    x = _rows16(_flat(x))
     m = x.shape[0]
     y = x.new_empty((m, w.rows))
     L = dfh.lib()
@@ -202,7 +207,7 @@ def _linear_grad(dy: torch.Tensor, w: U4Matrix, stream) -> torch.Tensor:
     L = dfh.lib()
 
     def call(handle):
-        d2 = dy if dy.dim() == 2 else dy.reshape(-1, w.rows)
+        d2 = _flat(dy)
         if w.rows % 8 == 0:
             d2 = _rows16(d2)
         elif d2.stride(1) != 1 or not w.rows <= d2.stride(0) <= _MAX_STRIDE:
@@ -330,43 +335,43 @@ class _Loss:
             d.top = int(index.shape[-1])
             if not 1 <= d.top <= 1024:
                 raise ValueError("top must lie in 1 .. 1024, got %d" % d.top)
-        self.inputs = (x, head, labels, teacher, index)
+        self.inputs = (x, head, labels) if labels is not None else (x, head, teacher, index)
         self.desc, self.dev = d, dev
         self.done = None   # an event behind the forward call, where that ran on another stream
 
     @staticmethod
-    def bind(d, x, head, labels, teacher, index):
+    def bind(d, x, head, *targets):
         """Lays the inputs out and points the descriptor d at them (on the call's
         stream).  Returns them as they lie, in the same order."""
-        x = _rows16(x.detach().reshape(-1, d.hidden))
-        head = _rows16(head.detach())
+        x, head = _rows16(_flat(x)), _rows16(head)
         d.rows = x.shape[0]
         d.x, d.x_stride, d.head, d.head_stride = x.data_ptr(), x.stride(0), head.data_ptr(), head.stride(0)
-        if labels is not None:
-            labels = labels.reshape(-1).contiguous()
+        if not d.top:
+            labels = targets[0] if targets[0].dim() == 1 else targets[0].reshape(-1)
+            if not labels.is_contiguous():
+                labels = labels.contiguous()
             d.labels = labels.data_ptr()
-        else:
-            teacher, index = teacher.detach().reshape(-1, d.top), index.reshape(-1, d.top)
-            if teacher.stride(1) != 1:
-                teacher = teacher.contiguous()
-            if index.stride(1) != 1:
-                index = index.contiguous()
-            d.teacher, d.teacher_stride = teacher.data_ptr(), teacher.stride(0)
-            d.index, d.index_stride = index.data_ptr(), index.stride(0)
-        return x, head, labels, teacher, index
+            return x, head, labels
+        teacher, index = _flat(targets[0].detach()), _flat(targets[1])
+        if teacher.stride(1) != 1:
+            teacher = teacher.contiguous()
+        if index.stride(1) != 1:
+            index = index.contiguous()
+        d.teacher, d.teacher_stride = teacher.data_ptr(), teacher.stride(0)
+        d.index, d.index_stride = index.data_ptr(), index.stride(0)
+        return x, head, teacher, index
 
     def forward(self, stream):
+        """The loss and what the gradient wants kept beside the inputs: their laid
+        out copies, where there are any, and the rows' statistics."""
         L, dev = dfh.lib(), self.dev
         none = self.reduction == "none"
         current = _raw_stream(dev.index)
 
         def call(handle):
             laid = self.bind(self.desc, *self.inputs)
-            # what was copied goes on to the gradient beside the inputs
-            self.copies = tuple(c if c is not None and c.data_ptr() != t.data_ptr() else None
-                                for t, c in zip(self.inputs, laid))
             ref = ctypes.byref(self.desc)
-            loss = torch.empty(int(self.desc.rows) if none else 1, dtype=torch.float32, device=dev)
+            loss = torch.empty(self.shape if none else (), dtype=torch.float32, device=dev)
             saved = torch.empty(max(L.df_loss_saved_bytes(ref) // 4, 1), dtype=torch.float32, device=dev)
             need = L.df_loss_workspace_bytes(ref)
             ws = _workspace(need, dev)
@@ -376,29 +381,45 @@ class _Loss:
             if handle != current:
                 self.done = torch.cuda.Event()
                 self.done.record()   # on the call's stream
-            return loss, saved
+            # which of the kept tensors the kernels read for each input, and where they lie
+            self.forms = [(t.shape, t.dtype) for t in self.inputs]
+            self.places, copies = list(range(len(laid))), []
+            for i, t in enumerate(self.inputs):
+                if laid[i].data_ptr() != t.data_ptr():
+                    self.places[i] = len(laid) + len(copies)
+                    copies.append(laid[i])
+            kept = (*copies, saved)
+            self.lie = self.where((*self.inputs, *kept))
+            return loss, kept
 
-        loss, saved = _launch(stream, dev, self.inputs, call)
-        return loss.view(self.shape if none else ()), saved
+        return _launch(stream, dev, self.inputs, call)
 
-    def grads(self, inputs, copies, saved, gout, want_x, want_head):
+    def where(self, kept):
+        return [(kept[i].data_ptr(), kept[i].stride()) for i in self.places]
+
+    def grads(self, kept, gout, want_x, want_head):
+        """kept: the inputs, then what the forward call returned."""
         L, dev = dfh.lib(), self.dev
-        x, head = inputs[:2]
-        desc = dfh.df_loss.from_buffer_copy(self.desc)
+        saved = kept[-1]
 
         def call(handle):
             if self.done is not None:
                 # what the forward call keeps is written, and was allocated, on its stream
                 here = torch.cuda.current_stream(dev)
                 here.wait_event(self.done)
-                for t in (*inputs, *copies, saved):
-                    if t is not None:
-                        t.record_stream(here)
-            laid = self.bind(desc, *(t if c is None else c for t, c in zip(inputs, copies)))
+                for t in kept:
+                    t.record_stream(here)
+            desc, laid = self.desc, None
+            if self.where(kept) != self.lie:   # saved-tensor hooks put them elsewhere
+                if [(t.shape, t.dtype) for t in kept[:len(self.forms)]] != self.forms:
+                    raise RuntimeError("the loss's inputs came back with other shapes or types")
+                desc = dfh.df_loss.from_buffer_copy(desc)
+                laid = self.bind(desc, *[kept[i] for i in self.places])
             ref = ctypes.byref(desc)
-            g = gout.to(torch.float32).reshape(-1).contiguous()
-            dx = torch.empty((int(desc.rows), head.shape[1]), dtype=x.dtype, device=dev) if want_x else None
-            dh = torch.empty(head.shape, dtype=head.dtype, device=dev) if want_head else None
+            g = gout.to(torch.float32).contiguous()
+            (xs, ty), (hs, _) = self.forms[:2]
+            dx = torch.empty(xs, dtype=ty, device=dev) if want_x else None
+            dh = torch.empty(hs, dtype=ty, device=dev) if want_head else None
             need = L.df_loss_grad_workspace_bytes(ref, int(want_head))
             ws = _workspace(need, dev)
             st = L.df_vocab_loss_grad(ref, saved.data_ptr(), g.data_ptr(), _p(dx), _p(dh), ws.data_ptr(), need, handle)
@@ -407,30 +428,28 @@ class _Loss:
             del laid   # enqueued: the copies' memory follows in the stream's order
             return dx, dh
 
-        dx, dh = _launch(None, dev, (), call)
-        return (None if dx is None else dx.view(x.shape)), dh
+        return _launch(None, dev, (), call)
 
 
 class _LossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, head, call, stream):
-        loss, saved = call.forward(stream)
+        loss, kept = call.forward(stream)
         # the tensors that the gradient reads again: kept by autograd alone, so that
         # a change made to one in between is refused and saved-tensor hooks see all
-        ctx.save_for_backward(*call.inputs, *call.copies, saved)
-        call.inputs = call.copies = None
+        ctx.save_for_backward(*call.inputs, *kept)
+        call.inputs = None
         ctx.call = call
         return loss
 
     @staticmethod
     def backward(ctx, gout):
         _no_tangent(gout)
-        call, (*kept, saved), want = ctx.call, ctx.saved_tensors, ctx.needs_input_grad[:2]
-        inputs, copies = kept[:5], kept[5:]
+        call, kept, want = ctx.call, ctx.saved_tensors, ctx.needs_input_grad
         if torch.is_grad_enabled():   # under create_graph
-            dx, dh = _LossGrad.apply(gout, *inputs[:2], call, (inputs, copies, saved), want)
+            dx, dh = _LossGrad.apply(gout, kept[0], kept[1], call, kept, want)
         else:
-            dx, dh = call.grads(inputs, copies, saved, gout, *want)
+            dx, dh = call.grads(kept, gout, want[0], want[1])
         return dx, dh, None, None
 
 
@@ -440,7 +459,7 @@ class _LossGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, gout, x, head, call, kept, want):
-        return call.grads(*kept, gout, *want)
+        return call.grads(kept, gout, want[0], want[1])
 
     @staticmethod
     def backward(ctx, *_):

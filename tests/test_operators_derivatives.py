@@ -69,14 +69,14 @@ class Squares:
     place of a _Loss."""
 
     def __init__(self, x, head):
-        self.inputs, self.copies = (x, head, None, None, None), (None,) * 5
+        self.inputs = (x, head)
 
     def forward(self, stream):
-        x, head = self.inputs[:2]
-        return (x @ head.t()).pow(2).sum(), torch.zeros(1)
+        x, head = self.inputs
+        return (x @ head.t()).pow(2).sum(), (torch.zeros(1),)
 
-    def grads(self, inputs, copies, saved, gout, want_x, want_head):
-        x, head = (t.detach() for t in inputs[:2])
+    def grads(self, kept, gout, want_x, want_head):
+        x, head = (t.detach() for t in kept[:2])
         z = 2 * gout * (x @ head.t())
         return z @ head if want_x else None, z.t() @ x if want_head else None
 
