@@ -162,15 +162,16 @@ __device__ __forceinline__ float dot_row(const Head &h, uint32_t m, int32_t v) {
   return s;
 }
 
-// picked[m, j] = x[m] . head[target j], one wave each (0 without a target).
+// picked[m, j] = x[m] . head[target j], one wave each (0 without a target), at most
+// 2^20 workgroups at once: a launch holds fewer than 2^32 threads.
 template <class T>
 __global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t rows, const Head h, float *picked) {
   const uint32_t per = t.top ? t.top : 1;
-  const uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (e >= (uint64_t)rows * per) return;
-  const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
-  const float s = dot_row<T>(h, m, target_of(t, m, j));
-  if ((threadIdx.x & 63) == 0) picked[e] = s;
+  for (uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); e < (uint64_t)rows * per; e += (uint64_t)gridDim.x * 4) {
+    const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
+    const float s = dot_row<T>(h, m, target_of(t, m, j));
+    if ((threadIdx.x & 63) == 0) picked[e] = s;
+  }
 }
 
 // Parts of a row: `main` in the first `rows` rows, `rest` in those behind them.
@@ -483,8 +484,8 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
   // x 4096 in four waves would take longer than the launch
   const bool pick = rows <= 256 && (uint64_t)per_row(d) * k <= 32768;
   if (!pick) {
-    const uint64_t entries = (uint64_t)rows * per_row(d);
-    hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)((entries + 3) / 4)), dim3(256), 0, s, t, rows, h, sv.picked);
+    const uint64_t groups = ((uint64_t)rows * per_row(d) + 3) / 4;
+    hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)(groups < 1u << 20 ? groups : 1u << 20)), dim3(256), 0, s, t, rows, h, sv.picked);
     DFH_TRY(hipGetLastError());
   }
   float2 *parts = (float2 *)ws;

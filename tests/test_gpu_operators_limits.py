@@ -1,0 +1,38 @@
+"""Calls within the stated limits whose launches would hold 2^32 threads or more."""
+import pytest
+
+import lossless_entropy_coded_huffman_amd as dfh
+from test_gpu_operators import E, dev, half_ulp, matrix, tiny, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield torch
+    torch.cuda.empty_cache()
+
+
+def test_distillation_of_many_entries(torch):
+    # 2^26 entries, one wave each
+    D = dev(torch)
+    rows, top, v, h = 1 << 16, 1024, 1500, 8
+    g = torch.Generator(device=D).manual_seed(1)
+    x = torch.randn(rows, h, generator=g, device=D).to(torch.bfloat16)
+    head = torch.randn(v, h, generator=g, device=D).to(torch.bfloat16)
+    teacher = (torch.randn(rows, top, generator=g, device=D) * 2).to(torch.bfloat16)
+    index = torch.randint(0, v, (rows, top), generator=g, device=D)
+    got = dfh.distill_loss(x, head, teacher, index, reduction="none").double()
+    for lo in (0, rows // 2, rows - 512):
+        s = slice(lo, lo + 512)
+        z = x[s].double() @ head.double().t()
+        logq, logt = torch.log_softmax(z, 1), torch.log_softmax(teacher[s].double(), 1)
+        ref = (logt.exp() * (logt - logq.gather(1, index[s]))).sum(1)
+        # a logit is off by (h + 8) e sum |x| |head|, in the log-sum and in the mean of
+        # the targets; float32 steps of the terms, and sums of up to 1500 of them
+        dz = ((h + 8) * E * (x[s].double().abs() @ head.double().abs().t())).amax(1)
+        bound = 2 * dz + (top + 16) * E * (logt.exp() * (logt.abs() + logq.gather(1, index[s]).abs())).sum(1) + v * E
+        assert bool(((got[s] - ref).abs() <= bound).all())
