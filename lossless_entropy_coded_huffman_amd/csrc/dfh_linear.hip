@@ -666,11 +666,12 @@ __global__ __launch_bounds__(256) void join_planes(const float *p, uint32_t spli
   }
 }
 
-// Rows of n elements into rows of np (n rounded up to 8), zeros past n.
-__global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss, uint32_t n, uint32_t np,
+// Rows of n elements into rows of np (n rounded up to 8), zeros past n.  At most
+// 2^20 workgroups, so that 2^24 rows stay under a launch's 2^32 threads.
+__global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss, uint32_t m, uint32_t n, uint32_t np,
                                                 uint16_t *dst) {
-  const uint64_t r = blockIdx.x;
-  for (uint32_t c = threadIdx.x; c < np; c += 256) dst[r * np + c] = c < n ? src[r * ss + c] : (uint16_t)0;
+  for (uint64_t r = blockIdx.x; r < m; r += gridDim.x)
+    for (uint32_t c = threadIdx.x; c < np; c += 256) dst[r * np + c] = c < n ? src[r * ss + c] : (uint16_t)0;
 }
 
 // Rows that u4_tile takes rather than an expansion: the expansion costs a fixed
@@ -830,7 +831,7 @@ df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, 
   uint8_t *next = ws + copy_bytes(w.n, w.k) + lift_bytes(w.n, true);
   const uint32_t np = (uint32_t)up(w.n, 8);
   if (np != w.n) {  // the summed index in whole 16-byte chunks
-    hipLaunchKernelGGL(pad_rows, dim3(m), dim3(256), 0, s, dy, ds, w.n, np, (uint16_t *)next);
+    hipLaunchKernelGGL(pad_rows, dim3(m < 1u << 20 ? m : 1u << 20), dim3(256), 0, s, dy, ds, m, w.n, np, (uint16_t *)next);
     dy = (const uint16_t *)next;
     ds = np;
     next += up((uint64_t)m * np * 2, 256);

@@ -36,3 +36,19 @@ def test_distillation_of_many_entries(torch):
         dz = ((h + 8) * E * (x[s].double().abs() @ head.double().abs().t())).amax(1)
         bound = 2 * dz + (top + 16) * E * (logt.exp() * (logt.abs() + logq.gather(1, index[s]).abs())).sum(1) + v * E
         assert bool(((got[s] - ref).abs() <= bound).all())
+
+
+def test_gradient_of_the_most_rows(torch):
+    # 2^24 rows of an odd number of outputs, which are padded for the product
+    D = dev(torch)
+    m, n, k = 1 << 24, 9, 8
+    w, w64, _ = matrix(torch, n, k, 32, "fp32", seed=1)
+    g = torch.Generator(device=D).manual_seed(2)
+    dy = torch.randn(m, n, generator=g, device=D, dtype=torch.float16)
+    dx = dfh.linear_u4_grad(dy, w)
+    u = half_ulp(torch, torch.float16)
+    for lo in (0, m // 2 - 100, m - 1000):
+        d = dy[lo: lo + 1000].double().cpu()
+        ref = d @ w64
+        bound = (u * 1.01 + (n + 16) * E) * (d.abs() @ w64.abs()) * (1 + u) + u * ref.abs() + tiny(torch, torch.float16)
+        within(dx[lo: lo + 1000], ref, bound)
