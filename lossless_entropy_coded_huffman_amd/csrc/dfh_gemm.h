@@ -100,6 +100,7 @@ struct Gemm {
   uint32_t m, n, k;           // [rows, k]: k a multiple of 8; [k, rows]: rows padded to 8
   uint32_t mt, nt;            // tiles
   uint32_t kb_per_split;      // 64-element steps per split of the summed index
+  uint32_t first;             // tile of the launch's first workgroup
 };
 
 constexpr int kBK = 64;
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const Gemm g, const Epi epi
   typedef Operand<T, BN, kWaves, KB> OB;
   extern __shared__ __align__(1024) uint8_t lds[];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = xcd_tile(blockIdx.x, g.mt * g.nt);
+  const uint32_t tile = xcd_tile(g.first + blockIdx.x, g.mt * g.nt);
   const uint32_t bm = tile % g.mt, bn = tile / g.mt;
   const uint32_t m0 = bm * BM, n0 = bn * BN;
   const uint32_t nkb = (g.k + kBK - 1) / kBK;
@@ -438,9 +439,16 @@ hipError_t gemm_launch(Gemm g, const Epi &epi, uint32_t splits, hipStream_t stre
   g.kb_per_split = (nkb + splits - 1) / splits;
   const hipError_t e = allow_lds((const void *)gemm<T, BM, BN, WM, WN, KA, KB, Epi>, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((gemm<T, BM, BN, WM, WN, KA, KB, Epi>), dim3(g.mt * g.nt, splits), dim3(64 * WM * WN), lds, stream,
-                     g, epi);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 threads: 2^21 rows of 2^18 columns are 2^23 tiles
+  const uint32_t tiles = g.mt * g.nt, most = 1u << 22;
+  for (g.first = 0; g.first < tiles; g.first += most) {
+    const uint32_t count = tiles - g.first < most ? tiles - g.first : most;
+    hipLaunchKernelGGL((gemm<T, BM, BN, WM, WN, KA, KB, Epi>), dim3(count, splits), dim3(64 * WM * WN), lds, stream, g,
+                       epi);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
+  }
+  return hipSuccess;
 }
 
 // The tiles a product is cut into.

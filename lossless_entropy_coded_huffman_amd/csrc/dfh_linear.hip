@@ -818,7 +818,7 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
                        : tile_launch<T, 4, 1>(w, x, xs, m, y, (float *)ws, p, s);
   } else {
     const float *back = expand<T>(w, ws, false, s);
-    Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0};
+    Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0, 0};
     return many_rows<T, false>(g, y, back, (float *)(ws + copy_bytes(w.n, w.k) + lift_bytes(w.n, false)), s);
   }
   return e == hipSuccess ? DF_OK : DF_ERR_HIP;
@@ -836,7 +836,7 @@ df_status linear_grad(const U4 &w, const uint16_t *dy, uint32_t m, uint64_t ds, 
     ds = np;
     next += up((uint64_t)m * np * 2, 256);
   }
-  Gemm g = {dy, (const uint16_t *)ws, ds, w.k, m, w.k, w.n, 0, 0, 0};
+  Gemm g = {dy, (const uint16_t *)ws, ds, w.k, m, w.k, w.n, 0, 0, 0, 0};
   return many_rows<T, true>(g, dx, back, (float *)next, s);
 }
 

@@ -491,7 +491,7 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
   float2 *parts = (float2 *)ws;
   const RowCut cut = rows_for(rows, vocab, k, false);
   const Parts np = parts_of(cut, vocab);
-  const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0};
+  const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0, 0};
   DFH_TRY((product_rows<T, false>(g, EpiStats{parts, rows, kLog2e / d->temperature}, cut, s)));
   float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + parts_bytes(d));
   auto *fn = pick ? finish_rows<T, 1, true> : rows <= 256 ? finish_rows<T, 1, false> : finish_rows<T, 8, false>;
@@ -555,17 +555,17 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
     const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);
     const uint16_t *hp = head + (uint64_t)v0 * d->head_stride;
-    const Gemm gz = {x, hp, d->x_stride, d->head_stride, rows, nv, k, 0, 0, 0};
+    const Gemm gz = {x, hp, d->x_stride, d->head_stride, rows, nv, k, 0, 0, 0, 0};
     DFH_TRY((product_rows<T, false>(gz, EpiDz{dz, ldz, sv.lse2, sv.state, c, mul}, rows_for(rows, nv, k, false), s)));
     hipLaunchKernelGGL((fix_targets<T>), dim3(rows), dim3(64), 0, s, t, sv, v0, nv, c, mul, dz, ldz);
     DFH_TRY(hipGetLastError());
     if (dhead) {
-      const Gemm gw = {dz, xm, ldz, mp, nv, k, rows, 0, 0, 0};
+      const Gemm gw = {dz, xm, ldz, mp, nv, k, rows, 0, 0, 0, 0};
       DFH_TRY((product<T, true, false>(gw, EpiStore<>{dhead + (uint64_t)v0 * k, k, own ? peak : grad, own ? peak + 1 : sv.share, d->temperature / mul, nullptr},
                                       cut_for(nv, k, rows, false).shape, 1, s)));
     }
     if (dx) {
-      const Gemm gx = {dz, hp, ldz, d->head_stride, rows, k, nv, 0, 0, 0};
+      const Gemm gx = {dz, hp, ldz, d->head_stride, rows, k, nv, 0, 0, 0, 0};
       DFH_TRY((product_rows<T, true>(gx, EpiPlane{planes, k, (uint64_t)rows * k, v0 != 0}, p.dx, s)));
     }
   }

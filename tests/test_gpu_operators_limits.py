@@ -52,3 +52,23 @@ def test_gradient_of_the_most_rows(torch):
         ref = d @ w64
         bound = (u * 1.01 + (n + 16) * E) * (d.abs() @ w64.abs()) * (1 + u) + u * ref.abs() + tiny(torch, torch.float16)
         within(dx[lo: lo + 1000], ref, bound)
+
+
+def test_loss_of_very_many_tiles(torch):
+    # 2^21 rows of 2^18 logits: 2^23 tiles of 256 x 256, more than a launch holds
+    D = dev(torch)
+    m, v, h = 1 << 21, 1 << 18, 8
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 70 GB for the statistics of the tiles")
+    g = torch.Generator(device=D).manual_seed(3)
+    x = torch.randn(m, h, generator=g, device=D).to(torch.bfloat16)
+    head = torch.randn(v, h, generator=g, device=D).to(torch.bfloat16)
+    labels = torch.randint(0, v, (m,), generator=g, device=D)
+    got = dfh.vocab_loss(x, head, labels, reduction="none").double()
+    for lo in (0, m // 2 - 50, m - 100):   # the halves of the launch, and its ends
+        s = slice(lo, lo + 100)
+        z = x[s].double() @ head.double().t()
+        ref = torch.logsumexp(z, 1) - z.gather(1, labels[s][:, None])[:, 0]
+        dz = ((h + 8) * E * (x[s].double().abs() @ head.double().abs().t())).amax(1)
+        # 2^18 exponentials in sums of at most 64, then 4096 parts in a tree of 32 and 256
+        assert bool(((got[s] - ref).abs() <= 2 * dz + 512 * E * (1 + ref.abs())).all())
