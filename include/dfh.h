@@ -371,9 +371,12 @@ typedef struct {
  * elements of `type` (BF16 or F16), x_stride elements apart (a multiple of 8,
  * at most 2^21); y: rows x w->rows of the same type, contiguous.  Both 16-byte
  * aligned.  Few rows (up to 192; 384 where W has at most 2^24 elements, 512 at most
- * 2^22) multiply the integers exactly (a group's FP32 sum is scaled); more expand W to `type` in the workspace (256-byte aligned),
- * each weight rounded once: to 2^-8 (BF16) or 2^-11 (FP16) of itself, in FP16 to 2^-31 of its row's largest scale
- * where that is more (a power of two a row keeps any scales within range).  Sums are FP32.  Up to 4 rows need no workspace.
+ * 2^22) round no weight: FP16 sums x (q - z) and BF16 x (16 + q), of which (16 + z)
+ * times the sum of x comes off, and a group's FP32 sum is scaled.  More expand W to
+ * `type` in the workspace (256-byte aligned), each weight rounded once: to 2^-8
+ * (BF16) or 2^-11 (FP16) of itself, in FP16 to 2^-31 of its row's largest scale where
+ * that is more (a power of two a row keeps any scales within range).  Sums are FP32.
+ * At most 2^24 rows; up to 4 need no workspace.
  * DF_ERR_ARG on a bad pointer, size, alignment or too small a workspace. */
 uint64_t df_linear_u4_workspace_bytes(const df_u4_matrix *w, uint64_t rows);
 df_status df_linear_u4(const df_u4_matrix *w, df_type type, const void *x, uint64_t rows, uint64_t x_stride, void *y,

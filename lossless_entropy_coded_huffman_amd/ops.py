@@ -283,8 +283,8 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     """y = x W^T for W[n, k] = scales[n, k // group_size] * (q[n, k] - zeros[...]),
     x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
     are float32; few rows (up to 192; 384 for at most 2^24 weights, 512 for at most
-    2^22) multiply the integer weights exactly, more (and every gradient) round each
-    weight once to x's type, with scales of any size within range.  Differentiable in x;
+    2^22) round no weight (float16 sums x (q - z); bfloat16 x (16 + q), and takes
+    16 + z times the sum of x off), more (and every gradient) round each weight once to x's type, with scales of any size within range.  Differentiable in x;
     the nibbles must stay as they are until the gradient has run (df_decompress
     into the same buffer is not seen by autograd)."""
     _no_tangent(x)

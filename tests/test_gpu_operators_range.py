@@ -93,3 +93,29 @@ def test_one_infinite_scale(torch):
         w2, _, _ = weights(torch, n, k, 32, s, False, 1)
         keep = [i for i in range(n) if i != 7]
         assert torch.equal(y[:, keep], dfh.linear_u4(x.to(D), w2).double().cpu()[:, keep])
+
+
+@pytest.mark.parametrize("m", [1, 4, 40, 200])
+@pytest.mark.parametrize("k,group,zeros", [(512, 128, True), (512, 32, True), (200, 64, False), (1416, 1416, True)])
+def test_a_large_input_at_a_zero_weight(torch, m, k, group, zeros):
+    # BF16: every sum of x (16 + q), x and (16 + z) x is a whole number under 2^24, so
+    # float32 has it exactly, and a large input whose weight is zero leaves no trace
+    D, n = dev(torch), 40
+    g = torch.Generator().manual_seed(k)
+    s = torch.full((n, (k + group - 1) // group), 0.5)
+    w, w64, _ = weights(torch, n, k, group, s, zeros, k)
+    x = torch.randint(-2, 3, (m, k), generator=g).to(torch.bfloat16)
+    big = 3 * 2.0 ** 17
+    # a column of zero weights: codes equal to the zero points there
+    q = torch.stack((w.packed & 15, w.packed >> 4), -1).view(n, k).cpu()
+    zp = w.zeros.cpu().expand(n, -1) if zeros else torch.full((n, s.shape[1]), 8, dtype=torch.uint8)
+    col = 77
+    q[:, col] = zp[:, col // group]
+    packed = (q[:, 0::2] | (q[:, 1::2] << 4)).reshape(-1).to(D)
+    w = dfh.U4Matrix(packed, w.scales, w.zeros, cols=k, group_size=group)
+    w64[:, col] = 0.0
+    x[:, col] = big
+    assert float((x.double().abs().sum(1) * 31).max()) < 2.0 ** 24
+    ref = (x.double() @ w64.t()).to(torch.bfloat16)
+    assert float(ref.abs().max()) > 0
+    assert torch.equal(dfh.linear_u4(x.to(D), w).cpu(), ref)
