@@ -8,7 +8,10 @@
 //
 // Forward: one pass of gemm whose epilogue reduces each wave's columns to a
 // maximum and a sum of exponentials per row; a second kernel joins them.  The
-// few logits that the targets name are dot products of their own.  Backward:
+// logits that the targets name have the bits of the ones under the sum, so no
+// probability exceeds one and a row that is sure of its label has loss and
+// gradient zero: the epilogue writes a label's, and a teacher's entries are
+// multiplied again in the same order.  Backward:
 // for a piece of the vocabulary that fits the workspace the logits are made
 // again, dz goes out in 16 bits, the target entries are put right, and two
 // more products take it.  Exponents are in base 2: c = log2(e) / T.
@@ -61,16 +64,34 @@ __device__ __forceinline__ int32_t target_of(const Targets &t, uint32_t m, uint3
 
 // ------------------------------------------------------------------ epilogues
 // Per row, over this wave's columns: max of z2 = c z and sum of 2^(z2 - max).
+// Where there are labels, the one wave whose columns hold a row's writes its z.
 struct EpiStats {
   float2 *parts;  // [part][rows]
   uint32_t rows;
   float c;
-  EpiStats from_row(uint32_t r) const { return EpiStats{parts + r, rows, c}; }
+  const int64_t *labels;
+  float *picked;
+  EpiStats from_row(uint32_t r) const {
+    return EpiStats{parts + r, rows, c, labels ? labels + r : labels, picked + r};
+  }
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t part, uint32_t) const {
+#pragma clang fp contract(off)  // c z is rounded wherever it is made
 #pragma unroll
     for (int i = 0; i < MT; i++) {
+      const uint32_t row = mb + i * 16;
+      if (labels && row < m) {
+        const int64_t l = labels[row];
+        const uint32_t at = (uint32_t)l - nb;
+        if (l >= 0 && l < (int64_t)n && at < NT * 16 && (at & 15) < 4) {
+#pragma unroll
+          for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (at == j * 16 + e) picked[row] = acc[j][i][e];
+        }
+      }
       float mx = -__builtin_huge_valf();
 #pragma unroll
       for (int j = 0; j < NT; j++)
@@ -90,7 +111,6 @@ struct EpiStats {
         for (int e = 0; e < 4; e++) s += exp2_(acc[j][i][e] - ref);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      const uint32_t row = mb + i * 16;
       if ((threadIdx.x & 48) == 0 && row < m) parts[(uint64_t)part * rows + row] = float2{mx, s};
     }
   }
@@ -110,6 +130,7 @@ struct EpiDz {
   template <class T, int NT, int MT>
   __device__ __forceinline__ void operator()(f32x4 (&acc)[NT][MT], uint32_t mb, uint32_t nb, uint32_t m, uint32_t n,
                                              uint32_t, uint32_t) const {
+#pragma clang fp contract(off)  // as in EpiStats, or p could exceed 1
     static_assert(NT % 2 == 0, "blocks in pairs");
     const uint32_t kg = (threadIdx.x >> 4) & 3, first = nb - 4 * kg + (kg & 1) * 16 + (kg >> 1) * 8;
 #pragma unroll
@@ -142,35 +163,45 @@ struct Head {
   uint64_t xs, hs;
   uint32_t k;
 };
-// x[m] . head[v] by a wave (0 for v < 0), in every lane.
+// x[m] . head[v] for sixteen entries a wave, entry lane % 16 (0 for v < 0; m a row
+// of x all the same): the diagonal of a matrix product that sums as gemm does, 32
+// elements a step in order, so the bits are the ones that its epilogue sees.  Returned
+// in the lane whose lane / 16 is a quarter of its entry.
 template <class T>
-__device__ __forceinline__ float dot_row(const Head &h, uint32_t m, int32_t v) {
-  float s = 0.f;
-  if (v >= 0) {
-    const u32x4 *px = (const u32x4 *)(h.x + m * h.xs), *ph = (const u32x4 *)(h.head + (uint64_t)v * h.hs);
-    for (uint32_t c = threadIdx.x & 63; c < h.k / 8; c += 64) {
-      const u32x4 a = px[c], b = ph[c];
+__device__ __forceinline__ float dots_16(const Head &h, uint32_t m, int32_t v) {
+  const uint32_t lane = threadIdx.x & 63, off = (lane >> 4) * 8;
+  const uint16_t *px = h.x + m * h.xs + off, *ph = h.head + (uint64_t)(v < 0 ? 0 : v) * h.hs + off;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = 8;  // steps in flight
+  for (uint32_t k = 0; k < h.k; k += 32 * kAhead) {
+    u32x4 a[kAhead], b[kAhead];
 #pragma unroll
-      for (int d = 0; d < 4; d++) {
-        s = __builtin_fmaf(from_bits(T{}, (uint16_t)a[d]), from_bits(T{}, (uint16_t)b[d]), s);
-        s = __builtin_fmaf(from_bits(T{}, (uint16_t)(a[d] >> 16)), from_bits(T{}, (uint16_t)(b[d] >> 16)), s);
+    for (int q = 0; q < kAhead; q++) {
+      const uint32_t at = k + q * 32;
+      a[q] = b[q] = u32x4{0, 0, 0, 0};
+      if (at + off < h.k) {
+        if (v >= 0) a[q] = *(const u32x4 *)(ph + at);
+        b[q] = *(const u32x4 *)(px + at);
       }
     }
-  }
 #pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  return s;
+    for (int q = 0; q < kAhead; q++) acc = mfma(T{}, a[q], b[q], acc);
+  }
+  const uint32_t e = lane & 3;
+  return e == 0 ? acc[0] : e == 1 ? acc[1] : e == 2 ? acc[2] : acc[3];
 }
 
-// picked[m, j] = x[m] . head[target j], one wave each (0 without a target), at most
-// 2^20 workgroups at once: a launch holds fewer than 2^32 threads.
+// picked[m, j] = x[m] . head[target j], sixteen entries a wave (0 without a target),
+// at most 2^20 workgroups at once: a launch holds fewer than 2^32 threads.
 template <class T>
-__global__ __launch_bounds__(256) void pick_logits(const Targets t, uint32_t rows, const Head h, float *picked) {
-  const uint32_t per = t.top ? t.top : 1;
-  for (uint64_t e = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); e < (uint64_t)rows * per; e += (uint64_t)gridDim.x * 4) {
-    const uint32_t m = (uint32_t)(e / per), j = (uint32_t)(e % per);
-    const float s = dot_row<T>(h, m, target_of(t, m, j));
-    if ((threadIdx.x & 63) == 0) picked[e] = s;
+__global__ __launch_bounds__(64) void pick_logits(const Targets t, uint32_t rows, const Head h, float *picked) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t all = (uint64_t)rows * t.top;
+  for (uint64_t first = (uint64_t)blockIdx.x * 16; first < all; first += (uint64_t)gridDim.x * 16) {
+    const uint64_t e = first + (lane & 15);
+    const uint32_t m = (uint32_t)((e < all ? e : first) / t.top), j = (uint32_t)(e % t.top);
+    const float z = dots_16<T>(h, m, e < all ? target_of(t, m, j) : -1);
+    if (e < all && (lane & 15) / 4 == lane / 16) picked[e] = z;
   }
 }
 
@@ -185,19 +216,21 @@ struct Parts {
 // likewise of row t % R.  R = 8 reads 64 bytes of a part at once; few rows take
 // R = 1, so that 256 threads share a row's parts (7 rows of 2004 parts: 64 us with
 // 16 rows a workgroup and one load in flight).  PICK (with R = 1, where a row has
-// few targets): the four waves make the picked logits themselves.
+// few teacher entries): the four waves make the picked logits themselves.
 template <class T, int R, bool PICK>
 __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, Parts np,
                                                    const Head h, Saved sv, float *loss) {
+#pragma clang fp contract(off)  // as in EpiStats
   constexpr uint32_t S = 256 / R;
   __shared__ float sa[S][R];
   const uint32_t r = threadIdx.x % R, sl = threadIdx.x / R, m = blockIdx.x * R + r;
   const bool in = m < rows;
   if (PICK) {  // written here, read below after several barriers
-    const uint32_t per = t.top ? t.top : 1;
-    for (uint32_t j = threadIdx.x >> 6; j < per; j += 4) {
-      const float z = dot_row<T>(h, m, target_of(t, m, j));
-      if ((threadIdx.x & 63) == 0) sv.picked[(uint64_t)m * per + j] = z;
+    const uint32_t lane = threadIdx.x & 63;
+    for (uint32_t first = (threadIdx.x >> 6) * 16; first < t.top; first += 64) {
+      const uint32_t j = first + (lane & 15);
+      const float z = dots_16<T>(h, m, j < t.top ? target_of(t, m, j) : -1);
+      if (j < t.top && (lane & 15) / 4 == lane / 16) sv.picked[(uint64_t)m * t.top + j] = z;
     }
   }
   // over a row's S threads, in a fixed order
@@ -236,8 +269,8 @@ __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t row
   }
   const float all = join(mx, most), ref = all == none ? 0.f : all;
   s = join(s * exp2_(mx - ref), add);
-  const float lse2 = ref + __builtin_amdgcn_logf(s);  // base 2
-  const float lse = lse2 * kLn2;
+  const float over = __builtin_amdgcn_logf(s), lse2 = ref + over;  // base 2
+  const float c = kLog2e / t.temp;
   const uint32_t per = t.top ? t.top : 1;
   // the target's softmax over its entries
   float tm = none, any = 0.f;
@@ -257,13 +290,13 @@ __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t row
   float l = 0.f;
   for (uint32_t j = sl; in && j < per; j += S)
     if (target_of(t, m, j) >= 0) {
-      const float z = sv.picked[(uint64_t)m * per + j];
+      // -log q; 2^(c z - ref) is one of the terms of s
+      const float nlq = ((ref - sv.picked[(uint64_t)m * per + j] * c) + over) * kLn2;
       if (!t.top) {
-        l = lse - z;
-        l = l < 0.f ? 0.f : l;  // z is one of the terms under the logarithm
+        l = nlq;
       } else {
         const float d = teacher_at(t, m, j) / t.temp - tref, w = expf(d) / ts;
-        if (!(w == 0.f)) l += w * ((d - lts) - (z / t.temp - lse));
+        if (!(w == 0.f)) l += w * ((d - lts) + nlq);
       }
     }
   l = join(l, add) * (t.top ? t.temp * t.temp : 1.f);
@@ -338,6 +371,7 @@ __global__ __launch_bounds__(1024) void row_factors(const uint32_t *state, uint3
 template <class T>
 __global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved sv, uint32_t v0, uint32_t nv, float c,
                                                   float mul, uint16_t *dz, uint32_t ldz) {
+#pragma clang fp contract(off)  // as in EpiStats
   __shared__ int32_t ids[kMaxTop];
   __shared__ float ws[kMaxTop];
   const uint32_t m = blockIdx.x, lane = threadIdx.x, per = t.top ? t.top : 1;
@@ -480,19 +514,19 @@ df_status loss_rows(const df_loss *d, float *loss, const Saved &sv, uint8_t *ws,
   const Targets t = targets_of(d);
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
   const Head h = {x, head, d->x_stride, d->head_stride, k};
-  // few rows with few targets: 96 rows of 16 x 1024, one launch less of 4.5 us; 64
+  // few rows with few entries: 96 rows of 16 x 1024, one launch less of 4.5 us; 64
   // x 4096 in four waves would take longer than the launch
-  const bool pick = rows <= 256 && (uint64_t)per_row(d) * k <= 32768;
-  if (!pick) {
-    const uint64_t groups = ((uint64_t)rows * per_row(d) + 3) / 4;
-    hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)(groups < 1u << 20 ? groups : 1u << 20)), dim3(256), 0, s, t, rows, h, sv.picked);
+  const bool pick = d->top && rows <= 256 && (uint64_t)d->top * k <= 32768;
+  if (d->top && !pick) {
+    const uint64_t groups = ((uint64_t)rows * d->top + 15) / 16;
+    hipLaunchKernelGGL((pick_logits<T>), dim3((uint32_t)(groups < 1u << 20 ? groups : 1u << 20)), dim3(64), 0, s, t, rows, h, sv.picked);
     DFH_TRY(hipGetLastError());
   }
   float2 *parts = (float2 *)ws;
   const RowCut cut = rows_for(rows, vocab, k, false);
   const Parts np = parts_of(cut, vocab);
   const Gemm g = {x, head, d->x_stride, d->head_stride, rows, vocab, k, 0, 0, 0, 0};
-  DFH_TRY((product_rows<T, false>(g, EpiStats{parts, rows, kLog2e / d->temperature}, cut, s)));
+  DFH_TRY((product_rows<T, false>(g, EpiStats{parts, rows, kLog2e / d->temperature, d->top ? nullptr : d->labels, sv.picked}, cut, s)));
   float *per = d->reduce == DF_REDUCE_NONE ? loss : (float *)(ws + parts_bytes(d));
   auto *fn = pick ? finish_rows<T, 1, true> : rows <= 256 ? finish_rows<T, 1, false> : finish_rows<T, 8, false>;
   hipLaunchKernelGGL(fn, dim3(rows <= 256 ? rows : (rows + 7) / 8), dim3(256), 0, s, t, rows, (const float2 *)parts, np,
