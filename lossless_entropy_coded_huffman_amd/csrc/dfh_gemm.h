@@ -59,6 +59,24 @@ __device__ __forceinline__ uint32_t pack2(T t, float lo, float hi) {
   return (uint32_t)to_bits(t, lo) | ((uint32_t)to_bits(t, hi) << 16);
 }
 
+// FP16 operands made here are lifted into its range by a power of two that the
+// FP32 sums lose again: the one that brings their largest size to 2^to .. 2^(to + 1).
+__device__ __forceinline__ int lift_bits(float largest, int to) {
+  if (largest == 0.f) return 0;
+  const int f = to - ((int)(__float_as_uint(largest) >> 23) - 127);
+  return f < -112 ? -112 : f > 112 ? 112 : f;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// The largest v of a workgroup of 256.
+__device__ __forceinline__ float most_of_256(float v) {
+  __shared__ float top[4];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
+  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return __builtin_fmaxf(__builtin_fmaxf(top[0], top[1]), __builtin_fmaxf(top[2], top[3]));
+}
+
 // Wait until all but the N youngest loads of this wave (to LDS too) have landed:
 // vmcnt(N), N < 64.
 template <int N>

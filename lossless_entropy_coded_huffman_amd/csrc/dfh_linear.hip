@@ -552,21 +552,6 @@ __device__ __forceinline__ float size_at(const U4 &w, const S *p) {
   const float v = __builtin_fabsf(scale_of(w, *p));
   return v < __builtin_huge_valf() ? v : 0.f;  // where not finite, all results are as they are
 }
-__device__ __forceinline__ float most_of_256(float v) {
-  __shared__ float top[4];
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
-  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return __builtin_fmaxf(__builtin_fmaxf(top[0], top[1]), __builtin_fmaxf(top[2], top[3]));
-}
-__device__ __forceinline__ int lift_bits(float peak) {
-  if (peak == 0.f) return 0;
-  const int f = 6 - ((int)(__float_as_uint(peak) >> 23) - 127);
-  return f < -112 ? -112 : f > 112 ? 112 : f;
-}
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
 // The largest finite scale of the matrix in 256 parts.
 template <class S>
 __global__ __launch_bounds__(256) void scale_peaks(const U4 w, float *peaks) {
@@ -612,7 +597,7 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out, cons
     } else {
       for (uint32_t g = threadIdx.x; g < w.groups; g += 256) v = __builtin_fmaxf(v, size_at(w, ps + g));
     }
-    const int bits = lift_bits(most_of_256(v));
+    const int bits = lift_bits(most_of_256(v), 6);
     up = power_of_two(bits);
     if (threadIdx.x == 0 && blockIdx.y == 0) {
       if (!lift.peaks) {

@@ -405,14 +405,45 @@ __global__ __launch_bounds__(64) void fix_targets(const Targets t, const Saved s
   }
 }
 
+// FP16: the largest finite |gn[m] x[m, c]| in 256 parts.
+__global__ __launch_bounds__(256) void weighed_peaks(const uint16_t *x, uint64_t xs, uint32_t rows, uint32_t k,
+                                                     const float *gn, float *peaks) {
+  float most = 0.f;
+  for (uint32_t m = blockIdx.x; m < rows; m += 256) {
+    const float f = __builtin_fabsf(gn[m]);
+    if (!(f > 0.f)) continue;  // uniform; whatever x holds there
+    for (uint32_t c = threadIdx.x; c < k / 8; c += 256) {
+      const u32x4 v = *(const u32x4 *)(x + m * xs + c * 8);
+#pragma unroll
+      for (int d = 0; d < 4; d++) {
+        const float a = __builtin_fabsf(from_bits(F16{}, (uint16_t)v[d])), b = __builtin_fabsf(from_bits(F16{}, (uint16_t)(v[d] >> 16)));
+        most = __builtin_fmaxf(most, a < __builtin_huge_valf() ? a * f : 0.f);
+        most = __builtin_fmaxf(most, b < __builtin_huge_valf() ? b * f : 0.f);
+      }
+    }
+  }
+  most = most_of_256(most);
+  if (threadIdx.x == 0) peaks[blockIdx.x] = most;
+}
+
 // out[c, m] = gn[m] x[m, c] (gn null: x), zeros in rows without a loss (whatever x holds
 // there) and in the columns that pad a row to mp: what dhead's sum over the rows
 // takes for x, so dz needs no row factor; turned, so that only dz is read across
 // there.  64 x 64 tiles through LDS, padded rows spread the column writes.
+// With row factors a product is rounded once more, to 2^-8 of itself (BF16) or, lifted
+// by the power of two that *back takes off, to 2^-11 or 2^-39 of the largest (FP16):
+// the price of 16-bit operands, which dhead rows of small factors pay alike.
 template <class T>
 __global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs, uint32_t rows, uint32_t k,
-                                                  const uint32_t *state, const float *gn, uint16_t *out, uint32_t mp) {
+                                                  const uint32_t *state, const float *gn, const float *peaks,
+                                                  float *back, uint16_t *out, uint32_t mp) {
   __shared__ uint16_t tile[64][72];  // [c][m]
+  float lift = 1.f;
+  if (peaks) {
+    const int bits = lift_bits(most_of_256(peaks[threadIdx.x]), 14);
+    lift = power_of_two(bits);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *back = power_of_two(-bits);
+  }
   const uint32_t m0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
 #pragma unroll
   for (uint32_t t = threadIdx.x; t < 512; t += 256) {
@@ -420,7 +451,7 @@ __global__ __launch_bounds__(256) void weigh_rows(const uint16_t *x, uint64_t xs
     u32x4 v = {0, 0, 0, 0};
     if (m < rows && c0 + c * 8 < k && state[m] == kLoss) {
       v = *(const u32x4 *)(x + m * xs + c0 + c * 8);
-      const float f = gn ? gn[m] : 1.f;
+      const float f = gn ? gn[m] * lift : 1.f;
 #pragma unroll
       for (int d = 0; gn && d < 4; d++)
         v[d] = pack2(T{}, from_bits(T{}, (uint16_t)v[d]) * f, from_bits(T{}, (uint16_t)(v[d] >> 16)) * f);
@@ -559,7 +590,7 @@ Plan plan_of(const df_loss *d, bool want_dx, bool want_dhead) {
     at += up(bytes, 256);
     return o;
   };
-  p.fac = take(4 * (rows + 2));
+  p.fac = take(4 * (2 + 256 + rows));
   p.dz = take(2 * rows * nv);
   p.xm = take(want_dhead ? 2 * up(rows, 8) * k : 0);
   p.planes = take(want_dx ? 4ull * p.splits().most() * rows * k : 0);
@@ -576,15 +607,19 @@ df_status loss_grad(const df_loss *d, const Saved &sv, const float *grad, uint16
   const Targets t = targets_of(d);
   const uint16_t *x = (const uint16_t *)d->x, *head = (const uint16_t *)d->head;
   const float c = kLog2e / d->temperature;
-  float *peak = (float *)(ws + p.fac), *gn = peak + 2;
+  float *peak = (float *)(ws + p.fac), *peaks = peak + 2, *gn = peaks + 256;
   uint16_t *dz = (uint16_t *)(ws + p.dz), *xm = (uint16_t *)(ws + p.xm);
   float *planes = (float *)(ws + p.planes);
   const bool own = d->reduce == DF_REDUCE_NONE;  // every row has its own gradient
   if (own && dhead)
     hipLaunchKernelGGL(row_factors, dim3(1), dim3(1024), 0, s, (const uint32_t *)sv.state, rows, grad, gn, peak);
+  const bool lifted = own && d->type == DF_TYPE_F16;
+  if (lifted && dhead)
+    hipLaunchKernelGGL(weighed_peaks, dim3(256), dim3(256), 0, s, x, d->x_stride, rows, k, (const float *)gn, peaks);
   if (dhead)
     hipLaunchKernelGGL((weigh_rows<T>), dim3((mp + 63) / 64, (k + 63) / 64), dim3(256), 0, s, x, d->x_stride, rows, k,
-                       (const uint32_t *)sv.state, own ? (const float *)gn : (const float *)nullptr, xm, mp);
+                       (const uint32_t *)sv.state, own ? (const float *)gn : (const float *)nullptr,
+                       lifted ? (const float *)peaks : (const float *)nullptr, peak + 1, xm, mp);
   DFH_TRY(hipGetLastError());
   for (uint32_t v0 = 0; v0 < vocab; v0 += p.nv) {
     const uint32_t nv = vocab - v0 < p.nv ? vocab - v0 : p.nv, ldz = (uint32_t)up(nv, 8);

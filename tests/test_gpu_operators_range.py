@@ -119,3 +119,38 @@ def test_a_large_input_at_a_zero_weight(torch, m, k, group, zeros):
     ref = (x.double() @ w64.t()).to(torch.bfloat16)
     assert float(ref.abs().max()) > 0
     assert torch.equal(dfh.linear_u4(x.to(D), w).cpu(), ref)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("m,v,h", [(64, 300, 64), (300, 2049, 136)])
+def test_rows_with_gradients_of_all_sizes(torch, m, v, h, dtype):
+    # reduction "none": dhead of an entry that only rows of small gradients name keeps
+    # its bits beside rows whose gradient is 10^7 times as large
+    dt, D = getattr(torch, dtype), dev(torch)
+    g = torch.Generator().manual_seed(m)
+    x = torch.randn(m, h, generator=g).to(dt)
+    head = (torch.randn(v, h, generator=g) * (40 / h ** 0.5)).to(dt)   # sure of one entry each
+    labels = torch.randperm(v, generator=g)[:m]
+    gout = 1024 * 10.0 ** (torch.rand(m, generator=g) * -7)
+    labels[3] = -100
+    x[3] = float("inf")
+    hs = head.to(D).requires_grad_()
+    loss = dfh.vocab_loss(x.to(D), hs, labels.to(D), reduction="none")
+    dh, = torch.autograd.grad(loss, hs, gout.to(D))
+    valid = labels >= 0
+    xz = x.double().masked_fill(~valid[:, None], 0.0)
+    z = xz @ head.double().t()
+    q = torch.softmax(z, 1)
+    t = torch.zeros_like(q).scatter(1, labels.clamp(min=0)[:, None], 1.0)
+    d = q - t
+    u, gw = half_ulp(torch, dt), gout.double() * valid
+    # p is off by twice its logits' error and float32 steps of the exponent, then rounded
+    # to 16 bits (FP16 times 2^15), and x times a row's gradient is rounded as well
+    dz = ((h + 8) * E * (xz.abs() @ head.double().abs().t())).amax(1)
+    lse, zt = torch.logsumexp(z, 1).abs(), z.abs().amax(1)
+    ed = (2 * dz[:, None] + 8 * E * (lse[:, None] + zt[:, None] + 4)) * q * 1.01 + 4 * E * t
+    ed = (ed * (1 + u) + u * d.abs() + (2.0 ** -40 if dt == torch.float16 else 2.0 ** -134)) * (1 + u) + u * d.abs()
+    ref = (d * gw[:, None]).t() @ xz
+    floor = 2.0 ** -39 * (gw[:, None] * xz.abs()).max() * 1.01 * (d.abs() + ed).sum(0)[:, None]
+    bound = ((ed + (m + 64) * E * d.abs()) * gw[:, None]).t() @ xz.abs() * (1 + 8 * E) + floor
+    within(dh, ref, bound * (1 + u) + (u + 8 * E) * ref.abs() + tiny(torch, dt))
