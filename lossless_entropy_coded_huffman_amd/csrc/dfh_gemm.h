@@ -133,9 +133,9 @@ __device__ __forceinline__ uint32_t swz_across(uint32_t k) {
   return R == 32 ? (k >> 2) & 2u : R == 64 ? (k & 2u) | ((k >> 1) & 4u) : ((k & 3u) << 1) | (k & 8u);
 }
 
-// Tile of a workgroup.  Workgroups go to the eight XCDs in turn, so workgroup
-// id works on tile (id % 8) * ceil(tiles / 8) + id / 8: an XCD gets a contiguous
-// run of tiles (m fastest), whose B panels its L2 then holds once.
+// Tile of a workgroup.  Workgroups go to the eight XCDs in turn, so XCD id % 8 gets
+// a contiguous run of tiles (m fastest), whose B panels its L2 then holds once:
+// floor(tiles / 8) of them, and one more in the first tiles % 8 XCDs.
 __device__ __forceinline__ uint32_t xcd_tile(uint32_t id, uint32_t tiles) {
   const uint32_t per = tiles / 8, rem = tiles % 8, x = id % 8, l = id / 8;
   return x * per + (x < rem ? x : rem) + l;

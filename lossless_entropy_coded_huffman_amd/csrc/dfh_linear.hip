@@ -132,67 +132,62 @@ __device__ float dot_plain(const U4 &w, const uint16_t *xr, uint32_t n) {
 
 // A byte 8 where a matrix has no zero points, read like any other.
 __device__ const uint32_t g_eights = 0x08080808u;
+// Says that zero points lie in global memory: a choice between the caller's and
+// g_eights hides it, and flat loads wait for LDS as well (14336 x 4096 for a token:
+// 11.4 us against 10.5).
+typedef const __attribute__((address_space(1))) uint8_t *GlobalBytes;
 
-// A wave's rows of the weights (16 NT of them, row n0 + 16 j + lane % 16) as
-// the operands below want them.  SUB, the groups that 128 elements hold (1, 2,
+// A wave's 16 rows of the weights (row n0 + lane % 16) as the operands below want
+// them.  SUB, the groups that 128 elements hold (1, 2,
 // 4), fixes how scales and zero points are read: a stage's 4 SUB (blocks of 128)
 // in a row where the group size is 128 / SUB, one by one otherwise (SUB = 4: any
 // multiple of 32; 0: a multiple of 128, or one group a row).  Raw values are
 // kept and converted at their use: a conversion at the load would wait for it.
-template <int NT, int BLOCKS, int SUB, class S>
+template <int BLOCKS, int SUB, class S>
 struct Scales {
   static constexpr int G = SUB ? SUB : 1, N = BLOCKS * G;
-  const S *ps[NT];
-  const uint8_t *pz[NT];
-  S raw[NT][N];
-  uint32_t zero[NT][(N + 3) / 4];  // four a word
+  const S *ps;
+  GlobalBytes pz;
+  S raw[N];
+  uint32_t zero[(N + 3) / 4];  // four a word
   __device__ __forceinline__ void rows(const U4 &w, uint32_t n0, uint32_t lr) {
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const uint32_t n = n0 + j * 16 + lr, nn = n < w.n ? n : w.n - 1;
-      ps[j] = (const S *)w.scales + nn * w.sstride;
-      pz[j] = w.zeros ? w.zeros + nn * w.zstride : (const uint8_t *)&g_eights;
-    }
+    const uint32_t n = n0 + lr, nn = n < w.n ? n : w.n - 1;
+    ps = (const S *)w.scales + nn * w.sstride;
+    pz = (GlobalBytes)(w.zeros ? w.zeros + nn * w.zstride : (const uint8_t *)&g_eights);
   }
   // those of the blocks at element 32 * b32 on
   __device__ __forceinline__ void request(const U4 &w, uint32_t b32) {
     const uint32_t zon = w.zeros ? 1 : 0;
     const uint32_t g0 = b32 / 4 * G;
     if (SUB && w.group32 * SUB == 4 && g0 + N <= w.groups) {
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        __builtin_memcpy(&raw[j], ps[j] + g0, sizeof raw[j]);
-        if (zon) {
-          if constexpr (N % 4 == 0) {
-            __builtin_memcpy(&zero[j], pz[j] + g0, N);
-          } else {
-            uint16_t h;
-            if constexpr (N == 2) __builtin_memcpy(&h, pz[j] + g0, 2);
-            if constexpr (N == 1) h = pz[j][g0];
-            zero[j][0] = h;
-          }
+      __builtin_memcpy(&raw, ps + g0, sizeof raw);
+      if (zon) {
+        if constexpr (N % 4 == 0) {
+          __builtin_memcpy(&zero, (const uint8_t *)(pz + g0), N);
         } else {
-#pragma unroll
-          for (int g = 0; g < (N + 3) / 4; g++) zero[j][g] = 0x08080808u;
+          uint16_t h;
+          if constexpr (N == 2) __builtin_memcpy(&h, (const uint8_t *)(pz + g0), 2);
+          if constexpr (N == 1) h = pz[g0];
+          zero[0] = h;
         }
+      } else {
+#pragma unroll
+        for (int g = 0; g < (N + 3) / 4; g++) zero[g] = 0x08080808u;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-#pragma unroll
-        for (int g = 0; g < N; g++) {
-          uint32_t gi = group_of(w, b32 + g * (4 / G));
-          gi = gi < w.groups ? gi : w.groups - 1;
-          raw[j][g] = ps[j][gi];
-          const uint32_t zb = pz[j][gi * zon];
-          zero[j][g / 4] = (g & 3 ? zero[j][g / 4] : 0) | zb << (8 * (g & 3));
-        }
+      for (int g = 0; g < N; g++) {
+        uint32_t gi = group_of(w, b32 + g * (4 / G));
+        gi = gi < w.groups ? gi : w.groups - 1;
+        raw[g] = ps[gi];
+        const uint32_t zb = pz[gi * zon];
+        zero[g / 4] = (g & 3 ? zero[g / 4] : 0) | zb << (8 * (g & 3));
       }
     }
   }
-  __device__ __forceinline__ float scale(const U4 &w, int j, int g) const { return scale_of(w, raw[j][g]); }
-  __device__ __forceinline__ float zero_point(int j, int g) const {
-    return (float)((zero[j][g / 4] >> (8 * (g & 3))) & 255u);
+  __device__ __forceinline__ float scale(const U4 &w, int g) const { return scale_of(w, raw[g]); }
+  __device__ __forceinline__ float zero_point(int g) const {
+    return (float)((zero[g / 4] >> (8 * (g & 3))) & 255u);
   }
 };
 
@@ -219,38 +214,30 @@ __device__ __forceinline__ float scaled(float acc, float s, float z, float t, fl
 }
 
 // The last k % 32 elements of the rows, one matrix step from guarded dwords:
-// adds to acc[j][i][0 .. J).  px: this lane's rows of x.
-template <class T, int J, int MT, int NT, class Acc>
+// adds to acc[i][0 .. J).  px: this lane's rows of x.
+template <class T, int J, int MT, class Acc>
 __device__ __forceinline__ void row_ends(const U4 &w, uint32_t n0, const uint16_t *const (&px)[MT], Acc &acc) {
   const uint32_t lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
   const uint32_t k32 = w.k & ~31u, k = k32 + kg * 8;
   const uint32_t one = (uint32_t)to_bits(T{}, 1.f) * 0x10001u;
   const uint32_t g = group_of(w, k32 / 32);
-  u32x4 xp[MT];
-  f32x4 sx[MT];
+  const uint32_t n = n0 + lr, nn = n < w.n ? n : w.n - 1;
+  uint32_t q = 0;
+  if (k < w.k) q = *(const uint32_t *)(w.packed + ((uint64_t)nn * w.k + k) / 2);
+  const float s = scale_at(w, nn, g), z = zero_at(w, nn, g);
+  const u32x4 f = widen<T>(q, minus_pair<T>(Bias<T>::value + z));
 #pragma unroll
   for (int i = 0; i < MT; i++) {
-    xp[i] = u32x4{0, 0, 0, 0};
-    if (k < w.k) xp[i] = *(const u32x4 *)(px[i] + k);
-    sx[i] = mfma(T{}, xp[i], u32x4{one, one, one, one}, f32x4{0.f, 0.f, 0.f, 0.f});
-  }
+    u32x4 xp = {0, 0, 0, 0};
+    if (k < w.k) xp = *(const u32x4 *)(px[i] + k);
+    const f32x4 sx = mfma(T{}, xp, u32x4{one, one, one, one}, f32x4{0.f, 0.f, 0.f, 0.f});
+    const f32x4 t = mfma(T{}, xp, f, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-  for (int j = 0; j < NT; j++) {
-    const uint32_t n = n0 + j * 16 + lr, nn = n < w.n ? n : w.n - 1;
-    uint32_t q = 0;
-    if (k < w.k) q = *(const uint32_t *)(w.packed + ((uint64_t)nn * w.k + k) / 2);
-    const float s = scale_at(w, nn, g), z = zero_at(w, nn, g);
-    const u32x4 f = widen<T>(q, minus_pair<T>(Bias<T>::value + z));
-#pragma unroll
-    for (int i = 0; i < MT; i++) {
-      const f32x4 t = mfma(T{}, xp[i], f, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-      for (int r = 0; r < J; r++) acc[j][i][r] = scaled<T>(acc[j][i][r], s, z, t[r], sx[i][r]);
-    }
+    for (int r = 0; r < J; r++) acc[i][r] = scaled<T>(acc[i][r], s, z, t[r], sx[r]);
   }
 }
 
-// y for up to four rows (tokens).  A workgroup makes 16 NT columns; each wave
+// y for up to four rows (tokens).  A workgroup makes 16 columns; each wave
 // has a part of the summed index, in stages of 512 elements, and the waves add
 // up through LDS.  Matrix operand A is x, B the weights (16 columns n): lane l
 // holds 16 bytes of weight row l % 16.  BF16: T = sum x (bias + q) and
@@ -266,19 +253,19 @@ __device__ __forceinline__ void row_ends(const U4 &w, uint32_t n0, const uint16_
 // do not meet before the sum; a stage is requested while the one before is
 // used.  LDS rows hold their 16-byte chunks at position chunk ^ row, exchanged
 // in the source address.
-template <class T, int NT, int W, int SUB, class S>
+template <class T, int W, int SUB, class S>
 __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *x, uint64_t xs, uint32_t m,
                                                     uint16_t *y) {
   extern __shared__ __align__(1024) uint8_t lds[];
-  typedef Scales<NT, 4, SUB, S> Sc;
+  typedef Scales<4, SUB, S> Sc;
   constexpr int G = Sc::G;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lr = lane & 15, kg = lane >> 4;
-  const uint32_t n0 = blockIdx.x * (16 * NT);
+  const uint32_t n0 = blockIdx.x * 16;
   const uint32_t k32 = w.k & ~31u;
   const uint32_t stages = (k32 + 511) / 512, per = (stages + W - 1) / W;
   const uint32_t s0 = wave * per, s1 = s0 + per < stages ? s0 + per : stages;
-  const uint32_t bytes = NT * 4096 + m * 1024;  // a buffer
+  const uint32_t bytes = 4096 + m * 1024;  // a buffer
   const uint32_t step = per > 1 ? bytes : 0;    // one buffer is enough for one stage
   uint8_t *buf = lds + wave * (bytes + step);
   const uint32_t one = (uint32_t)to_bits(T{}, 1.f) * 0x10001u;
@@ -287,43 +274,38 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
   Sc next, now;
   next.rows(w, n0, lr);
   // this lane's 16 bytes of four weight rows a load
-  const uint8_t *src[NT][4];
+  const uint8_t *src[4];
 #pragma unroll
-  for (int j = 0; j < NT; j++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t r = i * 4 + (lane >> 4), n = n0 + j * 16 + r;
-      src[j][i] = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2) + ((lane & 15) ^ r) * 16;
-    }
+  for (int i = 0; i < 4; i++) {
+    const uint32_t r = i * 4 + (lane >> 4), n = n0 + r;
+    src[i] = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2) + ((lane & 15) ^ r) * 16;
+  }
   auto request = [&](uint32_t st, uint8_t *dst) {
     const bool whole = st * 512 + 512 <= k32;  // uniform
+    const uint8_t *p[4];
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const uint8_t *p[4];
+    for (int i = 0; i < 4; i++) {
+      p[i] = src[i] + st * 256;
+      if (!whole && st * 512 + ((lane & 15) ^ (i * 4 + (lane >> 4))) * 32 >= k32) p[i] = (const uint8_t *)&g_zero16;
+    }
+    if (w.once) {  // uniform
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        p[i] = src[j][i] + st * 256;
-        if (!whole && st * 512 + ((lane & 15) ^ (i * 4 + (lane >> 4))) * 32 >= k32) p[i] = (const uint8_t *)&g_zero16;
-      }
-      if (w.once) {  // uniform
+      for (int i = 0; i < 4; i++) to_lds<true>(p[i], dst + i * 1024);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) to_lds<true>(p[i], dst + j * 4096 + i * 1024);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) to_lds(p[i], dst + j * 4096 + i * 1024);
-      }
+      for (int i = 0; i < 4; i++) to_lds(p[i], dst + i * 1024);
     }
     for (uint32_t r = 0; r < m; r++) {
       const uint32_t k = st * 512 + (lane ^ r) * 8;
-      to_lds(k < k32 ? (const void *)(x + r * xs + k) : (const void *)&g_zero16, dst + NT * 4096 + r * 1024);
+      to_lds(k < k32 ? (const void *)(x + r * xs + k) : (const void *)&g_zero16, dst + 4096 + r * 1024);
     }
     next.request(w, st * 16);
   };
-  float acc[NT][1][1] = {};
+  float acc[1][1] = {};
   if (s0 < s1) request(s0, buf);
   if (k32 < w.k && wave == W - 1) {
     const uint16_t *px[1] = {x + xr * xs};
-    row_ends<T, 1, 1, NT>(w, n0, px, acc);
+    row_ends<T, 1, 1>(w, n0, px, acc);
   }
   for (uint32_t st = s0; st < s1; st++) {
     uint8_t *p = buf + ((st - s0) & 1) * step;
@@ -334,11 +316,11 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
     if (st + 1 < s1) request(st + 1, buf + ((st + 1 - s0) & 1) * step);
     // x into widen_pairs' order where it lies: once a stage, 16 bytes a lane
     for (uint32_t r = 0; r < m; r++) {
-      u32x4 *c = (u32x4 *)(p + NT * 4096 + r * 1024) + lane;
+      u32x4 *c = (u32x4 *)(p + 4096 + r * 1024) + lane;
       *c = pair_up(*c);
     }
     asm volatile("" ::: "memory");
-    const uint8_t *px = p + NT * 4096 + xr * 1024;
+    const uint8_t *px = p + 4096 + xr * 1024;
 #pragma unroll
     for (int b = 0; b < 4; b++) {
       if (st * 512 + b * 128 >= k32) break;  // uniform
@@ -350,34 +332,29 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
         xp[d] = *(const u32x4 *)(px + (c ^ xr) * 16);
         if constexpr (Bias<T>::in_sum) sx[d * G / 4] = mfma(T{}, xp[d], ones, sx[d * G / 4]);
       }
+      u32x4 q = *(const u32x4 *)(p + lr * 256 + (((b * 4 + kg) ^ lr) * 16));
+      if (SUB > 1) q = by_step(q);
+      f32x4 t[G] = {};
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        u32x4 q = *(const u32x4 *)(p + j * 4096 + lr * 256 + (((b * 4 + kg) ^ lr) * 16));
-        if (SUB > 1) q = by_step(q);
-        f32x4 t[G] = {};
+      for (int d = 0; d < 4; d++)
+        t[d * G / 4] = mfma(T{}, xp[d],
+                            widen_pairs<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(b * G + d * G / 4))),
+                            t[d * G / 4]);
 #pragma unroll
-        for (int d = 0; d < 4; d++)
-          t[d * G / 4] =
-              mfma(T{}, xp[d],
-                   widen_pairs<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(j, b * G + d * G / 4))),
-                   t[d * G / 4]);
-#pragma unroll
-        for (int g = 0; g < G; g++)
-          acc[j][0][0] = scaled<T>(acc[j][0][0], now.scale(w, j, b * G + g), now.zero_point(j, b * G + g), t[g][0], sx[g][0]);
-      }
+      for (int g = 0; g < G; g++)
+        acc[0][0] = scaled<T>(acc[0][0], now.scale(w, b * G + g), now.zero_point(b * G + g), t[g][0], sx[g][0]);
     }
   }
   // every wave has its last buffer behind it; the sums take its place
   __syncthreads();
-  float *part = (float *)lds;  // [W][NT][64]
-#pragma unroll
-  for (int j = 0; j < NT; j++) part[(wave * NT + j) * 64 + lane] = acc[j][0][0];
+  float *part = (float *)lds;  // [W][64]
+  part[wave * 64 + lane] = acc[0][0];
   __syncthreads();
-  for (uint32_t t = threadIdx.x; t < NT * 64; t += 64 * W) {
-    const uint32_t j = t / 64, mm = (t % 64) / 16, n = n0 + j * 16 + (t & 15);
+  if (wave == 0) {
+    const uint32_t mm = lane / 16, n = n0 + (lane & 15);
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < W; q++) v += part[q * NT * 64 + t];
+    for (int q = 0; q < W; q++) v += part[q * 64 + lane];
     if (mm < m && n < w.n) {
       if (Bias<T>::in_sum && !(__builtin_fabsf(v) < __builtin_huge_valf())) v = dot_plain<T>(w, x + mm * xs, n);
       y[(uint64_t)mm * w.n + n] = to_bits(T{}, v);
@@ -385,22 +362,22 @@ __global__ __launch_bounds__(64 * W) void u4_tokens(const U4 w, const uint16_t *
   }
 }
 
-// y for a tile of 16 MT rows of x and 64 NT weight rows, for row counts between
-// tokens and prompts.  Eight waves: wave w takes weight rows 16 NT (w % 4) .. and
+// y for a tile of 16 MT rows of x and 64 weight rows, for row counts between
+// tokens and prompts.  Eight waves: wave w takes weight rows 16 (w % 4) .. and
 // the block w / 4 of a stage's two blocks of 128 elements; all share the stage's
 // x in LDS.  Arithmetic as in u4_tokens, all four result rows of a lane used.
 // blockIdx.y: split of the summed index; a split's sums go to its FP32 plane
 // (one split: straight to y).
-template <class T, int MT, int NT, int SUB, class S>
+template <class T, int MT, int SUB, class S>
 __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, uint64_t xs, uint32_t m, uint32_t mt,
                                                uint32_t per, uint16_t *y, float *planes, uint32_t ld) {
   extern __shared__ __align__(1024) uint8_t lds[];
-  typedef Scales<NT, 1, SUB, S> Sc;
-  constexpr int G = Sc::G, BN = 64 * NT, BM = 16 * MT;
+  typedef Scales<1, SUB, S> Sc;
+  constexpr int G = Sc::G, BN = 64, BM = 16 * MT;
   constexpr uint32_t kBuf = BN * 128 + BM * 512;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lr = lane & 15, kg = lane >> 4, wn = wave & 3, wk = wave >> 2;
-  const uint32_t m0 = blockIdx.x % mt * BM, nb = blockIdx.x / mt * BN, n0 = nb + wn * 16 * NT;
+  const uint32_t m0 = blockIdx.x % mt * BM, nb = blockIdx.x / mt * BN, n0 = nb + wn * 16;
   const uint32_t rows = m - m0 < BM ? m - m0 : BM;
   const uint32_t k32 = w.k & ~31u, stages = (k32 + 255) / 256;
   const uint32_t s0 = blockIdx.y * per, s1 = s0 + per < stages ? s0 + per : stages;
@@ -408,12 +385,9 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
   const u32x4 ones = {one, one, one, one};
   Sc next, now;
   next.rows(w, n0, lr);
-  const uint8_t *wsrc[NT];  // 8 weight rows of 128 bytes a load
-#pragma unroll
-  for (int i = 0; i < NT; i++) {
-    const uint32_t r = (i * 8 + wave) * 8 + lane / 8, n = nb + r;
-    wsrc[i] = w.packed + (uint64_t)(n < w.n ? n : w.n - 1) * (w.k / 2) + ((lane & 7) ^ swz(r)) * 16;
-  }
+  // 8 weight rows of 128 bytes a load
+  const uint32_t wr = wave * 8 + lane / 8, wrow = nb + wr < w.n ? nb + wr : w.n - 1;
+  const uint8_t *wsrc = w.packed + (uint64_t)wrow * (w.k / 2) + ((lane & 7) ^ swz(wr)) * 16;
   const uint16_t *xsrc[MT];  // 2 rows of x a load
 #pragma unroll
   for (int i = 0; i < MT; i++) {
@@ -422,12 +396,9 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
   }
   auto request = [&](uint32_t st, uint8_t *dst) {
     const bool whole = st * 256 + 256 <= k32;  // uniform
-#pragma unroll
-    for (int i = 0; i < NT; i++) {
-      const uint8_t *p = wsrc[i] + st * 128;
-      if (!whole && st * 256 + ((lane & 7) ^ swz((i * 8 + wave) * 8 + lane / 8)) * 32 >= k32) p = (const uint8_t *)&g_zero16;
-      to_lds(p, dst + (i * 8 + wave) * 1024);
-    }
+    const uint8_t *q = wsrc + st * 128;
+    if (!whole && st * 256 + ((lane & 7) ^ swz(wr)) * 32 >= k32) q = (const uint8_t *)&g_zero16;
+    to_lds(q, dst + wave * 1024);
 #pragma unroll
     for (int i = 0; i < MT; i++) {
       const uint32_t pair = i * 8 + wave;
@@ -438,13 +409,13 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
     }
     next.request(w, st * 8 + wk * 4);
   };
-  f32x4 acc[NT][MT] = {};
+  f32x4 acc[MT] = {};
   if (s0 < s1) request(s0, lds);
   if (k32 < w.k && blockIdx.y == 0 && wk == 1) {
     const uint16_t *px[MT];
 #pragma unroll
     for (int i = 0; i < MT; i++) px[i] = x + (uint64_t)(m0 + (i * 16 + lr < rows ? i * 16 + lr : rows - 1)) * xs;
-    row_ends<T, 4, MT, NT>(w, n0, px, acc);
+    row_ends<T, 4, MT>(w, n0, px, acc);
   }
   for (uint32_t st = s0; st < s1; st++) {
     const uint8_t *p = lds + ((st - s0) & 1) * kBuf;
@@ -453,14 +424,10 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
     now = next;
     if (st + 1 < s1) request(st + 1, lds + ((st + 1 - s0) & 1) * kBuf);
     if (st * 256 + wk * 128 < k32) {
-      const uint8_t *px = p + BN * 128 + lr * 512, *pw = p + (wn * 16 * NT + lr) * 128 + (((wk * 4 + kg) ^ swz(lr)) * 16);
-      u32x4 q[NT];
-      f32x4 t[G][NT][MT] = {}, sx[G][MT] = {};
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        q[j] = *(const u32x4 *)(pw + j * 2048);
-        if (SUB > 1) q[j] = by_step(q[j]);
-      }
+      const uint8_t *px = p + BN * 128 + lr * 512, *pw = p + (wn * 16 + lr) * 128 + (((wk * 4 + kg) ^ swz(lr)) * 16);
+      u32x4 q = *(const u32x4 *)pw;
+      f32x4 t[G][MT] = {}, sx[G][MT] = {};
+      if (SUB > 1) q = by_step(q);
 #pragma unroll
       for (int d = 0; d < 4; d++) {
         constexpr int step = 4 / G;
@@ -471,23 +438,18 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
           xp[i] = *(const u32x4 *)(px + i * 8192 + ((c ^ lr) * 16));
           if constexpr (Bias<T>::in_sum) sx[d / step][i] = mfma(T{}, xp[i], ones, sx[d / step][i]);
         }
+        const u32x4 f = widen<T>(q[d], minus_pair<T>(Bias<T>::value + now.zero_point(d / step)));
 #pragma unroll
-        for (int j = 0; j < NT; j++) {
-          const u32x4 f = widen<T>(q[j][d], minus_pair<T>(Bias<T>::value + now.zero_point(j, d / step)));
-#pragma unroll
-          for (int i = 0; i < MT; i++) t[d / step][j][i] = mfma(T{}, xp[i], f, t[d / step][j][i]);
-        }
+        for (int i = 0; i < MT; i++) t[d / step][i] = mfma(T{}, xp[i], f, t[d / step][i]);
       }
 #pragma unroll
-      for (int g = 0; g < G; g++)
+      for (int g = 0; g < G; g++) {
+        const float s = now.scale(w, g), z = now.zero_point(g);
 #pragma unroll
-        for (int j = 0; j < NT; j++) {
-          const float s = now.scale(w, j, g), z = now.zero_point(j, g);
+        for (int i = 0; i < MT; i++)
 #pragma unroll
-          for (int i = 0; i < MT; i++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) acc[j][i][r] = scaled<T>(acc[j][i][r], s, z, t[g][j][i][r], sx[g][i][r]);
-        }
+          for (int r = 0; r < 4; r++) acc[i][r] = scaled<T>(acc[i][r], s, z, t[g][i][r], sx[g][i][r]);
+      }
     }
   }
   // the second block's waves hand their sums to the first block's
@@ -495,28 +457,23 @@ __global__ __launch_bounds__(512) void u4_tile(const U4 w, const uint16_t *x, ui
   f32x4 *part = (f32x4 *)lds;
   if (wk == 1)
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-      for (int i = 0; i < MT; i++) part[((j * MT + i) * 4 + wn) * 64 + lane] = acc[j][i];
+    for (int i = 0; i < MT; i++) part[(i * 4 + wn) * 64 + lane] = acc[i];
   __syncthreads();
   if (wk == 1) return;
+  const uint32_t n = n0 + lr;
 #pragma unroll
-  for (int j = 0; j < NT; j++) {
-    const uint32_t n = n0 + j * 16 + lr;
+  for (int i = 0; i < MT; i++) {
+    const f32x4 v = acc[i] + part[(i * 4 + wn) * 64 + lane];
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-      const f32x4 v = acc[j][i] + part[((j * MT + i) * 4 + wn) * 64 + lane];
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const uint32_t row = m0 + i * 16 + kg * 4 + r;
-        if (row >= m || n >= w.n) continue;
-        if (planes) {
-          planes[((uint64_t)blockIdx.y * m + row) * ld + n] = v[r];
-        } else {
-          float o = v[r];
-          if (Bias<T>::in_sum && !(__builtin_fabsf(o) < __builtin_huge_valf())) o = dot_plain<T>(w, x + (uint64_t)row * xs, n);
-          y[(uint64_t)row * w.n + n] = to_bits(T{}, o);
-        }
+    for (int r = 0; r < 4; r++) {
+      const uint32_t row = m0 + i * 16 + kg * 4 + r;
+      if (row >= m || n >= w.n) continue;
+      if (planes) {
+        planes[((uint64_t)blockIdx.y * m + row) * ld + n] = v[r];
+      } else {
+        float o = v[r];
+        if (Bias<T>::in_sum && !(__builtin_fabsf(o) < __builtin_huge_valf())) o = dot_plain<T>(w, x + (uint64_t)row * xs, n);
+        y[(uint64_t)row * w.n + n] = to_bits(T{}, o);
       }
     }
   }
@@ -567,9 +524,9 @@ __global__ __launch_bounds__(256) void scale_peaks(const U4 w, float *peaks) {
   if (threadIdx.x == 0) peaks[blockIdx.x] = v;
 }
 
-// The weights as 16-bit floats, [n, k].  Each is rounded once from FP32
-// (relative 2^-8 / 2^-11 at most, but for what is said above); the sums over them
-// are FP32.
+// The weights as 16-bit floats, [n, k]: what the matrix instructions of a long product
+// take.  Each is rounded once from FP32 (relative 2^-8 / 2^-11 at most, but for what is
+// said above); the sums over them are FP32.
 // A workgroup takes 1024 chunks of 8 weights of a row, four a thread, all loaded
 // (scales unconverted) before the first is used.
 template <class T, class S>
@@ -717,24 +674,24 @@ df_status many_rows(const Gemm &g, uint16_t *out, const float *back, float *plan
 
 int sub_of(const U4 &w) { return w.group32 == 4 ? 1 : w.group32 == 2 ? 2 : w.group32 % 4 == 0 ? 0 : 4; }
 
-template <class T, int NT, int W, class S>
+template <class T, int W, class S>
 hipError_t tokens_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, hipStream_t s) {
   const int sub = sub_of(w);
-  auto *fn = sub == 0   ? u4_tokens<T, NT, W, 0, S>
-             : sub == 1 ? u4_tokens<T, NT, W, 1, S>
-             : sub == 2 ? u4_tokens<T, NT, W, 2, S>
-                        : u4_tokens<T, NT, W, 4, S>;
+  auto *fn = sub == 0   ? u4_tokens<T, W, 0, S>
+             : sub == 1 ? u4_tokens<T, W, 1, S>
+             : sub == 2 ? u4_tokens<T, W, 2, S>
+                        : u4_tokens<T, W, 4, S>;
   const uint32_t buffers = (w.k / 32 * 32 + 511) / 512 > W ? 2 : 1;
-  const uint32_t lds = W * buffers * (NT * 4096 + m * 1024);
+  const uint32_t lds = W * buffers * (4096 + m * 1024);
   const hipError_t e = allow_lds((const void *)fn, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3((w.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), lds, s, w, x, xs, m, y);
+  hipLaunchKernelGGL(fn, dim3((w.n + 15) / 16), dim3(64 * W), lds, s, w, x, xs, m, y);
   return hipGetLastError();
 }
-template <class T, int NT, int W>
+template <class T, int W>
 hipError_t tokens_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, hipStream_t s) {
-  return w.scale_type == DF_TYPE_F32 ? tokens_of<T, NT, W, float>(w, x, xs, m, y, s)
-                                     : tokens_of<T, NT, W, uint16_t>(w, x, xs, m, y, s);
+  return w.scale_type == DF_TYPE_F32 ? tokens_of<T, W, float>(w, x, xs, m, y, s)
+                                     : tokens_of<T, W, uint16_t>(w, x, xs, m, y, s);
 }
 
 // How u4_tile cuts a product: splits of the summed index so that up to two
@@ -743,14 +700,13 @@ hipError_t tokens_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m
 // 14336, 64 tiles: one 50, four 18.5, eight 17.7).  A third and fourth buffer a
 // workgroup measured the same.
 struct TilePlan {
-  uint32_t mtile, ntile, mt, splits, per, ld;
+  uint32_t mtile, mt, splits, per, ld;
 };
-TilePlan tile_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t mtile, uint32_t ntile) {
+TilePlan few_plan(uint32_t m, uint32_t n, uint32_t k) {
   TilePlan p;
-  p.mtile = mtile;
-  p.ntile = ntile;
+  p.mtile = m <= 16 ? 1 : m <= 32 ? 2 : 4;
   p.mt = (m + 16 * p.mtile - 1) / (16 * p.mtile);
-  const uint32_t tiles = p.mt * ((n + 64 * p.ntile - 1) / (64 * p.ntile)), stages = (k / 32 * 32 + 255) / 256;
+  const uint32_t tiles = p.mt * ((n + 63) / 64), stages = (k / 32 * 32 + 255) / 256;
   uint32_t want = tiles >= 512 ? 1 : 512 / tiles;
   const uint32_t most = stages / 4 < 1 ? 1 : stages / 4;
   want = want < most ? want : most;
@@ -761,18 +717,18 @@ TilePlan tile_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t mtile, uint32_t 
   return p;
 }
 
-template <class T, int MT, int NT, class S>
+template <class T, int MT, class S>
 hipError_t tile_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, float *planes,
                    const TilePlan &p, hipStream_t s) {
   const int sub = sub_of(w);
-  auto *fn = sub == 0   ? u4_tile<T, MT, NT, 0, S>
-             : sub == 1 ? u4_tile<T, MT, NT, 1, S>
-             : sub == 2 ? u4_tile<T, MT, NT, 2, S>
-                        : u4_tile<T, MT, NT, 4, S>;
-  constexpr uint32_t lds = 2 * (64 * NT * 128 + 16 * MT * 512);
+  auto *fn = sub == 0   ? u4_tile<T, MT, 0, S>
+             : sub == 1 ? u4_tile<T, MT, 1, S>
+             : sub == 2 ? u4_tile<T, MT, 2, S>
+                        : u4_tile<T, MT, 4, S>;
+  constexpr uint32_t lds = 2 * (64 * 128 + 16 * MT * 512);
   hipError_t e = allow_lds((const void *)fn, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(p.mt * ((w.n + 64 * NT - 1) / (64 * NT)), p.splits), dim3(512), lds, s, w, x, xs, m, p.mt,
+  hipLaunchKernelGGL(fn, dim3(p.mt * ((w.n + 63) / 64), p.splits), dim3(512), lds, s, w, x, xs, m, p.mt,
                      p.per, y, p.splits > 1 ? planes : (float *)nullptr, p.ld);
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -780,15 +736,14 @@ hipError_t tile_of(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint
                      p.splits, m, p.ld, y);
   return hipGetLastError();
 }
-template <class T, int MT, int NT>
+template <class T, int MT>
 hipError_t tile_launch(const U4 &w, const uint16_t *x, uint64_t xs, uint32_t m, uint16_t *y, float *planes,
                        const TilePlan &p, hipStream_t s) {
-  return w.scale_type == DF_TYPE_F32 ? tile_of<T, MT, NT, float>(w, x, xs, m, y, planes, p, s)
-                                     : tile_of<T, MT, NT, uint16_t>(w, x, xs, m, y, planes, p, s);
+  return w.scale_type == DF_TYPE_F32 ? tile_of<T, MT, float>(w, x, xs, m, y, planes, p, s)
+                                     : tile_of<T, MT, uint16_t>(w, x, xs, m, y, planes, p, s);
 }
 
 constexpr uint32_t kTokens = 4;
-TilePlan few_plan(uint32_t m, uint32_t n, uint32_t k) { return tile_plan(m, n, k, m <= 16 ? 1 : m <= 32 ? 2 : 4, 1); }
 
 template <class T>
 df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16_t *y, uint8_t *ws, hipStream_t s) {
@@ -798,14 +753,14 @@ df_status linear(const U4 &w, const uint16_t *x, uint32_t m, uint64_t xs, uint16
     // 10.5 us, with 8 11.8), 16 where they give one workgroup a CU or less and the
     // rows are long (4096 x 14336: 10.5 us, with 8 12.0), else 8 (4096 x 4096: 5.3
     // us, with 4 6.0); 16 have LDS for one row of x
-    e = w.n >= 8192                     ? tokens_launch<T, 1, 4>(w, x, xs, m, y, s)
-        : m == 1 && w.n <= 4096 && w.k > 8192 ? tokens_launch<T, 1, 16>(w, x, xs, m, y, s)
-                                        : tokens_launch<T, 1, 8>(w, x, xs, m, y, s);
+    e = w.n >= 8192                     ? tokens_launch<T, 4>(w, x, xs, m, y, s)
+        : m == 1 && w.n <= 4096 && w.k > 8192 ? tokens_launch<T, 16>(w, x, xs, m, y, s)
+                                        : tokens_launch<T, 8>(w, x, xs, m, y, s);
   } else if (few_rows(m, w.n, w.k)) {
     const TilePlan p = few_plan(m, w.n, w.k);
-    e = p.mtile == 1   ? tile_launch<T, 1, 1>(w, x, xs, m, y, (float *)ws, p, s)
-        : p.mtile == 2 ? tile_launch<T, 2, 1>(w, x, xs, m, y, (float *)ws, p, s)
-                       : tile_launch<T, 4, 1>(w, x, xs, m, y, (float *)ws, p, s);
+    e = p.mtile == 1   ? tile_launch<T, 1>(w, x, xs, m, y, (float *)ws, p, s)
+        : p.mtile == 2 ? tile_launch<T, 2>(w, x, xs, m, y, (float *)ws, p, s)
+                       : tile_launch<T, 4>(w, x, xs, m, y, (float *)ws, p, s);
   } else {
     const float *back = expand<T>(w, ws, false, s);
     Gemm g = {x, (const uint16_t *)ws, xs, w.k, m, w.n, w.k, 0, 0, 0, 0};

@@ -16,7 +16,8 @@ batched product takes contiguous operands.
 The EntroLLM summary ("Metodologia") stores quantised weights instead.
 ``QuantizedBlocks`` runs the same blocks from uint4 containers: a block's seven
 layers are decoded in one batch to packed nibbles and multiplied as they are
-(``linear_u4``), so no dequantised copy is kept; gradients to the activations
+(``linear_u4``; a long prompt and a gradient expand one layer at a time in a call's
+workspace), so no dequantised copy is kept; gradients to the activations
 decode a block again.  ``CompressedHead`` holds an LM head as one BF16 container
 and scores hidden states against it (``vocab_loss``, ``distill_loss``): what the
 quantised model loses against the lossless one, and the gradient to mend it.
@@ -223,7 +224,9 @@ class QuantizedBlocks:
 
     layers: per block a list of (container, scales, zeros) in
     BlockShape.matrices() order, as quantize_block makes them; scales [rows,
-    groups] in float32 (kept in scale_dtype), zeros uint8 of that shape or None.
+    groups] in float32, zeros uint8 of that shape or None.  Scales are kept in
+    scale_dtype: bfloat16, the weights' own type, rounds each by up to 2^-8 of itself
+    and halves their bytes; torch.float32 keeps the quantiser's.
     One scratch buffer of a block's nibbles is allocated up front.  Calls take turns
     with it, from any thread and on any stream (each waits for the one before); a
     captured call's replays are for the caller to order with what else uses these
