@@ -103,7 +103,7 @@ class _Bmm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        a, b = ctx.saved_tensors
+        a, b = (t.to(dy.dtype) for t in ctx.saved_tensors)   # autocast's type, where that was on
         dy = dy.contiguous()
         da = _Bmm.apply(dy, b.transpose(1, 2).contiguous()) if ctx.needs_input_grad[0] else None
         db = _Bmm.apply(a.transpose(1, 2).contiguous(), dy) if ctx.needs_input_grad[1] else None

@@ -124,3 +124,19 @@ def test_second_gradient_of_quantised_blocks_is_refused():
     assert torch.equal(first, plain) and torch.equal(plain, (2 * x + 3 * x * x).detach())
     with pytest.raises(RuntimeError):
         torch.autograd.grad(first.sum(), x)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_under_autocast(monkeypatch, dtype):
+    # the products run in autocast's type, and so do their gradients
+    w, u = {k: v.to(dtype) for k, v in weights().items()}, acts(3)
+
+    def grad():
+        x = acts(1).to(dtype).requires_grad_()
+        with torch.autocast("cpu", dtype=torch.bfloat16):
+            y = block(x, w)
+        return torch.autograd.grad((y.float() * u).sum(), x)[0].float()
+
+    got, want = both(monkeypatch, grad)
+    # the same sums in 16 bits: a few dozen roundings of 2^-8 at most
+    assert float((got - want).abs().max()) <= 64 * 2.0 ** -8 * float(want.abs().max())
