@@ -435,6 +435,12 @@ class _LossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, head, call, stream):
         loss, kept = call.forward(stream)
+        if call.done is not None and torch._C._autograd._top_saved_tensors_default_hooks(False) is not None:
+            # a hook reads what the call on the other stream still writes
+            here = torch.cuda.current_stream(call.dev)
+            here.wait_event(call.done)
+            for t in kept:
+                t.record_stream(here)
         # the tensors that the gradient reads again: kept by autograd alone, so that
         # a change made to one in between is refused and saved-tensor hooks see all
         ctx.save_for_backward(*call.inputs, *kept)

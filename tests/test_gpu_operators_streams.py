@@ -116,3 +116,22 @@ def test_gradient_of_a_product_on_another_stream(torch, m):
     got, = torch.autograd.grad(y, x, dy)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_saved_tensors_on_the_host_after_a_call_on_another_stream(torch):
+    # the call on s is late; what it keeps goes to the host behind it
+    g = torch.Generator().manual_seed(9)
+    m, v, h = 300, 2001, 256
+    head = (torch.randn(v, h, generator=g) * 0.1).to(torch.bfloat16).cuda().requires_grad_()
+    x = torch.randn(h, m, generator=g).to(torch.bfloat16).cuda().requires_grad_()
+    labels = torch.randint(0, v, (m,), generator=g).cuda()
+    want = torch.autograd.grad(dfh.vocab_loss(x.t(), head, labels), (x, head))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    with torch.autograd.graph.save_on_cpu():
+        loss = dfh.vocab_loss(x.t(), head, labels, stream=s)
+    got = torch.autograd.grad(loss, (x, head))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -58,3 +58,20 @@ def test_distillation_from_one_entry_is_cross_entropy(torch, m, v, h, dtype):
     a, b = both(torch, x, head, labels, "none")
     assert float(a[0].min()) > 0
     assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("temp", [0.5, 0.7, 3.0])
+def test_sure_rows_at_other_temperatures(torch, temp):
+    m, v, h = 60, 500, 264
+    g = torch.Generator().manual_seed(2)
+    head = (torch.randn(v, h, generator=g) * (72 / h) ** 0.5).to(torch.bfloat16)
+    labels = torch.randint(0, v, (m,), generator=g)
+    x = (head[labels].float() * 8 * temp).to(torch.bfloat16)
+    z = x.double() @ head.double().t() / temp
+    gap = (z.gather(1, labels[:, None]) - z).scatter(1, labels[:, None], float("inf")).amin(1)
+    assert float(gap.min()) > 110
+    D = dev(torch)
+    xs, hs = x.to(D).requires_grad_(), head.to(D).requires_grad_()
+    loss = dfh.distill_loss(xs, hs, torch.zeros(m, 1, device=D), labels.to(D)[:, None], temperature=temp, reduction="none")
+    grads = torch.autograd.grad(loss.sum(), (xs, hs))
+    assert all(float(t.abs().max()) == 0.0 for t in (loss.detach(), *grads))

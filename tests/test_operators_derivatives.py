@@ -68,6 +68,8 @@ class Squares:
     """A loss call over [rows, hidden] states and a head: sum of (x head^T)^2, in
     place of a _Loss."""
 
+    done = None
+
     def __init__(self, x, head):
         self.inputs = (x, head)
 

@@ -144,3 +144,36 @@ def test_what_an_object_made_is_waited_for_once_on_each_other_stream(monkeypatch
     made.use(2)
     made.use(3)
     assert log == [("made", 1)] + [(what, s) for s in (2, 3) for what in ("wait", "keep", "keep")]
+
+
+def test_saved_tensor_hooks_wait_for_the_stream_of_the_forward_call(monkeypatch):
+    log = []
+
+    class Current:
+        def wait_event(self, event):
+            log.append(("wait", event))
+
+    class Kept(torch.Tensor):
+        def record_stream(self, stream):
+            log.append("keep")
+
+    class Call:
+        done, dev = "end", None
+
+        def __init__(self, x):
+            self.inputs = (x, x.detach())
+
+        def forward(self, stream):
+            return self.inputs[0].sum(), (torch.zeros(1).as_subclass(Kept),)
+
+    def pack(t):
+        log.append("pack")
+        return t
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Current())
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        ops._run_loss(Call(torch.ones(3, requires_grad=True)), 5)
+    assert log[:3] == [("wait", "end"), "keep", "pack"]
+    del log[:]
+    ops._run_loss(Call(torch.ones(3, requires_grad=True)), 5)
+    assert not log
