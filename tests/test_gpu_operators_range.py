@@ -154,3 +154,31 @@ def test_rows_with_gradients_of_all_sizes(torch, m, v, h, dtype):
     floor = 2.0 ** -39 * (gw[:, None] * xz.abs()).max() * 1.01 * (d.abs() + ed).sum(0)[:, None]
     bound = ((ed + (m + 64) * E * d.abs()) * gw[:, None]).t() @ xz.abs() * (1 + 8 * E) + floor
     within(dh, ref, bound * (1 + u) + (u + 8 * E) * ref.abs() + tiny(torch, dt))
+
+
+@pytest.mark.parametrize("m", [1, 4, 17, 60, 200])
+@pytest.mark.parametrize("n,k,group", [(40, 200, 32), (259, 1416, 1416), (70, 4104, 128)])
+def test_every_row_ends_in_an_infinity(torch, m, n, k, group):
+    # BF16: inf times a weight of either sign, NaN at a zero weight, whatever the place
+    D = dev(torch)
+    g = torch.Generator().manual_seed(k)
+    s = torch.rand(n, (k + group - 1) // group, generator=g) + 0.5
+    w, w64, _ = weights(torch, n, k, group, s, True, k)
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16)
+    for at in (k - 1, 0, 45):
+        xi = x.clone()
+        xi[:, at] = float("inf")
+        xi[m // 2, at] = -float("inf")
+        ref = xi.double() @ w64.t()
+        got = dfh.linear_u4(xi.to(D), w).double().cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.equal(got.nan_to_num(0.5), ref.nan_to_num(0.5))
+    # a sum that is finite where the products with 16 + q are not
+    xi = x.clone()
+    xi[:, 45] = 2.0 ** 126
+    q = torch.stack((w.packed & 15, w.packed >> 4), -1).view(n, k).cpu()
+    q[:, 45] = w.zeros.cpu().expand(n, -1)[:, 45 // group]
+    w64[:, 45] = 0.0
+    w2 = dfh.U4Matrix((q[:, 0::2] | (q[:, 1::2] << 4)).reshape(-1).to(D), w.scales, w.zeros, cols=k, group_size=group)
+    ref = xi.double() @ w64.t()
+    bound = k * E * (xi.double().masked_fill(xi == 2.0 ** 126, 0.0).abs() @ w64.abs().t())
+    within(dfh.linear_u4(xi.to(D), w2), ref, bound + 2.0 ** -8 * ref.abs() * 1.01)
