@@ -79,3 +79,64 @@ def test_saved_tensors_on_the_host(torch, call):
     assert torch.cuda.memory_allocated() - before < 2 * m * h   # less than x alone
     got = torch.autograd.grad(kept, (xl, hl))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_checkpointed_step(torch):
+    # the forward call is made again in the backward pass, its tensors elsewhere
+    from torch.utils.checkpoint import checkpoint
+    D = dev(torch)
+    w, _, _ = matrix(torch, 128, 256, 64, "bf16", seed=6)
+    head = head_and_x(torch, 1, 900, 128, torch.bfloat16, 6)[1].to(D).t().contiguous().t()
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(3, 50, 256, generator=g).to(torch.bfloat16).to(D)
+    labels = torch.randint(0, 900, (50, 3), generator=g).to(D)
+
+    def step(a, b):
+        return dfh.vocab_loss(dfh.linear_u4(a.transpose(0, 1) * 2, w), b, labels)
+
+    a, b = x.clone().requires_grad_(), head.clone().requires_grad_()
+    want = torch.autograd.grad(step(a, b), (a, b))
+    got = torch.autograd.grad(checkpoint(step, a, b, use_reentrant=False), (a, b))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("m", [40, 600])
+def test_graph_of_a_float16_step_with_a_gradient_a_row(torch, m):
+    # products with expanded weights in float16, and a loss whose rows have gradients
+    # of their own: captured, replayed with other inputs and eager work between
+    D = dev(torch)
+    n, k, v = 129, 256, 1100
+    w, _, _ = matrix(torch, n, k, 64, "fp32", seed=6)
+    wy, _, _ = matrix(torch, 136, 136, 32, "fp32", seed=7)
+    head = head_and_x(torch, 1, v, 136, torch.float16, 6)[1].to(D)
+    x = torch.zeros(m, k, dtype=torch.float16, device=D)
+    weight = torch.ones(m, device=D)
+    labels = torch.zeros(m, dtype=torch.int64, device=D)
+
+    def step():
+        xl, hl = x.detach().requires_grad_(), head.detach().requires_grad_()
+        h = torch.nn.functional.pad(dfh.linear_u4(xl, w), (0, 7))
+        loss = dfh.vocab_loss(dfh.linear_u4(h, wy), hl, labels, reduction="none")
+        return (loss.detach(),) + torch.autograd.grad(loss, (xl, hl), weight)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for r in range(4):
+        g = torch.Generator().manual_seed(100 + r)
+        x.copy_(torch.randn(m, k, generator=g).to(torch.float16))
+        weight.copy_(64 * 10.0 ** (-4 * torch.rand(m, generator=g)))
+        labels.copy_(torch.randint(0, v, (m,), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), r
