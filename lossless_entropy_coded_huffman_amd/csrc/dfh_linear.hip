@@ -536,6 +536,17 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out, cons
   const S *ps = (const S *)w.scales + n * w.sstride;
   const uint8_t *pz = w.zeros ? w.zeros + n * w.zstride : (const uint8_t *)&g_eights;
   const uint32_t zon = w.zeros ? 1 : 0;
+  float most = 0.f;
+  if constexpr (!Bias<T>::in_sum) {
+    // by every wave for itself: the workgroup does not meet
+    const uint32_t lane = threadIdx.x & 63;
+    if (lift.peaks) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) most = __builtin_fmaxf(most, lift.peaks[lane + i * 64]);
+    } else {
+      for (uint32_t g = lane; g < w.groups; g += 64) most = __builtin_fmaxf(most, size_at(w, ps + g));
+    }
+  }
   uint32_t q[4];
   S s[4];
   uint8_t z[4];
@@ -548,13 +559,7 @@ __global__ __launch_bounds__(256) void u4_expand(const U4 w, uint16_t *out, cons
   }
   float up = 1.f;
   if constexpr (!Bias<T>::in_sum) {
-    float v = 0.f;
-    if (lift.peaks) {
-      v = lift.peaks[threadIdx.x];
-    } else {
-      for (uint32_t g = threadIdx.x; g < w.groups; g += 256) v = __builtin_fmaxf(v, size_at(w, ps + g));
-    }
-    const int bits = lift_bits(most_of_256(v), 6);
+    const int bits = lift_bits(most_of_wave(most), 6);
     up = power_of_two(bits);
     if (threadIdx.x == 0 && blockIdx.y == 0) {
       if (!lift.peaks) {
@@ -598,18 +603,25 @@ const float *expand(const U4 &w, uint8_t *ws, bool gradient, hipStream_t s) {
   return lift.back;
 }
 
-// Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n], times columns[n] and *all
-// (null: 1).
-template <class T>
+// Sum of FP32 planes [splits][m][ld] -> 16-bit [m, n], times back[n] (EACH) or *back,
+// where there is one.
+template <class T, bool EACH>
 __global__ __launch_bounds__(256) void join_planes(const float *p, uint32_t splits, uint32_t m, uint32_t n,
-                                                   uint32_t ld, const float *columns, const float *all, uint16_t *out) {
+                                                   uint32_t ld, const float *back, uint16_t *out) {
   const uint32_t row = blockIdx.x;
-  const float f = all ? *all : 1.f;
+  float all = 1.f;
+  if constexpr (!Bias<T>::in_sum && !EACH) all = *back;
   for (uint32_t c = threadIdx.x * 4; c < n; c += 1024) {
-    const f32x4 v = add_planes(p + (uint64_t)row * ld + c, (uint64_t)m * ld, splits);
+    f32x4 f = {all, all, all, all};
+    if constexpr (!Bias<T>::in_sum && EACH) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) f[e] = back[c + e < n ? c + e : n - 1];
+    }
+    f32x4 v = add_planes(p + (uint64_t)row * ld + c, (uint64_t)m * ld, splits);
+    if constexpr (!Bias<T>::in_sum) v *= f;
 #pragma unroll
     for (int e = 0; e < 4; e++)
-      if (c + e < n) out[(uint64_t)row * n + c + e] = to_bits(T{}, v[e] * (columns ? columns[c + e] : f));
+      if (c + e < n) out[(uint64_t)row * n + c + e] = to_bits(T{}, v[e]);
   }
 }
 
@@ -623,9 +635,10 @@ __global__ __launch_bounds__(256) void pad_rows(const uint16_t *src, uint64_t ss
 
 // Rows that u4_tile takes rather than an expansion: the expansion costs a fixed
 // time per weight (0.45 us a million), the tile kernel a time per weight and 64
-// rows (0.34 us a million once the chip is full, less before).  Tile against
-// expansion, us: 200 x 4096 x 4096 28 : 32, 512 rows of it 44 : 41; 64 x 14336 x
-// 4096 30 : 65, 256 rows of it 80 : 74; 333 x 2047 x 1416 17 : 22.
+// rows (0.3 us a million once the chip is full, less before).  Tile against
+// expansion, us, BF16 (FP16): 200 x 4096 x 4096 28 : 34 (24 : 36), 384 rows of it 38 :
+// 40 (33 : 42), 512 41 : 42 (34 : 44); 192 x 14336 x 4096 57 : 82 (54 : 92), 256 rows
+// of it 71 : 79 (62 : 87), where the rule does not follow yet; 333 x 2047 x 1416 13 : 23.
 bool few_rows(uint64_t m, uint64_t n, uint64_t k) {
   return m <= 192 || (m <= 384 && n * k <= 1u << 24) || (m <= 512 && n * k <= 1u << 22);
 }
@@ -667,8 +680,8 @@ df_status many_rows(const Gemm &g, uint16_t *out, const float *back, float *plan
   }
   const uint32_t ld = (uint32_t)up(g.n, 4);
   if (product<T, false, GRAD>(g, EpiPlane{planes, ld, (uint64_t)g.m * ld, false}, c.shape, c.splits, s) != hipSuccess) return DF_ERR_HIP;
-  hipLaunchKernelGGL((join_planes<T>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld,
-                     kColumns ? back : nullptr, GRAD ? back : nullptr, out);
+  hipLaunchKernelGGL((join_planes<T, !GRAD>), dim3(g.m), dim3(256), 0, s, (const float *)planes, c.splits, g.m, g.n, ld,
+                     back, out);
   return hipGetLastError() == hipSuccess ? DF_OK : DF_ERR_HIP;
 }
 
