@@ -112,7 +112,8 @@ __device__ __forceinline__ u32x4 pair_up(u32x4 v) {
 // One output from the definition, in order; taken where BF16's fast sum is not
 // finite (an infinite or very large x: the bias would turn inf * w into NaN).
 // 192 x 14336 x 4096, which takes 57 us: 247 us where x is all NaN, 31 ms where
-// every row ends in an infinity (43 ms with a wave to an output): no fast path is made for such rows.
+// every row ends in an infinity (43 ms with a wave to an output): no fast path is
+// made for such rows.
 template <class T>
 __device__ float dot_plain(const U4 &w, const uint16_t *xr, uint32_t n) {
   float acc = 0.f;
@@ -138,8 +139,7 @@ __device__ const uint32_t g_eights = 0x08080808u;
 typedef const __attribute__((address_space(1))) uint8_t *GlobalBytes;
 
 // A wave's 16 rows of the weights (row n0 + lane % 16) as the operands below want
-// them.  SUB, the groups that 128 elements hold (1, 2,
-// 4), fixes how scales and zero points are read: a stage's 4 SUB (blocks of 128)
+// them.  SUB, the groups that 128 elements hold (1, 2, 4), fixes how scales and zero points are read: a stage's 4 SUB (blocks of 128)
 // in a row where the group size is 128 / SUB, one by one otherwise (SUB = 4: any
 // multiple of 32; 0: a multiple of 128, or one group a row).  Raw values are
 // kept and converted at their use: a conversion at the load would wait for it.

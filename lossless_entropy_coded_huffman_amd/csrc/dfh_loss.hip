@@ -118,7 +118,8 @@ struct EpiStats {
 
 // dz / (T g) without the target's part, times `mul`: 2^(c z - lse2), rounded to the
 // operands' 16 bits, which the products that take it need (an FP32 dz would double
-// the traffic and fit no matrix instruction at their rate); zero in rows without a loss and in the columns that pad a row to ldz.
+// the traffic and fit no matrix instruction at their rate); zero in rows without a
+// loss and in the columns that pad a row to ldz.
 // FP16 takes mul = 2^15: probabilities of a large vocabulary lie where FP16
 // has few bits or none; the products' epilogues take the factor out again.
 struct EpiDz {
@@ -215,8 +216,9 @@ struct Parts {
 // Joins a row's parts and makes its loss.  R rows a workgroup of 256; thread t
 // takes parts t / R, t / R + 256 / R, ... (four loads in flight) and targets
 // likewise of row t % R.  R = 8 reads 64 bytes of a part at once; few rows take
-// R = 1, so that 256 threads share a row's parts (7 rows of 4008 parts: 8 us).  PICK (with R = 1, where a row has
-// few teacher entries): the four waves make the picked logits themselves.
+// R = 1, so that 256 threads share a row's parts (7 rows of 4008 parts: 8 us).
+// PICK (with R = 1, where a row has few teacher entries): the four waves make the
+// picked logits themselves.
 template <class T, int R, bool PICK>
 __global__ __launch_bounds__(256) void finish_rows(const Targets t, uint32_t rows, const float2 *parts, Parts np,
                                                    const Head h, Saved sv, float *loss) {

@@ -18,9 +18,10 @@ stream.
 
 In autograd a gradient runs on the stream that was current in the forward call,
 after a forward call that was given another one.  linear_u4 can be differentiated
-again, a gradient of a loss's gradient is refused, and so is forward mode.  To capture a training step into a HIP graph,
-make its leaves inside the capture (``x.detach().requires_grad_()``): a leaf that
-an eager graph still holds ties the captured backward to that graph's stream.
+again; a gradient of a loss's gradient is refused, and so is forward mode.  To
+capture a training step into a HIP graph, make its leaves inside the capture
+(``x.detach().requires_grad_()``): a leaf that an eager graph still holds ties the
+captured backward to that graph's stream.
 """
 from __future__ import annotations
 
@@ -284,7 +285,8 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     x [..., cols] in bfloat16 or float16, y [..., rows] in the same type.  Sums
     are float32; few rows (up to 192; 384 for at most 2^24 weights, 512 for at most
     2^22) round no weight (float16 sums x (q - z); bfloat16 x (16 + q), and takes
-    16 + z times the sum of x off), more (and every gradient) round each weight once to x's type, with scales of any size within range.  Differentiable in x;
+    16 + z times the sum of x off), more (and every gradient) round each weight once
+    to x's type, with scales of any size within range.  Differentiable in x;
     the nibbles must stay as they are until the gradient has run (df_decompress
     into the same buffer is not seen by autograd)."""
     _no_tangent(x)

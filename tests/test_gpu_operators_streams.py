@@ -1,5 +1,5 @@
-"""The gradient of a loss whose forward call was given a stream: the one that a call
-on the current stream gives."""
+"""Calls that are given a stream, with late work on it or on the current one: their
+results and gradients are those of a call on the current stream."""
 import numpy as np
 import pytest
 
