@@ -391,6 +391,48 @@ uint64_t df_linear_u4_grad_workspace_bytes(const df_u4_matrix *w, uint64_t rows)
 df_status df_linear_u4_grad(const df_u4_matrix *w, df_type type, const void *dy, uint64_t rows, uint64_t dy_stride,
                             void *dx, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------ products in 8-bit integers */
+
+/* The codes of a uint8 container as weights: a layer of `rows` outputs and `cols`
+ * inputs, with a scale (and zero point, else 128) for each output:
+ *     W[n, k] = scales[n] * (q[n, k] - zeros[n]).
+ * Activations are quantised with a scale for each of their rows,
+ *     top = max_k |x[m, k]|,  c[m, k] = rint(127 x[m, k] / top)  (ties to even),
+ *     xs[m] = top / 127,
+ * and multiplied as integers:
+ *     y[m, n] = xs[m] scales[n] sum over k of c[m, k] (q[n, k] - zeros[n]),
+ * the sum exact in 32 bits.  A row of x that holds an infinity or NaN has codes 0
+ * and the scale NaN: its outputs are NaN. */
+typedef struct {
+  uint64_t rows;          /* outputs, 1 .. 2^21                              */
+  uint64_t cols;          /* inputs, a multiple of 16, at most 65536         */
+  df_type scale_type;
+  uint64_t scale_stride;  /* elements from a row's scale to the next; 0: one for all */
+  uint64_t zero_stride;
+  const uint8_t *codes;   /* rows * cols bytes, 16-byte aligned              */
+  const void *scales;
+  const uint8_t *zeros;   /* any byte values; NULL: 128                      */
+} df_u8_matrix;
+
+/* codes [rows, cols], contiguous and 16-byte aligned, and scales [rows] of x: rows
+ * of cols (a multiple of 16, at most 65536) elements of BF16 or F16, x_stride
+ * elements apart (a multiple of 8, at most 2^21), 16-byte aligned.  At most 2^24
+ * rows. */
+df_status df_quantize_rows(df_type type, const void *x, uint64_t rows, uint64_t cols, uint64_t x_stride, int8_t *codes,
+                           float *scales, hipStream_t stream);
+
+/* y [rows, w->rows] of `type` (BF16 or F16), contiguous and 16-byte aligned, from x
+ * of the same type (as for df_quantize_rows), or from codes (any int8, rows `stride`
+ * bytes apart, a multiple of 16, 16-byte aligned) and their scales.  The workspace
+ * (256-byte aligned) holds the codes of x and, where the summed index is split, sums;
+ * up to 4 rows whose codes take at most 60 KiB need none.  `codes` not 0: the size
+ * for df_linear_u8_codes.  At most 2^24 rows. */
+uint64_t df_linear_u8_workspace_bytes(const df_u8_matrix *w, uint64_t rows, int codes);
+df_status df_linear_u8(const df_u8_matrix *w, df_type type, const void *x, uint64_t rows, uint64_t x_stride, void *y,
+                       void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+df_status df_linear_u8_codes(const df_u8_matrix *w, df_type type, const int8_t *codes, const float *scales, uint64_t rows,
+                             uint64_t stride, void *y, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------- losses over a large vocabulary */
 
 /* Hidden states x [rows, hidden] and head weights [vocab, hidden] (an LM head

@@ -19,5 +19,5 @@ from .dfh import (  # noqa: F401
     df_status_string, lib, output_bytes, to_device,
 )
 from .ops import (  # noqa: F401
-    U4Matrix, distill_loss, linear_u4, linear_u4_grad, vocab_loss,
+    U4Matrix, U8Matrix, distill_loss, linear_u4, linear_u4_grad, linear_u8, quantize_rows, vocab_loss,
 )

@@ -60,6 +60,12 @@ class df_u4_matrix(ctypes.Structure):
                 ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
+class df_u8_matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("scale_type", ctypes.c_int),
+                ("scale_stride", ctypes.c_uint64), ("zero_stride", ctypes.c_uint64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
 class df_loss(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("reduce", ctypes.c_int),
                 ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("hidden", ctypes.c_uint64),
@@ -118,6 +124,15 @@ _SIGNATURES = {
     "df_linear_u4_grad": (ctypes.c_int, [ctypes.POINTER(df_u4_matrix), ctypes.c_int, ctypes.c_void_p,
                                          ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_uint64, ctypes.c_void_p]),
+    "df_quantize_rows": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64,
+                                        ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "df_linear_u8_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_u8_matrix), ctypes.c_uint64, ctypes.c_int]),
+    "df_linear_u8": (ctypes.c_int, [ctypes.POINTER(df_u8_matrix), ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64,
+                                    ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64,
+                                    ctypes.c_void_p]),
+    "df_linear_u8_codes": (ctypes.c_int, [ctypes.POINTER(df_u8_matrix), ctypes.c_int, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
     "df_loss_saved_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_loss_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_vocab_loss": (ctypes.c_int, [ctypes.POINTER(df_loss), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,

@@ -3,6 +3,8 @@
 * ``linear_u4``: products with uint4 weights and group scales, the packed
   nibbles that ``df_decompress`` yields for a uint4 container, for one token up
   to long prompts, with the gradient to the input;
+* ``linear_u8``: products in 8-bit integers of a uint8 container's codes with
+  activations that ``quantize_rows`` gives a scale for each row;
 * ``vocab_loss``: softmax cross entropy of hidden states against an LM head,
   the logits never stored, with the gradients to both;
 * ``distill_loss``: the divergence from a teacher's top logits over the same
@@ -293,6 +295,158 @@ def linear_u4(x: torch.Tensor, w: U4Matrix, stream=None) -> torch.Tensor:
     if x.requires_grad and torch.is_grad_enabled():
         return _LinearU4.apply(x, w, stream)
     return _linear(x, w, stream)
+
+
+# ------------------------------------------------------------- uint8 products
+def _no_gradient(what: str, *tensors):
+    """Refuses inputs that a gradient is expected for: rounding to codes has none."""
+    _no_tangent(*tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError("%s has no gradient: call it under no_grad, or detach its inputs" % what)
+
+
+class U8Matrix:
+    """A layer's uint8 weights on the device (df_u8_matrix; the tensors are
+    borrowed and kept alive): W[n, k] = scales[n] * (q[n, k] - zeros[n]).
+
+    codes: rows * cols bytes (what ``df_decompress`` writes for a uint8 container
+    of the layer), 16-byte aligned; cols a multiple of 16, at most 65536.  scales
+    [rows] or [rows, 1] in bfloat16, float16 or float32; zeros: uint8 zero points of
+    the same shape, or None for 128.  Either may be broadcast (stride 0): one scale
+    for a layer is ``scale.expand(rows)``."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, *, cols: int):
+        cols = int(cols)
+        if not codes.is_cuda or not codes.is_contiguous() or codes.dtype != torch.uint8:
+            raise ValueError("codes must be a contiguous uint8 tensor on the device")
+        if cols < 16 or cols % 16 or cols > 1 << 16:
+            raise ValueError("cols must be a multiple of 16 from 16 to 65536, got %d" % cols)
+        if scales.dim() not in (1, 2) or (scales.dim() == 2 and scales.shape[1] != 1):
+            raise ValueError("scales must be [rows] or [rows, 1], got %s" % (tuple(scales.shape),))
+        rows = int(scales.shape[0])
+        if rows < 1 or rows > 1 << 21:
+            raise ValueError("scales must have 1 to 2^21 rows, got %d" % rows)
+        if codes.numel() < rows * cols:
+            raise ValueError("codes holds fewer than %d x %d bytes" % (rows, cols))
+        if codes.data_ptr() % 16:
+            raise ValueError("codes must be 16-byte aligned")
+        _on(scales, codes.device, "scales")
+        self.scale_type = _type(scales, "scales", f32=True)
+        if zeros is not None:
+            _on(zeros, codes.device, "zeros")
+            if zeros.dtype != torch.uint8 or zeros.shape != scales.shape:
+                raise ValueError("zeros must be uint8 of the scales' shape")
+        if scales.requires_grad:
+            raise ValueError("no gradient goes to the scales: detach them")
+        _no_tangent(scales)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        self.view = dfh.df_u8_matrix(rows, cols, self.scale_type, scales.stride(0),
+                                     0 if zeros is None else zeros.stride(0), codes.data_ptr(), scales.data_ptr(),
+                                     _p(zeros))
+        self._ref = ctypes.byref(self.view)
+        self._need = {}   # workspace bytes by row count and kind of input
+
+    def _tensors(self):
+        return (self.codes, self.scales, self.zeros)
+
+
+def quantize_rows(x: torch.Tensor, stream=None):
+    """(codes, scales) of x [..., cols] in bfloat16 or float16, cols a multiple of 16
+    up to 65536: int8 codes of x's shape, rint(127 x / top) with ties to even for a row's largest
+    magnitude top, and float32 scales [...], top / 127.  A row of zeros has scale 0; a
+    row that holds an infinity or NaN has codes 0 and scale NaN.  What linear_u8 does
+    with its input, for several products of one."""
+    _no_gradient("quantize_rows", x)
+    if not x.is_cuda:
+        raise ValueError("x must be a tensor on the device")
+    ty = _type(x, "x")
+    if x.dim() < 1 or not 16 <= x.shape[-1] <= 1 << 16 or x.shape[-1] % 16:
+        raise ValueError("x must be [..., cols] with cols a multiple of 16 from 16 to 65536, got %s" % (tuple(x.shape),))
+    dev, shape = x.device, x.shape
+
+    def call(handle):
+        x2 = _rows16(_flat(x))
+        m, k = x2.shape
+        codes = torch.empty(shape, dtype=torch.int8, device=dev)
+        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        st = dfh.lib().df_quantize_rows(ty, x2.data_ptr(), m, k, x2.stride(0), codes.data_ptr(), scales.data_ptr(),
+                                        handle)
+        if st:
+            dfh._check(st, "df_quantize_rows")
+        return codes, scales
+
+    return _launch(stream, dev, (x,), call)
+
+
+def _rows_of_codes(t: torch.Tensor) -> torch.Tensor:
+    """Codes [r, c] with a row stride that is a multiple of 16 bytes and at most 2^21,
+    unit column stride and a 16-byte aligned base: themselves, or a copy."""
+    step, one = t.stride()
+    if one == 1 and step % 16 == 0 and t.shape[1] <= step <= _MAX_STRIDE and t.data_ptr() % 16 == 0:
+        return t
+    return _copied(t)
+
+
+def linear_u8(x: torch.Tensor, w: U8Matrix, *, scales: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+              stream=None) -> torch.Tensor:
+    """y = x W^T for W[n, k] = w.scales[n] * (q[n, k] - zeros[n]), in 8-bit integers:
+    the rows of x [..., cols] (bfloat16 or float16) are quantised as quantize_rows
+    does, the sums of code products are exact in 32 bits, and y [..., rows] in x's
+    type is rounded once from float32.  With scales (float32 [...]) x holds int8 codes,
+    and y is of dtype (bfloat16 where none is given).  A row of x that holds an
+    infinity or NaN gives NaN.  Rounding to codes has no derivative: inputs that
+    require one are refused."""
+    _no_gradient("linear_u8", x, scales)
+    dev, shape = w.device, x.shape
+    if x.device != dev:
+        _on(x, dev, "x")
+    if scales is None:
+        if dtype is not None and dtype != x.dtype:
+            raise TypeError("y has x's type, got dtype %s for %s" % (dtype, x.dtype))
+        ty = _type(x, "x")
+    else:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("dtype must be bfloat16 or float16, got %s" % dtype)
+        if x.dtype != torch.int8:
+            raise TypeError("x must be int8 codes where scales are given, got %s" % x.dtype)
+        _on(scales, dev, "scales")
+        if scales.dtype != torch.float32 or scales.shape != shape[:-1]:
+            raise ValueError("scales must be float32 of shape %s" % (tuple(shape[:-1]),))
+        ty = _TYPES[dtype]
+    if not shape or shape[-1] != w.cols:
+        raise ValueError("x must be [..., %d], got %s" % (w.cols, tuple(shape)))
+
+    def call(handle):
+        x2 = _flat(x)
+        x2 = _rows16(x2) if scales is None else _rows_of_codes(x2)
+        m = x2.shape[0]
+        L = dfh.lib()
+        key = (m, scales is None)
+        need = w._need.get(key)
+        if need is None:
+            need = w._need[key] = L.df_linear_u8_workspace_bytes(w._ref, m, int(scales is not None))
+        ws = _workspace(need, dev) if need else None
+        if scales is None:
+            y = x2.new_empty((m, w.rows))
+            st = L.df_linear_u8(w._ref, ty, x2.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws), need, handle)
+        else:
+            y = torch.empty((m, w.rows), dtype=dtype, device=dev)
+            s = scales.contiguous()
+            st = L.df_linear_u8_codes(w._ref, ty, x2.data_ptr(), s.data_ptr(), m, x2.stride(0), y.data_ptr(), _p(ws),
+                                      need, handle)
+        if st:
+            dfh._check(st, "df_linear_u8")
+        return y
+
+    if stream is None and _current_device() == dev.index:
+        y = call(_raw_stream(dev.index))
+    else:
+        y = _launch(stream, dev, (x, scales) + w._tensors(), call)
+    return y if len(shape) == 2 else y.view(shape[:-1] + (w.rows,))
 
 
 # ---------------------------------------------------------------------- losses
