@@ -433,6 +433,54 @@ df_status df_linear_u8(const df_u8_matrix *w, df_type type, const void *x, uint6
 df_status df_linear_u8_codes(const df_u8_matrix *w, df_type type, const int8_t *codes, const float *scales, uint64_t rows,
                              uint64_t stride, void *y, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------ a cache of keys and values */
+
+/* Keys and values of sequences, in pages of page_size tokens: k and v are [pages,
+ * kv_heads, page_size, head_dim], contiguous.  bits 16: of `type`; bits 8: int8 codes
+ * with float scales [pages, kv_heads, page_size], a vector x kept as
+ *     c = rint(127 x / max |x|)  (ties to even),  scale = max |x| / 127,
+ * and read back as c * scale.  A vector that holds an infinity or NaN is kept as
+ * codes 0 with scale NaN. */
+typedef struct {
+  df_type type;           /* BF16 or F16: what calls take and give           */
+  uint32_t bits;          /* 16 or 8                                         */
+  uint32_t page_size;     /* a power of two from 16 to 256                   */
+  uint32_t kv_heads;      /* 1 .. 256                                        */
+  uint32_t head_dim;      /* 32, 64, 128 or 256                              */
+  uint64_t pages;         /* 1 .. 2^26                                       */
+  void *k, *v;            /* 16-byte aligned                                 */
+  float *k_scales, *v_scales; /* bits 8                                      */
+} df_cache;
+
+/* The sequences of a call, on the device.  Rows starts[s] .. starts[s + 1] - 1 of a
+ * call's tokens are the new tokens of sequence s, the last ones of its lengths[s]
+ * positions (new tokens counted); position p lies in row p % page_size of page
+ * tables[s, p / page_size].  starts begin at 0 and do not fall.  A position before 0 or outside
+ * the table, and a page outside the pool, are tokens that are not there: not
+ * written, read as zeros, not attended to.  Pages may be shared between sequences
+ * for reading; a position that is written has one owner. */
+typedef struct {
+  uint32_t seqs;          /* up to 65536                                     */
+  uint32_t width;         /* pages of a table's row, 1 .. 2^22               */
+  uint64_t table_stride;  /* elements, at least width, at most 2^30          */
+  const int32_t *tables;  /* [seqs, width]                                   */
+  const int32_t *lengths; /* [seqs]; at most 2^30 counts                     */
+  const int32_t *starts;  /* [seqs + 1]                                      */
+  uint32_t max_new;       /* the most new tokens of a sequence, where the caller knows it, else 0; only for speed */
+} df_cache_batch;
+
+/* New keys and values into the cache: [tokens, kv_heads, head_dim], unit stride in
+ * head_dim, the other strides in elements (multiples of 8, at most 2^30), 16-byte
+ * aligned.  Rows of no sequence are not read.  At most 2^24 tokens. */
+df_status df_cache_write(const df_cache *cache, const df_cache_batch *batch, const void *k, uint64_t k_token_stride,
+                         uint64_t k_head_stride, const void *v, uint64_t v_token_stride, uint64_t v_head_stride,
+                         uint64_t tokens, hipStream_t stream);
+
+/* The batch's rows back out of the cache, as df_cache_write took them, into
+ * contiguous k and v; rows of no sequence become zeros. */
+df_status df_cache_read(const df_cache *cache, const df_cache_batch *batch, void *k, void *v, uint64_t tokens,
+                        hipStream_t stream);
+
 /* ------------------------------------------- losses over a large vocabulary */
 
 /* Hidden states x [rows, hidden] and head weights [vocab, hidden] (an LM head

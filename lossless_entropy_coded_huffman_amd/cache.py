@@ -1,0 +1,178 @@
+"""A paged cache of keys and values, through the C ABI (include/dfh.h):
+
+* ``KVCache`` holds the pages, in 16 bits or quantised to 8 with a scale for each
+  token and head; ``CacheBatch`` says which sequences a call is about;
+* ``cache_write`` puts the keys and values of new tokens into the pages,
+  ``cache_read`` gives them back.
+
+A step of several sequences, each with any number of new tokens (a prompt, a part of
+one, a single token, none), is one batch: rows starts[s] .. starts[s + 1] - 1 of the
+step's tensors are the new tokens of sequence s, the last ones of its lengths[s]
+positions.  Streams, workspaces and captures are as in ``ops``: everything is enqueued
+on ``stream`` (default: the current stream of the cache's device) and returns without
+synchronising.  What the batch's tensors hold is read when the call runs, so a captured
+step is replayed after they were changed in place.  Nothing here has a gradient:
+inputs that require one are refused.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import dfh
+from .ops import _TYPES, _current_device, _launch, _no_gradient, _on, _raw_stream
+
+
+class KVCache:
+    """Pages of keys and values on the device (df_cache).
+
+    k and v: [pages, kv_heads, page_size, head_dim], in dtype (bfloat16 or float16)
+    with bits=16, int8 codes with bits=8, then with float32 k_scales and v_scales
+    [pages, kv_heads, page_size]; all start as zeros.  page_size is a power of two from
+    16 to 256, head_dim 32, 64, 128 or 256, kv_heads at most 256."""
+
+    def __init__(self, pages: int, kv_heads: int, head_dim: int, *, page_size: int = 64, dtype=torch.bfloat16,
+                 bits: int = 16, device=None):
+        pages, kv_heads, head_dim, page_size, bits = (int(v) for v in (pages, kv_heads, head_dim, page_size, bits))
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("dtype must be bfloat16 or float16, got %s" % dtype)
+        if bits not in (16, 8):
+            raise ValueError("bits must be 16 or 8, got %d" % bits)
+        if page_size < 16 or page_size > 256 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two from 16 to 256, got %d" % page_size)
+        if head_dim not in (32, 64, 128, 256):
+            raise ValueError("head_dim must be 32, 64, 128 or 256, got %d" % head_dim)
+        if not 1 <= kv_heads <= 256:
+            raise ValueError("kv_heads must lie in 1 .. 256, got %d" % kv_heads)
+        if not 1 <= pages <= 1 << 26:
+            raise ValueError("pages must lie in 1 .. 2^26, got %d" % pages)
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise ValueError("a cache lies on the device, got %s" % device)
+        shape = (pages, kv_heads, page_size, head_dim)
+        kept = torch.int8 if bits == 8 else dtype
+        self.k, self.v = (torch.zeros(shape, dtype=kept, device=device) for _ in range(2))
+        self.k_scales, self.v_scales = (torch.zeros(shape[:3], dtype=torch.float32, device=device) if bits == 8 else None
+                                        for _ in range(2))
+        self.pages, self.kv_heads, self.head_dim, self.page_size = pages, kv_heads, head_dim, page_size
+        self.dtype, self.bits, self.device = dtype, bits, self.k.device
+        self.view = dfh.df_cache(_TYPES[dtype], bits, page_size, kv_heads, head_dim, pages, self.k.data_ptr(),
+                                 self.v.data_ptr(), 0 if bits == 16 else self.k_scales.data_ptr(),
+                                 0 if bits == 16 else self.v_scales.data_ptr())
+        self._ref = ctypes.byref(self.view)
+
+    def _tensors(self):
+        return (self.k, self.v, self.k_scales, self.v_scales)
+
+
+class CacheBatch:
+    """The sequences of a step (df_cache_batch; the tensors are borrowed and kept
+    alive), int32 on the cache's device:
+
+    tables [seqs, width]: the pages of each sequence, position p in page
+    tables[s, p // page_size]; lengths [seqs]: its positions, new tokens counted;
+    starts [seqs + 1]: where its new tokens begin in the step's tensors, from 0 on,
+    not falling.  max_new: the most new tokens of a sequence, where the program knows
+    it; it only chooses kernels, any batch is computed right without or with a wrong one.
+
+    A position before 0 or outside the table, and a page outside the pool, are tokens
+    that are not there: not written, read back as zeros, not attended to.  Sequences may share
+    pages that they read; a position that a step writes has one owner."""
+
+    def __init__(self, tables: torch.Tensor, lengths: torch.Tensor, starts: torch.Tensor, *, max_new: int | None = None):
+        if not tables.is_cuda or tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[1] < 1:
+            raise ValueError("tables must be an int32 [seqs, width] tensor on the device")
+        seqs, width = (int(n) for n in tables.shape)
+        if seqs > 1 << 16 or width > 1 << 22:
+            raise ValueError("tables must have at most 65536 rows of 2^22 pages, got %s" % (tuple(tables.shape),))
+        for t, what, n in ((lengths, "lengths", seqs), (starts, "starts", seqs + 1)):
+            _on(t, tables.device, what)
+            if t.dtype != torch.int32 or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+                raise ValueError("%s must be a contiguous int32 tensor of %d elements" % (what, n))
+        stride = tables.stride(0) if seqs > 1 else width
+        if (width > 1 and tables.stride(1) != 1) or not width <= stride <= 1 << 30:
+            raise ValueError("tables must have contiguous rows")
+        if max_new is not None and int(max_new) < 0:
+            raise ValueError("max_new must not be negative, got %d" % int(max_new))
+        self.tables, self.lengths, self.starts = tables, lengths, starts
+        self.seqs, self.width, self.device = seqs, width, tables.device
+        self.max_new = None if max_new is None else int(max_new)
+        self.view = dfh.df_cache_batch(seqs, width, stride, tables.data_ptr(), lengths.data_ptr(), starts.data_ptr(),
+                                       min(self.max_new or 0, 1 << 24))
+        self._ref = ctypes.byref(self.view)
+
+    def _tensors(self):
+        return (self.tables, self.lengths, self.starts)
+
+
+def _heads16(t: torch.Tensor) -> torch.Tensor:
+    """t [tokens, heads, dim] with unit stride in dim, other strides that are multiples
+    of 8 elements and at most 2^30, and a 16-byte aligned base: itself, or a copy."""
+    a, b, one = t.stride()
+    if one == 1 and (a | b) % 8 == 0 and a <= 1 << 30 and b <= 1 << 30 and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _enqueue(stream, dev, tensors, call):
+    if stream is None and _current_device() == dev.index:
+        return call(_raw_stream(dev.index))
+    return _launch(stream, dev, tensors, call)
+
+
+def _new_tokens(t: torch.Tensor, cache: KVCache, batch: CacheBatch, what: str, heads: int | None):
+    _on(t, cache.device, what)
+    if batch.device != cache.device:
+        raise ValueError("the batch must lie on %s" % cache.device)
+    if t.dtype != cache.dtype:
+        raise TypeError("%s must be %s like the cache, got %s" % (what, cache.dtype, t.dtype))
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s must be [tokens, %s, %d], got %s" % (what, "heads" if heads is None else heads, cache.head_dim,
+                                                                  tuple(t.shape)))
+    if t.shape[0] > 1 << 24:
+        raise ValueError("%s has more than 2^24 tokens" % what)
+
+
+def cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: CacheBatch, stream=None) -> None:
+    """The keys and values of the batch's new tokens, [tokens, kv_heads, head_dim] in the
+    cache's dtype and any strides, into the cache's pages.  With 8 bits each token's
+    head is kept as rint(127 x / max |x|) (ties to even) and the scale max |x| / 127;
+    one that holds an infinity or NaN as codes 0 and the scale NaN.  Rows of no
+    sequence are left out, and every other row of the pages stays as it was."""
+    _no_gradient("cache_write", k, v)
+    _new_tokens(k, cache, batch, "k", cache.kv_heads)
+    _new_tokens(v, cache, batch, "v", cache.kv_heads)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape, got %s and %s" % (tuple(k.shape), tuple(v.shape)))
+
+    def call(handle):
+        k2, v2 = _heads16(k), _heads16(v)
+        st = dfh.lib().df_cache_write(cache._ref, batch._ref, k2.data_ptr(), k2.stride(0), k2.stride(1), v2.data_ptr(),
+                                      v2.stride(0), v2.stride(1), k2.shape[0], handle)
+        if st:
+            dfh._check(st, "df_cache_write")
+
+    _enqueue(stream, cache.device, (k, v) + cache._tensors() + batch._tensors(), call)
+
+
+def cache_read(cache: KVCache, batch: CacheBatch, tokens: int, stream=None):
+    """(k, v), [tokens, kv_heads, head_dim] in the cache's dtype: the rows that
+    cache_write took for the same batch, as the cache holds them (codes times scale,
+    rounded once).  starts that run over whole lengths give whole sequences.  Rows of
+    no sequence are zeros."""
+    tokens = int(tokens)
+    if not 0 <= tokens <= 1 << 24:
+        raise ValueError("tokens must lie in 0 .. 2^24, got %d" % tokens)
+    if batch.device != cache.device:
+        raise ValueError("the batch must lie on %s" % cache.device)
+
+    def call(handle):
+        k, v = (torch.empty((tokens, cache.kv_heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
+                for _ in range(2))
+        st = dfh.lib().df_cache_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), tokens, handle)
+        if st:
+            dfh._check(st, "df_cache_read")
+        return k, v
+
+    return _enqueue(stream, cache.device, cache._tensors() + batch._tensors(), call)

@@ -66,6 +66,19 @@ class df_u8_matrix(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
+class df_cache(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("bits", ctypes.c_uint32), ("page_size", ctypes.c_uint32),
+                ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("pages", ctypes.c_uint64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class df_cache_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_uint32), ("width", ctypes.c_uint32), ("table_stride", ctypes.c_uint64),
+                ("tables", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("max_new", ctypes.c_uint32)]
+
+
 class df_loss(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("reduce", ctypes.c_int),
                 ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64), ("hidden", ctypes.c_uint64),
@@ -133,6 +146,11 @@ _SIGNATURES = {
     "df_linear_u8_codes": (ctypes.c_int, [ctypes.POINTER(df_u8_matrix), ctypes.c_int, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
+    "df_cache_write": (ctypes.c_int, [ctypes.POINTER(df_cache), ctypes.POINTER(df_cache_batch), ctypes.c_void_p,
+                                      ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                                      ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p]),
+    "df_cache_read": (ctypes.c_int, [ctypes.POINTER(df_cache), ctypes.POINTER(df_cache_batch), ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
     "df_loss_saved_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_loss_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_vocab_loss": (ctypes.c_int, [ctypes.POINTER(df_loss), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
