@@ -481,6 +481,26 @@ df_status df_cache_write(const df_cache *cache, const df_cache_batch *batch, con
 df_status df_cache_read(const df_cache *cache, const df_cache_batch *batch, void *k, void *v, uint64_t tokens,
                         hipStream_t stream);
 
+/* Attention of the batch's new tokens over the cache, which holds their own keys and
+ * values already: for the row of position p and head h, whose key head is h / (heads /
+ * kv_heads),
+ *     out = sum over j of softmax_j(scale q . k[j]) v[j],
+ * over the positions 0 <= j <= p that are there, with window > 0 those with p - j <
+ * window alone (0: all).  A row that sees no position, and a row of no sequence, is 0
+ * (its log-sum -inf).  What a position holds that a row does not see, infinities and
+ * NaN among it, does not touch the row.
+ * q: [tokens, heads, head_dim] as k of df_cache_write; out: contiguous, 16-byte aligned;
+ * both of cache->type.  lse (may be NULL): float [tokens, heads], the log of the sum of
+ * exp(scale q . k[j]).  heads: a multiple of kv_heads, at most 256 times it, tokens * heads
+ * / kv_heads at most 2^30.  scale: positive and finite.  The workspace, 256-byte aligned, holds
+ * partial sums where a row's keys are split over workgroups.  The same inputs give the
+ * same bits. */
+uint64_t df_cached_attention_workspace_bytes(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens,
+                                             uint32_t heads, int64_t window);
+df_status df_cached_attention(const df_cache *cache, const df_cache_batch *batch, const void *q, uint64_t q_token_stride,
+                              uint64_t q_head_stride, uint64_t tokens, uint32_t heads, float scale, int64_t window,
+                              void *out, float *lse, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------- losses over a large vocabulary */
 
 /* Hidden states x [rows, hidden] and head weights [vocab, hidden] (an LM head

@@ -7,7 +7,8 @@ kernels; both sit behind the C ABI in include/dfh.h, which ``dfh`` binds
 with the same names.  ``ops`` holds the operators on what the codec stores:
 products with uint4 weights and group scales, and losses over a large
 vocabulary, with their gradients, and products in 8-bit integers of uint8
-codes; ``cache`` a paged cache of keys and values.  ``synth`` draws the seeded synthetic workloads.
+codes; ``cache`` a paged cache of keys and values and the
+attention over it.  ``synth`` draws the seeded synthetic workloads.
 """
 from .dfh import (  # noqa: F401
     KIND_BF16, KIND_U4, KIND_U8, MAX_LEN, SECTION_NAMES, DEVERR_CODE, DEVERR_COUNT, ENCODE_SCRATCH_BYTES, DFError,
@@ -23,5 +24,5 @@ from .ops import (  # noqa: F401
     U4Matrix, U8Matrix, distill_loss, linear_u4, linear_u4_grad, linear_u8, quantize_rows, vocab_loss,
 )
 from .cache import (  # noqa: F401
-    CacheBatch, KVCache, cache_read, cache_write,
+    CacheBatch, KVCache, cache_read, cache_write, cached_attention,
 )

@@ -15,7 +15,7 @@ LIB = os.path.join(BUILD, "libdfh.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
-HIP_SOURCES = ("dfh_decode", "dfh_encode", "dfh_linear", "dfh_linear8", "dfh_loss", "dfh_cache")
+HIP_SOURCES = ("dfh_decode", "dfh_encode", "dfh_linear", "dfh_linear8", "dfh_loss", "dfh_cache", "dfh_attend")
 HIP_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
     # keep the compiler from forming packed fp32 instructions

@@ -3,7 +3,9 @@
 * ``KVCache`` holds the pages, in 16 bits or quantised to 8 with a scale for each
   token and head; ``CacheBatch`` says which sequences a call is about;
 * ``cache_write`` puts the keys and values of new tokens into the pages,
-  ``cache_read`` gives them back.
+  ``cache_read`` gives them back;
+* ``cached_attention`` is the attention of the new tokens over all that their
+  sequences hold.
 
 A step of several sequences, each with any number of new tokens (a prompt, a part of
 one, a single token, none), is one batch: rows starts[s] .. starts[s + 1] - 1 of the
@@ -21,7 +23,7 @@ import ctypes
 import torch
 
 from . import dfh
-from .ops import _TYPES, _current_device, _launch, _no_gradient, _on, _raw_stream
+from .ops import _TYPES, _current_device, _launch, _no_gradient, _on, _p, _raw_stream, _workspace
 
 
 class KVCache:
@@ -101,6 +103,7 @@ class CacheBatch:
         self.view = dfh.df_cache_batch(seqs, width, stride, tables.data_ptr(), lengths.data_ptr(), starts.data_ptr(),
                                        min(self.max_new or 0, 1 << 24))
         self._ref = ctypes.byref(self.view)
+        self._need = {}   # workspace bytes by shapes
 
     def _tensors(self):
         return (self.tables, self.lengths, self.starts)
@@ -176,3 +179,58 @@ def cache_read(cache: KVCache, batch: CacheBatch, tokens: int, stream=None):
         return k, v
 
     return _enqueue(stream, cache.device, cache._tensors() + batch._tensors(), call)
+
+
+def cached_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, scale: float | None = None,
+                     window: int | None = None, return_lse: bool = False, stream=None):
+    """Attention of the batch's new tokens over the cache, into which their own keys and
+    values are written already (cache_write with the same batch): for a token at
+    position p
+
+        out = sum_j softmax_j(scale q . k[j]) v[j]   over 0 <= j <= p, p - j < window
+
+    q [tokens, heads, head_dim] in the cache's dtype and any strides, heads a multiple
+    (up to 256) of the cache's kv_heads: head h reads key head h // (heads //
+    kv_heads).  scale (positive; default head_dim ** -0.5); window: a positive count of
+    positions, the token's own among them, or None for all.  Returns out like q,
+    contiguous, and with return_lse the float32 [tokens, heads] logarithms of the
+    rows' sums of exponentials.
+
+    A row that sees no position (an empty sequence, a token before position 0) and a
+    row of no sequence give 0, and -inf as logarithm.  What a position holds that a row
+    does not see does not touch that row, infinities and NaN among it.  Sums are float32; weights
+    are rounded to q's type before they multiply values, and float16 rounds 8-bit values
+    as cache_read does."""
+    _no_gradient("cached_attention", q)
+    _new_tokens(q, cache, batch, "q", None)
+    tokens, heads, dim = q.shape
+    if heads < 1 or heads % cache.kv_heads or heads // cache.kv_heads > 256:
+        raise ValueError("heads must be a multiple of kv_heads = %d, at most 256 times it, got %d" % (cache.kv_heads, heads))
+    if tokens * (heads // cache.kv_heads) > 1 << 30:
+        raise ValueError("more than 2^30 rows a key head")
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale <= 3e38:
+        raise ValueError("scale must be positive and finite, got %r" % (scale,))
+    if window is not None and int(window) < 1:
+        raise ValueError("window must be a positive count or None, got %r" % (window,))
+    window = 0 if window is None else min(int(window), 1 << 40)
+    dev = cache.device
+
+    def call(handle):
+        L = dfh.lib()
+        q2 = _heads16(q)
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+        key = (cache.kv_heads, cache.head_dim, cache.page_size, cache.bits, tokens, heads, window)
+        need = batch._need.get(key)
+        if need is None:
+            need = L.df_cached_attention_workspace_bytes(cache._ref, batch._ref, tokens, heads, window)
+            batch._need[key] = need
+        ws = _workspace(need, dev) if need else None
+        st = L.df_cached_attention(cache._ref, batch._ref, q2.data_ptr(), q2.stride(0), q2.stride(1), tokens, heads, scale,
+                                   window, out.data_ptr(), _p(lse), _p(ws), need, handle)
+        if st:
+            dfh._check(st, "df_cached_attention")
+        return (out, lse) if return_lse else out
+
+    return _enqueue(stream, dev, (q,) + cache._tensors() + batch._tensors(), call)

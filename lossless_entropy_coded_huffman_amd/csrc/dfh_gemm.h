@@ -37,8 +37,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-struct BF16 {};
-struct F16 {};
+struct BF16 {
+  static constexpr bool kRange = true;  // FP32's
+};
+struct F16 {
+  static constexpr bool kRange = false;
+};
 
 __device__ __forceinline__ f32x4 mfma(BF16, u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
@@ -439,9 +443,9 @@ __device__ __forceinline__ f32x4 add_planes(const float *p, uint64_t stride, uin
 
 // ------------------------------------------------------------------- launch
 // Raises a kernel's LDS limit where a launch needs more than 64 KiB, once per
-// kernel and device.
-hipError_t allow_lds(const void *fn, uint32_t bytes) {
-  if (bytes <= 65536) return hipSuccess;
+// kernel and device: to all that a CU has, less what the kernel declares itself.
+hipError_t allow_lds(const void *fn, uint32_t bytes, uint32_t declared = 0) {
+  if (bytes + declared <= 65536) return hipSuccess;
   static std::mutex mu;
   static std::map<std::pair<int, const void *>, bool> raised;
   int dev = 0;
@@ -451,7 +455,7 @@ hipError_t allow_lds(const void *fn, uint32_t bytes) {
     std::lock_guard<std::mutex> lk(mu);
     bool &have = raised[{dev, fn}];
     if (!have) {
-      e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - declared);
       have = e == hipSuccess;
     }
   } catch (...) {  // nothing throws across the C entries

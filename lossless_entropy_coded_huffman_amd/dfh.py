@@ -151,6 +151,12 @@ _SIGNATURES = {
                                       ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p]),
     "df_cache_read": (ctypes.c_int, [ctypes.POINTER(df_cache), ctypes.POINTER(df_cache_batch), ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
+    "df_cached_attention_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_cache), ctypes.POINTER(df_cache_batch),
+                                                              ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int64]),
+    "df_cached_attention": (ctypes.c_int, [ctypes.POINTER(df_cache), ctypes.POINTER(df_cache_batch), ctypes.c_void_p,
+                                           ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32,
+                                           ctypes.c_float, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
     "df_loss_saved_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_loss_workspace_bytes": (ctypes.c_uint64, [ctypes.POINTER(df_loss)]),
     "df_vocab_loss": (ctypes.c_int, [ctypes.POINTER(df_loss), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,

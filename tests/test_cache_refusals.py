@@ -75,3 +75,41 @@ def test_host_tensors_are_refused():
     t = torch.zeros(1, 2, dtype=torch.int32)
     with pytest.raises(ValueError):
         dfh.CacheBatch(t, t[0, :1], t[0])
+
+
+def attend(c, b, q=P, qt=4096, qh=128, tokens=5, heads=32, scale=0.1, window=0, out=P, lse=None, ws=P, nbytes=1 << 40):
+    return dfh.lib().df_cached_attention(ctypes.byref(c), ctypes.byref(b), q, qt, qh, tokens, heads, scale, window, out,
+                                         lse, ws, nbytes, None)
+
+
+def space(c, b, tokens=5, heads=32, window=0):
+    return dfh.lib().df_cached_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), tokens, heads, window)
+
+
+@pytest.mark.parametrize("kw", BAD_CACHE)
+def test_bad_cache_of_attention(kw):
+    assert attend(cache(**kw), batch()) == ARG and space(cache(**kw), batch()) == 0
+
+
+@pytest.mark.parametrize("kw", BAD_BATCH)
+def test_bad_batch_of_attention(kw):
+    assert attend(cache(), batch(**kw)) == ARG and space(cache(), batch(**kw)) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(q=P + 8), dict(qt=4100), dict(qh=4), dict(qt=(1 << 30) + 8), dict(out=None),
+                                dict(out=P + 8), dict(lse=P + 2), dict(heads=0), dict(heads=12), dict(heads=8 * 257),
+                                dict(tokens=(1 << 24) + 1), dict(tokens=1 << 23, heads=2048), dict(scale=0.0),
+                                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
+                                dict(ws=None), dict(ws=P + 16), dict(nbytes=100)])
+def test_bad_attention(kw):
+    # 4000 pages of 64: the keys are split, and a workspace is needed
+    assert attend(cache(), batch(width=4000, table_stride=4000), **kw) == ARG
+
+
+def test_attention_sizes():
+    assert attend(cache(), batch(), tokens=0, q=None, out=None) == 0
+    # partial sums take what the rows need, and never more than 256 MiB and a little for their statistics
+    small = space(cache(), batch(seqs=1, width=16, table_stride=16, max_new=1), tokens=1)
+    assert 0 < small <= 512 * 32 * 130 * 4 + 512
+    for seqs, tokens, width in ((1, 1, 1 << 22), (64, 64, 4096), (65536, 65536, 100), (1, 16384, 1 << 16), (300, 40000, 2000)):
+        assert space(cache(), batch(seqs=seqs, width=width, table_stride=width), tokens=tokens) <= 2 * (256 << 20) + 4096
