@@ -21,10 +21,8 @@
 //
 // Roundings: q and 16-bit keys and values are taken as they are, codes of 8 bits are
 // exact in both 16-bit types.  A token's scale of keys multiplies the FP32 scores; its
-// scale of values multiplies p before that is rounded to 16 bits where the type is BF16
-// (p times scale is the one rounding), while in FP16, whose range p times scale may leave,
-// the value is rounded to FP16 as cache_read gives it.  p is rounded to 16 bits (half a step:
-// 2^-9 or 2^-12 of it), sums are FP32.
+// scale of values multiplies p before that is rounded to 16 bits: the one rounding (half a
+// step, 2^-9 or 2^-12 of it) beside the output's.  Sums are FP32.
 #include <hip/hip_runtime.h>
 
 #include "dfh.h"
@@ -63,6 +61,15 @@ __device__ __forceinline__ f32x2 both_halves(float v) {
   return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
+// Infinities and NaN made zero.
+template <class T>
+__device__ __forceinline__ u32x4 finite_part(T, u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    v[i] &= ((v[i] & 0x7FFFu) > finite_bits(T{}) ? 0u : 0xFFFFu) | ((v[i] >> 16 & 0x7FFFu) > finite_bits(T{}) ? 0u : 0xFFFF0000u);
+  return v;
+}
+
 // Eight codes as 16-bit floats, exactly.  FP16: a byte of offset 128 in the mantissa of
 // 1024, then 1152 off; BF16 has no bits for that and goes by FP32.
 __device__ __forceinline__ u32x4 widen8(F16, u32x2 w) {
@@ -85,18 +92,6 @@ __device__ __forceinline__ u32x4 widen8(BF16, u32x2 w) {
   }
   return o;
 }
-// Eight codes times a scale each, rounded.
-template <class T>
-__device__ __forceinline__ u32x4 widen8_by(T, u32x2 w, const float *f) {
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const uint32_t v = w[i / 2] >> (16 * (i & 1));
-    o[i] = pair(T{}, (float)(int8_t)v * f[2 * i], (float)(int8_t)(v >> 8) * f[2 * i + 1]);
-  }
-  return o;
-}
-
 struct Attend {
   const uint16_t *q;
   uint64_t q_token, q_head;  // strides in elements
@@ -138,87 +133,116 @@ __device__ __forceinline__ Cuts cuts_of(const Pages &c, const Sequences &b, int3
 }
 constexpr int kFewShift = 5, kFewLeast = 4, kTileShift = 6, kTileLeast = 8;
 
-// A tile of keys or values in LDS: rows of D values of BITS, 16-byte chunks exchanged
-// within a row (in the source address, since a load writes LDS linearly).  Keys are
+// What codes of 8 bits become to multiply q: FP16, which is made of bytes with half of the
+// instructions that BF16 takes, for a lifted q (lift_q).
+template <class T, int BITS>
+struct KeyType {
+  typedef T type;
+};
+template <class T>
+struct KeyType<T, 8> {
+  typedef F16 type;
+};
+
+// A tile of keys or values in LDS, 16 bits a value: rows of D, 16-byte chunks exchanged
+// within a row (in the source address, where a load writes LDS linearly).  Keys are
 // read 16 bytes at one chunk of 32 rows: 8 rows in a row fall into 8 places.  Values are
-// read transposed, 64 (BITS 8: 32) bytes of 8 (16) rows: neighbours fall into different ones.
-template <int BITS, int D>
+// read transposed, 64 bytes of 8 rows: neighbours fall into different ones.
+template <int D>
 struct Rows {
-  static constexpr int kBytes = D * BITS / 8, kChunks = kBytes / 16;
+  static constexpr int kBytes = D * 2, kChunks = kBytes / 16;
   static constexpr int kPer = kBytes >= 128 ? 1 : 128 / kBytes;  // rows in 128 bytes
   static constexpr int kKeyPlaces = kChunks < 8 ? kChunks : 8;
-  static constexpr int kUnit = BITS == 16 ? 4 : 2;
-  static constexpr int kUnits = kChunks / kUnit < 1 ? 1 : kChunks / kUnit < 16 / kUnit ? kChunks / kUnit : 16 / kUnit;
+  static constexpr int kUnits = kChunks < 4 ? 1 : kChunks / 4 < 4 ? kChunks / 4 : 4;
   static __device__ __forceinline__ uint32_t key_swap(uint32_t r) { return (r / kPer) & (kKeyPlaces - 1); }
-  static __device__ __forceinline__ uint32_t value_swap(uint32_t r) { return ((r / kPer) & (kUnits - 1)) * kUnit; }
+  static __device__ __forceinline__ uint32_t value_swap(uint32_t r) { return ((r / kPer) & (kUnits - 1)) * 4; }
 };
 
 // Key of a lane's register r (of 16) in a block of 32, without the 4 * (lane / 32).
 __device__ __forceinline__ constexpr int key_of(int r) { return 8 * (r / 4) + r % 4; }
+
+// q's elements lifted into FP16 by a power of two that brings the row's largest (most) to
+// 2^14 .. 2^15, so that what is 2^-28 of that keeps all its bits; returns what takes it back.
+template <int N>
+__device__ __forceinline__ float lift_q(u32x4 (&q)[N], float most) {
+  const int up = lift_bits(most, 14);
+#pragma unroll
+  for (int st = 0; st < N; st++)
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      q[st][i] = pair(F16{}, __builtin_ldexpf(from_bits(BF16{}, (uint16_t)q[st][i]), up),
+                      __builtin_ldexpf(from_bits(BF16{}, (uint16_t)(q[st][i] >> 16)), up));
+  return power_of_two(-up);
+}
 
 // What 32 queries of a wave gather: lane l has query l % 32.
 template <class T, int BITS, int D>
 struct Wave {
   u32x4 q[D / 16];
   f32x16 o[D / 32];
-  float m, l;  // maximum (times c), and this half's sum
+  float m, l;       // reference of the exponentials (times log2 e), this half's sum
+  float z, lift;    // the largest score, where m lies below it
+  float mul;        // what a score is multiplied by
   int32_t pos;
 
   // row: this lane's query
-  __device__ __forceinline__ void init(const uint16_t *row, int32_t position) {
+  __device__ __forceinline__ void init(const uint16_t *row, int32_t position, float c) {
     const uint32_t h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-    for (int s = 0; s < D / 16; s++) {
-      // a step's 16 elements: 8 of each half; of keys of 8 bits a lane reads two steps' at once
-      const uint32_t chunk = BITS == 8 ? (s / 2) * 4 + h * 2 + (s & 1) : s * 2 + h;
-      q[s] = *(const u32x4 *)(row + chunk * 8);
+    for (int s = 0; s < D / 16; s++) q[s] = *(const u32x4 *)(row + (s * 2 + h) * 8);
+    mul = BITS == 8 ? 1.f : c;
+    if constexpr (BITS == 8 && T::kRange) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int s = 0; s < D / 16; s++) top = most_bits(q[s], top);
+      const f32x2 tops = both_halves(from_bits(T{}, (uint16_t)joined(top)));
+      mul = lift_q(q, __builtin_fmaxf(tops[0], tops[1]));
     }
 #pragma unroll
     for (int d = 0; d < D / 32; d++) o[d] = f32x16{};
-    m = -__builtin_huge_valf();
+    m = z = -__builtin_huge_valf();
     l = 0.f;
+    lift = 64.f;
     pos = position;
   }
 };
 
+// FP16 with codes: exponentials are taken off a reference that lies `lift` below the row's
+// largest score, the least lift of the tiles so far that brings the largest scale of the
+// values it sees to 2^14 .. 2^15, so p times a scale neither overflows nor loses
+// bits until it is 2^-28 of the largest.  Values of FP16 span 2^40, so what is lost below lies under
+// their own steps.  The sum of p is off by the same power of two.
+constexpr bool lifts(bool range, int bits) { return bits == 8 && !range; }
+__device__ __forceinline__ float value_lift(float largest, float so_far) {
+  const int up = lift_bits(largest, 14);
+  const float f = (float)(up < -64 ? -64 : up > 64 ? 64 : up);
+  return largest > 0.f && f < so_far ? f : so_far;
+}
+
 // Whether a query at pos sees the key at pos - gap.
 __device__ __forceinline__ bool sees(int32_t gap, int32_t window) { return (uint32_t)gap < (uint32_t)window; }
 
-// NB blocks of 32 keys at position `base` in LDS (LB bits a value there): adds them to w.
-// SCALED: scales of the keys (times c) and of the values in LDS, `there` bit j of a block: the key
-// exists; whole: every query sees every key.  BARE: values are codes, p takes their
-// scale.
-template <class T, int BITS, int LB, int D, int NB, bool SCALED, bool BARE, class Mask>
+// 64 keys at position `base` in LDS, 16 bits a value.  BITS 8: codes, with ks scales of the keys
+// times c, vs of the values; there: bit j: key j exists; whole: every query sees all.
+template <class T, int BITS, int D>
 __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
-                                         const float *vs, int32_t base, Mask there, bool whole, float c, int32_t window) {
-  typedef Rows<LB, D> R;
+                                         const float *vs, int32_t base, uint64_t there, bool whole, int32_t window) {
+  typedef Rows<D> R;
+  typedef typename KeyType<T, BITS>::type K;
   const uint32_t lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
   // scores
-  f32x16 s[NB];
+  f32x16 s[2];
 #pragma unroll
-  for (int n = 0; n < NB; n++) {
+  for (int n = 0; n < 2; n++) {
     s[n] = f32x16{};
     const uint8_t *p = lk + (n * 32 + row) * R::kBytes;
     const uint32_t f = R::key_swap(row);
-    if constexpr (LB == 16) {
 #pragma unroll
-      for (int st = 0; st < D / 16; st++) {
-        // the order of a lane's 8 elements is q's
-        const uint32_t chunk = BITS == 8 ? (st / 2) * 4 + h * 2 + (st & 1) : st * 2 + h;
-        s[n] = mfma32(T{}, *(const u32x4 *)(p + ((chunk ^ f) * 16)), w.q[st], s[n]);
-      }
-    } else {
-#pragma unroll
-      for (int st = 0; st < D / 32; st++) {
-        const u32x4 k = *(const u32x4 *)(p + (((st * 2 + h) ^ f) * 16));
-        s[n] = mfma32(T{}, widen8(T{}, u32x2{k[0], k[1]}), w.q[2 * st], s[n]);
-        s[n] = mfma32(T{}, widen8(T{}, u32x2{k[2], k[3]}), w.q[2 * st + 1], s[n]);
-      }
-    }
+    for (int st = 0; st < D / 16; st++) s[n] = mfma32(K{}, *(const u32x4 *)(p + (((st * 2 + h) ^ f) * 16)), w.q[st], s[n]);
   }
-  if constexpr (SCALED) {
+  if constexpr (BITS == 8) {
 #pragma unroll
-    for (int n = 0; n < NB; n++)
+    for (int n = 0; n < 2; n++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const f32x4 k = *(const f32x4 *)(ks + n * 32 + 8 * i + 4 * h);
@@ -227,10 +251,11 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
       }
   }
   const int32_t gap = w.pos - base - 4 * (int32_t)h;  // to the key of register 0 of block 0
+  const uint64_t mine = there >> (4 * h);
   if (!whole) {
 #pragma unroll
-    for (int n = 0; n < NB; n++) {
-      const uint32_t t = there(n) >> (4 * h);
+    for (int n = 0; n < 2; n++) {
+      const uint32_t t = (uint32_t)(mine >> (32 * n));
 #pragma unroll
       for (int r = 0; r < 16; r++)
         if (!(sees(gap - n * 32 - key_of(r), window) && (t >> key_of(r) & 1))) s[n][r] = -__builtin_huge_valf();
@@ -238,12 +263,35 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
   }
   float top = s[0][0];
 #pragma unroll
-  for (int n = 0; n < NB; n++)
+  for (int n = 0; n < 2; n++)
 #pragma unroll
     for (int r = 0; r < 16; r++) top = __builtin_fmaxf(top, s[n][r]);
   const f32x2 tops = both_halves(top);
-  top = __builtin_fmaxf(tops[0], tops[1]);
-  if constexpr (!SCALED) top *= c;
+  top = __builtin_fmaxf(tops[0], tops[1]) * w.mul;
+  f32x4 vf[BITS == 8 ? 8 : 1];
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) vf[i] = *(const f32x4 *)(vs + 8 * i + 4 * h);
+    if (!whole) {
+      // a scale that is no number belongs to the queries that see its key alone
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (!(sees(gap - 8 * i - e, window) && (mine >> (8 * i + e) & 1))) vf[i][e] = 0.f;
+    }
+  }
+  if constexpr (lifts(T::kRange, BITS)) {
+    float largest = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) largest = __builtin_fmaxf(largest, __builtin_fabsf(vf[i][e]));
+    const f32x2 both = both_halves(largest);
+    w.lift = value_lift(__builtin_fmaxf(both[0], both[1]), w.lift);
+    w.z = __builtin_fmaxf(top, w.z);
+    top = w.z - w.lift;
+  }
   top = __builtin_fmaxf(top, w.m);
   const float ref = top == -__builtin_huge_valf() ? 0.f : top;
   if (__ballot(top > w.m)) {
@@ -255,59 +303,32 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
   }
   float sum = 0.f;
 #pragma unroll
-  for (int n = 0; n < NB; n++)
+  for (int n = 0; n < 2; n++)
 #pragma unroll
     for (int r = 0; r < 16; r++) {
-      s[n][r] = exp2_of(SCALED ? s[n][r] - ref : __builtin_fmaf(s[n][r], c, -ref));
+      s[n][r] = exp2_of(__builtin_fmaf(s[n][r], w.mul, -ref));
       sum += s[n][r];
     }
   w.l += sum;
-  // values
-  float f[SCALED ? NB * 16 : 1];
-  if constexpr (SCALED) {
+  if constexpr (BITS == 8) {
 #pragma unroll
-    for (int n = 0; n < NB; n++)
+    for (int n = 0; n < 2; n++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const f32x4 v = *(const f32x4 *)(vs + n * 32 + 8 * i + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; e++) f[n * 16 + 4 * i + e] = v[e];
-      }
-    if constexpr (BARE) {
-#pragma unroll
-      for (int n = 0; n < NB; n++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-          float p = s[n][r] * f[n * 16 + r];
-          // a scale that is no number belongs to the queries that see its key alone
-          if (!whole && !(sees(gap - n * 32 - key_of(r), window) && (there(n) >> (4 * h) >> key_of(r) & 1))) p = 0.f;
-          s[n][r] = p;
-        }
-    }
+      for (int r = 0; r < 16; r++) s[n][r] *= vf[n * 4 + r / 4][r % 4];
   }
   const uint32_t l16 = lane & 15, dh = (lane >> 4) & 1;
   auto value = [&](int st, int d) -> u32x4 {  // 16 keys, 32 of D
-    if constexpr (LB == 16) {
-      const uint32_t r = 4 * h + l16 / 4, fs = R::value_swap(r);
-      const uint8_t *p = lv + (st * 16 + r) * R::kBytes + (((d * 4 + dh * 2 + ((l16 >> 1) & 1)) ^ fs) * 16) + (l16 & 1) * 8;
-      const u32x2 lo = read_turned(p), hi = read_turned(p + 8 * R::kBytes);
-      return u32x4{lo[0], lo[1], hi[0], hi[1]};
-    } else {
-      const uint32_t slot = l16 / 2, r = 8 * (slot / 4) + 4 * h + slot % 4, fs = R::value_swap(r);
-      const uint8_t *p = lv + (st * 16 + r) * R::kBytes + (((d * 2 + dh) ^ fs) * 16) + (l16 & 1) * 8;
-      const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-          (__attribute__((address_space(3))) i32x2 *)(__attribute__((address_space(3))) void *)p);
-      const u32x2 u = __builtin_bit_cast(u32x2, v);
-      if constexpr (BARE) return widen8(T{}, u);
-      return widen8_by(T{}, u, f + st * 8);
-    }
+    const uint32_t r = 4 * h + l16 / 4, fs = R::value_swap(r);
+    const uint8_t *p = lv + (st * 16 + r) * R::kBytes + (((d * 4 + dh * 2 + ((l16 >> 1) & 1)) ^ fs) * 16) + (l16 & 1) * 8;
+    const u32x2 lo = read_turned(p), hi = read_turned(p + 8 * R::kBytes);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
-  u32x4 p[2 * NB];
+  u32x4 p[4];
 #pragma unroll
-  for (int st = 0; st < 2 * NB; st++)
+  for (int st = 0; st < 4; st++)
 #pragma unroll
     for (int i = 0; i < 4; i++) p[st][i] = pair(T{}, s[st / 2][8 * (st & 1) + 2 * i], s[st / 2][8 * (st & 1) + 2 * i + 1]);
-  if constexpr (!BARE) {
+  if constexpr (BITS == 16) {
     // Values that are not finite count for the queries that see them, and zero times one
     // is no number: a tile in which some query does not see every key is looked
     // through, and where there is one, those are left out of the products and
@@ -315,30 +336,24 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     if (!whole) {
       uint32_t most = 0;
 #pragma unroll
-      for (int st = 0; st < 2 * NB; st++)
+      for (int st = 0; st < 4; st++)
 #pragma unroll
         for (int d = 0; d < D / 32; d++) most = most_bits(value(st, d), most);
       if (__ballot(joined(most) > finite_bits(T{}))) {
-        auto finite = [](u32x4 v) {
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            v[i] &= ((v[i] & 0x7FFFu) > finite_bits(T{}) ? 0u : 0xFFFFu) | ((v[i] >> 16 & 0x7FFFu) > finite_bits(T{}) ? 0u : 0xFFFF0000u);
-          return v;
-        };
+        for (int st = 0; st < 4; st++) {
 #pragma unroll
-        for (int st = 0; st < 2 * NB; st++) {
-#pragma unroll
-          for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, finite(value(st, d)), p[st], w.o[d]);
+          for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, finite_part(T{}, value(st, d)), p[st], w.o[d]);
 #pragma unroll 1
           for (uint32_t e = 0; e < 16; e++) {
             const uint32_t half = e >> 3, word = (e & 7) >> 1, at = st * 16 + 8 * ((e & 7) / 4) + 4 * half + (e & 3);
             const uint32_t bits = h == half ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
             const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
-            const bool seen = sees(w.pos - base - (int32_t)at, window) && (there(at / 32) >> (at % 32) & 1);
+            const bool seen = sees(w.pos - base - (int32_t)at, window) && (there >> at & 1);
 #pragma unroll
             for (int d = 0; d < D / 32; d++) {
               const u32x4 v = value(st, d);
-              const f32x16 t = mfma32(T{}, (v ^ finite(v)) & only, p[st] & only, f32x16{});
+              const f32x16 t = mfma32(T{}, (v ^ finite_part(T{}, v)) & only, p[st] & only, f32x16{});
 #pragma unroll
               for (int r = 0; r < 16; r++) w.o[d][r] += seen ? t[r] : 0.f;
             }
@@ -349,7 +364,7 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     }
   }
 #pragma unroll
-  for (int st = 0; st < 2 * NB; st++)
+  for (int st = 0; st < 4; st++)
 #pragma unroll
     for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, value(st, d), p[st], w.o[d]);
 }
@@ -374,13 +389,231 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -__builtin_huge_valf() : (m + __builtin_log2f(l)) * 0.693147180559945309f;
 }
 
-template <class T, int BITS, int D, int W>
-__global__ __launch_bounds__(64 * W) void attend_few(const Pages c, const Sequences b, const Attend a) {
-  typedef Rows<BITS, D> R;
-  constexpr int kTile = 32 * R::kBytes, kLoads = kTile / 1024, kRowsPer = 32 / kLoads;
-  constexpr bool SCALED = BITS == 8, BARE = SCALED && T::kRange;
+// The largest of the four lanes of a query (l % 16), and their sum.
+__device__ __forceinline__ float most_of_four(float v) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  const f32x2 b = both_halves(__builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  return __builtin_fmaxf(b[0], b[1]);
+}
+__device__ __forceinline__ float sum_of_four(float v) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  const f32x2 b = both_halves(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+  return b[0] + b[1];
+}
+
+// What 16 NQ queries of a wave gather: lane l has queries l % 16 (+ 16).  As Wave, on
+// v_mfma_f32_16x16x32, whose results leave a lane 8 keys of 32: with a few queries a tile
+// half of the exponentials, and of the registers, that 32 columns take.
+template <class T, int BITS, int D, int NQ>
+struct Few {
+  u32x4 q[NQ][D / 32];
+  f32x4 o[NQ][D / 16];
+  float m[NQ], l[NQ], z[NQ], lift[NQ], mul[NQ];
+  int32_t pos[NQ];
+
+  // the element of D that q's step st, part u (of 8) starts at in lane group g
+  static __device__ __forceinline__ uint32_t chunk_of(int st, uint32_t g) {
+    return BITS == 8 && D >= 64 ? (st / 2) * 8 + g * 2 + (st & 1) : st * 4 + g;
+  }
+  __device__ __forceinline__ void init(int n, const uint16_t *row, int32_t position, float c) {
+    const uint32_t g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int st = 0; st < D / 32; st++) q[n][st] = *(const u32x4 *)(row + chunk_of(st, g) * 8);
+    mul[n] = BITS == 8 ? 1.f : c;
+    if constexpr (BITS == 8 && T::kRange) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int st = 0; st < D / 32; st++) top = most_bits(q[n][st], top);
+      const float most = most_of_four(from_bits(T{}, (uint16_t)joined(top)));
+      mul[n] = lift_q(q[n], most);
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m[n] = z[n] = -__builtin_huge_valf();
+    l[n] = 0.f;
+    lift[n] = 64.f;
+    pos[n] = position;
+  }
+};
+// Key of a lane's register r (of 8) among 32, without the 4 * (lane / 16).
+__device__ __forceinline__ constexpr int few_key(int r) { return 16 * (r / 4) + r % 4; }
+
+// A tile of 32 rows of D values of BITS in LDS.  As Rows; values are read transposed
+// in 32 (16) bytes of 16 (32) rows.
+template <int BITS, int D>
+struct FewRows {
+  static constexpr int kBytes = D * BITS / 8, kChunks = kBytes / 16;
+  static constexpr int kPer = kBytes >= 128 ? 1 : 128 / kBytes;
+  static constexpr int kPlaces = kChunks < 8 ? kChunks : 8;
+  static constexpr int kUnit = BITS == 16 ? 2 : 1;
+  static constexpr int kUnits = kChunks / kUnit < 16 / kUnit ? kChunks / kUnit : 16 / kUnit;
+  static __device__ __forceinline__ uint32_t key_swap(uint32_t r) { return (r / kPer) & (kPlaces - 1); }
+  static __device__ __forceinline__ uint32_t value_swap(uint32_t r) { return ((r / kPer) & (kUnits - 1)) * kUnit; }
+};
+
+// 32 keys at position `base` in LDS.  BITS 8: ks scales of the keys times c, vs of the
+// values; there: bit j: key j exists; whole: every query sees all.
+template <class T, int BITS, int D, int NQ>
+__device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
+                                        const float *vs, int32_t base, uint32_t there, bool whole, int32_t window) {
+  typedef FewRows<BITS, D> R;
+  const uint32_t lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  f32x4 s[NQ][2];
+#pragma unroll
+  for (int b = 0; b < 2; b++) {
+#pragma unroll
+    for (int n = 0; n < NQ; n++) s[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint8_t *p = lk + (b * 16 + l16) * R::kBytes;
+    const uint32_t f = R::key_swap(b * 16 + l16);
+    if constexpr (BITS == 16) {
+#pragma unroll
+      for (int st = 0; st < D / 32; st++) {
+        const u32x4 k = *(const u32x4 *)(p + (((st * 4 + g) ^ f) * 16));
+#pragma unroll
+        for (int n = 0; n < NQ; n++) s[n][b] = mfma(T{}, k, w.q[n][st], s[n][b]);
+      }
+    } else if constexpr (D == 32) {
+      const u32x4 k = widen8(F16{}, *(const u32x2 *)(p + (((g >> 1) ^ f) * 16) + (g & 1) * 8));
+#pragma unroll
+      for (int n = 0; n < NQ; n++) s[n][b] = mfma(F16{}, k, w.q[n][0], s[n][b]);
+    } else {
+#pragma unroll
+      for (int st = 0; st < D / 64; st++) {
+        const u32x4 k = *(const u32x4 *)(p + (((st * 4 + g) ^ f) * 16));
+        const u32x4 k0 = widen8(F16{}, u32x2{k[0], k[1]}), k1 = widen8(F16{}, u32x2{k[2], k[3]});
+#pragma unroll
+        for (int n = 0; n < NQ; n++) {
+          s[n][b] = mfma(F16{}, k0, w.q[n][2 * st], s[n][b]);
+          s[n][b] = mfma(F16{}, k1, w.q[n][2 * st + 1], s[n][b]);
+        }
+      }
+    }
+  }
+  f32x4 kf[2], vf[2];
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+      kf[b] = *(const f32x4 *)(ks + b * 16 + 4 * g);
+      vf[b] = *(const f32x4 *)(vs + b * 16 + 4 * g);
+    }
+  }
+  u32x4 p[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; n++) {
+    const int32_t gap = w.pos[n] - base - 4 * (int32_t)g;
+    const uint32_t mine = there >> (4 * g);
+    float z[8];
+#pragma unroll
+    for (int r = 0; r < 8; r++) {
+      z[r] = s[n][r / 4][r % 4];
+      if constexpr (BITS == 8) z[r] *= kf[r / 4][r % 4];
+    }
+    if (!whole) {
+#pragma unroll
+      for (int r = 0; r < 8; r++)
+        if (!(sees(gap - few_key(r), window) && (mine >> few_key(r) & 1))) z[r] = -__builtin_huge_valf();
+    }
+    float top = z[0];
+#pragma unroll
+    for (int r = 1; r < 8; r++) top = __builtin_fmaxf(top, z[r]);
+    top = most_of_four(top) * w.mul[n];
+    float f[8];
+    if constexpr (BITS == 8) {
+      // a scale that is no number belongs to the queries that see its key alone
+#pragma unroll
+      for (int r = 0; r < 8; r++)
+        f[r] = whole || (sees(gap - few_key(r), window) && (mine >> few_key(r) & 1)) ? vf[r / 4][r % 4] : 0.f;
+    }
+    if constexpr (lifts(T::kRange, BITS)) {
+      float largest = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; r++) largest = __builtin_fmaxf(largest, __builtin_fabsf(f[r]));
+      w.lift[n] = value_lift(most_of_four(largest), w.lift[n]);
+      w.z[n] = __builtin_fmaxf(top, w.z[n]);
+      top = w.z[n] - w.lift[n];
+    }
+    top = __builtin_fmaxf(top, w.m[n]);
+    const float ref = top == -__builtin_huge_valf() ? 0.f : top;
+    if (__ballot(top > w.m[n])) {
+      const float back = exp2_of(w.m[n] - ref);
+      w.l[n] *= back;
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) w.o[n][d] *= back;
+      w.m[n] = top;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; r++) {
+      z[r] = exp2_of(__builtin_fmaf(z[r], w.mul[n], -ref));
+      sum += z[r];
+    }
+    w.l[n] += sum;
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int r = 0; r < 8; r++) z[r] *= f[r];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) p[n][i] = pair(T{}, z[2 * i], z[2 * i + 1]);
+  }
+  auto value = [&](int d) -> u32x4 {  // 32 keys in the order of p, 16 of D
+    if constexpr (BITS == 16) {
+      const uint32_t r = 4 * g + l16 / 4;
+      const uint8_t *lo = lv + r * R::kBytes + (((d * 2 + ((l16 >> 1) & 1)) ^ R::value_swap(r)) * 16) + (l16 & 1) * 8;
+      const uint8_t *hi = lv + (r + 16) * R::kBytes + (((d * 2 + ((l16 >> 1) & 1)) ^ R::value_swap(r + 16)) * 16) + (l16 & 1) * 8;
+      const u32x2 a = read_turned(lo), b = read_turned(hi);
+      return u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+      const uint32_t slot = l16 / 2, r = 16 * (slot / 4) + 4 * g + slot % 4;
+      const uint8_t *at = lv + r * R::kBytes + ((d ^ R::value_swap(r)) * 16) + (l16 & 1) * 8;
+      return widen8(T{}, __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                             (__attribute__((address_space(3))) i32x2 *)(__attribute__((address_space(3))) void *)at)));
+    }
+  };
+  if constexpr (BITS == 16) {
+    if (!whole) {  // as in add_keys
+      uint32_t most = 0;
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) most = most_bits(value(d), most);
+      if (__ballot(joined(most) > finite_bits(T{}))) {
+#pragma unroll
+        for (int d = 0; d < D / 16; d++)
+#pragma unroll
+          for (int n = 0; n < NQ; n++) w.o[n][d] = mfma(T{}, finite_part(T{}, value(d)), p[n], w.o[n][d]);
+#pragma unroll 1
+        for (uint32_t e = 0; e < 32; e++) {
+          const uint32_t group = e >> 3, word = (e & 7) >> 1, at = 16 * ((e & 7) / 4) + 4 * group + (e & 3);
+          const uint32_t bits = g == group ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+          const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
+#pragma unroll
+          for (int n = 0; n < NQ; n++) {
+            const bool seen = sees(w.pos[n] - base - (int32_t)at, window) && (there >> at & 1);
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) {
+              const u32x4 v = value(d);
+              const f32x4 t = mfma(T{}, (v ^ finite_part(T{}, v)) & only, p[n] & only, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+              for (int r = 0; r < 4; r++) w.o[n][d][r] += seen ? t[r] : 0.f;
+            }
+          }
+        }
+        return;
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < D / 16; d++) {
+    const u32x4 v = value(d);
+#pragma unroll
+    for (int n = 0; n < NQ; n++) w.o[n][d] = mfma(T{}, v, p[n], w.o[n][d]);
+  }
+}
+
+template <class T, int BITS, int D, int NQ, int W>
+__global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_few(const Pages c, const Sequences b, const Attend a) {
+  typedef FewRows<BITS, D> R;
+  constexpr int kTile = 32 * R::kBytes, kLoads = kTile / 1024, kRowsPer = 32 / kLoads, kRows = 16 * NQ;
   extern __shared__ __align__(1024) uint8_t lds[];  // [W][2][keys, values], then joined
-  __shared__ float scales[W][64], ms[W][32], ls[W][32];
+  __shared__ float scales[W][64], ms[W][kRows], ls[W][kRows];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t *buf = lds + wave * (4 * kTile);
   const uint64_t units = (uint64_t)b.count * c.heads * a.few_splits;
@@ -401,76 +634,89 @@ __global__ __launch_bounds__(64 * W) void attend_few(const Pages c, const Sequen
     }
     if (rows == 0 || (!a.alone && rows > a.cap)) continue;
     const int32_t *table = b.tables + s * b.stride;
-    for (uint32_t r0 = 0; r0 < rows; r0 += r0 ? 32 : a.cap) {
+    for (uint32_t r0 = 0; r0 < rows; r0 += r0 ? kRows : a.cap) {
       if (r0 && z) break;  // rows behind the capacity are not split
-      const uint32_t most = r0 ? 32 : a.cap, count = rows - r0 < most ? rows - r0 : most;
+      const uint32_t most = r0 ? kRows : a.cap, count = rows - r0 < most ? rows - r0 : most;
       const int32_t first = sp.first + (int32_t)(r0 / a.group), last = sp.first + (int32_t)((r0 + count - 1) / a.group);
       const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kFewShift, r0 ? 1 : a.few_splits, kFewLeast);
       if (z >= (uint32_t)k.count && z) break;
       const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
-      const uint32_t mine = r0 + ((lane & 31) < count ? (lane & 31) : count - 1);
-      const int32_t token = sp.first + (int32_t)(mine / a.group);
-      Wave<T, BITS, D> w;
-      w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead);
       // a tile's pages and scales come a tile ahead of its rows
       int32_t page = -1;
+      uint32_t there = 0, next = 0;
       float scale = 0.f;
       auto look = [&](int32_t t) { page = t < t1 ? page_at(c, table, t * 32 + (int32_t)(lane & 31), k.stop) : -1; };
-      auto request = [&](int32_t t, uint8_t *dst) {
+      auto request = [&](int32_t t, uint8_t *dst, uint32_t in) {
+        if (in == 0xFFFFFFFFu && kRowsPer <= 16) {
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-          const uint32_t row = i * kRowsPer + lane / R::kChunks;
-          const int32_t pg = kRowsPer <= 16 ? __builtin_amdgcn_readlane(page, i * kRowsPer) : __shfl(page, (int)row);
-          // (the last tile's pages begin in it, and its rows end in it)
-          const bool in = pg >= 0 && t * 32 + (int32_t)row < k.stop;
-          const uint64_t at = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 32) + row) * R::kBytes;
-          const void *none = &g_zero16;
-          to_lds(in ? c.k + at + (((lane % R::kChunks) ^ R::key_swap(row)) * 16) : none, dst + i * 1024);
-          to_lds(in ? c.v + at + (((lane % R::kChunks) ^ R::value_swap(row)) * 16) : none, dst + kTile + i * 1024);
+          for (int i = 0; i < kLoads; i++) {
+            const uint32_t row = i * kRowsPer + lane / R::kChunks;
+            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, i * kRowsPer), head, (uint32_t)(t * 32 + i * kRowsPer)) *
+                                R::kBytes;
+            to_lds(c.k + at + (lane / R::kChunks * R::kBytes + ((lane % R::kChunks) ^ R::key_swap(row)) * 16), dst + i * 1024);
+            to_lds(c.v + at + (lane / R::kChunks * R::kBytes + ((lane % R::kChunks) ^ R::value_swap(row)) * 16), dst + kTile + i * 1024);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; i++) {
+            const uint32_t row = i * kRowsPer + lane / R::kChunks;
+            const int32_t pg = __shfl(page, (int)row);
+            const uint64_t at = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 32) + row) * R::kBytes;
+            const void *none = &g_zero16;
+            to_lds(pg >= 0 ? c.k + at + (((lane % R::kChunks) ^ R::key_swap(row)) * 16) : none, dst + i * 1024);
+            to_lds(pg >= 0 ? c.v + at + (((lane % R::kChunks) ^ R::value_swap(row)) * 16) : none, dst + kTile + i * 1024);
+          }
         }
-        if constexpr (SCALED) {
+        if constexpr (BITS == 8) {
           scale = 0.f;
           if (page >= 0) scale = (lane < 32 ? c.k_scales : c.v_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 32) + (lane & 31))];
         }
       };
       const int32_t mine0 = t0 + (int32_t)wave;
       look(mine0);
-      uint32_t there = (uint32_t)__ballot(page >= 0), next = 0;
+      Few<T, BITS, D, NQ> w;
+      there = (uint32_t)__ballot(page >= 0);
       if (mine0 < t1) {
-        request(mine0, buf);
+        request(mine0, buf, there);
         look(mine0 + W);
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; n++) {
+        const uint32_t r = n * 16 + (lane & 15), mine = r0 + (r < count ? r : count - 1);
+        const int32_t token = sp.first + (int32_t)(mine / a.group);
+        w.init(n, a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
       }
       for (int32_t t = mine0; t < t1; t += W) {
         const uint32_t odd = ((t - mine0) / W) & 1;
         wait_but<0>();
-        if constexpr (SCALED) scales[wave][lane] = lane < 32 ? scale * a.c : scale;
+        if constexpr (BITS == 8) scales[wave][lane] = lane < 32 ? scale * a.c : scale;
         next = (uint32_t)__ballot(page >= 0);
         if (t + W < t1) {
-          request(t + W, buf + (odd ^ 1) * (2 * kTile));
+          request(t + W, buf + (odd ^ 1) * (2 * kTile), next);
           look(t + 2 * W);
         }
         const bool whole = there == 0xFFFFFFFFu && t * 32 + 31 <= first + sp.ahead && last + sp.ahead - t * 32 < a.window;
         const uint8_t *p = buf + odd * (2 * kTile);
-        add_keys<T, BITS, BITS, D, 1, SCALED, BARE>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32,
-                                                    [=](int) { return there; }, whole, a.c, a.window);
+        add_few<T, BITS, D, NQ>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, whole, a.window);
         there = next;
         wait_reads();  // the buffer is asked for again
       }
-      // the waves' sums: [W][32][D] in place of the tiles, 16-byte chunks exchanged
-      const f32x2 sums = both_halves(w.l);
+      // the waves' sums: [W][16 NQ][D] in place of the tiles, 16-byte chunks exchanged
       __syncthreads();
       float *part = (float *)lds;
-      if ((lane & 31) < count) {
 #pragma unroll
-        for (int d = 0; d < D / 32; d++)
+      for (int n = 0; n < NQ; n++) {
+        const uint32_t r = n * 16 + (lane & 15);
+        const float sum = sum_of_four(w.l[n]);
+        if (r < count) {
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const uint32_t chunk = d * 8 + i * 2 + (lane >> 5);
-            *(f32x4 *)(part + (wave * 32 + (lane & 31)) * D + ((chunk ^ (lane & 7)) * 4)) =
-                f32x4{w.o[d][4 * i], w.o[d][4 * i + 1], w.o[d][4 * i + 2], w.o[d][4 * i + 3]};
+          for (int d = 0; d < D / 16; d++) {
+            const uint32_t chunk = d * 4 + (lane >> 4);
+            *(f32x4 *)(part + (wave * kRows + r) * D + ((chunk ^ (lane & 7)) * 4)) = w.o[n][d];
           }
-        ms[wave][lane & 31] = w.m;
-        ls[wave][lane & 31] = sums[0] + sums[1];
+          ms[wave][r] = w.m[n];
+          ls[wave][r] = sum;
+        }
       }
       __syncthreads();
       const bool direct = k.count <= 1;
@@ -485,7 +731,7 @@ __global__ __launch_bounds__(64 * W) void attend_few(const Pages c, const Sequen
 #pragma unroll
         for (int q = 0; q < W; q++) {
           const float f = exp2_of(ms[q][r] - ref);
-          v += *(const f32x4 *)(part + (q * 32 + r) * D + ((chunk ^ (r & 7)) * 4)) * f;
+          v += *(const f32x4 *)(part + (q * kRows + r) * D + ((chunk ^ (r & 7)) * 4)) * f;
           l += ls[q][r] * f;
         }
         const uint32_t row = r0 + r;
@@ -501,6 +747,63 @@ __global__ __launch_bounds__(64 * W) void attend_few(const Pages c, const Sequen
       }
       __syncthreads();
     }
+  }
+}
+
+// The parts of a row of few, a workgroup to a row (sequence, key head, row): D / 4 lanes
+// hold it, and 1024 / D groups of them take the parts in turn, so that all are read at
+// once (2000 positions for a token in 16 parts: 3 us against 10 with one after the other).
+template <class T, int D>
+__global__ __launch_bounds__(256) void join_few(const Pages c, const Sequences b, const Attend a) {
+  constexpr uint32_t kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ f32x4 vs[256];
+  __shared__ float ms[kGroups], ls[kGroups];
+  const uint32_t chunk = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const uint64_t all = (uint64_t)b.count * c.heads * a.cap;
+  for (uint64_t row = blockIdx.x; row < all; row += gridDim.x) {
+    const uint32_t r = (uint32_t)(row % a.cap), head = (uint32_t)(row / a.cap % c.heads), s = (uint32_t)(row / a.cap / c.heads);
+    const Span sp = span_of(b, s);
+    const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
+    if (r >= rows || (!a.alone && rows > a.cap)) continue;
+    const uint32_t count = rows < a.cap ? rows : a.cap;
+    const int32_t parts = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window,
+                                  kFewShift, a.few_splits, kFewLeast).count;
+    if (parts <= 1) continue;
+    float m = -__builtin_huge_valf();
+#pragma unroll 4
+    for (int32_t p = group; p < parts; p += kGroups) m = __builtin_fmaxf(m, a.few_ml[(p * all + row) * 2]);
+    float ref = m == -__builtin_huge_valf() ? 0.f : m, l = 0.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int32_t p = group; p < parts; p += kGroups) {
+      const f32x2 t = *(const f32x2 *)(a.few_ml + (p * all + row) * 2);
+      const float f = exp2_of(t[0] - ref);
+      v += *(const f32x4 *)(a.few_o + (p * all + row) * D + chunk * 4) * f;
+      l += t[1] * f;
+    }
+    vs[threadIdx.x] = v;
+    if (chunk == 0) {
+      ms[group] = m;
+      ls[group] = l;
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (uint32_t q = 1; q < kGroups; q++) m = __builtin_fmaxf(m, ms[q]);
+      ref = m == -__builtin_huge_valf() ? 0.f : m;
+      v = f32x4{0.f, 0.f, 0.f, 0.f};
+      l = 0.f;
+#pragma unroll
+      for (uint32_t q = 0; q < kGroups; q++) {
+        const float f = exp2_of(ms[q] - ref);
+        v += vs[q * kLanes + chunk] * f;
+        l += ls[q] * f;
+      }
+      const uint64_t to = (uint64_t)(sp.first + r / a.group) * a.heads + head * a.group + r % a.group;
+      store4(a.out + to * D + chunk * 4, T{}, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * (1.f / l));
+      if (a.lse && chunk == 0) a.lse[to] = lse_of(m, l);
+    }
+    __syncthreads();
   }
 }
 
@@ -527,9 +830,9 @@ __device__ __forceinline__ uint32_t tile_owner(const Sequences &b, uint32_t grou
 
 template <class T, int BITS, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages c, const Sequences b, const Attend a) {
-  typedef Rows<16, D> R;  // in LDS
+  typedef Rows<D> R;
+  typedef typename KeyType<T, BITS>::type K;
   constexpr int kTile = 64 * R::kBytes, kLoads = kTile / 4096, kRowsPer = 1024 / R::kBytes;
-  constexpr bool SCALED = BITS == 8, BARE = SCALED && T::kRange;
   constexpr int kRaw = D < 64 ? 1 : D / 64;  // 16 bytes of codes a thread
   extern __shared__ __align__(1024) uint8_t lds[];  // [2][keys, values]
   __shared__ float scales[2][128];
@@ -557,11 +860,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     const uint32_t w0 = wave * 32 < count ? wave * 32 : count - 1, w1 = wave * 32 + 31 < count ? wave * 32 + 31 : count - 1;
     const int32_t wfirst = sp.first + (int32_t)(((uint32_t)r0 + w0) / a.group) + sp.ahead, wlast = sp.first + (int32_t)(((uint32_t)r0 + w1) / a.group) + sp.ahead;
     Wave<T, BITS, D> w;
-    w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead);
+    w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
     int32_t page = -1;  // of key `lane` of the tile to be asked for next
     auto look = [&](int32_t t) { page = t < t1 ? page_at(c, table, t * 64 + (int32_t)lane, k.stop) : -1; };
     u32x4 raw_k[kRaw], raw_v[kRaw];
-    float raw_f[kRaw], scale = 0.f;
+    float scale = 0.f;
     auto request = [&](int32_t t, uint8_t *dst) {
       const void *none = &g_zero16;
       if constexpr (BITS == 16) {
@@ -583,11 +886,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
           const bool in = pg >= 0 && at16 < 64 * (D / 16);
           const uint64_t r = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 64) + row);
           raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0};
-          raw_f[i] = 0.f;
           if (in) {
             raw_k[i] = *(const u32x4 *)(c.k + r * D + (at16 % (D / 16)) * 16);
             raw_v[i] = *(const u32x4 *)(c.v + r * D + (at16 % (D / 16)) * 16);
-            if constexpr (!BARE) raw_f[i] = c.v_scales[r];
           }
         }
         scale = 0.f;
@@ -595,24 +896,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       }
     };
     // codes of 8 bits become 16-bit values on their way to LDS, once for all waves
-    auto spread = [&](uint8_t *dst, float *sc) {
+    auto spread = [&](uint32_t odd) {
+      uint8_t *dst = lds + odd * (2 * kTile);
       if constexpr (BITS == 8) {
 #pragma unroll
         for (int i = 0; i < kRaw; i++) {
           const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
           if (at16 >= 64 * (D / 16)) break;
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; e++) f[e] = raw_f[i];
 #pragma unroll
           for (int e = 0; e < 2; e++) {
             const u32x2 kc = {raw_k[i][2 * e], raw_k[i][2 * e + 1]}, vc = {raw_v[i][2 * e], raw_v[i][2 * e + 1]};
-            *(u32x4 *)(dst + row * R::kBytes + (((chunk + e) ^ R::key_swap(row)) * 16)) = widen8(T{}, kc);
-            *(u32x4 *)(dst + kTile + row * R::kBytes + (((chunk + e) ^ R::value_swap(row)) * 16)) =
-                BARE ? widen8(T{}, vc) : widen8_by(T{}, vc, f);
+            *(u32x4 *)(dst + row * R::kBytes + (((chunk + e) ^ R::key_swap(row)) * 16)) = widen8(K{}, kc);
+            *(u32x4 *)(dst + kTile + row * R::kBytes + (((chunk + e) ^ R::value_swap(row)) * 16)) = widen8(T{}, vc);
           }
         }
-        if (wave < 2) sc[wave * 64 + lane] = wave ? scale : scale * a.c;
+        if (wave < 2) scales[odd][wave * 64 + lane] = wave ? scale : scale * a.c;
       }
     };
     look(t0);
@@ -621,7 +919,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       request(t0, lds);
       look(t0 + 1);
       if constexpr (BITS == 8) {
-        spread(lds, scales[0]);
+        spread(0);
         next = __ballot(page >= 0);
         if (t0 + 1 < t1) {
           request(t0 + 1, nullptr);
@@ -644,7 +942,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       } else {
         __syncthreads();
         if (t + 1 < t1) {
-          spread(other, scales[odd ^ 1]);
+          spread(odd ^ 1);
           after = __ballot(page >= 0);
           if (t + 2 < t1) {
             request(t + 2, nullptr);
@@ -654,9 +952,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       }
       if (t * 64 <= wlast && wfirst - (t * 64 + 63) < a.window) {  // some row of this wave sees some key
         const bool whole = there == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window;
-        const uint32_t lo = (uint32_t)there, hi = (uint32_t)(there >> 32);
-        add_keys<T, BITS, 16, D, 2, SCALED, BARE>(w, p, p + kTile, scales[odd], scales[odd] + 64, t * 64,
-                                                  [=](int n) { return n ? hi : lo; }, whole, a.c, a.window);
+        add_keys<T, BITS, D>(w, p, p + kTile, scales[odd], scales[odd] + 64, t * 64, there, whole, a.window);
       }
       there = next;
       if constexpr (BITS == 8) next = after;
@@ -692,80 +988,50 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
   }
 }
 
-// A row's parts added up, D / 4 lanes to a row: the rows of few (sequence, key head,
-// row), then those of tiles (token, head), where either was split.
+// The parts of a row of tiles (token, head) added up, D / 4 lanes to a row.
 template <class T, int D>
-__global__ __launch_bounds__(256) void attend_join(const Pages c, const Sequences b, const Attend a) {
+__global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences b, const Attend a) {
   constexpr uint32_t kLanes = D / 4;
-  const uint64_t few = a.few_splits > 1 ? (uint64_t)b.count * c.heads * a.cap : 0;
-  const uint64_t tiled = a.tile_splits > 1 ? (uint64_t)b.tokens * a.heads : 0;
   const uint32_t chunk = threadIdx.x % kLanes;
   // a wave's rows go together: the search below is the whole wave's
-  const uint64_t all = (few + tiled) * kLanes;
+  const uint64_t rows_all = (uint64_t)b.tokens * a.heads, all = rows_all * kLanes;
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i - (threadIdx.x & 63) < all; i += (uint64_t)gridDim.x * 256) {
     const bool in = i < all;
-    uint64_t row = (in ? i : all - 1) / kLanes;
-    const float *o, *ml;
-    uint64_t to, stride;
+    const uint64_t row = (in ? i : all - 1) / kLanes;
+    const int32_t t = (int32_t)(row / a.heads);
+    const int32_t t0 = __builtin_amdgcn_readfirstlane(t);
+    const uint32_t up_to = starts_up_to(b.starts, b.count + 1, t0);  // 0: before the first
+    uint32_t owner = up_to ? up_to - 1 : 0;
+    Span sp = {0, 0, 0, 0};
+    if (owner < b.count) {
+      sp = span_of(b, owner);
+      // a wave holds at most 8 rows: walk on to this one's sequence
+      while (t >= sp.last && owner + 1 < b.count) sp = span_of(b, ++owner);
+    }
+    const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     int32_t parts = 0;
-    const uint64_t base = (i - (threadIdx.x & 63)) / kLanes, top = base + 64 / kLanes - 1;  // the wave's first and last row
-    uint32_t owner = b.count;
-    if (top >= few) {
-      // rows of a wave may lie in several sequences: each looks for its own in turn
-#pragma unroll 1
-      for (uint32_t r = 0; r < 64 / kLanes; r++) {
-        const uint64_t rr = base + r;
-        if (rr < few || rr >= few + tiled) continue;
-        const uint32_t s = sequence_of(b, (int32_t)((rr - few) / a.heads));
-        if (row == rr) owner = s;
-      }
+    if (in && t >= sp.first && t < sp.last && rows > a.cap) {
+      const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~127u;
+      const uint32_t count = rows - r0 < 128 ? rows - r0 : 128;
+      parts = cuts_of(c, b, sp.first + (int32_t)(r0 / a.group) + sp.ahead, sp.first + (int32_t)((r0 + count - 1) / a.group) + sp.ahead,
+                      sp.length, a.window, kTileShift, a.tile_splits, kTileLeast).count;
     }
-    if (row < few) {
-      const uint32_t r = (uint32_t)(row % a.cap), head = (uint32_t)(row / a.cap % c.heads), s = (uint32_t)(row / a.cap / c.heads);
-      const Span sp = span_of(b, s);
-      const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
-      o = a.few_o;
-      ml = a.few_ml;
-      stride = few;
-      to = (uint64_t)(sp.first + r / a.group) * a.heads + head * a.group + r % a.group;
-      if (r < rows && (a.alone || rows <= a.cap)) {
-        const uint32_t count = rows < a.cap ? rows : a.cap;
-        parts = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window, kFewShift,
-                        a.few_splits, kFewLeast).count;
-      }
-    } else {
-      row -= few;
-      o = a.tile_o;
-      ml = a.tile_ml;
-      stride = tiled;
-      to = row;
-      const int32_t t = (int32_t)(row / a.heads);
-      if (owner < b.count) {
-        const Span sp = span_of(b, owner);
-        const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
-        if (t >= sp.first && t < sp.last && rows > a.cap) {
-          const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~127u;
-          const uint32_t count = rows - r0 < 128 ? rows - r0 : 128;
-          parts = cuts_of(c, b, sp.first + (int32_t)(r0 / a.group) + sp.ahead, sp.first + (int32_t)((r0 + count - 1) / a.group) + sp.ahead,
-                          sp.length, a.window, kTileShift, a.tile_splits, kTileLeast).count;
-        }
-      }
-    }
-    if (!in || parts <= 1) continue;
+    if (parts <= 1) continue;
     float m = -__builtin_huge_valf();
-    for (int32_t p = 0; p < parts; p++) m = __builtin_fmaxf(m, ml[(p * stride + row) * 2]);
+#pragma unroll 4
+    for (int32_t p = 0; p < parts; p++) m = __builtin_fmaxf(m, a.tile_ml[(p * rows_all + row) * 2]);
     const float ref = m == -__builtin_huge_valf() ? 0.f : m;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
 #pragma unroll 4
     for (int32_t p = 0; p < parts; p++) {
-      const f32x2 t = *(const f32x2 *)(ml + (p * stride + row) * 2);
-      const float f = exp2_of(t[0] - ref);
-      v += *(const f32x4 *)(o + (p * stride + row) * D + chunk * 4) * f;
-      l += t[1] * f;
+      const f32x2 ml = *(const f32x2 *)(a.tile_ml + (p * rows_all + row) * 2);
+      const float f = exp2_of(ml[0] - ref);
+      v += *(const f32x4 *)(a.tile_o + (p * rows_all + row) * D + chunk * 4) * f;
+      l += ml[1] * f;
     }
-    store4(a.out + to * D + chunk * 4, T{}, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * (1.f / l));
-    if (a.lse && chunk == 0) a.lse[to] = lse_of(m, l);
+    store4(a.out + row * D + chunk * 4, T{}, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * (1.f / l));
+    if (a.lse && chunk == 0) a.lse[row] = lse_of(m, l);
   }
 }
 
@@ -786,9 +1052,10 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
   a.group = heads / cache->kv_heads;
   a.window = window <= 0 || window > INT32_MAX ? INT32_MAX : (int32_t)window;
   const uint64_t hint = batch->max_new && batch->max_new < tokens ? batch->max_new : tokens;
-  p.tile = hint * a.group > 32;
+  // heads of 256: two blocks of 16 rows do not fit a wave's registers
+  const uint64_t rows = dim == 256 ? 16 : 32, fit = rows / a.group;
+  p.tile = hint * a.group > rows;
   a.alone = !p.tile;
-  const uint64_t fit = 32 / a.group;
   a.cap = (uint32_t)((hint < fit ? hint : fit) * a.group);
   a.few_splits = a.tile_splits = 1;
   // the most keys that a sequence's rows may see
@@ -837,20 +1104,32 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
 constexpr uint32_t kDeclared = 4096;  // LDS that the kernels declare beside what a launch gives, at most
 uint32_t grid_of(uint64_t units) { return (uint32_t)(units < (1u << 20) ? units : 1u << 20); }
 
+template <class T, int BITS, int D, int NQ>
+hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {
+  constexpr int W = BITS == 16 && D == 256 ? 2 : 4;
+  constexpr uint32_t lds = W * 4 * 32 * FewRows<BITS, D>::kBytes;
+  static_assert(lds >= W * 16 * NQ * D * 4, "the waves' sums lie in the tiles' place");
+  const hipError_t e = allow_lds((const void *)attend_few<T, BITS, D, NQ, W>, lds, kDeclared);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.few_splits)), dim3(64 * W), lds, s, c,
+                     b, p.a);
+  const hipError_t st = hipGetLastError();
+  if (st != hipSuccess || p.a.few_splits == 1) return st;
+  hipLaunchKernelGGL((join_few<T, D>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.cap)), dim3(256), 0, s, c, b, p.a);
+  return hipGetLastError();
+}
 template <class T, int BITS, int D>
 hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {
   // attend_few goes always: it clears the rows of no sequence
-  constexpr int W = BITS == 16 && D == 256 ? 2 : 4;
-  constexpr uint32_t few = W * 4 * 32 * Rows<BITS, D>::kBytes;
-  static_assert(few >= W * 32 * D * 4, "the waves' sums lie in the tiles' place");
-  const hipError_t e = allow_lds((const void *)attend_few<T, BITS, D, W>, few, kDeclared);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attend_few<T, BITS, D, W>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.few_splits)), dim3(64 * W), few, s, c,
-                     b, p.a);
-  const hipError_t launched = hipGetLastError();
-  if (launched != hipSuccess) return launched;
+  hipError_t few;
+  if constexpr (D == 256) {
+    few = few_rows<T, BITS, D, 1>(p, c, b, s);
+  } else {
+    few = p.a.cap <= 16 ? few_rows<T, BITS, D, 1>(p, c, b, s) : few_rows<T, BITS, D, 2>(p, c, b, s);
+  }
+  if (few != hipSuccess) return few;
   if (p.tile) {
-    constexpr uint32_t lds = 4 * 64 * Rows<16, D>::kBytes;
+    constexpr uint32_t lds = 4 * 64 * Rows<D>::kBytes;
     const hipError_t st0 = allow_lds((const void *)attend_tile<T, BITS, D>, lds, kDeclared);
     if (st0 != hipSuccess) return st0;
     hipLaunchKernelGGL((attend_tile<T, BITS, D>), dim3(grid_of((uint64_t)p.a.tiles * c.heads * p.a.tile_splits)), dim3(256), lds, s, c,
@@ -858,10 +1137,9 @@ hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t
     const hipError_t st = hipGetLastError();
     if (st != hipSuccess) return st;
   }
-  const uint64_t rows = (p.a.few_splits > 1 ? (uint64_t)b.count * c.heads * p.a.cap : 0) +
-                        (p.a.tile_splits > 1 ? (uint64_t)b.tokens * p.a.heads : 0);
-  if (rows) {
-    hipLaunchKernelGGL((attend_join<T, D>), dim3(grid_of((rows * (D / 4) + 255) / 256)), dim3(256), 0, s, c, b, p.a);
+  if (p.a.tile_splits > 1) {
+    hipLaunchKernelGGL((join_tiles<T, D>), dim3(grid_of(((uint64_t)b.tokens * p.a.heads * (D / 4) + 255) / 256)), dim3(256), 0, s, c, b,
+                       p.a);
     return hipGetLastError();
   }
   return hipSuccess;

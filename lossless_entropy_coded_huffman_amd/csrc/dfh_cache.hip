@@ -47,6 +47,7 @@ __global__ __launch_bounds__(256) void move(const Pages c, const Sequences b, co
   const uint64_t groups = (all + PER - 1) / PER, per = (groups + waves - 1) / waves;
   const uint64_t g0 = wave * per, g1 = g0 + per < groups ? g0 + per : groups;
   if (g0 >= g1) return;
+  const int32_t first = b.count ? b.starts[0] : 0;
   uint32_t s = sequence_of(b, (int32_t)(g0 * PER / c.heads));
   Span p = {0, 0, 0, 0};
   if (s < b.count) p = span_of(b, s);
@@ -64,6 +65,7 @@ __global__ __launch_bounds__(256) void move(const Pages c, const Sequences b, co
     uint32_t mine = s;
     Span q = p;
     if (there && t >= p.last) {
+      if (mine == b.count && t0 < first) mine = 0;  // a group that begins before the first sequence
       // starts are in order: walk on (a group holds at most 16 tokens)
       while (mine < b.count) {
         q = span_of(b, mine);

@@ -4,9 +4,9 @@ Tolerances.  e = 2^-24; u is half a step of the call's 16-bit type.  A score is 
 float32 sum of D products, off by at most (D + 4) e scale sum |q k| with its scales; an
 exponential by that, by the rounding of its argument (2 e |z - max|) and by 4 e of
 its own, and every further tile or part multiplies by factors that are off by a few e:
-with n keys (n + 8) e covers these and the sums.  Together r[j], relative.  Weights are rounded to
-the type (u, and half of float16's smallest subnormal), 8-bit values in float16 too, and
-the output.  So with w the exact weights
+with n keys (n + 8) e covers these and the sums.  Together r[j], relative.  Weights (times the
+values' scales, with 8 bits) are rounded to the type (u, and half of float16's smallest
+subnormal), and so is the output.  So with w the exact weights
     |out - ref| <= sum w |v| (r + u) + |ref| sum w r + u |ref| + subnormals,
 where the magnitudes come from the float64 computation; half as much again covers
 products of these terms.  The pool is full of NaN but for the live positions of the
@@ -104,8 +104,7 @@ def check(torch, got, lse, q, kvs, new, lengths, scale, window, bits, rows=None)
             r = (k.shape[2] + 4) * E * a + (2 * (m - z).masked_fill(~seen, 0.0) + length + 12) * E
             spread = (w * r).sum(1, keepdim=True)
             small = tiny / total * (seen.double() @ vv.abs()) if dt == torch.float16 else 0.0
-            more = u * (w @ vv.abs()) + tiny if bits == 8 and dt == torch.float16 else 0.0
-            bound = 1.5 * ((w * (r + u)) @ vv.abs() + ref.abs() * spread + u * ref.abs() + small + more) + tiny
+            bound = 1.5 * ((w * (r + u)) @ vv.abs() + ref.abs() * spread + u * ref.abs() + small) + tiny
             err = (got[ts, h] - ref).abs()
             assert bool((err <= bound).all()), "head %d: %g of the bound" % (h, float((err / bound).max()))
             full = (m + total.log())[:, 0]
@@ -172,6 +171,52 @@ def test_scores_of_any_size(torch, scale, size, bits):
         q = (torch.randn(sum(new), 6, 64, generator=torch.Generator().manual_seed(1)) * size).to(dt).cuda()
         got, lse = dfh.cached_attention(q, cache, b, scale=scale, return_lse=True)
         check(torch, got, lse, q, kvs, new, lengths, scale, None, bits)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new,lengths", [([1, 2], [300, 77]), ([90, 60], [300, 60])])
+def test_scales_that_differ_widely(torch, new, lengths, dtype):
+    # 8 bits: tokens' scales from the smallest to the largest that the type has values for,
+    # growing, falling and mixed along the sequence
+    dt = types(torch)[dtype]
+    lo, hi = (-14, 15) if dtype == "fp16" else (-60, 60)
+    for order in ("up", "down", "mixed"):
+        b, tables, pages = batch_of(torch, new, lengths, 16)
+        cache = spoiled(torch, dfh.KVCache(pages, 1, 64, page_size=16, dtype=dt, bits=8))
+        kvs = filled(torch, cache, tables, lengths)
+        for i, (table, n) in enumerate(zip(tables, lengths)):
+            e = torch.linspace(lo, hi, n).round()
+            e = e.flip(0) if order == "down" else e[torch.randperm(n, generator=torch.Generator().manual_seed(i))] if order == "mixed" else e
+            f = (2.0 ** e.double()) / 127
+            p = torch.tensor([table[j // 16] for j in range(n)], device="cuda")
+            r = torch.arange(n, device="cuda") % 16
+            cache.v_scales[p, 0, r] = f.float().cuda()
+            kvs[i][1] = cache.v[p, 0, r].double()[:, None] * f.float().double().cuda()[:, None, None]
+        q = torch.randn(sum(new), 3, 64, generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+        got, lse = dfh.cached_attention(q, cache, b, return_lse=True)
+        check(torch, got, lse, q, kvs, new, lengths, 0.125, None, 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [[3], [100]])
+def test_queries_of_any_size(torch, new, dtype):
+    # 8 bits: rows of q from the type's smallest to its largest, and elements of one row far apart
+    dt, length = types(torch)[dtype], 200
+    b, tables, pages = batch_of(torch, new, [length], 16)
+    cache = spoiled(torch, dfh.KVCache(pages, 1, 128, page_size=16, dtype=dt, bits=8))
+    kvs = filled(torch, cache, tables, [length])
+    n = new[0]
+    g = torch.Generator().manual_seed(2)
+    for size in ((-24.0, -10.0, 0.0, 10.0) if dtype == "fp16" else (-130.0, -60.0, 0.0, 60.0, 110.0)):
+        q = torch.randn(n, 2, 128, generator=g).double() * 2.0 ** size
+        q = q.clamp(-torch.finfo(dt).max, torch.finfo(dt).max).to(dt).cuda()
+        # scores of ordinary size, as far as the scale's type reaches
+        scale = min(max(2.0 ** -size / 12, 2.0 ** -120), 2.0 ** 120)
+        got, lse = dfh.cached_attention(q, cache, b, scale=scale, return_lse=True)
+        check(torch, got, lse, q, kvs, new, [length], scale, None, 8)
+    q = (torch.randn(n, 2, 128, generator=g) * 2.0 ** torch.randint(-12, 1, (n, 2, 128), generator=g)).to(dt).cuda()
+    got, lse = dfh.cached_attention(q, cache, b, return_lse=True)
+    check(torch, got, lse, q, kvs, new, [length], 128 ** -0.5, None, 8)
 
 
 @pytest.mark.parametrize("bits", [16, 8])

@@ -159,6 +159,22 @@ def test_tokens_that_are_not_there(torch, bits):
         assert torch.equal(rv.cpu()[~gone], v[~gone])
 
 
+@pytest.mark.parametrize("begin", [1, 3, 70])
+def test_rows_before_the_first_sequence(torch, begin):
+    # the first tokens share a wave with rows of no sequence
+    page, kv, dim, new, lengths = 16, 1, 32, [2, 0, 9], [2, 5, 30]
+    b, tables, pages = batch_of(torch, new, lengths, page)
+    b = dfh.CacheBatch(b.tables, b.lengths, b.starts + begin)
+    cache = filled(torch, dfh.KVCache(pages, kv, dim, page_size=page), 7)
+    n = begin + sum(new) + 2
+    k = torch.randn(n, kv, dim, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    dfh.cache_write(k.cuda(), -k.cuda(), cache, b)
+    where = [None] * begin + places(tables, new, lengths, page) + [None] * 2
+    check_written(torch, cache, k, -k, where, 7)
+    back = dfh.cache_read(cache, b, n)[0].cpu()
+    assert torch.equal(back[begin: -2], k[begin: -2]) and not back[:begin].any() and not back[-2:].any()
+
+
 def test_no_sequences_and_no_tokens(torch):
     cache = filled(torch, dfh.KVCache(2, 1, 32, page_size=16), 1)
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
