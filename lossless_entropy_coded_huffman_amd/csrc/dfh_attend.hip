@@ -25,6 +25,8 @@
 // step, 2^-9 or 2^-12 of it) beside the output's.  Sums are FP32.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "dfh.h"
 #include "dfh_gemm.h"
 #include "dfh_pages.h"
@@ -223,23 +225,21 @@ __device__ __forceinline__ float value_lift(float largest, float so_far) {
 __device__ __forceinline__ bool sees(int32_t gap, int32_t window) { return (uint32_t)gap < (uint32_t)window; }
 
 // 64 keys at position `base` in LDS, 16 bits a value.  BITS 8: codes, with ks scales of the keys
-// times c, vs of the values; there: bit j: key j exists; whole: every query sees all.
-template <class T, int BITS, int D>
+// times c, vs of the values; there: bit j: key j exists.  Not MASKED: every query sees all.
+template <class T, int BITS, int D, bool MASKED>
 __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
-                                         const float *vs, int32_t base, uint64_t there, bool whole, int32_t window) {
+                                         const float *vs, int32_t base, uint64_t there, int32_t window) {
   typedef Rows<D> R;
   typedef typename KeyType<T, BITS>::type K;
   const uint32_t lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
   // scores
   f32x16 s[2];
+  s[0] = s[1] = f32x16{};
 #pragma unroll
-  for (int n = 0; n < 2; n++) {
-    s[n] = f32x16{};
-    const uint8_t *p = lk + (n * 32 + row) * R::kBytes;
-    const uint32_t f = R::key_swap(row);
+  for (int st = 0; st < D / 16; st++)
 #pragma unroll
-    for (int st = 0; st < D / 16; st++) s[n] = mfma32(K{}, *(const u32x4 *)(p + (((st * 2 + h) ^ f) * 16)), w.q[st], s[n]);
-  }
+    for (int n = 0; n < 2; n++)
+      s[n] = mfma32(K{}, *(const u32x4 *)(lk + (n * 32 + row) * R::kBytes + (((st * 2 + h) ^ R::key_swap(row)) * 16)), w.q[st], s[n]);
   if constexpr (BITS == 8) {
 #pragma unroll
     for (int n = 0; n < 2; n++)
@@ -252,7 +252,7 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
   }
   const int32_t gap = w.pos - base - 4 * (int32_t)h;  // to the key of register 0 of block 0
   const uint64_t mine = there >> (4 * h);
-  if (!whole) {
+  if constexpr (MASKED) {
 #pragma unroll
     for (int n = 0; n < 2; n++) {
       const uint32_t t = (uint32_t)(mine >> (32 * n));
@@ -272,7 +272,7 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
   if constexpr (BITS == 8) {
 #pragma unroll
     for (int i = 0; i < 8; i++) vf[i] = *(const f32x4 *)(vs + 8 * i + 4 * h);
-    if (!whole) {
+    if constexpr (MASKED) {
       // a scale that is no number belongs to the queries that see its key alone
 #pragma unroll
       for (int i = 0; i < 8; i++)
@@ -333,7 +333,7 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     // is no number: a tile in which some query does not see every key is looked
     // through, and where there is one, those are left out of the products and
     // come after, key by key.  The other queries' sums keep their bits.
-    if (!whole) {
+    if constexpr (MASKED) {
       uint32_t most = 0;
 #pragma unroll
       for (int st = 0; st < 4; st++)
@@ -452,10 +452,10 @@ struct FewRows {
 };
 
 // 32 keys at position `base` in LDS.  BITS 8: ks scales of the keys times c, vs of the
-// values; there: bit j: key j exists; whole: every query sees all.
-template <class T, int BITS, int D, int NQ>
+// values; there: bit j: key j exists.  Not MASKED: every query sees all.
+template <class T, int BITS, int D, int NQ, bool MASKED>
 __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
-                                        const float *vs, int32_t base, uint32_t there, bool whole, int32_t window) {
+                                        const float *vs, int32_t base, uint32_t there, int32_t window) {
   typedef FewRows<BITS, D> R;
   const uint32_t lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   f32x4 s[NQ][2];
@@ -508,7 +508,7 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
       z[r] = s[n][r / 4][r % 4];
       if constexpr (BITS == 8) z[r] *= kf[r / 4][r % 4];
     }
-    if (!whole) {
+    if constexpr (MASKED) {
 #pragma unroll
       for (int r = 0; r < 8; r++)
         if (!(sees(gap - few_key(r), window) && (mine >> few_key(r) & 1))) z[r] = -__builtin_huge_valf();
@@ -522,7 +522,7 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
       // a scale that is no number belongs to the queries that see its key alone
 #pragma unroll
       for (int r = 0; r < 8; r++)
-        f[r] = whole || (sees(gap - few_key(r), window) && (mine >> few_key(r) & 1)) ? vf[r / 4][r % 4] : 0.f;
+        f[r] = !MASKED || (sees(gap - few_key(r), window) && (mine >> few_key(r) & 1)) ? vf[r / 4][r % 4] : 0.f;
     }
     if constexpr (lifts(T::kRange, BITS)) {
       float largest = 0.f;
@@ -570,7 +570,7 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
     }
   };
   if constexpr (BITS == 16) {
-    if (!whole) {  // as in add_keys
+    if constexpr (MASKED) {  // as in add_keys
       uint32_t most = 0;
 #pragma unroll
       for (int d = 0; d < D / 16; d++) most = most_bits(value(d), most);
@@ -697,7 +697,11 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
         }
         const bool whole = there == 0xFFFFFFFFu && t * 32 + 31 <= first + sp.ahead && last + sp.ahead - t * 32 < a.window;
         const uint8_t *p = buf + odd * (2 * kTile);
-        add_few<T, BITS, D, NQ>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, whole, a.window);
+        if (whole) {
+          add_few<T, BITS, D, NQ, false>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, a.window);
+        } else {
+          add_few<T, BITS, D, NQ, true>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, a.window);
+        }
         there = next;
         wait_reads();  // the buffer is asked for again
       }
@@ -865,18 +869,30 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     auto look = [&](int32_t t) { page = t < t1 ? page_at(c, table, t * 64 + (int32_t)lane, k.stop) : -1; };
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float scale = 0.f;
-    auto request = [&](int32_t t, uint8_t *dst) {
-      const void *none = &g_zero16;
+    auto request = [&](int32_t t, uint8_t *dst, uint64_t all) {  // all: the keys that exist
       if constexpr (BITS == 16) {
+        // (rows of a load lie in one page; the exchange is the same in all of a wave's loads)
+        const uint32_t in_load = lane / R::kChunks, mine = wave * kRowsPer + in_load, chunk = lane % R::kChunks;
+        const uint32_t off_k = in_load * R::kBytes + (chunk ^ R::key_swap(mine)) * 16, off_v = in_load * R::kBytes + (chunk ^ R::value_swap(mine)) * 16;
+        static_assert(4 * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
+        if (all == ~0ull) {
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) {
-          const uint32_t r = (i * 4 + wave) * kRowsPer, row = r + lane / R::kChunks;
-          const int32_t pg = __builtin_amdgcn_readlane(page, r);
-          const bool in = pg >= 0 && t * 64 + (int32_t)row < k.stop;
-          const uint64_t at = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 64) + row) * R::kBytes;
-          to_lds(in ? c.k + at + (((lane % R::kChunks) ^ R::key_swap(row)) * 16) : none, dst + (i * 4 + wave) * 1024);
-          to_lds(in ? c.v + at + (((lane % R::kChunks) ^ R::value_swap(row)) * 16) : none,
-                 dst + kTile + (i * 4 + wave) * 1024);
+          for (int i = 0; i < kLoads; i++) {
+            const uint32_t r = (i * 4 + wave) * kRowsPer;
+            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
+            to_lds(c.k + at + off_k, dst + (i * 4 + wave) * 1024);
+            to_lds(c.v + at + off_v, dst + kTile + (i * 4 + wave) * 1024);
+          }
+        } else {
+          const void *none = &g_zero16;
+#pragma unroll
+          for (int i = 0; i < kLoads; i++) {
+            const uint32_t r = (i * 4 + wave) * kRowsPer;
+            const bool in = all >> (r + in_load) & 1;
+            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
+            to_lds(in ? c.k + at + off_k : none, dst + (i * 4 + wave) * 1024);
+            to_lds(in ? c.v + at + off_v : none, dst + kTile + (i * 4 + wave) * 1024);
+          }
         }
       } else {
 #pragma unroll
@@ -916,27 +932,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     look(t0);
     uint64_t there = __ballot(page >= 0), next = 0;
     if (t0 < t1) {
-      request(t0, lds);
+      request(t0, lds, there);
       look(t0 + 1);
       if constexpr (BITS == 8) {
         spread(0);
         next = __ballot(page >= 0);
         if (t0 + 1 < t1) {
-          request(t0 + 1, nullptr);
+          request(t0 + 1, nullptr, next);
           look(t0 + 2);
         }
       }
     }
-    for (int32_t t = t0; t < t1; t++) {
+    auto step = [&](int32_t t, auto masked) {
       const uint32_t odd = (t - t0) & 1;
-      uint8_t *p = lds + odd * (2 * kTile), *other = lds + (odd ^ 1) * (2 * kTile);
+      const uint8_t *p = lds + odd * (2 * kTile);
       uint64_t after = 0;
       if constexpr (BITS == 16) {
         wait_but<0>();
         meet();  // tile t is whole, and tile t - 1 read by all
         next = __ballot(page >= 0);
         if (t + 1 < t1) {
-          request(t + 1, other);
+          request(t + 1, lds + (odd ^ 1) * (2 * kTile), next);
           look(t + 2);
         }
       } else {
@@ -945,17 +961,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
           spread(odd ^ 1);
           after = __ballot(page >= 0);
           if (t + 2 < t1) {
-            request(t + 2, nullptr);
+            request(t + 2, nullptr, after);
             look(t + 3);
           }
         }
       }
-      if (t * 64 <= wlast && wfirst - (t * 64 + 63) < a.window) {  // some row of this wave sees some key
-        const bool whole = there == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window;
-        add_keys<T, BITS, D>(w, p, p + kTile, scales[odd], scales[odd] + 64, t * 64, there, whole, a.window);
-      }
+      // (a masked tile may have nothing for this wave's rows)
+      if (!masked.value || (t * 64 <= wlast && wfirst - (t * 64 + 63) < a.window))
+        add_keys<T, BITS, D, masked.value>(w, p, p + kTile, scales[odd], scales[odd] + 64, t * 64, there, a.window);
       there = next;
       if constexpr (BITS == 8) next = after;
+    };
+    // tiles of which every row of this wave sees every key have a loop of their own
+    for (int32_t t = t0; t < t1; t++) {
+      for (; t < t1 && there == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window; t++) step(t, std::false_type{});
+      if (t < t1) step(t, std::true_type{});
     }
     __syncthreads();  // the buffers are read
     const f32x2 sums = both_halves(w.l);
