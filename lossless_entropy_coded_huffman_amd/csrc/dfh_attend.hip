@@ -369,18 +369,31 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, value(st, d), p[st], w.o[d]);
 }
 
+// 16 bytes a lane from base + off (of each lane) to LDS address at + 16 lane.  The
+// compiler is not told of these loads: before a transposing read it would wait for all that it
+// knows of, the next tile's among them (4096 x 16384 x 32 heads: MEASURED).  A load
+// of this kind writes no register; what it writes in LDS is waited for by wait_but.
+__device__ __forceinline__ void ask(const void *base, uint32_t off, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void ask(const void *src, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
 // The address of a head's row in the pool.
 __device__ __forceinline__ uint64_t pool_row(const Pages &c, uint32_t page, uint32_t head, uint32_t at) {
   return (((uint64_t)page * c.heads + head) << c.shift) + (at & ((1u << c.shift) - 1));
 }
-// Page of a position below stop, -1 where there is none.
+// What a table says of a position (of the last one, from stop on), unchecked: it is looked at
+// a tile later, when it is there.
 __device__ __forceinline__ int32_t page_at(const Pages &c, const int32_t *table, int32_t pos, int32_t stop) {
-  if (pos >= stop) return -1;
-  const int32_t page = table[(uint32_t)pos >> c.shift];
-  return (uint32_t)page < c.pages ? page : -1;
+  return table[(uint32_t)(pos < stop ? pos : stop - 1) >> c.shift];
 }
 
-// Four outputs of a row, as they are or for attend_join.
+// Four outputs of a row, as they are or for the join.
 template <class T>
 __device__ __forceinline__ void store4(uint16_t *out, T, f32x4 v) {
   *(u32x2 *)out = u32x2{pair(T{}, v[0], v[1]), pair(T{}, v[2], v[3])};
@@ -642,42 +655,48 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
       if (z >= (uint32_t)k.count && z) break;
       const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
       // a tile's pages and scales come a tile ahead of its rows
-      int32_t page = -1;
+      int32_t page = 0;
       uint32_t there = 0, next = 0;
       float scale = 0.f;
-      auto look = [&](int32_t t) { page = t < t1 ? page_at(c, table, t * 32 + (int32_t)(lane & 31), k.stop) : -1; };
-      auto request = [&](int32_t t, uint8_t *dst, uint32_t in) {
+      auto look = [&](int32_t t) {
+        if (t < t1) page = page_at(c, table, t * 32 + (int32_t)(lane & 31), k.stop);
+      };
+      auto known = [&](int32_t t) { return (uint32_t)__ballot(t * 32 + (int32_t)(lane & 31) < k.stop && (uint32_t)page < c.pages); };
+      const uint32_t in_load = lane / R::kChunks, chunk = lane % R::kChunks;
+      auto request = [&](int32_t t, uint32_t dst, uint32_t in) {  // in: the keys that exist
         if (in == 0xFFFFFFFFu && kRowsPer <= 16) {
 #pragma unroll
           for (int i = 0; i < kLoads; i++) {
-            const uint32_t row = i * kRowsPer + lane / R::kChunks;
+            // (rows of a load lie in one page)
+            const uint32_t row = i * kRowsPer + in_load;
             const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, i * kRowsPer), head, (uint32_t)(t * 32 + i * kRowsPer)) *
                                 R::kBytes;
-            to_lds(c.k + at + (lane / R::kChunks * R::kBytes + ((lane % R::kChunks) ^ R::key_swap(row)) * 16), dst + i * 1024);
-            to_lds(c.v + at + (lane / R::kChunks * R::kBytes + ((lane % R::kChunks) ^ R::value_swap(row)) * 16), dst + kTile + i * 1024);
+            ask(c.k + at, in_load * R::kBytes + (chunk ^ R::key_swap(row)) * 16, dst + i * 1024);
+            ask(c.v + at, in_load * R::kBytes + (chunk ^ R::value_swap(row)) * 16, dst + kTile + i * 1024);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < kLoads; i++) {
-            const uint32_t row = i * kRowsPer + lane / R::kChunks;
-            const int32_t pg = __shfl(page, (int)row);
-            const uint64_t at = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 32) + row) * R::kBytes;
-            const void *none = &g_zero16;
-            to_lds(pg >= 0 ? c.k + at + (((lane % R::kChunks) ^ R::key_swap(row)) * 16) : none, dst + i * 1024);
-            to_lds(pg >= 0 ? c.v + at + (((lane % R::kChunks) ^ R::value_swap(row)) * 16) : none, dst + kTile + i * 1024);
+            const uint32_t row = i * kRowsPer + in_load;
+            const uint64_t at = pool_row(c, (uint32_t)__shfl(page, (int)row), head, (uint32_t)(t * 32) + row) * R::kBytes;
+            const uint8_t *none = (const uint8_t *)&g_zero16;
+            const bool is = in >> row & 1;
+            ask(is ? c.k + at + (chunk ^ R::key_swap(row)) * 16 : none, dst + i * 1024);
+            ask(is ? c.v + at + (chunk ^ R::value_swap(row)) * 16 : none, dst + kTile + i * 1024);
           }
         }
         if constexpr (BITS == 8) {
           scale = 0.f;
-          if (page >= 0) scale = (lane < 32 ? c.k_scales : c.v_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 32) + (lane & 31))];
+          if (in >> (lane & 31) & 1)
+            scale = (lane < 32 ? c.k_scales : c.v_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 32) + (lane & 31))];
         }
       };
       const int32_t mine0 = t0 + (int32_t)wave;
       look(mine0);
       Few<T, BITS, D, NQ> w;
-      there = (uint32_t)__ballot(page >= 0);
       if (mine0 < t1) {
-        request(mine0, buf, there);
+        there = known(mine0);
+        request(mine0, lds_address(buf), there);
         look(mine0 + W);
       }
 #pragma unroll
@@ -690,9 +709,9 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
         const uint32_t odd = ((t - mine0) / W) & 1;
         wait_but<0>();
         if constexpr (BITS == 8) scales[wave][lane] = lane < 32 ? scale * a.c : scale;
-        next = (uint32_t)__ballot(page >= 0);
         if (t + W < t1) {
-          request(t + W, buf + (odd ^ 1) * (2 * kTile), next);
+          next = known(t + W);
+          request(t + W, lds_address(buf) + (odd ^ 1) * (2 * kTile), next);
           look(t + 2 * W);
         }
         const bool whole = there == 0xFFFFFFFFu && t * 32 + 31 <= first + sp.ahead && last + sp.ahead - t * 32 < a.window;
@@ -865,11 +884,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     const int32_t wfirst = sp.first + (int32_t)(((uint32_t)r0 + w0) / a.group) + sp.ahead, wlast = sp.first + (int32_t)(((uint32_t)r0 + w1) / a.group) + sp.ahead;
     Wave<T, BITS, D> w;
     w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
-    int32_t page = -1;  // of key `lane` of the tile to be asked for next
-    auto look = [&](int32_t t) { page = t < t1 ? page_at(c, table, t * 64 + (int32_t)lane, k.stop) : -1; };
+    int32_t page = 0;  // of key `lane` of the tile to be asked for next
+    auto look = [&](int32_t t) {
+      if (t < t1) page = page_at(c, table, t * 64 + (int32_t)lane, k.stop);
+    };
+    auto known = [&](int32_t t) { return __ballot(t * 64 + (int32_t)lane < k.stop && (uint32_t)page < c.pages); };
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float scale = 0.f;
-    auto request = [&](int32_t t, uint8_t *dst, uint64_t all) {  // all: the keys that exist
+    auto request = [&](int32_t t, uint32_t dst, uint64_t all) {  // all: the keys that exist
       if constexpr (BITS == 16) {
         // (rows of a load lie in one page; the exchange is the same in all of a wave's loads)
         const uint32_t in_load = lane / R::kChunks, mine = wave * kRowsPer + in_load, chunk = lane % R::kChunks;
@@ -880,18 +902,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
           for (int i = 0; i < kLoads; i++) {
             const uint32_t r = (i * 4 + wave) * kRowsPer;
             const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
-            to_lds(c.k + at + off_k, dst + (i * 4 + wave) * 1024);
-            to_lds(c.v + at + off_v, dst + kTile + (i * 4 + wave) * 1024);
+            ask(c.k + at, off_k, dst + (i * 4 + wave) * 1024);
+            ask(c.v + at, off_v, dst + kTile + (i * 4 + wave) * 1024);
           }
         } else {
-          const void *none = &g_zero16;
+          const uint8_t *none = (const uint8_t *)&g_zero16;
 #pragma unroll
           for (int i = 0; i < kLoads; i++) {
             const uint32_t r = (i * 4 + wave) * kRowsPer;
             const bool in = all >> (r + in_load) & 1;
             const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
-            to_lds(in ? c.k + at + off_k : none, dst + (i * 4 + wave) * 1024);
-            to_lds(in ? c.v + at + off_v : none, dst + kTile + (i * 4 + wave) * 1024);
+            ask(in ? c.k + at + off_k : none, dst + (i * 4 + wave) * 1024);
+            ask(in ? c.v + at + off_v : none, dst + kTile + (i * 4 + wave) * 1024);
           }
         }
       } else {
@@ -899,7 +921,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
         for (int i = 0; i < kRaw; i++) {
           const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16) & 63;
           const int32_t pg = __shfl(page, (int)row);
-          const bool in = pg >= 0 && at16 < 64 * (D / 16);
+          const bool in = (all >> row & 1) && at16 < 64 * (D / 16);
           const uint64_t r = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 64) + row);
           raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0};
           if (in) {
@@ -908,7 +930,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
           }
         }
         scale = 0.f;
-        if (wave < 2 && page >= 0) scale = (wave ? c.v_scales : c.k_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 64) + lane)];
+        if (wave < 2 && (all >> lane & 1)) scale = (wave ? c.v_scales : c.k_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 64) + lane)];
       }
     };
     // codes of 8 bits become 16-bit values on their way to LDS, once for all waves
@@ -930,15 +952,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       }
     };
     look(t0);
-    uint64_t there = __ballot(page >= 0), next = 0;
+    uint64_t there = 0, next = 0;
     if (t0 < t1) {
-      request(t0, lds, there);
+      there = known(t0);
+      request(t0, lds_address(lds), there);
       look(t0 + 1);
       if constexpr (BITS == 8) {
         spread(0);
-        next = __ballot(page >= 0);
         if (t0 + 1 < t1) {
-          request(t0 + 1, nullptr, next);
+          next = known(t0 + 1);
+          request(t0 + 1, 0, next);
           look(t0 + 2);
         }
       }
@@ -950,18 +973,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       if constexpr (BITS == 16) {
         wait_but<0>();
         meet();  // tile t is whole, and tile t - 1 read by all
-        next = __ballot(page >= 0);
         if (t + 1 < t1) {
-          request(t + 1, lds + (odd ^ 1) * (2 * kTile), next);
+          next = known(t + 1);
+          request(t + 1, lds_address(lds) + (odd ^ 1) * (2 * kTile), next);
           look(t + 2);
         }
       } else {
         __syncthreads();
         if (t + 1 < t1) {
           spread(odd ^ 1);
-          after = __ballot(page >= 0);
           if (t + 2 < t1) {
-            request(t + 2, nullptr, after);
+            after = known(t + 2);
+            request(t + 2, 0, after);
             look(t + 3);
           }
         }
