@@ -231,15 +231,33 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
                                          const float *vs, int32_t base, uint64_t there, int32_t window) {
   typedef Rows<D> R;
   typedef typename KeyType<T, BITS>::type K;
+  constexpr float kSlack = lifts(T::kRange, BITS) ? 0.f : 8.f;
   const uint32_t lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
   // scores
   f32x16 s[2];
   s[0] = s[1] = f32x16{};
+  // reads run two steps ahead of the products
+  constexpr int kSteps = D / 16, kAhead = kSteps < 2 ? kSteps : 2;
+  u32x4 kf[kSteps][2];
+  auto read = [&](int st) {
 #pragma unroll
-  for (int st = 0; st < D / 16; st++)
+    for (int n = 0; n < 2; n++) kf[st][n] = *(const u32x4 *)(lk + (n * 32 + row) * R::kBytes + (((st * 2 + h) ^ R::key_swap(row)) * 16));
+  };
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < 2; n++)
-      s[n] = mfma32(K{}, *(const u32x4 *)(lk + (n * 32 + row) * R::kBytes + (((st * 2 + h) ^ R::key_swap(row)) * 16)), w.q[st], s[n]);
+  for (int st = 0; st < kAhead; st++) read(st);
+#pragma unroll
+  for (int st = 0; st < kSteps; st++) {
+    if (st + kAhead < kSteps) read(st + kAhead);
+#pragma unroll
+    for (int n = 0; n < 2; n++) s[n] = mfma32(K{}, kf[st][n], w.q[st], s[n]);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+#pragma unroll
+  for (int st = 0; st < kSteps; st++) {
+    if (st + kAhead < kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  }
   if constexpr (BITS == 8) {
 #pragma unroll
     for (int n = 0; n < 2; n++)
@@ -292,15 +310,17 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     w.z = __builtin_fmaxf(top, w.z);
     top = w.z - w.lift;
   }
-  top = __builtin_fmaxf(top, w.m);
-  const float ref = top == -__builtin_huge_valf() ? 0.f : top;
-  if (__ballot(top > w.m)) {
-    const float back = exp2_of(w.m - ref);
+  // A row's reference stays while no score is more than 2^8 above it (codes of FP16: none): p and
+  // its sums bear that, and most tiles take nothing off (32 rows with a maximum of their own
+  // would in every third of 256).
+  if (__ballot(top > w.m + kSlack)) {
+    const float up = top > w.m + kSlack ? top : w.m, back = exp2_of(w.m - (up == -__builtin_huge_valf() ? 0.f : up));
     w.l *= back;
 #pragma unroll
     for (int d = 0; d < D / 32; d++) w.o[d] *= back;
-    w.m = top;
+    w.m = up;
   }
+  const float ref = w.m == -__builtin_huge_valf() ? 0.f : w.m;
   float sum = 0.f;
 #pragma unroll
   for (int n = 0; n < 2; n++)
