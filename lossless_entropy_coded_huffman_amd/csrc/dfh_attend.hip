@@ -163,6 +163,25 @@ struct Rows {
 // Key of a lane's register r (of 16) in a block of 32, without the 4 * (lane / 32).
 __device__ __forceinline__ constexpr int key_of(int r) { return 8 * (r / 4) + r % 4; }
 
+// 16 bytes a lane from base + off (of each lane) to LDS address at + 16 lane.  The
+// compiler is not told of these loads: before a transposing read it would wait for all that it
+// knows of, the next tile's among them (4096 x 16384 x 32 heads: MEASURED).  A load
+// of this kind writes no register; what it writes in LDS is waited for by wait_but.
+__device__ __forceinline__ uint32_t same(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t same(uint64_t v) { return (uint64_t)same((uint32_t)(v >> 32)) << 32 | same((uint32_t)v); }
+__device__ __forceinline__ void ask(const uint8_t *base, uint32_t off, uint32_t at) {
+  base = (const uint8_t *)same((uint64_t)base);
+  at = same(at);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void ask(const uint8_t *src, uint32_t at) {
+  at = same(at);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
 // q's elements lifted into FP16 by a power of two that brings the row's largest (most) to
 // 2^14 .. 2^15, so that what is 2^-28 of that keeps all its bits; returns what takes it back.
 template <int N>
@@ -186,6 +205,7 @@ struct Wave {
   float z, lift;    // the largest score, where m lies below it
   float mul;        // what a score is multiplied by
   int32_t pos;
+  uint32_t key_at, value_at;  // this lane's part of a tile in LDS
 
   // row: this lane's query
   __device__ __forceinline__ void init(const uint16_t *row, int32_t position, float c) {
@@ -206,6 +226,12 @@ struct Wave {
     l = 0.f;
     lift = 64.f;
     pos = position;
+    // chunk h of row lane % 32 (step st: that ^ 2 st); of 4 rows by 16 values a group of 16 lanes, 8 bytes
+    // (of values 32 d on: that ^ 4 d chunks)
+    typedef Rows<D> R;
+    const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, r = 4 * h + l16 / 4;
+    key_at = (lane & 31) * R::kBytes + (h ^ R::key_swap(lane & 31)) * 16;
+    value_at = r * R::kBytes + ((((lane >> 4) & 1) * 2 + ((l16 >> 1) & 1)) ^ R::value_swap(r)) * 16 + (l16 & 1) * 8;
   }
 };
 
@@ -224,95 +250,99 @@ __device__ __forceinline__ float value_lift(float largest, float so_far) {
 // Whether a query at pos sees the key at pos - gap.
 __device__ __forceinline__ bool sees(int32_t gap, int32_t window) { return (uint32_t)gap < (uint32_t)window; }
 
-// 64 keys at position `base` in LDS, 16 bits a value.  BITS 8: codes, with ks scales of the keys
-// times c, vs of the values; there: bit j: key j exists.  Not MASKED: every query sees all.
-template <class T, int BITS, int D, bool MASKED>
-__device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
-                                         const float *vs, int32_t base, uint64_t there, int32_t window) {
-  typedef Rows<D> R;
+// LDS by address.
+template <class V>
+__device__ __forceinline__ V read_lds(uint32_t at) {
+  return *(const __attribute__((address_space(3))) V *)at;
+}
+__device__ __forceinline__ u32x2 turned_lds(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at));
+}
+// The same value, in a register that the compiler knows nothing of: what is made of it is
+// made again where it is used, not kept from one tile to the next in registers that the
+// sums need.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Blocks of 32 keys in LDS, 16 bits a value, go through four steps: scores (matrix), settle (scale,
+// mask, maximum), weigh (exponentials) and gather (matrix).  BITS 8: ks are scales of the
+// keys times c, vs of the values.  Not MASKED: every query sees every key.
+template <class T, int BITS, int D>
+__device__ __forceinline__ f32x16 scores(const Wave<T, BITS, D> &w, uint32_t lk) {
   typedef typename KeyType<T, BITS>::type K;
-  constexpr float kSlack = lifts(T::kRange, BITS) ? 0.f : 8.f;
-  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
-  // scores
-  f32x16 s[2];
-  s[0] = s[1] = f32x16{};
-  // reads run two steps ahead of the products
-  constexpr int kSteps = D / 16, kAhead = kSteps < 2 ? kSteps : 2;
-  u32x4 kf[kSteps][2];
-  auto read = [&](int st) {
+  const uint32_t at = lk + fresh(w.key_at);
+  f32x16 s = {};
 #pragma unroll
-    for (int n = 0; n < 2; n++) kf[st][n] = *(const u32x4 *)(lk + (n * 32 + row) * R::kBytes + (((st * 2 + h) ^ R::key_swap(row)) * 16));
-  };
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int st = 0; st < kAhead; st++) read(st);
-#pragma unroll
-  for (int st = 0; st < kSteps; st++) {
-    if (st + kAhead < kSteps) read(st + kAhead);
-#pragma unroll
-    for (int n = 0; n < 2; n++) s[n] = mfma32(K{}, kf[st][n], w.q[st], s[n]);
+  for (int st = 0; st < D / 16; st++) s = mfma32(K{}, read_lds<u32x4>(at ^ st * 32), w.q[st], s);
+  return s;
+}
+
+// Which of a lane's keys, by register, its query sees.  there: bit j: key j of the block exists.
+struct Seen {
+  int32_t gap, window;
+  uint32_t there;
+  template <class W>
+  __device__ __forceinline__ Seen(const W &w, int32_t base, uint32_t all, int32_t win) {
+    const uint32_t h = (threadIdx.x >> 5) & 1;
+    gap = w.pos - base - 4 * (int32_t)h;
+    there = all >> (4 * h);
+    window = win;
   }
-  __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+  __device__ __forceinline__ bool operator()(int r) const { return sees(gap - key_of(r), window) && (there >> key_of(r) & 1); }
+};
+
+// The reference that a row's largest score asks for, where that is lifted.
+template <class W, class S>
+__device__ __forceinline__ float lifted(W &w, float top, const float *vs, S seen) {
+  const uint32_t h = (threadIdx.x >> 5) & 1;
+  float largest = 0.f;
 #pragma unroll
-  for (int st = 0; st < kSteps; st++) {
-    if (st + kAhead < kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  for (int i = 0; i < 4; i++) {
+    const f32x4 v = *(const f32x4 *)(vs + 8 * i + 4 * h);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (seen(4 * i + e)) largest = __builtin_fmaxf(largest, __builtin_fabsf(v[e]));
   }
+  const f32x2 both = both_halves(largest);
+  w.lift = value_lift(__builtin_fmaxf(both[0], both[1]), w.lift);
+  w.z = __builtin_fmaxf(top, w.z);
+  return w.z - w.lift;
+}
+
+// Scores times the keys' scales, -inf where a key is not seen; returns the row's largest (times log2 e).
+template <class T, int BITS, int D, bool MASKED>
+__device__ __forceinline__ float settle(Wave<T, BITS, D> &w, f32x16 &s, const float *ks, const float *vs, const Seen &seen) {
+  const uint32_t h = (threadIdx.x >> 5) & 1;
   if constexpr (BITS == 8) {
 #pragma unroll
-    for (int n = 0; n < 2; n++)
+    for (int i = 0; i < 4; i++) {
+      const f32x4 k = *(const f32x4 *)(ks + 8 * i + 4 * h);
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const f32x4 k = *(const f32x4 *)(ks + n * 32 + 8 * i + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; e++) s[n][4 * i + e] *= k[e];
-      }
+      for (int e = 0; e < 4; e++) s[4 * i + e] *= k[e];
+    }
   }
-  const int32_t gap = w.pos - base - 4 * (int32_t)h;  // to the key of register 0 of block 0
-  const uint64_t mine = there >> (4 * h);
   if constexpr (MASKED) {
 #pragma unroll
-    for (int n = 0; n < 2; n++) {
-      const uint32_t t = (uint32_t)(mine >> (32 * n));
-#pragma unroll
-      for (int r = 0; r < 16; r++)
-        if (!(sees(gap - n * 32 - key_of(r), window) && (t >> key_of(r) & 1))) s[n][r] = -__builtin_huge_valf();
-    }
+    for (int r = 0; r < 16; r++)
+      if (!seen(r)) s[r] = -__builtin_huge_valf();
   }
-  float top = s[0][0];
+  float top = s[0];
 #pragma unroll
-  for (int n = 0; n < 2; n++)
-#pragma unroll
-    for (int r = 0; r < 16; r++) top = __builtin_fmaxf(top, s[n][r]);
+  for (int r = 1; r < 16; r++) top = __builtin_fmaxf(top, s[r]);
   const f32x2 tops = both_halves(top);
   top = __builtin_fmaxf(tops[0], tops[1]) * w.mul;
-  f32x4 vf[BITS == 8 ? 8 : 1];
-  if constexpr (BITS == 8) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) vf[i] = *(const f32x4 *)(vs + 8 * i + 4 * h);
-    if constexpr (MASKED) {
-      // a scale that is no number belongs to the queries that see its key alone
-#pragma unroll
-      for (int i = 0; i < 8; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (!(sees(gap - 8 * i - e, window) && (mine >> (8 * i + e) & 1))) vf[i][e] = 0.f;
-    }
-  }
-  if constexpr (lifts(T::kRange, BITS)) {
-    float largest = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) largest = __builtin_fmaxf(largest, __builtin_fabsf(vf[i][e]));
-    const f32x2 both = both_halves(largest);
-    w.lift = value_lift(__builtin_fmaxf(both[0], both[1]), w.lift);
-    w.z = __builtin_fmaxf(top, w.z);
-    top = w.z - w.lift;
-  }
-  // A row's reference stays while no score is more than 2^8 above it (codes of FP16: none): p and
-  // its sums bear that, and most tiles take nothing off (32 rows with a maximum of their own
-  // would in every third of 256).
+  if constexpr (lifts(T::kRange, BITS)) top = lifted(w, top, vs, [&](int r) { return !MASKED || seen(r); });
+  return top;
+}
+
+// A row's reference stays while no score is more than 2^8 above it (codes of FP16: none): p and
+// its sums bear that, and most tiles take nothing off (32 rows with a maximum of their own
+// would in every third of 256).
+template <class T, int BITS, int D>
+__device__ __forceinline__ void refer(Wave<T, BITS, D> &w, float top) {
+  constexpr float kSlack = lifts(T::kRange, BITS) ? 0.f : 8.f;
   if (__ballot(top > w.m + kSlack)) {
     const float up = top > w.m + kSlack ? top : w.m, back = exp2_of(w.m - (up == -__builtin_huge_valf() ? 0.f : up));
     w.l *= back;
@@ -320,87 +350,173 @@ __device__ __forceinline__ void add_keys(Wave<T, BITS, D> &w, const uint8_t *lk,
     for (int d = 0; d < D / 32; d++) w.o[d] *= back;
     w.m = up;
   }
+}
+
+// Exponentials of settled scores, as the operand of gather.
+template <class T, int BITS, int D, bool MASKED>
+__device__ __forceinline__ void weigh(Wave<T, BITS, D> &w, const f32x16 &s, u32x4 (&p)[2], const float *vs, const Seen &seen) {
+  const uint32_t h = (threadIdx.x >> 5) & 1;
   const float ref = w.m == -__builtin_huge_valf() ? 0.f : w.m;
-  float sum = 0.f;
+  float sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int n = 0; n < 2; n++)
+  for (int st = 0; st < 2; st++) {
+    float z[8];
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-      s[n][r] = exp2_of(__builtin_fmaf(s[n][r], w.mul, -ref));
-      sum += s[n][r];
+    for (int e = 0; e < 8; e++) {
+      z[e] = exp2_of(__builtin_fmaf(s[8 * st + e], w.mul, -ref));
+      sum[e & 1] += z[e];
     }
-  w.l += sum;
-  if constexpr (BITS == 8) {
+    if constexpr (BITS == 8) {
 #pragma unroll
-    for (int n = 0; n < 2; n++)
+      for (int i = 0; i < 2; i++) {
+        const f32x4 v = *(const f32x4 *)(vs + st * 16 + 8 * i + 4 * h);
+        // a scale that is no number belongs to the queries that see its key alone
 #pragma unroll
-      for (int r = 0; r < 16; r++) s[n][r] *= vf[n * 4 + r / 4][r % 4];
+        for (int e = 0; e < 4; e++) z[4 * i + e] = !MASKED || seen(8 * st + 4 * i + e) ? z[4 * i + e] * v[e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) p[st][i] = pair(T{}, z[2 * i], z[2 * i + 1]);
   }
-  const uint32_t l16 = lane & 15, dh = (lane >> 4) & 1;
-  auto value = [&](int st, int d) -> u32x4 {  // 16 keys, 32 of D
-    const uint32_t r = 4 * h + l16 / 4, fs = R::value_swap(r);
-    const uint8_t *p = lv + (st * 16 + r) * R::kBytes + (((d * 4 + dh * 2 + ((l16 >> 1) & 1)) ^ fs) * 16) + (l16 & 1) * 8;
-    const u32x2 lo = read_turned(p), hi = read_turned(p + 8 * R::kBytes);
-    return u32x4{lo[0], lo[1], hi[0], hi[1]};
-  };
-  u32x4 p[4];
+  w.l += sum[0] + sum[1];
+}
+
+// Sixteen keys (from 16 st on, in the order of p) of 32 values (from 32 d on), turned.
+// at: of a lane's part of the tile (value_at).
+template <int D>
+__device__ __forceinline__ u32x4 turned_values(uint32_t at, int st, int d) {
+  typedef Rows<D> R;
+  const uint32_t p = (at ^ d * 64) + st * 16 * R::kBytes;
+  const u32x2 lo = turned_lds(p), hi = turned_lds(p + 8 * R::kBytes);
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+template <class T, int BITS, int D, bool MASKED>
+__device__ __forceinline__ void gather(Wave<T, BITS, D> &w, const u32x4 (&p)[2], uint32_t lv, int32_t base, uint32_t there,
+                                       int32_t window) {
+  const uint32_t at = lv + fresh(w.value_at);
+  // Values that are not finite count for the queries that see them, and zero times one is no
+  // number: a block in which some query does not see every key is looked through, and where
+  // there is one, those are left out of the products and come after, key by key.  The
+  // other queries' sums keep their bits.  (One after the other: a rare way does not need the
+  // registers that the usual one lives on.)
+  bool odd = false;
+  if constexpr (BITS == 16 && MASKED) {
+    uint32_t most = 0;
 #pragma unroll
-  for (int st = 0; st < 4; st++)
+    for (int st = 0; st < 2; st++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) p[st][i] = pair(T{}, s[st / 2][8 * (st & 1) + 2 * i], s[st / 2][8 * (st & 1) + 2 * i + 1]);
-  if constexpr (BITS == 16) {
-    // Values that are not finite count for the queries that see them, and zero times one
-    // is no number: a tile in which some query does not see every key is looked
-    // through, and where there is one, those are left out of the products and
-    // come after, key by key.  The other queries' sums keep their bits.
-    if constexpr (MASKED) {
-      uint32_t most = 0;
+      for (int d = 0; d < D / 32; d++) {
+        most = most_bits(turned_values<D>(at, st, d), most);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    odd = __ballot(joined(most) > finite_bits(T{})) != 0;
+  }
 #pragma unroll
-      for (int st = 0; st < 4; st++)
+  for (int st = 0; st < 2; st++)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++) most = most_bits(value(st, d), most);
-      if (__ballot(joined(most) > finite_bits(T{}))) {
+    for (int d = 0; d < D / 32; d++) {
+      u32x4 v = turned_values<D>(at, st, d);
+      if (odd) v = finite_part(T{}, v);
+      w.o[d] = mfma32(T{}, v, p[st], w.o[d]);
+    }
+  if (odd) {
+    const uint32_t h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-        for (int st = 0; st < 4; st++) {
-#pragma unroll
-          for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, finite_part(T{}, value(st, d)), p[st], w.o[d]);
+    for (int st = 0; st < 2; st++) {
 #pragma unroll 1
-          for (uint32_t e = 0; e < 16; e++) {
-            const uint32_t half = e >> 3, word = (e & 7) >> 1, at = st * 16 + 8 * ((e & 7) / 4) + 4 * half + (e & 3);
-            const uint32_t bits = h == half ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
-            const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
-            const bool seen = sees(w.pos - base - (int32_t)at, window) && (there >> at & 1);
+      for (uint32_t e = 0; e < 16; e++) {
+        const uint32_t half = e >> 3, word = (e & 7) >> 1, key = st * 16 + 8 * ((e & 7) / 4) + 4 * half + (e & 3);
+        const uint32_t bits = h == half ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+        const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
+        const bool is = sees(w.pos - base - (int32_t)key, window) && (there >> key & 1);
 #pragma unroll
-            for (int d = 0; d < D / 32; d++) {
-              const u32x4 v = value(st, d);
-              const f32x16 t = mfma32(T{}, (v ^ finite_part(T{}, v)) & only, p[st] & only, f32x16{});
+        for (int d = 0; d < D / 32; d++) {
+          const u32x4 v = turned_values<D>(at, st, d);
+          const f32x16 t = mfma32(T{}, (v ^ finite_part(T{}, v)) & only, p[st] & only, f32x16{});
 #pragma unroll
-              for (int r = 0; r < 16; r++) w.o[d][r] += seen ? t[r] : 0.f;
-            }
-          }
+          for (int r = 0; r < 16; r++) w.o[d][r] += is ? t[r] : 0.f;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        return;
       }
     }
   }
-#pragma unroll
-  for (int st = 0; st < 4; st++)
-#pragma unroll
-    for (int d = 0; d < D / 32; d++) w.o[d] = mfma32(T{}, value(st, d), p[st], w.o[d]);
 }
 
-// 16 bytes a lane from base + off (of each lane) to LDS address at + 16 lane.  The
-// compiler is not told of these loads: before a transposing read it would wait for all that it
-// knows of, the next tile's among them (4096 x 16384 x 32 heads: MEASURED).  A load
-// of this kind writes no register; what it writes in LDS is waited for by wait_but.
-__device__ __forceinline__ void ask(const void *base, uint32_t off, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void ask(const void *src, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
-}
-__device__ __forceinline__ uint32_t lds_address(const void *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+// All of that at once for keys that every query sees: the scores of the next 32 keys (at lk, left
+// settled in next; returns their largest) beside the weights of these (settled scores s) and
+// their sums (values at lv).  Products and vector instructions are dealt out by
+// hand, a slot to a product: in slots of the scores the first half of the exponentials, in those
+// of the sums the second half, which the later sums take, then the maximum; reads
+// run two slots ahead.  (Left to itself the compiler puts the parts one after the other:
+// 4096 x 16384 x 32 heads MEASURED.)
+template <class T, int BITS, int D>
+__device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s, f32x16 &next, uint32_t lk, uint32_t lv, const float *vs,
+                                           const float *next_ks, const float *next_vs) {
+  typedef typename KeyType<T, BITS>::type K;
+  typedef Rows<D> R;
+  constexpr int N = D / 16;  // products of the scores, and of the sums
+  const uint32_t h = (threadIdx.x >> 5) & 1;
+  const float ref = w.m == -__builtin_huge_valf() ? 0.f : w.m;
+  const uint32_t ka = lk + fresh(w.key_at), va = lv + fresh(w.value_at);
+  u32x4 kf[N], vf[N], p[2];
+  f32x4 by[BITS == 8 ? 4 : 1], keys[BITS == 8 ? 4 : 1];
+  float z[16], sum[2] = {0.f, 0.f}, top = -__builtin_huge_valf();
+  auto weight = [&](int e) {
+    z[e] = exp2_of(__builtin_fmaf(s[e], w.mul, -ref));
+    sum[e & 1] += z[e];
+    if constexpr (BITS == 8) z[e] *= by[e / 4][e % 4];
+    if (e & 1) p[e / 8][e % 8 / 2] = pair(T{}, z[e - 1], z[e]);
+  };
+  // what a slot makes stays in it
+  auto slot_ends = [&] {
+    asm volatile("" : "+v"(sum[0]), "+v"(sum[1]), "+v"(top));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_key = [&](int i) { kf[i] = read_lds<u32x4>(ka ^ i * 32); };
+  auto read_value = [&](int i) { vf[i] = turned_values<D>(va, i / (D / 32), i % (D / 32)); };
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) by[i] = *(const f32x4 *)(vs + 8 * i + 4 * h);
+  }
+  next = f32x16{};
+  __builtin_amdgcn_sched_barrier(0);
+  read_key(0);
+  if (N > 1) read_key(1);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (i + 2 < N) read_key(i + 2);
+    else read_value(i + 2 - N);
+    next = mfma32(K{}, kf[i], w.q[i], next);
+#pragma unroll
+    for (int e = 8 * i / N; e < 8 * (i + 1) / N; e++) weight(e);
+    slot_ends();
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (i + 2 < N) read_value(i + 2);
+    if (BITS == 8 && i == N / 2 - 1) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) keys[j] = *(const f32x4 *)(next_ks + 8 * j + 4 * h);
+    }
+    w.o[i % (D / 32)] = mfma32(T{}, vf[i], p[i / (D / 32)], w.o[i % (D / 32)]);
+    if (i < N / 2) {
+#pragma unroll
+      for (int e = 8 + 16 * i / N; e < 8 + 16 * (i + 1) / N; e++) weight(e);
+    } else {
+#pragma unroll
+      for (int r = 32 * (i - N / 2) / N; r < 32 * (i + 1 - N / 2) / N; r++) {
+        if constexpr (BITS == 8) next[r] *= keys[r / 4][r % 4];
+        top = __builtin_fmaxf(top, next[r]);
+      }
+    }
+    slot_ends();
+  }
+  w.l += sum[0] + sum[1];
+  const f32x2 tops = both_halves(top);
+  top = __builtin_fmaxf(tops[0], tops[1]) * w.mul;
+  if constexpr (lifts(T::kRange, BITS)) top = lifted(w, top, next_vs, [](int) { return true; });
+  return top;
 }
 
 // The address of a head's row in the pool.
@@ -877,8 +993,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
   typedef typename KeyType<T, BITS>::type K;
   constexpr int kTile = 64 * R::kBytes, kLoads = kTile / 4096, kRowsPer = 1024 / R::kBytes;
   constexpr int kRaw = D < 64 ? 1 : D / 64;  // 16 bytes of codes a thread
-  extern __shared__ __align__(1024) uint8_t lds[];  // [2][keys, values]
-  __shared__ float scales[2][128];
+  extern __shared__ __align__(1024) uint8_t lds[];  // keys [2], values [2]
+  __shared__ float scales[3][128];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t units = (uint64_t)a.tiles * c.heads * a.tile_splits;
   for (uint64_t id = blockIdx.x; id < units; id += gridDim.x) {
@@ -904,121 +1020,178 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     const int32_t wfirst = sp.first + (int32_t)(((uint32_t)r0 + w0) / a.group) + sp.ahead, wlast = sp.first + (int32_t)(((uint32_t)r0 + w1) / a.group) + sp.ahead;
     Wave<T, BITS, D> w;
     w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
-    int32_t page = 0;  // of key `lane` of the tile to be asked for next
+    // Keys come half a tile ahead of values, and pages (16 keys lie in one) a tile ahead of keys,
+    // by scalar loads: a wait for those is no wait for rows in flight.
+    struct Table { int32_t of[4]; } page = {}, page_before = {};
+    uint64_t before = 0, there[4] = {0, 0, 0, 0};  // the keys that exist: of page_before's tile; of t, t + 1, ..
+    const auto *entries = (const __attribute__((address_space(4))) int32_t *)table;
     auto look = [&](int32_t t) {
-      if (t < t1) page = page_at(c, table, t * 64 + (int32_t)lane, k.stop);
+      if (t < t1)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int32_t pos = t * 64 + 16 * j;
+          page.of[j] = entries[(uint32_t)(pos < k.stop ? pos : k.stop - 1) >> c.shift];
+        }
     };
-    auto known = [&](int32_t t) { return __ballot(t * 64 + (int32_t)lane < k.stop && (uint32_t)page < c.pages); };
+    auto known = [&](int32_t t) {
+      uint64_t all = 0;
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if ((uint32_t)page.of[j] < c.pages) all |= 0xFFFFull << (16 * j);
+      const int32_t left = k.stop - t * 64;
+      return left < 64 ? all & ((1ull << left) - 1) : all;
+    };
+    auto page_of = [](const Table &t, uint32_t j) { return (uint32_t)(j == 0 ? t.of[0] : j == 1 ? t.of[1] : j == 2 ? t.of[2] : t.of[3]); };
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float scale = 0.f;
-    auto request = [&](int32_t t, uint32_t dst, uint64_t all) {  // all: the keys that exist
-      if constexpr (BITS == 16) {
-        // (rows of a load lie in one page; the exchange is the same in all of a wave's loads)
-        const uint32_t in_load = lane / R::kChunks, mine = wave * kRowsPer + in_load, chunk = lane % R::kChunks;
-        const uint32_t off_k = in_load * R::kBytes + (chunk ^ R::key_swap(mine)) * 16, off_v = in_load * R::kBytes + (chunk ^ R::value_swap(mine)) * 16;
-        static_assert(4 * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
+    // rows of a load lie in one page; the exchange is the same in all of a wave's loads
+    const uint32_t in_load = lane / R::kChunks, chunk = lane % R::kChunks;
+    static_assert(4 * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
+    auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, uint32_t swap, uint32_t dst) {
+      const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) {
+        const uint32_t r = (i * 4 + wave) * kRowsPer;
+        const uint64_t at = pool_row(c, page_of(pages, kRowsPer <= 4 ? i * 4 * kRowsPer / 16 : r / 16), head, (uint32_t)(t * 64) + r) * R::kBytes;
         if (all == ~0ull) {
-#pragma unroll
-          for (int i = 0; i < kLoads; i++) {
-            const uint32_t r = (i * 4 + wave) * kRowsPer;
-            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
-            ask(c.k + at, off_k, dst + (i * 4 + wave) * 1024);
-            ask(c.v + at, off_v, dst + kTile + (i * 4 + wave) * 1024);
-          }
+          ask(pool + at, off, dst + (i * 4 + wave) * 1024);
         } else {
-          const uint8_t *none = (const uint8_t *)&g_zero16;
-#pragma unroll
-          for (int i = 0; i < kLoads; i++) {
-            const uint32_t r = (i * 4 + wave) * kRowsPer;
-            const bool in = all >> (r + in_load) & 1;
-            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, r), head, (uint32_t)(t * 64) + r) * R::kBytes;
-            ask(in ? c.k + at + off_k : none, dst + (i * 4 + wave) * 1024);
-            ask(in ? c.v + at + off_v : none, dst + kTile + (i * 4 + wave) * 1024);
-          }
+          ask(all >> (r + in_load) & 1 ? pool + at + off : (const uint8_t *)&g_zero16, dst + (i * 4 + wave) * 1024);
         }
+      }
+    };
+    auto fetch = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, u32x4 (&raw)[kRaw]) {
+#pragma unroll
+      for (int i = 0; i < kRaw; i++) {
+        const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16) & 63;
+        const uint64_t r = pool_row(c, page_of(pages, row / 16), head, (uint32_t)(t * 64) + row);
+        raw[i] = u32x4{0, 0, 0, 0};
+        if ((all >> row & 1) && at16 < 64 * (D / 16)) raw[i] = *(const u32x4 *)(pool + r * D + (at16 % (D / 16)) * 16);
+      }
+    };
+    const uint32_t mine_row = wave * kRowsPer + in_load;
+    // keys of tile t (and scales); returns those that exist
+    auto request_keys = [&](int32_t t) -> uint64_t {
+      if (t >= t1) return 0;
+      const uint64_t all = known(t);
+      if constexpr (BITS == 16) {
+        bring(c.k, t, page, all, R::key_swap(mine_row), lds_address(lds) + ((t - t0) & 1) * kTile);
       } else {
-#pragma unroll
-        for (int i = 0; i < kRaw; i++) {
-          const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16) & 63;
-          const int32_t pg = __shfl(page, (int)row);
-          const bool in = (all >> row & 1) && at16 < 64 * (D / 16);
-          const uint64_t r = pool_row(c, (uint32_t)pg, head, (uint32_t)(t * 64) + row);
-          raw_k[i] = raw_v[i] = u32x4{0, 0, 0, 0};
-          if (in) {
-            raw_k[i] = *(const u32x4 *)(c.k + r * D + (at16 % (D / 16)) * 16);
-            raw_v[i] = *(const u32x4 *)(c.v + r * D + (at16 % (D / 16)) * 16);
-          }
-        }
+        fetch(c.k, t, page, all, raw_k);
         scale = 0.f;
-        if (wave < 2 && (all >> lane & 1)) scale = (wave ? c.v_scales : c.k_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 64) + lane)];
+        if (wave < 2 && (all >> lane & 1))
+          scale = (wave ? c.v_scales : c.k_scales)[pool_row(c, page_of(page, lane / 16), head, (uint32_t)(t * 64) + lane)];
+      }
+      page_before = page;
+      before = all;
+      look(t + 1);
+      return all;
+    };
+    // values of tile t, whose keys were asked for last
+    auto request_values = [&](int32_t t) {
+      if (t >= t1) return;
+      if constexpr (BITS == 16) {
+        bring(c.v, t, page_before, before, R::value_swap(mine_row), lds_address(lds) + (2 + ((t - t0) & 1)) * kTile);
+      } else {
+        fetch(c.v, t, page_before, before, raw_v);
       }
     };
     // codes of 8 bits become 16-bit values on their way to LDS, once for all waves
-    auto spread = [&](uint32_t odd) {
-      uint8_t *dst = lds + odd * (2 * kTile);
-      if constexpr (BITS == 8) {
+    auto spread = [&](int32_t t, const u32x4 (&raw)[kRaw], bool values) {
+      if (t >= t1) return;
+      uint8_t *dst = lds + ((values ? 2 : 0) + ((t - t0) & 1)) * kTile;
 #pragma unroll
-        for (int i = 0; i < kRaw; i++) {
-          const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
-          if (at16 >= 64 * (D / 16)) break;
+      for (int i = 0; i < kRaw; i++) {
+        const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
+        if (at16 >= 64 * (D / 16)) break;
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const u32x2 kc = {raw_k[i][2 * e], raw_k[i][2 * e + 1]}, vc = {raw_v[i][2 * e], raw_v[i][2 * e + 1]};
-            *(u32x4 *)(dst + row * R::kBytes + (((chunk + e) ^ R::key_swap(row)) * 16)) = widen8(K{}, kc);
-            *(u32x4 *)(dst + kTile + row * R::kBytes + (((chunk + e) ^ R::value_swap(row)) * 16)) = widen8(T{}, vc);
-          }
+        for (int e = 0; e < 2; e++) {
+          const u32x2 codes = {raw[i][2 * e], raw[i][2 * e + 1]};
+          const uint32_t to = row * R::kBytes + (((chunk + e) ^ (values ? R::value_swap(row) : R::key_swap(row))) * 16);
+          *(u32x4 *)(dst + to) = values ? widen8(T{}, codes) : widen8(K{}, codes);
         }
-        if (wave < 2) scales[odd][wave * 64 + lane] = wave ? scale : scale * a.c;
       }
+      if (!values && wave < 2) scales[(t - t0) % 3][wave * 64 + lane] = wave ? scale : scale * a.c;
     };
-    look(t0);
-    uint64_t there = 0, next = 0;
+    f32x16 s0, s1;  // settled scores of the first, second 32 keys of a tile
     if (t0 < t1) {
-      there = known(t0);
-      request(t0, lds_address(lds), there);
-      look(t0 + 1);
-      if constexpr (BITS == 8) {
-        spread(0);
-        if (t0 + 1 < t1) {
-          next = known(t0 + 1);
-          request(t0 + 1, 0, next);
-          look(t0 + 2);
-        }
-      }
-    }
-    auto step = [&](int32_t t, auto masked) {
-      const uint32_t odd = (t - t0) & 1;
-      const uint8_t *p = lds + odd * (2 * kTile);
-      uint64_t after = 0;
+      look(t0);
+      there[0] = request_keys(t0);
       if constexpr (BITS == 16) {
+        request_values(t0);
+        there[1] = request_keys(t0 + 1);
         wait_but<0>();
-        meet();  // tile t is whole, and tile t - 1 read by all
-        if (t + 1 < t1) {
-          next = known(t + 1);
-          request(t + 1, lds_address(lds) + (odd ^ 1) * (2 * kTile), next);
-          look(t + 2);
-        }
+      } else {
+        spread(t0, raw_k, false);
+        request_values(t0);
+        spread(t0, raw_v, true);
+        there[1] = request_keys(t0 + 1);
+        spread(t0 + 1, raw_k, false);
+        request_values(t0 + 1);
+        there[2] = request_keys(t0 + 2);
+      }
+      __syncthreads();
+      s0 = scores(w, lds_address(lds));
+      const Seen seen(w, t0 * 64, (uint32_t)there[0], a.window);
+      refer(w, settle<T, BITS, D, true>(w, s0, scales[0], scales[0] + 64, seen));
+    }
+    // Tile t, whose s0 is settled; leaves that of tile t + 1.  Each half has the scores of
+    // the next 32 keys beside the exponentials of these, on either unit of the SIMD.
+    auto step = [&](int32_t t, auto masked) {
+      constexpr bool M = decltype(masked)::value;
+      const uint32_t at = (uint32_t)(t - t0), base = lds_address(lds);
+      const bool more = !M || t + 1 < t1;
+      const float *now = scales[at % 3], *then = scales[(at + 1) % 3];
+      const uint32_t lk = base + (at & 1) * kTile, next = base + ((at + 1) & 1) * kTile, lv = base + (2 + (at & 1)) * kTile;
+      const Seen seen0(w, t * 64, (uint32_t)there[0], a.window), seen1(w, t * 64 + 32, (uint32_t)(there[0] >> 32), a.window),
+          seen2(w, t * 64 + 64, (uint32_t)there[1], a.window);
+      u32x4 p[2];
+      // values of t are there (keys of t + 1 may still come), those of t - 1 read by all
+      if constexpr (BITS == 16) {
+        if (more) wait_but<kLoads>();
+        else wait_but<0>();
+        meet();
+        request_values(t + 1);
       } else {
         __syncthreads();
-        if (t + 1 < t1) {
-          spread(odd ^ 1);
-          if (t + 2 < t1) {
-            after = known(t + 2);
-            request(t + 2, 0, after);
-            look(t + 3);
-          }
-        }
+        spread(t + 1, raw_v, true);
+        request_values(t + 2);
       }
-      // (a masked tile may have nothing for this wave's rows)
-      if (!masked.value || (t * 64 <= wlast && wfirst - (t * 64 + 63) < a.window))
-        add_keys<T, BITS, D, masked.value>(w, p, p + kTile, scales[odd], scales[odd] + 64, t * 64, there, a.window);
-      there = next;
-      if constexpr (BITS == 8) next = after;
+      if constexpr (M) {
+        s1 = scores(w, lk + 32 * R::kBytes);
+        weigh<T, BITS, D, M>(w, s0, p, now + 64, seen0);
+        gather<T, BITS, D, M>(w, p, lv, t * 64, (uint32_t)there[0], a.window);
+        refer(w, settle<T, BITS, D, M>(w, s1, now + 32, now + 96, seen1));
+      } else {
+        refer(w, half_step(w, s0, s1, lk + 32 * R::kBytes, lv, now + 64, now + 32, now + 96));
+      }
+      // keys of t + 1 are there (values of t + 1 may still come), those of t read by all
+      if constexpr (BITS == 16) {
+        if (more) wait_but<kLoads>();
+        meet();
+        there[2] = request_keys(t + 2);
+      } else {
+        __syncthreads();
+        spread(t + 2, raw_k, false);
+        there[3] = request_keys(t + 3);
+      }
+      if constexpr (M) {
+        if (more) s0 = scores(w, next);
+        weigh<T, BITS, D, M>(w, s1, p, now + 96, seen1);
+        gather<T, BITS, D, M>(w, p, lv + 32 * R::kBytes, t * 64 + 32, (uint32_t)(there[0] >> 32), a.window);
+        if (more) refer(w, settle<T, BITS, D, M>(w, s0, then, then + 64, seen2));
+      } else {
+        refer(w, half_step(w, s1, s0, next, lv + 32 * R::kBytes, now + 96, then, then + 64));
+      }
+      there[0] = there[1];
+      there[1] = there[2];
+      there[2] = there[3];
     };
-    // tiles of which every row of this wave sees every key have a loop of their own
+    // tiles of which every row of this wave sees every key, like the next one's, go by themselves
+    auto whole = [&](int32_t t, uint64_t all) { return t < t1 && all == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window; };
     for (int32_t t = t0; t < t1; t++) {
-      for (; t < t1 && there == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window; t++) step(t, std::false_type{});
-      if (t < t1) step(t, std::true_type{});
+      for (; whole(t, there[0]) && whole(t + 1, there[1]); t++) step(t, std::false_type{});
+      step(t, std::true_type{});
     }
     __syncthreads();  // the buffers are read
     const f32x2 sums = both_halves(w.l);
