@@ -987,13 +987,17 @@ __device__ __forceinline__ uint32_t tile_owner(const Sequences &b, uint32_t grou
   return lo ? lo - 1 : b.count;
 }
 
+// Tiles of keys in LDS.  With three a step of 16 bits meets once: the tile that is asked for is none
+// that is read; two leave room for the scales of 8 bits beside two workgroups' tiles.
+constexpr uint32_t key_buffers(int bits) { return bits == 16 ? 3 : 2; }
 template <class T, int BITS, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages c, const Sequences b, const Attend a) {
   typedef Rows<D> R;
   typedef typename KeyType<T, BITS>::type K;
   constexpr int kTile = 64 * R::kBytes, kLoads = kTile / 4096, kRowsPer = 1024 / R::kBytes;
   constexpr int kRaw = D < 64 ? 1 : D / 64;  // 16 bytes of codes a thread
-  extern __shared__ __align__(1024) uint8_t lds[];  // keys [2], values [2]
+  constexpr uint32_t kKeys = key_buffers(BITS);
+  extern __shared__ __align__(1024) uint8_t lds[];  // keys [kKeys], values [2]
   __shared__ float scales[3][128];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t units = (uint64_t)a.tiles * c.heads * a.tile_splits;
@@ -1020,28 +1024,38 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     const int32_t wfirst = sp.first + (int32_t)(((uint32_t)r0 + w0) / a.group) + sp.ahead, wlast = sp.first + (int32_t)(((uint32_t)r0 + w1) / a.group) + sp.ahead;
     Wave<T, BITS, D> w;
     w.init(a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
-    // Keys come half a tile ahead of values, and pages (16 keys lie in one) a tile ahead of keys,
-    // by scalar loads: a wait for those is no wait for rows in flight.
+    // Keys come ahead of values, and pages (16 keys lie in one) a tile ahead of keys, by
+    // scalar loads: a wait for those is no wait for rows in flight.
     struct Table { int32_t of[4]; } page = {}, page_before = {};
     uint64_t before = 0, there[4] = {0, 0, 0, 0};  // the keys that exist: of page_before's tile; of t, t + 1, ..
     const auto *entries = (const __attribute__((address_space(4))) int32_t *)table;
+    const bool one = c.shift >= 6;  // page of a tile
     auto look = [&](int32_t t) {
-      if (t < t1)
+      if (t >= t1) return;
+      if (one) {
+        page.of[0] = entries[(uint32_t)(t * 64) >> c.shift];
+      } else {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           const int32_t pos = t * 64 + 16 * j;
           page.of[j] = entries[(uint32_t)(pos < k.stop ? pos : k.stop - 1) >> c.shift];
         }
+      }
     };
     auto known = [&](int32_t t) {
-      uint64_t all = 0;
+      uint64_t all = (uint32_t)page.of[0] < c.pages ? ~0ull : 0;
+      if (!one) {
+        all &= 0xFFFF;
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        if ((uint32_t)page.of[j] < c.pages) all |= 0xFFFFull << (16 * j);
+        for (int j = 1; j < 4; j++)
+          if ((uint32_t)page.of[j] < c.pages) all |= 0xFFFFull << (16 * j);
+      }
       const int32_t left = k.stop - t * 64;
       return left < 64 ? all & ((1ull << left) - 1) : all;
     };
-    auto page_of = [](const Table &t, uint32_t j) { return (uint32_t)(j == 0 ? t.of[0] : j == 1 ? t.of[1] : j == 2 ? t.of[2] : t.of[3]); };
+    // this head's part of a page, and where it begins
+    const uint32_t part = (uint32_t)R::kBytes << c.shift, page_bytes = part * c.heads, row_mask = (1u << c.shift) - 1;
+    auto page_of = [&](const Table &t, uint32_t j) { return (uint32_t)(one || j == 0 ? t.of[0] : j == 1 ? t.of[1] : j == 2 ? t.of[2] : t.of[3]); };
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float scale = 0.f;
     // rows of a load lie in one page; the exchange is the same in all of a wave's loads
@@ -1049,14 +1063,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     static_assert(4 * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
     auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, uint32_t swap, uint32_t dst) {
       const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
+      const uint8_t *mine = pool + (uint64_t)head * part;
+      if (one && all == ~0ull) {
+        const uint8_t *src = mine + ((uint64_t)(uint32_t)pages.of[0] * page_bytes + (((uint32_t)(t * 64) & row_mask) + wave * kRowsPer) * R::kBytes);
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) ask(src + i * 4096, off, dst + (i * 4 + wave) * 1024);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < kLoads; i++) {
         const uint32_t r = (i * 4 + wave) * kRowsPer;
-        const uint64_t at = pool_row(c, page_of(pages, kRowsPer <= 4 ? i * 4 * kRowsPer / 16 : r / 16), head, (uint32_t)(t * 64) + r) * R::kBytes;
+        const uint32_t pg = page_of(pages, kRowsPer <= 4 ? i * 4 * kRowsPer / 16 : r / 16);
+        const uint8_t *src = mine + ((uint64_t)pg * page_bytes + (((uint32_t)(t * 64) + r) & row_mask) * R::kBytes);
         if (all == ~0ull) {
-          ask(pool + at, off, dst + (i * 4 + wave) * 1024);
+          ask(src, off, dst + (i * 4 + wave) * 1024);
         } else {
-          ask(all >> (r + in_load) & 1 ? pool + at + off : (const uint8_t *)&g_zero16, dst + (i * 4 + wave) * 1024);
+          ask(all >> (r + in_load) & 1 ? src + off : (const uint8_t *)&g_zero16, dst + (i * 4 + wave) * 1024);
         }
       }
     };
@@ -1075,7 +1097,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       if (t >= t1) return 0;
       const uint64_t all = known(t);
       if constexpr (BITS == 16) {
-        bring(c.k, t, page, all, R::key_swap(mine_row), lds_address(lds) + ((t - t0) & 1) * kTile);
+        bring(c.k, t, page, all, R::key_swap(mine_row), lds_address(lds) + (uint32_t)(t - t0) % kKeys * kTile);
       } else {
         fetch(c.k, t, page, all, raw_k);
         scale = 0.f;
@@ -1091,7 +1113,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     auto request_values = [&](int32_t t) {
       if (t >= t1) return;
       if constexpr (BITS == 16) {
-        bring(c.v, t, page_before, before, R::value_swap(mine_row), lds_address(lds) + (2 + ((t - t0) & 1)) * kTile);
+        bring(c.v, t, page_before, before, R::value_swap(mine_row), lds_address(lds) + (kKeys + ((t - t0) & 1)) * kTile);
       } else {
         fetch(c.v, t, page_before, before, raw_v);
       }
@@ -1099,7 +1121,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     // codes of 8 bits become 16-bit values on their way to LDS, once for all waves
     auto spread = [&](int32_t t, const u32x4 (&raw)[kRaw], bool values) {
       if (t >= t1) return;
-      uint8_t *dst = lds + ((values ? 2 : 0) + ((t - t0) & 1)) * kTile;
+      uint8_t *dst = lds + ((values ? kKeys : 0) + ((t - t0) & 1)) * kTile;
 #pragma unroll
       for (int i = 0; i < kRaw; i++) {
         const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
@@ -1142,16 +1164,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       const uint32_t at = (uint32_t)(t - t0), base = lds_address(lds);
       const bool more = !M || t + 1 < t1;
       const float *now = scales[at % 3], *then = scales[(at + 1) % 3];
-      const uint32_t lk = base + (at & 1) * kTile, next = base + ((at + 1) & 1) * kTile, lv = base + (2 + (at & 1)) * kTile;
+      const uint32_t lk = base + at % kKeys * kTile, next = base + (at + 1) % kKeys * kTile, lv = base + (kKeys + (at & 1)) * kTile;
       const Seen seen0(w, t * 64, (uint32_t)there[0], a.window), seen1(w, t * 64 + 32, (uint32_t)(there[0] >> 32), a.window),
           seen2(w, t * 64 + 64, (uint32_t)there[1], a.window);
       u32x4 p[2];
-      // values of t are there (keys of t + 1 may still come), those of t - 1 read by all
+      // values of t are there (16 bits: and keys of t + 1), those of t - 1 read by all
       if constexpr (BITS == 16) {
-        if (more) wait_but<kLoads>();
-        else wait_but<0>();
+        wait_but<0>();
         meet();
         request_values(t + 1);
+        there[2] = request_keys(t + 2);
       } else {
         __syncthreads();
         spread(t + 1, raw_v, true);
@@ -1165,12 +1187,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       } else {
         refer(w, half_step(w, s0, s1, lk + 32 * R::kBytes, lv, now + 64, now + 32, now + 96));
       }
-      // keys of t + 1 are there (values of t + 1 may still come), those of t read by all
-      if constexpr (BITS == 16) {
-        if (more) wait_but<kLoads>();
-        meet();
-        there[2] = request_keys(t + 2);
-      } else {
+      if constexpr (BITS == 8) {
+        // keys of t + 1 are there, those of t read by all
         __syncthreads();
         spread(t + 2, raw_k, false);
         there[3] = request_keys(t + 3);
@@ -1187,10 +1205,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       there[1] = there[2];
       there[2] = there[3];
     };
-    // tiles of which every row of this wave sees every key, like the next one's, go by themselves
-    auto whole = [&](int32_t t, uint64_t all) { return t < t1 && all == ~0ull && t * 64 + 63 <= wfirst && wlast - t * 64 < a.window; };
+    // tiles of which every row of this wave sees every key (from h0 on, before h1), like the next
+    // one's, go by themselves
+    const int32_t h0 = wlast < a.window ? 0 : ((wlast - a.window) >> 6) + 1, h1 = wfirst + 1 < t1 * 64 ? (wfirst + 1) >> 6 : t1;
     for (int32_t t = t0; t < t1; t++) {
-      for (; whole(t, there[0]) && whole(t + 1, there[1]); t++) step(t, std::false_type{});
+      for (; t >= h0 && t + 1 < h1 && (there[0] & there[1]) == ~0ull; t++) step(t, std::false_type{});
       step(t, std::true_type{});
     }
     __syncthreads();  // the buffers are read
@@ -1365,8 +1384,8 @@ hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t
   }
   if (few != hipSuccess) return few;
   if (p.tile) {
-    constexpr uint32_t lds = 4 * 64 * Rows<D>::kBytes;
-    const hipError_t st0 = allow_lds((const void *)attend_tile<T, BITS, D>, lds, kDeclared);
+    constexpr uint32_t lds = (key_buffers(BITS) + 2) * 64 * Rows<D>::kBytes;
+    const hipError_t st0 = allow_lds((const void *)attend_tile<T, BITS, D>, lds, BITS == 8 ? kDeclared : 0);
     if (st0 != hipSuccess) return st0;
     hipLaunchKernelGGL((attend_tile<T, BITS, D>), dim3(grid_of((uint64_t)p.a.tiles * c.heads * p.a.tile_splits)), dim3(256), lds, s, c,
                        b, p.a);
