@@ -107,7 +107,7 @@ struct Attend {
   uint32_t alone;            // no attend_tile follows: sequences of more rows are taken too
   float *few_o, *few_ml;     // [splits][seqs][kv heads][cap][D], [..][2]
   // tiles
-  uint32_t tiles, tile_splits;
+  uint32_t tiles, tile_rows, tile_splits;
   float *tile_o, *tile_ml;   // [splits][tokens][heads][D], [..][2]
 };
 
@@ -479,6 +479,7 @@ __device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s,
     for (int i = 0; i < 4; i++) by[i] = *(const f32x4 *)(vs + 8 * i + 4 * h);
   }
   next = f32x16{};
+  __builtin_amdgcn_s_setprio(1);
   __builtin_amdgcn_sched_barrier(0);
   read_key(0);
   if (N > 1) read_key(1);
@@ -512,6 +513,7 @@ __device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s,
     }
     slot_ends();
   }
+  __builtin_amdgcn_s_setprio(0);
   w.l += sum[0] + sum[1];
   const f32x2 tops = both_halves(top);
   top = __builtin_fmaxf(tops[0], tops[1]) * w.mul;
@@ -966,18 +968,20 @@ __global__ __launch_bounds__(256) void join_few(const Pages c, const Sequences b
   }
 }
 
-// Tile i of 128 rows lies in sequence s, whose tiles begin at starts[s] * group / 128
+// Tile i of ROWS rows lies in sequence s, whose tiles begin at starts[s] * group / ROWS
 // (rounded down) + s: no two sequences' overlap, and what lies between them is empty.
+template <uint32_t ROWS>
 __device__ __forceinline__ int64_t first_tile(const Sequences &b, uint32_t s, uint32_t group) {
   const int32_t at = b.starts[s];
-  return (int64_t)((uint64_t)(at < 0 ? 0 : at) * group / 128) + s;
+  return (int64_t)((uint64_t)(at < 0 ? 0 : at) * group / ROWS) + s;
 }
+template <uint32_t ROWS>
 __device__ __forceinline__ uint32_t tile_owner(const Sequences &b, uint32_t group, int64_t tile) {
   const uint32_t lane = threadIdx.x & 63;
   uint32_t lo = 0, n = b.count;  // as starts_up_to
   while (n) {
     const uint32_t step = (n + 63) / 64;
-    const bool in = lane * step < n && first_tile(b, lo + lane * step, group) <= tile;
+    const bool in = lane * step < n && first_tile<ROWS>(b, lo + lane * step, group) <= tile;
     const uint32_t k = __popcll(__ballot(in));
     if (k == 0) break;
     const uint32_t before = lo + n;
@@ -990,12 +994,13 @@ __device__ __forceinline__ uint32_t tile_owner(const Sequences &b, uint32_t grou
 // Tiles of keys in LDS.  With three a step of 16 bits meets once: the tile that is asked for is none
 // that is read; two leave room for the scales of 8 bits beside two workgroups' tiles.
 constexpr uint32_t key_buffers(int bits) { return bits == 16 ? 3 : 2; }
-template <class T, int BITS, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages c, const Sequences b, const Attend a) {
+template <class T, int BITS, int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const Pages c, const Sequences b, const Attend a) {
   typedef Rows<D> R;
   typedef typename KeyType<T, BITS>::type K;
-  constexpr int kTile = 64 * R::kBytes, kLoads = kTile / 4096, kRowsPer = 1024 / R::kBytes;
-  constexpr int kRaw = D < 64 ? 1 : D / 64;  // 16 bytes of codes a thread
+  constexpr int kTile = 64 * R::kBytes, kLoads = kTile / 1024 / NW, kRowsPer = 1024 / R::kBytes;
+  constexpr uint32_t kRows = 32 * NW;
+  constexpr int kRaw = D / 16 <= NW ? 1 : D / 16 / NW;  // 16 bytes of codes a thread
   constexpr uint32_t kKeys = key_buffers(BITS);
   extern __shared__ __align__(1024) uint8_t lds[];  // keys [kKeys], values [2]
   __shared__ float scales[3][128];
@@ -1005,13 +1010,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     // the last tiles of a prompt see the most keys: they go first
     const uint32_t head = (uint32_t)(id % c.heads), z = (uint32_t)(id / c.heads % a.tile_splits);
     const int64_t tile = (int64_t)a.tiles - 1 - (int64_t)(id / c.heads / a.tile_splits);
-    const uint32_t s = tile_owner(b, a.group, tile);
+    const uint32_t s = tile_owner<kRows>(b, a.group, tile);
     if (s >= b.count) continue;
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
-    const int64_t r0 = (tile - first_tile(b, s, a.group)) * 128;
+    const int64_t r0 = (tile - first_tile<kRows>(b, s, a.group)) * kRows;
     if (rows <= a.cap || r0 >= (int64_t)rows) continue;
-    const uint32_t count = rows - (uint32_t)r0 < 128 ? rows - (uint32_t)r0 : 128;
+    const uint32_t count = rows - (uint32_t)r0 < kRows ? rows - (uint32_t)r0 : kRows;
     const int32_t first = sp.first + (int32_t)((uint32_t)r0 / a.group), last = sp.first + (int32_t)(((uint32_t)r0 + count - 1) / a.group);
     const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, kTileLeast);
     if (z && z >= (uint32_t)k.count) continue;
@@ -1060,32 +1065,32 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
     float scale = 0.f;
     // rows of a load lie in one page; the exchange is the same in all of a wave's loads
     const uint32_t in_load = lane / R::kChunks, chunk = lane % R::kChunks;
-    static_assert(4 * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
+    static_assert(kLoads >= 1 && NW * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
     auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, uint32_t swap, uint32_t dst) {
       const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
       const uint8_t *mine = pool + (uint64_t)head * part;
       if (one && all == ~0ull) {
         const uint8_t *src = mine + ((uint64_t)(uint32_t)pages.of[0] * page_bytes + (((uint32_t)(t * 64) & row_mask) + wave * kRowsPer) * R::kBytes);
 #pragma unroll
-        for (int i = 0; i < kLoads; i++) ask(src + i * 4096, off, dst + (i * 4 + wave) * 1024);
+        for (int i = 0; i < kLoads; i++) ask(src + i * NW * 1024, off, dst + (i * NW + wave) * 1024);
         return;
       }
 #pragma unroll
       for (int i = 0; i < kLoads; i++) {
-        const uint32_t r = (i * 4 + wave) * kRowsPer;
-        const uint32_t pg = page_of(pages, kRowsPer <= 4 ? i * 4 * kRowsPer / 16 : r / 16);
+        const uint32_t r = (i * NW + wave) * kRowsPer;
+        const uint32_t pg = page_of(pages, NW * kRowsPer <= 16 ? i * NW * kRowsPer / 16 : r / 16);
         const uint8_t *src = mine + ((uint64_t)pg * page_bytes + (((uint32_t)(t * 64) + r) & row_mask) * R::kBytes);
         if (all == ~0ull) {
-          ask(src, off, dst + (i * 4 + wave) * 1024);
+          ask(src, off, dst + (i * NW + wave) * 1024);
         } else {
-          ask(all >> (r + in_load) & 1 ? src + off : (const uint8_t *)&g_zero16, dst + (i * 4 + wave) * 1024);
+          ask(all >> (r + in_load) & 1 ? src + off : (const uint8_t *)&g_zero16, dst + (i * NW + wave) * 1024);
         }
       }
     };
     auto fetch = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, u32x4 (&raw)[kRaw]) {
 #pragma unroll
       for (int i = 0; i < kRaw; i++) {
-        const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16) & 63;
+        const uint32_t at16 = i * 64 * NW + threadIdx.x, row = at16 / (D / 16) & 63;
         const uint64_t r = pool_row(c, page_of(pages, row / 16), head, (uint32_t)(t * 64) + row);
         raw[i] = u32x4{0, 0, 0, 0};
         if ((all >> row & 1) && at16 < 64 * (D / 16)) raw[i] = *(const u32x4 *)(pool + r * D + (at16 % (D / 16)) * 16);
@@ -1124,7 +1129,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tile(const Pages
       uint8_t *dst = lds + ((values ? kKeys : 0) + ((t - t0) & 1)) * kTile;
 #pragma unroll
       for (int i = 0; i < kRaw; i++) {
-        const uint32_t at16 = i * 256 + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
+        const uint32_t at16 = i * 64 * NW + threadIdx.x, row = at16 / (D / 16), chunk = at16 % (D / 16) * 2;
         if (at16 >= 64 * (D / 16)) break;
 #pragma unroll
         for (int e = 0; e < 2; e++) {
@@ -1266,8 +1271,8 @@ __global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     int32_t parts = 0;
     if (in && t >= sp.first && t < sp.last && rows > a.cap) {
-      const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~127u;
-      const uint32_t count = rows - r0 < 128 ? rows - r0 : 128;
+      const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~(a.tile_rows - 1);
+      const uint32_t count = rows - r0 < a.tile_rows ? rows - r0 : a.tile_rows;
       parts = cuts_of(c, b, sp.first + (int32_t)(r0 / a.group) + sp.ahead, sp.first + (int32_t)((r0 + count - 1) / a.group) + sp.ahead,
                       sp.length, a.window, kTileShift, a.tile_splits, kTileLeast).count;
     }
@@ -1328,8 +1333,11 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
     a.few_splits = n < 1 ? 1 : (uint32_t)n;
   }
   if (p.tile) {
-    a.tiles = (uint32_t)(tokens * a.group / 128 + seqs);
-    const uint64_t units = (tokens * a.group + 127) / 128 * kv, most = (seen + 63) / 64 + 1;
+    // 256 rows to a tile where those fill the chip: half of the reads of keys and values
+    const uint64_t all = tokens * a.group;
+    a.tile_rows = (dim == 64 || dim == 128) && (all + 255) / 256 * kv >= 256 ? 256 : 128;
+    a.tiles = (uint32_t)(all / a.tile_rows + seqs);
+    const uint64_t units = (all + a.tile_rows - 1) / a.tile_rows * kv, most = (seen + 63) / 64 + 1;
     uint64_t n = units >= 512 ? 1 : 512 / units;
     if (n > most / kTileLeast) n = most / kTileLeast;
     const uint64_t part = tokens * heads * (dim + 2) * 4;
@@ -1373,6 +1381,15 @@ hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream
   hipLaunchKernelGGL((join_few<T, D>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.cap)), dim3(256), 0, s, c, b, p.a);
   return hipGetLastError();
 }
+template <class T, int BITS, int D, int NW>
+hipError_t tiles(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {
+  constexpr uint32_t lds = (key_buffers(BITS) + 2) * 64 * Rows<D>::kBytes;
+  const hipError_t e = allow_lds((const void *)attend_tile<T, BITS, D, NW>, lds, BITS == 8 ? kDeclared : 0);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attend_tile<T, BITS, D, NW>), dim3(grid_of((uint64_t)p.a.tiles * c.heads * p.a.tile_splits)), dim3(64 * NW), lds, s,
+                     c, b, p.a);
+  return hipGetLastError();
+}
 template <class T, int BITS, int D>
 hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {
   // attend_few goes always: it clears the rows of no sequence
@@ -1384,12 +1401,12 @@ hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t
   }
   if (few != hipSuccess) return few;
   if (p.tile) {
-    constexpr uint32_t lds = (key_buffers(BITS) + 2) * 64 * Rows<D>::kBytes;
-    const hipError_t st0 = allow_lds((const void *)attend_tile<T, BITS, D>, lds, BITS == 8 ? kDeclared : 0);
-    if (st0 != hipSuccess) return st0;
-    hipLaunchKernelGGL((attend_tile<T, BITS, D>), dim3(grid_of((uint64_t)p.a.tiles * c.heads * p.a.tile_splits)), dim3(256), lds, s, c,
-                       b, p.a);
-    const hipError_t st = hipGetLastError();
+    hipError_t st;
+    if constexpr (D == 64 || D == 128) {
+      st = p.a.tile_rows == 256 ? tiles<T, BITS, D, 8>(p, c, b, s) : tiles<T, BITS, D, 4>(p, c, b, s);
+    } else {
+      st = tiles<T, BITS, D, 4>(p, c, b, s);
+    }
     if (st != hipSuccess) return st;
   }
   if (p.a.tile_splits > 1) {
