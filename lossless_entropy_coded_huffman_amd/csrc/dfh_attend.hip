@@ -103,7 +103,7 @@ struct Attend {
   int32_t window;            // INT32_MAX: none
   float c;                   // scale times log2 e
   // few rows
-  uint32_t cap, few_splits;
+  uint32_t cap, few_fill, few_splits;
   uint32_t alone;            // no attend_tile follows: sequences of more rows are taken too
   float *few_o, *few_ml;     // [splits][seqs][kv heads][cap][D], [..][2]
   // tiles
@@ -112,12 +112,13 @@ struct Attend {
 };
 
 // The keys that rows at positions first .. last see, in units of 2^shift, cut into
-// `count` parts of `per`.
+// `count` parts of `per`: `fill` parts of `least` units or more, or parts of `chunk` units where
+// that is more of them, and at most `splits`.
 struct Cuts {
   int32_t begin, end, per, count, stop;  // stop: the first position that is not seen
 };
 __device__ __forceinline__ Cuts cuts_of(const Pages &c, const Sequences &b, int32_t first, int32_t last, int32_t length,
-                                        int32_t window, int shift, uint32_t splits, int32_t least) {
+                                        int32_t window, int shift, uint32_t splits, uint32_t fill, int32_t least, int32_t chunk) {
   Cuts k;
   const uint64_t held = (uint64_t)b.width << c.shift;
   k.stop = last + 1 < length ? last + 1 : length;
@@ -127,13 +128,15 @@ __device__ __forceinline__ Cuts cuts_of(const Pages &c, const Sequences &b, int3
   k.begin = from >> shift;
   k.end = k.stop > from ? (k.stop + (1 << shift) - 1) >> shift : k.begin;
   const int32_t n = k.end - k.begin;
-  int32_t want = (n + least - 1) / least;
+  int32_t want = (n + least - 1) / least, pieces = (n + chunk - 1) / chunk;
+  want = want < (int32_t)fill ? want : (int32_t)fill;
+  want = want > pieces ? want : pieces;
   want = want < (int32_t)splits ? want : (int32_t)splits;
   k.per = want > 0 ? (n + want - 1) / want : 0;
   k.count = k.per > 0 ? (n + k.per - 1) / k.per : 0;
   return k;
 }
-constexpr int kFewShift = 5, kFewLeast = 4, kTileShift = 6, kTileLeast = 8;
+constexpr int kFewShift = 5, kFewLeast = 4, kFewChunk = 32, kTileShift = 6, kTileLeast = 8, kTileChunk = 1 << 30;
 
 // What codes of 8 bits become to multiply q: FP16, which is made of bytes with half of the
 // instructions that BF16 takes, for a lifted q (lift_q).
@@ -177,6 +180,10 @@ __device__ __forceinline__ void ask(const uint8_t *base, uint32_t off, uint32_t 
 __device__ __forceinline__ void ask(const uint8_t *src, uint32_t at) {
   at = same(at);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void ask_word(const uint8_t *src, uint32_t at) {  // 4 bytes a lane
+  at = same(at);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
@@ -570,13 +577,13 @@ struct Few {
     const uint32_t g = (threadIdx.x >> 4) & 3;
 #pragma unroll
     for (int st = 0; st < D / 32; st++) q[n][st] = *(const u32x4 *)(row + chunk_of(st, g) * 8);
-    mul[n] = BITS == 8 ? 1.f : c;
+    mul[n] = c;
     if constexpr (BITS == 8 && T::kRange) {
       uint32_t top = 0;
 #pragma unroll
       for (int st = 0; st < D / 32; st++) top = most_bits(q[n][st], top);
       const float most = most_of_four(from_bits(T{}, (uint16_t)joined(top)));
-      mul[n] = lift_q(q[n], most);
+      mul[n] *= lift_q(q[n], most);
     }
 #pragma unroll
     for (int d = 0; d < D / 16; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -602,11 +609,11 @@ struct FewRows {
   static __device__ __forceinline__ uint32_t value_swap(uint32_t r) { return ((r / kPer) & (kUnits - 1)) * kUnit; }
 };
 
-// 32 keys at position `base` in LDS.  BITS 8: ks scales of the keys times c, vs of the
-// values; there: bit j: key j exists.  Not MASKED: every query sees all.
+// 32 keys at position `base` in LDS: the weights p of their values.  BITS 8: ks are scales of the
+// keys, vs of the values; there: bit j: key j exists.  Not MASKED: every query sees all.
 template <class T, int BITS, int D, int NQ, bool MASKED>
-__device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *lk, const uint8_t *lv, const float *ks,
-                                        const float *vs, int32_t base, uint32_t there, int32_t window) {
+__device__ __forceinline__ void weigh_few(Few<T, BITS, D, NQ> &w, u32x4 (&p)[NQ], const uint8_t *lk, const float *ks, const float *vs,
+                                          int32_t base, uint32_t there, int32_t window) {
   typedef FewRows<BITS, D> R;
   const uint32_t lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   f32x4 s[NQ][2];
@@ -614,23 +621,23 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
   for (int b = 0; b < 2; b++) {
 #pragma unroll
     for (int n = 0; n < NQ; n++) s[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint8_t *p = lk + (b * 16 + l16) * R::kBytes;
+    const uint8_t *row = lk + (b * 16 + l16) * R::kBytes;
     const uint32_t f = R::key_swap(b * 16 + l16);
     if constexpr (BITS == 16) {
 #pragma unroll
       for (int st = 0; st < D / 32; st++) {
-        const u32x4 k = *(const u32x4 *)(p + (((st * 4 + g) ^ f) * 16));
+        const u32x4 k = *(const u32x4 *)(row + (((st * 4 + g) ^ f) * 16));
 #pragma unroll
         for (int n = 0; n < NQ; n++) s[n][b] = mfma(T{}, k, w.q[n][st], s[n][b]);
       }
     } else if constexpr (D == 32) {
-      const u32x4 k = widen8(F16{}, *(const u32x2 *)(p + (((g >> 1) ^ f) * 16) + (g & 1) * 8));
+      const u32x4 k = widen8(F16{}, *(const u32x2 *)(row + (((g >> 1) ^ f) * 16) + (g & 1) * 8));
 #pragma unroll
       for (int n = 0; n < NQ; n++) s[n][b] = mfma(F16{}, k, w.q[n][0], s[n][b]);
     } else {
 #pragma unroll
       for (int st = 0; st < D / 64; st++) {
-        const u32x4 k = *(const u32x4 *)(p + (((st * 4 + g) ^ f) * 16));
+        const u32x4 k = *(const u32x4 *)(row + (((st * 4 + g) ^ f) * 16));
         const u32x4 k0 = widen8(F16{}, u32x2{k[0], k[1]}), k1 = widen8(F16{}, u32x2{k[2], k[3]});
 #pragma unroll
         for (int n = 0; n < NQ; n++) {
@@ -648,7 +655,6 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
       vf[b] = *(const f32x4 *)(vs + b * 16 + 4 * g);
     }
   }
-  u32x4 p[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; n++) {
     const int32_t gap = w.pos[n] - base - 4 * (int32_t)g;
@@ -706,6 +712,13 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
 #pragma unroll
     for (int i = 0; i < 4; i++) p[n][i] = pair(T{}, z[2 * i], z[2 * i + 1]);
   }
+}
+// Their values in LDS, times p.
+template <class T, int BITS, int D, int NQ, bool MASKED>
+__device__ __forceinline__ void gather_few(Few<T, BITS, D, NQ> &w, const u32x4 (&p)[NQ], const uint8_t *lv, int32_t base, uint32_t there,
+                                           int32_t window) {
+  typedef FewRows<BITS, D> R;
+  const uint32_t lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   auto value = [&](int d) -> u32x4 {  // 32 keys in the order of p, 16 of D
     if constexpr (BITS == 16) {
       const uint32_t r = 4 * g + l16 / 4;
@@ -720,147 +733,223 @@ __device__ __forceinline__ void add_few(Few<T, BITS, D, NQ> &w, const uint8_t *l
                              (__attribute__((address_space(3))) i32x2 *)(__attribute__((address_space(3))) void *)at)));
     }
   };
-  if constexpr (BITS == 16) {
-    if constexpr (MASKED) {  // as in add_keys
-      uint32_t most = 0;
+  bool odd = false;  // as in gather
+  if constexpr (BITS == 16 && MASKED) {
+    uint32_t most = 0;
 #pragma unroll
-      for (int d = 0; d < D / 16; d++) most = most_bits(value(d), most);
-      if (__ballot(joined(most) > finite_bits(T{}))) {
-#pragma unroll
-        for (int d = 0; d < D / 16; d++)
-#pragma unroll
-          for (int n = 0; n < NQ; n++) w.o[n][d] = mfma(T{}, finite_part(T{}, value(d)), p[n], w.o[n][d]);
-#pragma unroll 1
-        for (uint32_t e = 0; e < 32; e++) {
-          const uint32_t group = e >> 3, word = (e & 7) >> 1, at = 16 * ((e & 7) / 4) + 4 * group + (e & 3);
-          const uint32_t bits = g == group ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
-          const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
-#pragma unroll
-          for (int n = 0; n < NQ; n++) {
-            const bool seen = sees(w.pos[n] - base - (int32_t)at, window) && (there >> at & 1);
-#pragma unroll
-            for (int d = 0; d < D / 16; d++) {
-              const u32x4 v = value(d);
-              const f32x4 t = mfma(T{}, (v ^ finite_part(T{}, v)) & only, p[n] & only, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int r = 0; r < 4; r++) w.o[n][d][r] += seen ? t[r] : 0.f;
-            }
-          }
-        }
-        return;
-      }
+    for (int d = 0; d < D / 16; d++) {
+      most = most_bits(value(d), most);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    odd = __ballot(joined(most) > finite_bits(T{})) != 0;
   }
 #pragma unroll
   for (int d = 0; d < D / 16; d++) {
-    const u32x4 v = value(d);
+    u32x4 v = value(d);
+    if (odd) v = finite_part(T{}, v);
 #pragma unroll
     for (int n = 0; n < NQ; n++) w.o[n][d] = mfma(T{}, v, p[n], w.o[n][d]);
   }
+  if (odd) {
+#pragma unroll 1
+    for (uint32_t e = 0; e < 32; e++) {
+      const uint32_t group = e >> 3, word = (e & 7) >> 1, at = 16 * ((e & 7) / 4) + 4 * group + (e & 3);
+      const uint32_t bits = g == group ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+      const u32x4 only = {word == 0 ? bits : 0u, word == 1 ? bits : 0u, word == 2 ? bits : 0u, word == 3 ? bits : 0u};
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) {
+        const u32x4 v = value(d), rest = (v ^ finite_part(T{}, v)) & only;
+#pragma unroll
+        for (int n = 0; n < NQ; n++) {
+          const bool seen = sees(w.pos[n] - base - (int32_t)at, window) && (there >> at & 1);
+          const f32x4 t = mfma(T{}, rest, p[n] & only, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int r = 0; r < 4; r++) w.o[n][d][r] += seen ? t[r] : 0.f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
 }
+
+constexpr uint32_t kListed = 512;  // sequences
 
 template <class T, int BITS, int D, int NQ, int W>
 __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_few(const Pages c, const Sequences b, const Attend a) {
   typedef FewRows<BITS, D> R;
   constexpr int kTile = 32 * R::kBytes, kLoads = kTile / 1024, kRowsPer = 32 / kLoads, kRows = 16 * NQ;
   extern __shared__ __align__(1024) uint8_t lds[];  // [W][2][keys, values], then joined
-  __shared__ float scales[W][64], ms[W][kRows], ls[W][kRows];
+  __shared__ float scales[W][2][64], ms[W][kRows], ls[W][kRows];
+  __shared__ int32_t before[kListed + 1];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t *buf = lds + wave * (4 * kTile);
-  const uint64_t units = (uint64_t)b.count * c.heads * a.few_splits;
-  for (uint64_t id = blockIdx.x; id < units; id += gridDim.x) {
-    const uint32_t head = (uint32_t)(id % c.heads), s = (uint32_t)(id / c.heads % b.count), z = (uint32_t)(id / c.heads / b.count);
+  // Pieces of work: parts of sequences, for each key head.  Where a table of the parts that
+  // come before each sequence fits, a workgroup finds its pieces in it; otherwise every
+  // sequence has few_splits places, of which some are empty.
+  const bool listed = b.count <= kListed;
+  auto parts_of = [&](uint32_t s) -> int32_t {
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
-    if (s == 0 && z == 0) {
-      // rows of no sequence
-      const int32_t begin = sp.first, end = span_of(b, b.count - 1).last;
-      const uint32_t per = a.group * (D / 8);
-      const uint64_t all = ((uint64_t)begin + (b.tokens - end)) * per;
-      for (uint64_t i = threadIdx.x; i < all; i += 64 * W) {
-        const uint64_t t = i / per < (uint64_t)begin ? i / per : i / per - begin + end, e = i % per;
-        ((u32x4 *)(a.out + (t * a.heads + head * a.group) * D))[e] = u32x4{0, 0, 0, 0};
-        if (a.lse && e < a.group) a.lse[t * a.heads + head * a.group + e] = -__builtin_huge_valf();
+    if (rows == 0 || (!a.alone && rows > a.cap)) return 0;
+    const uint32_t count = rows < a.cap ? rows : a.cap;
+    const Cuts k = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window, kFewShift,
+                           a.few_splits, a.few_fill, kFewLeast, kFewChunk);
+    return k.count > 1 ? k.count : 1;
+  };
+  uint64_t units = (uint64_t)b.count * c.heads * a.few_splits;
+  if (listed) {
+    // places 1 .. count: parts up to and with a sequence's
+    if (threadIdx.x == 0) before[0] = 0;
+    int32_t so_far = 0;
+    for (uint32_t s0 = 0; s0 < b.count; s0 += 64) {
+      if (wave == 0) {
+        int32_t n = s0 + lane < b.count ? parts_of(s0 + lane) : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int32_t o = __shfl_up(n, d);
+          if ((int)lane >= d) n += o;
+        }
+        if (s0 + lane < b.count) before[s0 + lane + 1] = so_far + n;
+        so_far += __builtin_amdgcn_readlane(n, 63);
       }
     }
+    __syncthreads();
+    units = (uint64_t)(uint32_t)before[b.count] * c.heads;
+  }
+  if (blockIdx.x < c.heads) {
+    // rows of no sequence
+    const int32_t begin = span_of(b, 0).first, end = span_of(b, b.count - 1).last;
+    const uint32_t per = a.group * (D / 8), head = blockIdx.x;
+    const uint64_t all = ((uint64_t)begin + (b.tokens - end)) * per;
+    for (uint64_t i = threadIdx.x; i < all; i += 64 * W) {
+      const uint64_t t = i / per < (uint64_t)begin ? i / per : i / per - begin + end, e = i % per;
+      ((u32x4 *)(a.out + (t * a.heads + head * a.group) * D))[e] = u32x4{0, 0, 0, 0};
+      if (a.lse && e < a.group) a.lse[t * a.heads + head * a.group + e] = -__builtin_huge_valf();
+    }
+  }
+  for (uint64_t id = blockIdx.x; id < units; id += gridDim.x) {
+    const uint32_t head = (uint32_t)(id % c.heads);
+    uint32_t s, z;
+    if (listed) {
+      const int32_t j = (int32_t)(id / c.heads);
+      s = starts_up_to(before, b.count + 1, j) - 1;
+      z = (uint32_t)(j - before[s]);
+    } else {
+      s = (uint32_t)(id / c.heads % b.count);
+      z = (uint32_t)(id / c.heads / b.count);
+    }
+    s = same(s);
+    z = same(z);
+    const Span sp = span_of(b, s);
+    const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     if (rows == 0 || (!a.alone && rows > a.cap)) continue;
     const int32_t *table = b.tables + s * b.stride;
     for (uint32_t r0 = 0; r0 < rows; r0 += r0 ? kRows : a.cap) {
       if (r0 && z) break;  // rows behind the capacity are not split
       const uint32_t most = r0 ? kRows : a.cap, count = rows - r0 < most ? rows - r0 : most;
       const int32_t first = sp.first + (int32_t)(r0 / a.group), last = sp.first + (int32_t)((r0 + count - 1) / a.group);
-      const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kFewShift, r0 ? 1 : a.few_splits, kFewLeast);
+      const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kFewShift, r0 ? 1 : a.few_splits, a.few_fill,
+                              kFewLeast, kFewChunk);
       if (z >= (uint32_t)k.count && z) break;
       const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
-      // a tile's pages and scales come a tile ahead of its rows
-      int32_t page = 0;
-      uint32_t there = 0, next = 0;
-      float scale = 0.f;
+      // Pages (16 keys lie in one) come a tile ahead, by scalar loads; all other loads go to
+      // LDS, so that the counts waited for below are those of the rows in flight.  A tile's
+      // keys are asked for as soon as those of two tiles before have been multiplied, its
+      // values likewise: up to two tiles are in flight with two buffers.
+      constexpr int kWait = kLoads + (BITS == 8);  // loads of a tile's keys and scales
+      struct Table { int32_t of[2]; } page = {}, page_then = {};
+      uint32_t there = 0, next = 0, then = 0;  // the keys that exist: of tile t, t + W, t + 2 W
+      const auto *entries = (const __attribute__((address_space(4))) int32_t *)table;
       auto look = [&](int32_t t) {
-        if (t < t1) page = page_at(c, table, t * 32 + (int32_t)(lane & 31), k.stop);
+        if (t >= t1) return;
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const int32_t pos = t * 32 + 16 * j;
+          page.of[j] = entries[(uint32_t)(pos < k.stop ? pos : k.stop - 1) >> c.shift];
+        }
       };
-      auto known = [&](int32_t t) { return (uint32_t)__ballot(t * 32 + (int32_t)(lane & 31) < k.stop && (uint32_t)page < c.pages); };
+      auto known = [&](int32_t t) {
+        const uint32_t all = ((uint32_t)page.of[0] < c.pages ? 0xFFFFu : 0u) | ((uint32_t)page.of[1] < c.pages ? 0xFFFF0000u : 0u);
+        const int32_t left = k.stop - t * 32;
+        return left < 32 ? all & ((1u << left) - 1) : all;
+      };
       const uint32_t in_load = lane / R::kChunks, chunk = lane % R::kChunks;
-      auto request = [&](int32_t t, uint32_t dst, uint32_t in) {  // in: the keys that exist
-        if (in == 0xFFFFFFFFu && kRowsPer <= 16) {
+      const uint32_t head_bytes = (uint32_t)R::kBytes << c.shift, page_bytes = head_bytes * c.heads, row_mask = (1u << c.shift) - 1;
+      const uint32_t at_lds = lds_address(buf);
+      auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint32_t all, bool values, uint32_t dst) {
+        const uint8_t *mine = pool + (uint64_t)head * head_bytes;
 #pragma unroll
-          for (int i = 0; i < kLoads; i++) {
-            // (rows of a load lie in one page)
-            const uint32_t row = i * kRowsPer + in_load;
-            const uint64_t at = pool_row(c, (uint32_t)__builtin_amdgcn_readlane(page, i * kRowsPer), head, (uint32_t)(t * 32 + i * kRowsPer)) *
-                                R::kBytes;
-            ask(c.k + at, in_load * R::kBytes + (chunk ^ R::key_swap(row)) * 16, dst + i * 1024);
-            ask(c.v + at, in_load * R::kBytes + (chunk ^ R::value_swap(row)) * 16, dst + kTile + i * 1024);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kLoads; i++) {
-            const uint32_t row = i * kRowsPer + in_load;
-            const uint64_t at = pool_row(c, (uint32_t)__shfl(page, (int)row), head, (uint32_t)(t * 32) + row) * R::kBytes;
-            const uint8_t *none = (const uint8_t *)&g_zero16;
-            const bool is = in >> row & 1;
-            ask(is ? c.k + at + (chunk ^ R::key_swap(row)) * 16 : none, dst + i * 1024);
-            ask(is ? c.v + at + (chunk ^ R::value_swap(row)) * 16 : none, dst + kTile + i * 1024);
+        for (int i = 0; i < kLoads; i++) {
+          const uint32_t row = i * kRowsPer + in_load, swap = values ? R::value_swap(row) : R::key_swap(row);
+          const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
+          if (all == 0xFFFFFFFFu && kRowsPer <= 16) {  // (rows of a load lie in one page)
+            ask(mine + ((uint64_t)(uint32_t)pages.of[i * kRowsPer / 16] * page_bytes + (((uint32_t)(t * 32) + i * kRowsPer) & row_mask) * R::kBytes),
+                off, dst + i * 1024);
+          } else {
+            const uint8_t *src = mine + ((uint64_t)(uint32_t)(row < 16 ? pages.of[0] : pages.of[1]) * page_bytes +
+                                         (((uint32_t)(t * 32) + row) & row_mask) * R::kBytes + (chunk ^ swap) * 16);
+            ask(all >> row & 1 ? src : (const uint8_t *)&g_zero16, dst + i * 1024);
           }
         }
+      };
+      auto request_keys = [&](int32_t t) -> uint32_t {  // and scales
+        if (t >= t1) return 0;
+        const uint32_t all = known(t), odd = ((t - t0) / W) & 1;
+        bring(c.k, t, page, all, false, at_lds + odd * (2 * kTile));
         if constexpr (BITS == 8) {
-          scale = 0.f;
-          if (in >> (lane & 31) & 1)
-            scale = (lane < 32 ? c.k_scales : c.v_scales)[pool_row(c, (uint32_t)page, head, (uint32_t)(t * 32) + (lane & 31))];
+          const uint32_t row = lane & 31;
+          const uint64_t at = (((uint64_t)(uint32_t)(row < 16 ? page.of[0] : page.of[1]) * c.heads + head) << c.shift) + (((uint32_t)(t * 32) + row) & row_mask);
+          ask_word(all >> row & 1 ? (const uint8_t *)((lane < 32 ? c.k_scales : c.v_scales) + at) : (const uint8_t *)&g_zero16,
+                   lds_address(scales[wave][odd]));
         }
+        page_then = page;
+        look(t + W);
+        return all;
+      };
+      auto request_values = [&](int32_t t, uint32_t all) {
+        if (t < t1) bring(c.v, t, page_then, all, true, at_lds + (((t - t0) / W) & 1) * (2 * kTile) + kTile);
       };
       const int32_t mine0 = t0 + (int32_t)wave;
       look(mine0);
       Few<T, BITS, D, NQ> w;
-      if (mine0 < t1) {
-        there = known(mine0);
-        request(mine0, lds_address(buf), there);
-        look(mine0 + W);
-      }
+      there = request_keys(mine0);
+      request_values(mine0, there);
 #pragma unroll
       for (int n = 0; n < NQ; n++) {
         const uint32_t r = n * 16 + (lane & 15), mine = r0 + (r < count ? r : count - 1);
         const int32_t token = sp.first + (int32_t)(mine / a.group);
         w.init(n, a.q + token * a.q_token + (head * a.group + mine % a.group) * a.q_head, token + sp.ahead, a.c);
       }
+      next = request_keys(mine0 + W);
+      request_values(mine0 + W, next);
       for (int32_t t = mine0; t < t1; t += W) {
-        const uint32_t odd = ((t - mine0) / W) & 1;
-        wait_but<0>();
-        if constexpr (BITS == 8) scales[wave][lane] = lane < 32 ? scale * a.c : scale;
-        if (t + W < t1) {
-          next = known(t + W);
-          request(t + W, lds_address(buf) + (odd ^ 1) * (2 * kTile), next);
-          look(t + 2 * W);
-        }
+        const uint32_t odd = ((t - t0) / W) & 1;
         const bool whole = there == 0xFFFFFFFFu && t * 32 + 31 <= first + sp.ahead && last + sp.ahead - t * 32 < a.window;
         const uint8_t *p = buf + odd * (2 * kTile);
+        u32x4 weights[NQ];
+        // behind the keys of t: its values, and all of t + W
+        if (t + W < t1) wait_but<kLoads + kWait + kLoads>();
+        else wait_but<kLoads>();
         if (whole) {
-          add_few<T, BITS, D, NQ, false>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, a.window);
+          weigh_few<T, BITS, D, NQ, false>(w, weights, p, scales[wave][odd], scales[wave][odd] + 32, t * 32, there, a.window);
         } else {
-          add_few<T, BITS, D, NQ, true>(w, p, p + kTile, scales[wave], scales[wave] + 32, t * 32, there, a.window);
+          weigh_few<T, BITS, D, NQ, true>(w, weights, p, scales[wave][odd], scales[wave][odd] + 32, t * 32, there, a.window);
         }
+        wait_reads();  // their place is asked for again
+        then = request_keys(t + 2 * W);
+        // behind the values of t: all of t + W, the keys of t + 2 W
+        if (t + 2 * W < t1) wait_but<kWait + kLoads + kWait>();
+        else if (t + W < t1) wait_but<kWait + kLoads>();
+        else wait_but<0>();
+        if (whole) {
+          gather_few<T, BITS, D, NQ, false>(w, weights, p + kTile, t * 32, there, a.window);
+        } else {
+          gather_few<T, BITS, D, NQ, true>(w, weights, p + kTile, t * 32, there, a.window);
+        }
+        wait_reads();
+        request_values(t + 2 * W, then);
         there = next;
-        wait_reads();  // the buffer is asked for again
+        next = then;
       }
       // the waves' sums: [W][16 NQ][D] in place of the tiles, 16-byte chunks exchanged
       __syncthreads();
@@ -928,7 +1017,7 @@ __global__ __launch_bounds__(256) void join_few(const Pages c, const Sequences b
     if (r >= rows || (!a.alone && rows > a.cap)) continue;
     const uint32_t count = rows < a.cap ? rows : a.cap;
     const int32_t parts = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window,
-                                  kFewShift, a.few_splits, kFewLeast).count;
+                                  kFewShift, a.few_splits, a.few_fill, kFewLeast, kFewChunk).count;
     if (parts <= 1) continue;
     float m = -__builtin_huge_valf();
 #pragma unroll 4
@@ -1018,7 +1107,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     if (rows <= a.cap || r0 >= (int64_t)rows) continue;
     const uint32_t count = rows - (uint32_t)r0 < kRows ? rows - (uint32_t)r0 : kRows;
     const int32_t first = sp.first + (int32_t)((uint32_t)r0 / a.group), last = sp.first + (int32_t)(((uint32_t)r0 + count - 1) / a.group);
-    const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, kTileLeast);
+    const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, a.tile_splits, kTileLeast, kTileChunk);
     if (z && z >= (uint32_t)k.count) continue;
     const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
     const int32_t *table = b.tables + s * b.stride;
@@ -1059,7 +1148,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
       return left < 64 ? all & ((1ull << left) - 1) : all;
     };
     // this head's part of a page, and where it begins
-    const uint32_t part = (uint32_t)R::kBytes << c.shift, page_bytes = part * c.heads, row_mask = (1u << c.shift) - 1;
+    const uint32_t head_bytes = (uint32_t)R::kBytes << c.shift, page_bytes = head_bytes * c.heads, row_mask = (1u << c.shift) - 1;
     auto page_of = [&](const Table &t, uint32_t j) { return (uint32_t)(one || j == 0 ? t.of[0] : j == 1 ? t.of[1] : j == 2 ? t.of[2] : t.of[3]); };
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float scale = 0.f;
@@ -1068,7 +1157,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     static_assert(kLoads >= 1 && NW * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
     auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, uint32_t swap, uint32_t dst) {
       const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
-      const uint8_t *mine = pool + (uint64_t)head * part;
+      const uint8_t *mine = pool + (uint64_t)head * head_bytes;
       if (one && all == ~0ull) {
         const uint8_t *src = mine + ((uint64_t)(uint32_t)pages.of[0] * page_bytes + (((uint32_t)(t * 64) & row_mask) + wave * kRowsPer) * R::kBytes);
 #pragma unroll
@@ -1274,7 +1363,7 @@ __global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences
       const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~(a.tile_rows - 1);
       const uint32_t count = rows - r0 < a.tile_rows ? rows - r0 : a.tile_rows;
       parts = cuts_of(c, b, sp.first + (int32_t)(r0 / a.group) + sp.ahead, sp.first + (int32_t)((r0 + count - 1) / a.group) + sp.ahead,
-                      sp.length, a.window, kTileShift, a.tile_splits, kTileLeast).count;
+                      sp.length, a.window, kTileShift, a.tile_splits, a.tile_splits, kTileLeast, kTileChunk).count;
     }
     if (parts <= 1) continue;
     float m = -__builtin_huge_valf();
@@ -1317,15 +1406,16 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
   p.tile = hint * a.group > rows;
   a.alone = !p.tile;
   a.cap = (uint32_t)((hint < fit ? hint : fit) * a.group);
-  a.few_splits = a.tile_splits = 1;
+  a.few_fill = a.few_splits = a.tile_splits = 1;
   // the most keys that a sequence's rows may see
   const uint64_t held = (uint64_t)batch->width * cache->page_size;
   const uint64_t seen = held < (uint64_t)a.window + hint ? held : (uint64_t)a.window + hint;
   if (a.cap) {
-    // a round or two of workgroups, and no part longer than 2048 keys
+    // a round or two of workgroups, and parts of one length where sequences are longer
     const uint64_t units = seqs * kv, most = (seen + 31) / 32 + 1, slots = cache->bits == 16 ? 512 : 1024;
     uint64_t n = (slots + units - 1) / units;
-    if (n < (most + 63) / 64) n = (most + 63) / 64;
+    a.few_fill = (uint32_t)n;
+    if (n < (most + kFewChunk - 1) / kFewChunk) n = (most + kFewChunk - 1) / kFewChunk;
     if (n > (most + kFewLeast - 1) / kFewLeast) n = (most + kFewLeast - 1) / kFewLeast;
     const uint64_t part = units * a.cap * (dim + 2) * 4;
     if (n * part > kMostParts) n = kMostParts / part;
@@ -1364,8 +1454,28 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
   return p;
 }
 
-constexpr uint32_t kDeclared = 4096;  // LDS that the kernels declare beside what a launch gives, at most
+constexpr uint32_t kDeclared = 8192;  // LDS that the kernels declare beside what a launch gives, at most
 uint32_t grid_of(uint64_t units) { return (uint32_t)(units < (1u << 20) ? units : 1u << 20); }
+
+// Workgroups of a kernel that the current device holds at once (asked once a kernel and device); at least 256.
+uint64_t resident(const void *fn, int threads, uint32_t lds) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void *>, uint64_t> known;
+  int dev = 0, cus = 0, per = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    uint64_t &n = known[{dev, fn}];
+    if (!n) {
+      if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) cus = 256;
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, lds) != hipSuccess || per < 1) per = 1;
+      n = (uint64_t)cus * per < 256 ? 256 : (uint64_t)cus * per;
+    }
+    return n;
+  } catch (...) {  // nothing throws across the C entries
+    return 256;
+  }
+}
 
 template <class T, int BITS, int D, int NQ>
 hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {
@@ -1374,8 +1484,10 @@ hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream
   static_assert(lds >= W * 16 * NQ * D * 4, "the waves' sums lie in the tiles' place");
   const hipError_t e = allow_lds((const void *)attend_few<T, BITS, D, NQ, W>, lds, kDeclared);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.few_splits)), dim3(64 * W), lds, s, c,
-                     b, p.a);
+  // as many workgroups as the chip holds, each with piece after piece
+  const uint64_t pieces = (uint64_t)b.count * c.heads * p.a.few_splits, held = resident((const void *)attend_few<T, BITS, D, NQ, W>, 64 * W, lds);
+  hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3((uint32_t)(pieces < held || b.count > kListed ? grid_of(pieces) : held)), dim3(64 * W),
+                     lds, s, c, b, p.a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess || p.a.few_splits == 1) return st;
   hipLaunchKernelGGL((join_few<T, D>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.cap)), dim3(256), 0, s, c, b, p.a);
