@@ -103,22 +103,23 @@ struct Attend {
   int32_t window;            // INT32_MAX: none
   float c;                   // scale times log2 e
   // few rows
-  uint32_t cap, few_fill, few_splits;
+  uint32_t cap;
   uint32_t alone;            // no attend_tile follows: sequences of more rows are taken too
-  float *few_o, *few_ml;     // [splits][seqs][kv heads][cap][D], [..][2]
+  uint32_t few_splits;       // whether rows may be split
+  float *few_o, *few_ml;     // [workgroups + seqs * kv heads][cap][D], [..][2]
+  uint32_t *few_parts;       // [seqs][kv heads][2]: parts, and the first one's place in few_o
   // tiles
   uint32_t tiles, tile_rows, tile_splits;
   float *tile_o, *tile_ml;   // [splits][tokens][heads][D], [..][2]
 };
 
 // The keys that rows at positions first .. last see, in units of 2^shift, cut into
-// `count` parts of `per`: `fill` parts of `least` units or more, or parts of `chunk` units where
-// that is more of them, and at most `splits`.
+// `count` parts of `per`: `splits` of them, of `least` units or more.
 struct Cuts {
   int32_t begin, end, per, count, stop;  // stop: the first position that is not seen
 };
 __device__ __forceinline__ Cuts cuts_of(const Pages &c, const Sequences &b, int32_t first, int32_t last, int32_t length,
-                                        int32_t window, int shift, uint32_t splits, uint32_t fill, int32_t least, int32_t chunk) {
+                                        int32_t window, int shift, uint32_t splits, int32_t least) {
   Cuts k;
   const uint64_t held = (uint64_t)b.width << c.shift;
   k.stop = last + 1 < length ? last + 1 : length;
@@ -128,15 +129,13 @@ __device__ __forceinline__ Cuts cuts_of(const Pages &c, const Sequences &b, int3
   k.begin = from >> shift;
   k.end = k.stop > from ? (k.stop + (1 << shift) - 1) >> shift : k.begin;
   const int32_t n = k.end - k.begin;
-  int32_t want = (n + least - 1) / least, pieces = (n + chunk - 1) / chunk;
-  want = want < (int32_t)fill ? want : (int32_t)fill;
-  want = want > pieces ? want : pieces;
+  int32_t want = (n + least - 1) / least;
   want = want < (int32_t)splits ? want : (int32_t)splits;
   k.per = want > 0 ? (n + want - 1) / want : 0;
   k.count = k.per > 0 ? (n + k.per - 1) / k.per : 0;
   return k;
 }
-constexpr int kFewShift = 5, kFewLeast = 4, kFewChunk = 32, kTileShift = 6, kTileLeast = 8, kTileChunk = 1 << 30;
+constexpr int kFewShift = 5, kFewLeast = 4, kTileShift = 6, kTileLeast = 8;
 
 // What codes of 8 bits become to multiply q: FP16, which is made of bytes with half of the
 // instructions that BF16 takes, for a lifted q (lift_q).
@@ -773,6 +772,19 @@ __device__ __forceinline__ void gather_few(Few<T, BITS, D, NQ> &w, const u32x4 (
 }
 
 constexpr uint32_t kListed = 512;  // sequences
+constexpr int kFewCost = 12;
+// Sums of the lanes up to each: within rows of 16, then rows before, then halves.
+__device__ __forceinline__ uint32_t sums_of_wave(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 15, 15, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 15, 15, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 15, 15, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 15, 15, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 10, 15, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 12, 15, false);
+  return v;
+}
+// a / b, mostly of small numbers.
+__device__ __forceinline__ int64_t ratio(int64_t a, uint32_t b) { return a >> 32 ? a / b : (int64_t)((uint32_t)a / b); }
 
 template <class T, int BITS, int D, int NQ, int W>
 __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_few(const Pages c, const Sequences b, const Attend a) {
@@ -780,41 +792,39 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
   constexpr int kTile = 32 * R::kBytes, kLoads = kTile / 1024, kRowsPer = 32 / kLoads, kRows = 16 * NQ;
   extern __shared__ __align__(1024) uint8_t lds[];  // [W][2][keys, values], then joined
   __shared__ float scales[W][2][64], ms[W][kRows], ls[W][kRows];
-  __shared__ int32_t before[kListed + 1];
+  __shared__ int64_t before[kListed + 1];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t *buf = lds + wave * (4 * kTile);
-  // Pieces of work: parts of sequences, for each key head.  Where a table of the parts that
-  // come before each sequence fits, a workgroup finds its pieces in it; otherwise every
-  // sequence has few_splits places, of which some are empty.
-  const bool listed = b.count <= kListed;
-  auto parts_of = [&](uint32_t s) -> int32_t {
+  // The work is the tiles of all sequences, head by head, in one row: each workgroup has an
+  // equal run of it, which ends in one sequence and goes on in the next, so parts are
+  // as long as they can be and all workgroups end together.  A head's keys count for kFewCost
+  // tiles more than they are, what beginning and ending them takes; they are split where
+  // a run ends.  (More than kListed sequences are not split: a piece for each of their heads.)
+  const bool listed = a.few_splits > 1;
+  auto tiles_of = [&](uint32_t s) -> uint32_t {
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     if (rows == 0 || (!a.alone && rows > a.cap)) return 0;
     const uint32_t count = rows < a.cap ? rows : a.cap;
-    const Cuts k = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window, kFewShift,
-                           a.few_splits, a.few_fill, kFewLeast, kFewChunk);
-    return k.count > 1 ? k.count : 1;
+    const Cuts k = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window, kFewShift, 1, 1);
+    return (k.end > k.begin ? (uint32_t)(k.end - k.begin) : 1) + kFewCost;  // (rows that see nothing are cleared)
   };
-  uint64_t units = (uint64_t)b.count * c.heads * a.few_splits;
+  int64_t run = 1, end = (int64_t)b.count * c.heads;  // of places
   if (listed) {
-    // places 1 .. count: parts up to and with a sequence's
-    if (threadIdx.x == 0) before[0] = 0;
-    int32_t so_far = 0;
+    // places 1 .. count: tiles up to and with a sequence's
+    int64_t so_far = 0;
     for (uint32_t s0 = 0; s0 < b.count; s0 += 64) {
-      if (wave == 0) {
-        int32_t n = s0 + lane < b.count ? parts_of(s0 + lane) : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int32_t o = __shfl_up(n, d);
-          if ((int)lane >= d) n += o;
-        }
-        if (s0 + lane < b.count) before[s0 + lane + 1] = so_far + n;
-        so_far += __builtin_amdgcn_readlane(n, 63);
-      }
+      if (wave != 0) break;
+      // (64 times 2^25 tiles of a sequence fit)
+      const uint32_t n = sums_of_wave(s0 + lane < b.count ? tiles_of(s0 + lane) : 0);
+      if (s0 + lane < b.count) before[s0 + lane + 1] = so_far + n;
+      so_far += (uint32_t)__builtin_amdgcn_readlane(n, 63);
     }
+    if (threadIdx.x == 0) before[0] = 0;
     __syncthreads();
-    units = (uint64_t)(uint32_t)before[b.count] * c.heads;
+    end = before[b.count] * c.heads;
+    run = ratio(end + gridDim.x - 1, gridDim.x);
+    run = run < kFewLeast ? kFewLeast : run;
   }
   if (blockIdx.x < c.heads) {
     // rows of no sequence
@@ -827,31 +837,40 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
       if (a.lse && e < a.group) a.lse[t * a.heads + head * a.group + e] = -__builtin_huge_valf();
     }
   }
-  for (uint64_t id = blockIdx.x; id < units; id += gridDim.x) {
-    const uint32_t head = (uint32_t)(id % c.heads);
-    uint32_t s, z;
+  const int64_t last_place = listed ? (blockIdx.x + 1) * run < end ? (blockIdx.x + 1) * run : end : end;
+  for (int64_t place = blockIdx.x * run, taken = 0; place < last_place; place += listed ? taken : gridDim.x) {
+    uint32_t s, head, tile = 0, all_tiles = 0;
     if (listed) {
-      const int32_t j = (int32_t)(id / c.heads);
-      s = starts_up_to(before, b.count + 1, j) - 1;
-      z = (uint32_t)(j - before[s]);
+      s = same(starts_up_to(before, b.count + 1, ratio(place, c.heads)) - 1);
+      const uint32_t places = same((uint32_t)(before[s + 1] - before[s]));
+      const int64_t in = place - before[s] * c.heads;
+      head = same((uint32_t)ratio(in, places));
+      tile = same((uint32_t)(in - (int64_t)head * places));
+      all_tiles = places - kFewCost;
+      taken = places - tile < last_place - place ? places - tile : last_place - place;
+      if (tile >= all_tiles) continue;
     } else {
-      s = (uint32_t)(id / c.heads % b.count);
-      z = (uint32_t)(id / c.heads / b.count);
+      s = same((uint32_t)(place / c.heads));
+      head = same((uint32_t)(place % c.heads));
     }
-    s = same(s);
-    z = same(z);
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     if (rows == 0 || (!a.alone && rows > a.cap)) continue;
+    // whether this is all of the head's keys; its parts lie in workgroups' order
+    const bool direct = !listed || (tile == 0 && taken >= all_tiles);
+    const uint64_t slot = blockIdx.x + (uint64_t)s * c.heads + head;
+    if (listed && tile == 0 && threadIdx.x == 0) {
+      // (of those after the first, runs of `run` tiles each)
+      a.few_parts[((uint64_t)s * c.heads + head) * 2] = direct ? 1 : (uint32_t)((all_tiles - taken + run - 1) / run) + 1;
+      a.few_parts[((uint64_t)s * c.heads + head) * 2 + 1] = (uint32_t)slot;
+    }
     const int32_t *table = b.tables + s * b.stride;
     for (uint32_t r0 = 0; r0 < rows; r0 += r0 ? kRows : a.cap) {
-      if (r0 && z) break;  // rows behind the capacity are not split
+      if (r0 && tile) break;  // rows behind the capacity are not split
       const uint32_t most = r0 ? kRows : a.cap, count = rows - r0 < most ? rows - r0 : most;
       const int32_t first = sp.first + (int32_t)(r0 / a.group), last = sp.first + (int32_t)((r0 + count - 1) / a.group);
-      const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kFewShift, r0 ? 1 : a.few_splits, a.few_fill,
-                              kFewLeast, kFewChunk);
-      if (z >= (uint32_t)k.count && z) break;
-      const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
+      const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kFewShift, 1, 1);
+      const int32_t t0 = k.begin + (r0 ? 0 : (int32_t)tile), t1 = listed && !r0 && t0 + taken < k.end ? t0 + (int32_t)taken : k.end;
       // Pages (16 keys lie in one) come a tile ahead, by scalar loads; all other loads go to
       // LDS, so that the counts waited for below are those of the rows in flight.  A tile's
       // keys are asked for as soon as those of two tiles before have been multiplied, its
@@ -969,7 +988,6 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
         }
       }
       __syncthreads();
-      const bool direct = k.count <= 1;
       for (uint32_t i = threadIdx.x; i < count * (D / 4); i += 64 * W) {
         const uint32_t r = i / (D / 4), chunk = i % (D / 4);
         float m = ms[0][r];
@@ -986,11 +1004,11 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
         }
         const uint32_t row = r0 + r;
         const uint64_t to = (uint64_t)(sp.first + row / a.group) * a.heads + head * a.group + row % a.group;
-        if (direct) {
+        if (direct || r0) {
           store4(a.out + to * D + chunk * 4, T{}, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * (1.f / l));
           if (a.lse && chunk == 0) a.lse[to] = lse_of(m, l);
         } else {
-          const uint64_t at = (((uint64_t)z * b.count + s) * c.heads + head) * a.cap + row;
+          const uint64_t at = slot * a.cap + row;
           *(f32x4 *)(a.few_o + at * D + chunk * 4) = v;
           if (chunk == 0) *(f32x2 *)(a.few_ml + at * 2) = f32x2{m, l};
         }
@@ -1015,20 +1033,20 @@ __global__ __launch_bounds__(256) void join_few(const Pages c, const Sequences b
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     if (r >= rows || (!a.alone && rows > a.cap)) continue;
-    const uint32_t count = rows < a.cap ? rows : a.cap;
-    const int32_t parts = cuts_of(c, b, sp.first + sp.ahead, sp.first + (int32_t)((count - 1) / a.group) + sp.ahead, sp.length, a.window,
-                                  kFewShift, a.few_splits, a.few_fill, kFewLeast, kFewChunk).count;
+    const uint32_t *which = a.few_parts + ((uint64_t)s * c.heads + head) * 2;
+    const int32_t parts = (int32_t)which[0];
     if (parts <= 1) continue;
+    const uint64_t first = (uint64_t)which[1] * a.cap + r;  // the parts' rows lie cap apart
     float m = -__builtin_huge_valf();
 #pragma unroll 4
-    for (int32_t p = group; p < parts; p += kGroups) m = __builtin_fmaxf(m, a.few_ml[(p * all + row) * 2]);
+    for (int32_t p = group; p < parts; p += kGroups) m = __builtin_fmaxf(m, a.few_ml[(first + (uint64_t)p * a.cap) * 2]);
     float ref = m == -__builtin_huge_valf() ? 0.f : m, l = 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int32_t p = group; p < parts; p += kGroups) {
-      const f32x2 t = *(const f32x2 *)(a.few_ml + (p * all + row) * 2);
+      const f32x2 t = *(const f32x2 *)(a.few_ml + (first + (uint64_t)p * a.cap) * 2);
       const float f = exp2_of(t[0] - ref);
-      v += *(const f32x4 *)(a.few_o + (p * all + row) * D + chunk * 4) * f;
+      v += *(const f32x4 *)(a.few_o + (first + (uint64_t)p * a.cap) * D + chunk * 4) * f;
       l += t[1] * f;
     }
     vs[threadIdx.x] = v;
@@ -1107,7 +1125,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     if (rows <= a.cap || r0 >= (int64_t)rows) continue;
     const uint32_t count = rows - (uint32_t)r0 < kRows ? rows - (uint32_t)r0 : kRows;
     const int32_t first = sp.first + (int32_t)((uint32_t)r0 / a.group), last = sp.first + (int32_t)(((uint32_t)r0 + count - 1) / a.group);
-    const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, a.tile_splits, kTileLeast, kTileChunk);
+    const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, kTileLeast);
     if (z && z >= (uint32_t)k.count) continue;
     const int32_t t0 = k.begin + (int32_t)z * k.per, t1 = t0 + k.per < k.end ? t0 + k.per : k.end;
     const int32_t *table = b.tables + s * b.stride;
@@ -1363,7 +1381,7 @@ __global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences
       const uint32_t r = (uint32_t)(t - sp.first) * a.group + (uint32_t)(row % a.heads) % a.group, r0 = r & ~(a.tile_rows - 1);
       const uint32_t count = rows - r0 < a.tile_rows ? rows - r0 : a.tile_rows;
       parts = cuts_of(c, b, sp.first + (int32_t)(r0 / a.group) + sp.ahead, sp.first + (int32_t)((r0 + count - 1) / a.group) + sp.ahead,
-                      sp.length, a.window, kTileShift, a.tile_splits, a.tile_splits, kTileLeast, kTileChunk).count;
+                      sp.length, a.window, kTileShift, a.tile_splits, kTileLeast).count;
     }
     if (parts <= 1) continue;
     float m = -__builtin_huge_valf();
@@ -1389,9 +1407,10 @@ __global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences
 struct Plan {
   Attend a;
   bool tile;
-  uint64_t few_o, few_ml, tile_o, tile_ml, all;  // workspace offsets
+  uint64_t few_o, few_ml, few_parts, tile_o, tile_ml, all;  // workspace offsets
 };
-constexpr uint64_t kMostParts = 256u << 20;  // bytes of partial sums
+constexpr uint64_t kMostParts = 256u << 20;  // bytes of partial sums of tiles
+constexpr uint32_t kMostResident = 2048;     // workgroups of attend_few
 
 Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens, uint32_t heads, int64_t window) {
   Plan p = {};
@@ -1406,22 +1425,12 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
   p.tile = hint * a.group > rows;
   a.alone = !p.tile;
   a.cap = (uint32_t)((hint < fit ? hint : fit) * a.group);
-  a.few_fill = a.few_splits = a.tile_splits = 1;
+  a.few_splits = a.tile_splits = 1;
   // the most keys that a sequence's rows may see
   const uint64_t held = (uint64_t)batch->width * cache->page_size;
   const uint64_t seen = held < (uint64_t)a.window + hint ? held : (uint64_t)a.window + hint;
-  if (a.cap) {
-    // a round or two of workgroups, and parts of one length where sequences are longer
-    const uint64_t units = seqs * kv, most = (seen + 31) / 32 + 1, slots = cache->bits == 16 ? 512 : 1024;
-    uint64_t n = (slots + units - 1) / units;
-    a.few_fill = (uint32_t)n;
-    if (n < (most + kFewChunk - 1) / kFewChunk) n = (most + kFewChunk - 1) / kFewChunk;
-    if (n > (most + kFewLeast - 1) / kFewLeast) n = (most + kFewLeast - 1) / kFewLeast;
-    const uint64_t part = units * a.cap * (dim + 2) * 4;
-    if (n * part > kMostParts) n = kMostParts / part;
-    if (n > 512) n = 512;
-    a.few_splits = n < 1 ? 1 : (uint32_t)n;
-  }
+  // few rows are split where there is a table of their sequences, and keys for two parts
+  if (a.cap && seqs <= kListed && (seen + 31) / 32 + 1 > kFewLeast) a.few_splits = 2;
   if (p.tile) {
     // 256 rows to a tile where those fill the chip: half of the reads of keys and values
     const uint64_t all = tokens * a.group;
@@ -1437,11 +1446,14 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
   }
   uint64_t at = 0;
   if (a.few_splits > 1) {
-    const uint64_t rows = a.few_splits * seqs * kv * a.cap;
+    // every run's end makes a part more
+    const uint64_t rows = (kMostResident + seqs * kv) * a.cap;
     p.few_o = at;
     at += up(rows * dim * 4, 256);
     p.few_ml = at;
     at += up(rows * 8, 256);
+    p.few_parts = at;
+    at += up(seqs * kv * 8, 256);
   }
   if (a.tile_splits > 1) {
     const uint64_t rows = a.tile_splits * tokens * heads;
@@ -1457,19 +1469,21 @@ Plan plan_of(const df_cache *cache, const df_cache_batch *batch, uint64_t tokens
 constexpr uint32_t kDeclared = 8192;  // LDS that the kernels declare beside what a launch gives, at most
 uint32_t grid_of(uint64_t units) { return (uint32_t)(units < (1u << 20) ? units : 1u << 20); }
 
-// Workgroups of a kernel that the current device holds at once (asked once a kernel and device); at least 256.
-uint64_t resident(const void *fn, int threads, uint32_t lds) {
+// Workgroups of a kernel that the current device holds at once (asked once a kernel and device), 256 to
+// kMostResident.
+uint32_t resident(const void *fn, int threads, uint32_t lds) {
   static std::mutex mu;
-  static std::map<std::pair<int, const void *>, uint64_t> known;
+  static std::map<std::pair<int, const void *>, uint32_t> known;
   int dev = 0, cus = 0, per = 0;
   if (hipGetDevice(&dev) != hipSuccess) return 256;
   try {
     std::lock_guard<std::mutex> lk(mu);
-    uint64_t &n = known[{dev, fn}];
+    uint32_t &n = known[{dev, fn}];
     if (!n) {
       if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) cus = 256;
       if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, lds) != hipSuccess || per < 1) per = 1;
-      n = (uint64_t)cus * per < 256 ? 256 : (uint64_t)cus * per;
+      const uint32_t held = (uint32_t)cus * (uint32_t)per;
+      n = held < 256 ? 256 : held < kMostResident ? held : kMostResident;
     }
     return n;
   } catch (...) {  // nothing throws across the C entries
@@ -1484,10 +1498,9 @@ hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream
   static_assert(lds >= W * 16 * NQ * D * 4, "the waves' sums lie in the tiles' place");
   const hipError_t e = allow_lds((const void *)attend_few<T, BITS, D, NQ, W>, lds, kDeclared);
   if (e != hipSuccess) return e;
-  // as many workgroups as the chip holds, each with piece after piece
-  const uint64_t pieces = (uint64_t)b.count * c.heads * p.a.few_splits, held = resident((const void *)attend_few<T, BITS, D, NQ, W>, 64 * W, lds);
-  hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3((uint32_t)(pieces < held || b.count > kListed ? grid_of(pieces) : held)), dim3(64 * W),
-                     lds, s, c, b, p.a);
+  // as many workgroups as the chip holds
+  hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3(resident((const void *)attend_few<T, BITS, D, NQ, W>, 64 * W, lds)), dim3(64 * W), lds,
+                     s, c, b, p.a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess || p.a.few_splits == 1) return st;
   hipLaunchKernelGGL((join_few<T, D>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.cap)), dim3(256), 0, s, c, b, p.a);
@@ -1585,6 +1598,7 @@ df_status df_cached_attention(const df_cache *cache, const df_cache_batch *batch
   a.c = scale * 1.44269504088896341f;
   a.few_o = (float *)(ws + p.few_o);
   a.few_ml = (float *)(ws + p.few_ml);
+  a.few_parts = (uint32_t *)(ws + p.few_parts);
   a.tile_o = (float *)(ws + p.tile_o);
   a.tile_ml = (float *)(ws + p.tile_ml);
   const Pages c = pages_of(cache);

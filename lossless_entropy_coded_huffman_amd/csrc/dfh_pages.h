@@ -49,7 +49,8 @@ __device__ __forceinline__ Span span_of(const Sequences &b, uint32_t s) {
 
 // How many of starts[0 .. count] are at most t, by a whole wave: each round looks at 64
 // places at equal distances, so 64 sequences take one load, 4096 two.
-__device__ __forceinline__ uint32_t starts_up_to(const int32_t *starts, uint32_t count, int32_t t) {
+template <class I>
+__device__ __forceinline__ uint32_t starts_up_to(const I *starts, uint32_t count, I t) {
   const uint32_t lane = threadIdx.x & 63;
   uint32_t lo = 0, n = count;  // the answer lies in lo .. lo + n
   while (n) {
