@@ -167,7 +167,7 @@ __device__ __forceinline__ constexpr int key_of(int r) { return 8 * (r / 4) + r 
 
 // 16 bytes a lane from base + off (of each lane) to LDS address at + 16 lane.  The
 // compiler is not told of these loads: before a transposing read it would wait for all that it
-// knows of, the next tile's among them (4096 x 16384 x 32 heads: MEASURED).  A load
+// knows of, the next tile's among them (4096 x 16384 x 32 heads 1038 us, unknown 967).  A load
 // of this kind writes no register; what it writes in LDS is waited for by wait_but.
 __device__ __forceinline__ uint32_t same(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint64_t same(uint64_t v) { return (uint64_t)same((uint32_t)(v >> 32)) << 32 | same((uint32_t)v); }
@@ -454,7 +454,7 @@ __device__ __forceinline__ void gather(Wave<T, BITS, D> &w, const u32x4 (&p)[2],
 // hand, a slot to a product: in slots of the scores the first half of the exponentials, in those
 // of the sums the second half, which the later sums take, then the maximum; reads
 // run two slots ahead.  (Left to itself the compiler puts the parts one after the other:
-// 4096 x 16384 x 32 heads MEASURED.)
+// 4096 x 16384 x 32 heads 1101 us where this order took 967.)
 template <class T, int BITS, int D>
 __device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s, f32x16 &next, uint32_t lk, uint32_t lv, const float *vs,
                                            const float *next_ks, const float *next_vs) {
@@ -1205,13 +1205,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     };
     const uint32_t mine_row = wave * kRowsPer + in_load;
     // keys of tile t (and scales); returns those that exist
-    auto request_keys = [&](int32_t t) -> uint64_t {
+    auto request_keys = [&](int32_t t, u32x4 (&raw)[kRaw]) -> uint64_t {
       if (t >= t1) return 0;
       const uint64_t all = known(t);
       if constexpr (BITS == 16) {
         bring(c.k, t, page, all, R::key_swap(mine_row), lds_address(lds) + (uint32_t)(t - t0) % kKeys * kTile);
       } else {
-        fetch(c.k, t, page, all, raw_k);
+        fetch(c.k, t, page, all, raw);
         scale = 0.f;
         if (wave < 2 && (all >> lane & 1))
           scale = (wave ? c.v_scales : c.k_scales)[pool_row(c, page_of(page, lane / 16), head, (uint32_t)(t * 64) + lane)];
@@ -1222,16 +1222,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
       return all;
     };
     // values of tile t, whose keys were asked for last
-    auto request_values = [&](int32_t t) {
+    auto request_values = [&](int32_t t, u32x4 (&raw)[kRaw]) {
       if (t >= t1) return;
       if constexpr (BITS == 16) {
         bring(c.v, t, page_before, before, R::value_swap(mine_row), lds_address(lds) + (kKeys + ((t - t0) & 1)) * kTile);
       } else {
-        fetch(c.v, t, page_before, before, raw_v);
+        fetch(c.v, t, page_before, before, raw);
       }
     };
     // codes of 8 bits become 16-bit values on their way to LDS, once for all waves
-    auto spread = [&](int32_t t, const u32x4 (&raw)[kRaw], bool values) {
+    auto spread = [&](int32_t t, const u32x4 (&raw)[kRaw], float f, bool values) {
       if (t >= t1) return;
       uint8_t *dst = lds + ((values ? kKeys : 0) + ((t - t0) & 1)) * kTile;
 #pragma unroll
@@ -1245,24 +1245,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
           *(u32x4 *)(dst + to) = values ? widen8(T{}, codes) : widen8(K{}, codes);
         }
       }
-      if (!values && wave < 2) scales[(t - t0) % 3][wave * 64 + lane] = wave ? scale : scale * a.c;
+      if (!values && wave < 2) scales[(t - t0) % 3][wave * 64 + lane] = wave ? f : f * a.c;
     };
     f32x16 s0, s1;  // settled scores of the first, second 32 keys of a tile
     if (t0 < t1) {
       look(t0);
-      there[0] = request_keys(t0);
+      there[0] = request_keys(t0, raw_k);
       if constexpr (BITS == 16) {
-        request_values(t0);
-        there[1] = request_keys(t0 + 1);
+        request_values(t0, raw_v);
+        there[1] = request_keys(t0 + 1, raw_k);
         wait_but<0>();
       } else {
-        spread(t0, raw_k, false);
-        request_values(t0);
-        spread(t0, raw_v, true);
-        there[1] = request_keys(t0 + 1);
-        spread(t0 + 1, raw_k, false);
-        request_values(t0 + 1);
-        there[2] = request_keys(t0 + 2);
+        // (all loads of the first two tiles at once)
+        u32x4 raw_k1[kRaw], raw_v0[kRaw];
+        const float scale0 = scale;
+        request_values(t0, raw_v0);
+        there[1] = request_keys(t0 + 1, raw_k1);
+        const float scale1 = scale;
+        request_values(t0 + 1, raw_v);
+        spread(t0, raw_k, scale0, false);
+        spread(t0, raw_v0, 0.f, true);
+        there[2] = request_keys(t0 + 2, raw_k);
+        spread(t0 + 1, raw_k1, scale1, false);
       }
       __syncthreads();
       s0 = scores(w, lds_address(lds));
@@ -1284,12 +1288,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
       if constexpr (BITS == 16) {
         wait_but<0>();
         meet();
-        request_values(t + 1);
-        there[2] = request_keys(t + 2);
+        request_values(t + 1, raw_v);
+        there[2] = request_keys(t + 2, raw_k);
       } else {
         __syncthreads();
-        spread(t + 1, raw_v, true);
-        request_values(t + 2);
+        spread(t + 1, raw_v, 0.f, true);
+        request_values(t + 2, raw_v);
       }
       if constexpr (M) {
         s1 = scores(w, lk + 32 * R::kBytes);
@@ -1302,8 +1306,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
       if constexpr (BITS == 8) {
         // keys of t + 1 are there, those of t read by all
         __syncthreads();
-        spread(t + 2, raw_k, false);
-        there[3] = request_keys(t + 3);
+        spread(t + 2, raw_k, scale, false);
+        there[3] = request_keys(t + 3, raw_k);
       }
       if constexpr (M) {
         if (more) s0 = scores(w, next);

@@ -73,14 +73,14 @@ __device__ __forceinline__ int sum_of_wave(int v) {
   return v;
 }
 
-// Rows of x -> codes, scales and (where wanted) sums of codes.  THREADS to a row;
-// the row's first 4 chunks a thread stay in registers between the two passes.
-template <class T, int THREADS>
-__global__ __launch_bounds__(256) void quantise(const uint16_t *x, uint64_t xs, uint32_t m, uint32_t k, uint8_t *codes,
+// Rows of x -> codes, scales and (where wanted) sums of codes.  THREADS to a row, of a workgroup's
+// BLOCK; the row's first 4 chunks a thread stay in registers between the two passes.
+template <class T, int THREADS, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void quantise(const uint16_t *x, uint64_t xs, uint32_t m, uint32_t k, uint8_t *codes,
                                                 uint64_t cs, float *scales, int *sums) {
-  constexpr int kRows = 256 / THREADS, kKeep = 4;
-  __shared__ uint32_t tops[4];
-  __shared__ int totals[4];
+  constexpr int kRows = BLOCK / THREADS, kKeep = 4, kWaves = THREADS / 64;
+  __shared__ uint32_t tops[BLOCK / 64];
+  __shared__ int totals[BLOCK / 64];
   const uint32_t t = threadIdx.x % THREADS, chunks = k / 8;
   for (uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / THREADS; row < m; row += (uint64_t)gridDim.x * kRows) {
     const u32x4 *src = (const u32x4 *)(x + row * xs);
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void quantise(const uint16_t *x, uint64_t xs, 
       if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; i++) top = top > tops[i] ? top : tops[i];
+      for (int i = 0; i < kWaves; i++) top = top > tops[i] ? top : tops[i];
     }
     Quantiser q;
     q.init(T{}, top);
@@ -121,7 +121,9 @@ __global__ __launch_bounds__(256) void quantise(const uint16_t *x, uint64_t xs, 
       if (THREADS > 64) {
         if ((threadIdx.x & 63) == 0) totals[threadIdx.x >> 6] = sum;
         __syncthreads();
-        sum = totals[0] + totals[1] + totals[2] + totals[3];
+        sum = 0;
+#pragma unroll
+        for (int i = 0; i < kWaves; i++) sum += totals[i];
       }
       if (t == 0) sums[row] = sum;
     }
@@ -381,6 +383,16 @@ df_status matrix_of(const df_u8_matrix *m, U8 *w) {
 // Rows that u8_tokens takes: their codes have to fit in 60 KiB of LDS.
 bool tokens(uint64_t m, uint64_t k) { return m <= 4 && m * up(k, 1024) <= 61440; }
 
+// Tiles and splits of a product: cut_for's, but for few steps (k up to 2048, which cut_for would
+// split) where 64 x 64 tiles without splits are up to 4 to a CU: their sums need no second launch
+// (128 x 4096 x 1424 14.5 us against 19.4, 333 x 2047 x 1424 16.1 against 22.6; with more steps it
+// turns, 333 x 2047 x 4096 29.5 against 24.5, and with more tiles, 768 x 6144 x 2048 32.2
+// against 28.8).
+Cut cut_of(uint64_t m, uint64_t n, uint64_t k) {
+  if (m > 64 && k <= 2048 && up(m, 64) / 64 * (up(n, 64) / 64) <= 1024) return Cut{2, 1, 0.0};
+  return cut_for(m, n, k / 2, true);
+}
+
 // The workspace of a product of more rows.
 struct Space {
   uint64_t codes, scales, sums, planes, all;  // offsets
@@ -391,7 +403,7 @@ Space space_of(uint64_t m, uint64_t n, uint64_t k, bool floats) {
   s.scales = floats ? up(m * k, 256) : 0;
   s.sums = s.scales + (floats ? up(m * 4, 256) : 0);
   s.planes = s.sums + up(m * 4, 256);
-  const Cut c = cut_for(m, n, k / 2, true);
+  const Cut c = cut_of(m, n, k);
   s.all = s.planes + (c.splits > 1 ? 4ull * c.splits * m * up(n, 4) : 0);
   return s;
 }
@@ -399,9 +411,14 @@ Space space_of(uint64_t m, uint64_t n, uint64_t k, bool floats) {
 template <class T>
 hipError_t quantise_rows(const uint16_t *x, uint64_t xs, uint32_t m, uint32_t k, uint8_t *codes, float *scales, int *sums,
                          hipStream_t s) {
+  // a wave to a short row, and 16 to one that the registers of 4 do not hold: all its loads are
+  // in flight at once (23 x 14336 3.9 us, 4 waves 4.7; 1024 x 14336 10.2 and 10.3; shorter rows
+  // wait for one another instead, 2048 x 4096 11.8 us against 7.1)
+  const bool wide = k > 8192;
   const uint32_t per = k <= 2048 ? 4 : 1, blocks = (m + per - 1) / per;
-  hipLaunchKernelGGL((k <= 2048 ? quantise<T, 64> : quantise<T, 256>), dim3(blocks < 1u << 20 ? blocks : 1u << 20),
-                     dim3(256), 0, s, x, xs, m, k, codes, (uint64_t)k, scales, sums);
+  hipLaunchKernelGGL((wide ? quantise<T, 1024, 1024> : k <= 2048 ? quantise<T, 64, 256> : quantise<T, 256, 256>),
+                     dim3(blocks < 1u << 20 ? blocks : 1u << 20), dim3(wide ? 1024 : 256), 0, s, x, xs, m, k, codes,
+                     (uint64_t)k, scales, sums);
   return hipGetLastError();
 }
 
@@ -446,7 +463,7 @@ df_status linear(const U8 &w, Rows x, uint32_t m, uint16_t *y, uint8_t *ws, hipS
     if (hipGetLastError() != hipSuccess) return DF_ERR_HIP;
   }
   const Gemm g = {(const uint16_t *)codes, (const uint16_t *)w.codes, stride / 2, w.k / 2, m, w.n, w.k / 2, 0, 0, 0, 0};
-  const Cut c = cut_for(m, w.n, w.k / 2, true);
+  const Cut c = cut_of(m, w.n, w.k);
   if (c.splits <= 1)
     return product<I8, false, false>(g, EpiU8<T>{w, scales, sums, y}, c.shape, 1, s) == hipSuccess ? DF_OK : DF_ERR_HIP;
   const uint32_t ld = (uint32_t)up(w.n, 4);

@@ -115,6 +115,32 @@ def test_codes_of_hard_rows(torch, k, dtype):
     assert bool(((s.cpu().double() - xs).abs() <= xs * E + 2.0 ** -150).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_codes_at_every_exponent(torch, dtype):
+    # rows whose largest value has each exponent that the type has, subnormals' too
+    dt = types(torch)[dtype]
+    low, high = (-24, 15) if dtype == "fp16" else (-133, 127)
+    e = torch.arange(low, high + 1, dtype=torch.float64)
+    g = torch.Generator().manual_seed(8)
+    part = torch.rand(len(e), 96, generator=g).double() * 2 - 1
+    part[:, 5] = 1
+    x = (part * torch.exp2(e)[:, None]).to(dt)
+    codes, xs = quantised(torch, x)
+    c, sc = dfh.quantize_rows(x.cuda())
+    assert torch.equal(c.cpu().double(), codes)
+    assert bool(((sc.cpu().double() - xs).abs() <= xs * E + 2.0 ** -150).all())
+    # few rows are quantised by the product itself
+    w = dfh.U8Matrix(torch.full((96, 96), 128, dtype=torch.uint8).cuda() + torch.eye(96, dtype=torch.uint8).cuda(),
+                     torch.ones(96).cuda(), None, cols=96)
+    for i in range(0, len(e), 4):
+        y = dfh.linear_u8(x[i:i + 4].cuda(), w)
+        tiny = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
+        ref = codes[i:i + 4] * xs[i:i + 4, None]
+        u = torch.finfo(dt).eps / 2
+        near = ref.abs() * ((1 + 5 * E) * (1 + u) - 1) + tiny + 127 * 2.0 ** -150
+        assert bool(((y.double().cpu() - ref).abs() <= near).all())
+
+
 @pytest.mark.parametrize("m", [1, 3, 40])
 def test_rows_that_are_not_finite(torch, m):
     # each spoils its own row alone
