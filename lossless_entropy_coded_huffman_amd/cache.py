@@ -108,6 +108,22 @@ class CacheBatch:
     def _tensors(self):
         return (self.tables, self.lengths, self.starts)
 
+    def positions(self, tokens: int) -> torch.Tensor:
+        """int64 [tokens]: the position of each row of the step's tensors in its
+        sequence, -1 for rows of no sequence; plain torch operations on the current
+        stream."""
+        return _positions(self.lengths, self.starts, int(tokens))
+
+
+def _positions(lengths: torch.Tensor, starts: torch.Tensor, tokens: int) -> torch.Tensor:
+    row = torch.arange(tokens, dtype=torch.int32, device=starts.device)
+    if not len(lengths):
+        return torch.full_like(row, -1, dtype=torch.int64)
+    after = torch.searchsorted(starts[1:], row, right=True)
+    seq = after.clamp(max=len(lengths) - 1)
+    at = lengths[seq].long() - starts[1:][seq].long() + row
+    return torch.where((row < starts[0]) | (row >= starts[-1]), -1, at).clamp(min=-1)
+
 
 def _heads16(t: torch.Tensor) -> torch.Tensor:
     """t [tokens, heads, dim] with unit stride in dim, other strides that are multiples
@@ -205,7 +221,8 @@ def cached_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, scal
     _new_tokens(q, cache, batch, "q", None)
     tokens, heads, dim = q.shape
     if heads < 1 or heads % cache.kv_heads or heads // cache.kv_heads > 256:
-        raise ValueError("heads must be a multiple of kv_heads = %d, at most 256 times it, got %d" % (cache.kv_heads, heads))
+        raise ValueError("heads must be a multiple of kv_heads = %d, at most 256 times it, got %d"
+                         % (cache.kv_heads, heads))
     if tokens * (heads // cache.kv_heads) > 1 << 30:
         raise ValueError("more than 2^30 rows a key head")
     scale = dim ** -0.5 if scale is None else float(scale)
@@ -221,7 +238,7 @@ def cached_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, scal
         q2 = _heads16(q)
         out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-        key = (cache.kv_heads, cache.head_dim, cache.page_size, cache.bits, tokens, heads, window)
+        key = (cache.dtype, cache.kv_heads, cache.head_dim, cache.page_size, cache.bits, tokens, heads, window)
         need = batch._need.get(key)
         if need is None:
             need = L.df_cached_attention_workspace_bytes(cache._ref, batch._ref, tokens, heads, window)

@@ -18,9 +18,14 @@ The EntroLLM summary ("Metodologia") stores quantised weights instead.
 layers are decoded in one batch to packed nibbles and multiplied as they are
 (``linear_u4``; a long prompt and a gradient expand one layer at a time in a call's
 workspace), so no dequantised copy is kept; gradients to the activations
-decode a block again.  ``CompressedHead`` holds an LM head as one BF16 container
+decode a block again.  uint8 containers are decoded to bytes and multiplied in 8-bit
+integers (``linear_u8``), without gradients.  ``CompressedHead`` holds an LM head as one BF16 container
 and scores hidden states against it (``vocab_loss``, ``distill_loss``): what the
 quantised model loses against the lossless one, and the gradient to mend it.
+
+A model that answers runs its blocks by ``step``: the new tokens of several
+sequences at once, whose keys and values go into paged caches (one ``KVCache`` a
+block) that their attention reads (``block_step``).
 """
 from __future__ import annotations
 
@@ -32,7 +37,8 @@ import numpy as np
 import torch
 
 from . import dfh
-from .ops import U4Matrix, distill_loss, linear_u4, vocab_loss
+from .cache import CacheBatch, KVCache, cache_write, cached_attention
+from .ops import U4Matrix, U8Matrix, _no_gradient, distill_loss, linear_u4, linear_u8, quantize_rows, vocab_loss
 
 
 @dataclass(frozen=True)
@@ -74,12 +80,14 @@ def _rms_norm(x: torch.Tensor, eps: float = 1e-5) -> torch.Tensor:
     return (xf * torch.rsqrt(xf.pow(2).mean(-1, keepdim=True) + eps)).to(x.dtype)
 
 
-def _rope(x: torch.Tensor, theta: float) -> torch.Tensor:
-    # x: [heads, T, head_dim]; rotate pairs (i, i + head_dim / 2) in float32
+def _rope(x: torch.Tensor, theta: float, positions: torch.Tensor | None = None) -> torch.Tensor:
+    # x: [heads, T, head_dim]; rotate pairs (i, i + head_dim / 2) in float32, by positions
+    # [T] (none: 0 .. T - 1)
     _, t, hd = x.shape
     half = hd // 2
     inv = 1.0 / (theta ** (torch.arange(0, half, device=x.device, dtype=torch.float32) / half))
-    ang = torch.arange(t, device=x.device, dtype=torch.float32)[:, None] * inv[None, :]
+    at = torch.arange(t, device=x.device, dtype=torch.float32) if positions is None else positions.float()
+    ang = at[:, None] * inv[None, :]
     cos, sin = ang.cos(), ang.sin()
     xf = x.float()
     a, b = xf[..., :half], xf[..., half:]
@@ -141,6 +149,47 @@ def block_forward(x: torch.Tensor, w: dict, shape: BlockShape, linear=torch.nn.f
     return x + linear(torch.nn.functional.silu(g) * u, w["down"])
 
 
+def _products(linear):
+    return lambda x, *ws: [linear(x, w) for w in ws]
+
+
+def _products_u8(x, *ws):
+    # few rows are quantised by the product's own kernel, more are quantised once for all
+    if len(ws) > 1 and x.shape[0] > 4:
+        codes, scales = quantize_rows(x)
+        return [linear_u8(codes, w, scales=scales, dtype=x.dtype) for w in ws]
+    return [linear_u8(x, w) for w in ws]
+
+
+def block_step(x: torch.Tensor, w: dict, shape: BlockShape, cache: KVCache, batch: CacheBatch, positions: torch.Tensor,
+               products=_products(torch.nn.functional.linear)) -> torch.Tensor:
+    """One Llama block on the new tokens x [tokens, hidden] of a batch of sequences, in
+    the cache's dtype: their keys and values are written into the cache, and each token
+    attends to what its sequence holds up to itself.  positions: batch.positions(tokens).
+    products(x, *weights) multiplies x by some layers' weights."""
+    t = x.shape[0]
+    hd, nh, nkv = shape.head_dim, shape.heads, shape.kv_heads
+    q, k, v = products(_rms_norm(x), w["q"], w["k"], w["v"])
+    q = _rope(q.view(t, nh, hd).transpose(0, 1), shape.rope_theta, positions).transpose(0, 1)
+    k = _rope(k.view(t, nkv, hd).transpose(0, 1), shape.rope_theta, positions).transpose(0, 1)
+    cache_write(k, v.view(t, nkv, hd), cache, batch)
+    att, = products(cached_attention(q, cache, batch).view(t, nh * hd), w["o"])
+    x = x + att
+    g, u = products(_rms_norm(x), w["gate"], w["up"])
+    return x + products(torch.nn.functional.silu(g) * u, w["down"])[0]
+
+
+def _check_step(x, caches, blocks: int, shape: BlockShape):
+    _no_gradient("step", x)
+    if x.dim() != 2 or x.shape[1] != shape.hidden:
+        raise ValueError("x must be [tokens, %d], got %s" % (shape.hidden, tuple(x.shape)))
+    if len(caches) != blocks:
+        raise ValueError("%d blocks need as many caches, got %d" % (blocks, len(caches)))
+    for c in caches:
+        if c.kv_heads != shape.kv_heads or c.head_dim != shape.head_dim or c.dtype != x.dtype:
+            raise ValueError("a cache must hold %d heads of %d in %s" % (shape.kv_heads, shape.head_dim, x.dtype))
+
+
 class CompressedBlocks:
     """Blocks held as device-resident containers, decoded one block ahead.
 
@@ -174,6 +223,19 @@ class CompressedBlocks:
     def forward(self, x: torch.Tensor, overlap: bool = True) -> torch.Tensor:
         """All blocks in order.  overlap=False decodes each block on the
         caller's stream right before it runs (no overlap)."""
+        return self._each(x, overlap, lambda i, x, w: block_forward(x, w, self.shape))
+
+    def step(self, x: torch.Tensor, caches, batch: CacheBatch, overlap: bool = False) -> torch.Tensor:
+        """All blocks on the new tokens x [tokens, hidden] (BF16) of a batch of
+        sequences, block i with caches[i] (block_step); no gradient.  Decoding beside
+        the blocks (overlap) is forward's default; few tokens' kernels are bound by
+        memory as the decoder is, so a step decodes in turn."""
+        _check_step(x, caches, len(self.blocks), self.shape)
+        with torch.no_grad(), torch.cuda.device(self.device):
+            at = batch.positions(x.shape[0])
+            return self._each(x, overlap, lambda i, x, w: block_step(x, w, self.shape, caches[i], batch, at))
+
+    def _each(self, x: torch.Tensor, overlap: bool, run) -> torch.Tensor:
         main = torch.cuda.current_stream(self.device)
         for j in range(2):
             self.released[j].record(main)
@@ -187,7 +249,7 @@ class CompressedBlocks:
                 main.wait_event(self.decoded[j])
             else:
                 dfh.df_decompress(self.blocks[i], self.scratch[j], main)
-            x = block_forward(x, weight_views(self.scratch[j], self.shape), self.shape)
+            x = run(i, x, weight_views(self.scratch[j], self.shape))
             self.released[j].record(main)
         return x
 
@@ -220,36 +282,47 @@ class _Made:
 
 class QuantizedBlocks:
     """Blocks held as uint4 containers with group scales, decoded to packed
-    nibbles right before they run.
+    nibbles right before they run, or (bits=8) as uint8 containers with a scale for each
+    row, decoded to bytes.
 
     layers: per block a list of (container, scales, zeros) in
     BlockShape.matrices() order, as quantize_block makes them; scales [rows,
-    groups] in float32, zeros uint8 of that shape or None.  Scales are kept in
-    scale_dtype: bfloat16, the weights' own type, rounds each by up to 2^-8 of itself
-    and halves their bytes; torch.float32 keeps the quantiser's.
-    One scratch buffer of a block's nibbles is allocated up front.  Calls take turns
+    groups] (group_size columns a group; uint8 has [rows] and no group_size) in float32,
+    zeros uint8 of that shape or None.  Scales are kept in scale_dtype: for uint4
+    bfloat16 if none is given, the weights' own type, which rounds each by up to 2^-8 of
+    itself and halves their bytes; torch.float32, uint8's own, keeps the quantiser's.
+    One scratch buffer of a block's codes is allocated up front.  Calls take turns
     with it, from any thread and on any stream (each waits for the one before); a
     captured call's replays are for the caller to order with what else uses these
     blocks."""
 
-    def __init__(self, layers, shape: BlockShape, device, group_size: int, scale_dtype=torch.bfloat16):
-        self.shape = shape
+    def __init__(self, layers, shape: BlockShape, device, group_size: int | None, scale_dtype=None, *, bits: int = 4):
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8, got %r" % (bits,))
+        if (group_size is None) != (bits == 8):
+            raise ValueError("uint4 layers need a group_size, uint8 layers have none")
+        if scale_dtype is None:
+            scale_dtype = torch.bfloat16 if bits == 4 else torch.float32
+        self.shape, self.bits = shape, bits
         self.device = torch.device(device)
+        self._linear, self._products = (linear_u4, _products(linear_u4)) if bits == 4 else (linear_u8, _products_u8)
         mats = shape.matrices()
-        self.scratch = [torch.empty(r * c // 2, dtype=torch.uint8, device=self.device) for _, r, c in mats]
+        self.scratch = [torch.empty(r * c * bits // 8, dtype=torch.uint8, device=self.device) for _, r, c in mats]
         self.blocks, self.weights = [], []
         for block in layers:
             if len(block) != len(mats):
                 raise ValueError("a block needs %d layers" % len(mats))
             dcs, ws = [], {}
-            for (name, r, c), packed, (con, scales, zeros) in zip(mats, self.scratch, block):
+            for (name, r, c), codes, (con, scales, zeros) in zip(mats, self.scratch, block):
                 inf = con.info()
-                if int(inf["n"]) != r * c or int(inf["kind"]) != dfh.KIND_U4:
-                    raise ValueError("container does not hold the uint4 codes of layer %r" % name)
+                if int(inf["n"]) != r * c or int(inf["kind"]) != (dfh.KIND_U4 if bits == 4 else dfh.KIND_U8):
+                    raise ValueError("container does not hold the uint%d codes of layer %r" % (bits, name))
                 dcs.append(dfh.to_device(con, self.device))
                 s = torch.as_tensor(scales).to(self.device, scale_dtype)
                 z = None if zeros is None else torch.as_tensor(zeros).to(self.device)
-                ws[name] = U4Matrix(packed, s, z, cols=c, group_size=group_size)
+                if bits == 8 and s.shape[0] != r:
+                    raise ValueError("layer %r needs %d scales, got %s" % (name, r, tuple(s.shape)))
+                ws[name] = U4Matrix(codes, s, z, cols=c, group_size=group_size) if bits == 4 else U8Matrix(codes, s, z, cols=c)
             self.blocks.append(dcs)
             self.weights.append(ws)
         self._made = _Made(self.device, self.scratch
@@ -274,13 +347,30 @@ class QuantizedBlocks:
                     self._used.record(stream)
                     self._stream = stream
 
-    def _run(self, i: int, x: torch.Tensor) -> torch.Tensor:
+    def _decode(self, i: int):
         dfh.df_decompress_batch(self.blocks[i], self.scratch, torch.cuda.current_stream(self.device))
-        return block_forward(x, self.weights[i], self.shape, linear_u4)
+
+    def _run(self, i: int, x: torch.Tensor) -> torch.Tensor:
+        self._decode(i)
+        return block_forward(x, self.weights[i], self.shape, self._linear)
+
+    def step(self, x: torch.Tensor, caches, batch: CacheBatch) -> torch.Tensor:
+        """All blocks on the new tokens x [tokens, hidden] of a batch of sequences, block
+        i with caches[i] (block_step), on the current stream; no gradient."""
+        _check_step(x, caches, len(self.blocks), self.shape)
+        with torch.no_grad(), torch.cuda.device(self.device):
+            at = batch.positions(x.shape[0])
+            for i, cache in enumerate(caches):
+                with self._turn():
+                    self._decode(i)
+                    x = block_step(x, self.weights[i], self.shape, cache, batch, at, self._products)
+        return x
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """All blocks in order on the current stream.  Differentiable in x, once: a
-        block keeps its input and is decoded and run again for its gradient."""
+        """All blocks in order on the current stream.  With uint4 layers differentiable
+        in x, once: a block keeps its input and is decoded and run again for its gradient."""
+        if self.bits == 8:
+            _no_gradient("uint8 blocks", x)
         for i in range(len(self.blocks)):
             if x.requires_grad and torch.is_grad_enabled():
                 x = _QuantizedBlock.apply(x, self, i)
@@ -365,15 +455,20 @@ def random_blocks(n_blocks: int, shape: BlockShape, seed: int = 0):
             for b in range(n_blocks)]
 
 
-def quantize_block(host: np.ndarray, shape: BlockShape, group_size: int, asymmetric: bool = True):
+def quantize_block(host: np.ndarray, shape: BlockShape, group_size: int | None, asymmetric: bool = True, bits: int = 4):
     """One block's host BF16 weights -> QuantizedBlocks' layers: per matrix the
-    uint4 container of its codes, its group scales and zero points."""
+    uint4 container of its codes, its group scales and zero points; with bits=8 (and no
+    group_size) the uint8 container, a scale and a zero point for each row."""
     from . import synth
     out, off = [], 0
     for _, r, c in shape.matrices():
         w = synth.bf16_to_f32(host[off: off + r * c]).reshape(r, c)
-        codes, scales, zeros = synth.quantize_u4_groups(w, group_size, asymmetric)
-        out.append((dfh.compress(dfh.KIND_U4, synth.pack_u4(codes), n=r * c), scales, zeros))
+        if bits == 8:
+            codes, scales, zeros = synth.quantize_u8_rows(w, asymmetric)
+            out.append((dfh.compress(dfh.KIND_U8, codes.reshape(-1), n=r * c), scales, zeros))
+        else:
+            codes, scales, zeros = synth.quantize_u4_groups(w, group_size, asymmetric)
+            out.append((dfh.compress(dfh.KIND_U4, synth.pack_u4(codes), n=r * c), scales, zeros))
         off += r * c
     return out
 

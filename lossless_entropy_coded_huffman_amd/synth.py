@@ -213,6 +213,25 @@ def quantize_u4_groups(x: np.ndarray, group_size: int, asymmetric: bool):
     return codes, scales, zeros
 
 
+def quantize_u8_rows(x: np.ndarray, asymmetric: bool):
+    """quantize_u8 for each row of x [rows, cols]: (codes [rows, cols], scales float32
+    [rows], zeros uint8 [rows]), x ~ scales * (codes - zeros).  As there the zero
+    point is a code, so an asymmetric row whose values all lie on one side of zero is
+    clipped at 255 steps from zero."""
+    x = np.ascontiguousarray(x, np.float32)
+    if asymmetric:
+        lo, hi = x.min(axis=1), x.max(axis=1)
+        s = ((hi - lo) / np.float32(255)).astype(np.float32)
+        s[s <= 0] = 1
+        z = np.clip(np.rint(-lo / s), 0, 255)
+    else:
+        s = (np.abs(x).max(axis=1) / np.float32(127)).astype(np.float32)
+        s[s <= 0] = 1
+        z = np.full(len(x), 128, np.float32)
+    codes = np.clip(np.rint(x / s[:, None]) + z[:, None], 0, 255).astype(np.uint8)
+    return codes, s, z.astype(np.uint8)
+
+
 def bf16_to_f32(bits: np.ndarray) -> np.ndarray:
     """BF16 bit patterns -> float32."""
     return (np.asarray(bits, np.uint16).astype(np.uint32) << np.uint32(16)).view(np.float32)
