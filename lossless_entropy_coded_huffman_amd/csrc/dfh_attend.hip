@@ -17,12 +17,13 @@
 // attend_few takes sequences with at most 32 rows (tokens times heads a key head),
 // whose time is the reading of the cache: each wave has tiles of 32 keys of its own,
 // read straight to LDS, and the key range is split over workgroups too.  attend_tile takes the
-// others: 128 rows share tiles of 64 keys.  attend_join adds up what splits leave.
+// others: 128 or 256 rows share tiles of 64 keys.  join_few and join_tiles add up what splits
+// leave.
 //
 // Roundings: q and 16-bit keys and values are taken as they are, codes of 8 bits are
 // exact in both 16-bit types.  A token's scale of keys multiplies the FP32 scores; its
 // scale of values multiplies p before that is rounded to 16 bits: the one rounding (half a
-// step, 2^-9 or 2^-12 of it) beside the output's.  Sums are FP32.
+// step, up to 2^-8 or 2^-11 of it) beside the output's.  Sums are FP32.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -1122,7 +1123,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
     const int64_t r0 = (tile - first_tile<kRows>(b, s, a.group)) * kRows;
-    if (rows <= a.cap || r0 >= (int64_t)rows) continue;
+    if (rows <= a.cap || r0 < 0 || r0 >= (int64_t)rows) continue;  // (before: starts that fall)
     const uint32_t count = rows - (uint32_t)r0 < kRows ? rows - (uint32_t)r0 : kRows;
     const int32_t first = sp.first + (int32_t)((uint32_t)r0 / a.group), last = sp.first + (int32_t)(((uint32_t)r0 + count - 1) / a.group);
     const Cuts k = cuts_of(c, b, first + sp.ahead, last + sp.ahead, sp.length, a.window, kTileShift, a.tile_splits, kTileLeast);

@@ -427,6 +427,46 @@ def test_a_pool_beyond_32_bits(torch):
         check(torch, got, lse, q, kvs, new, lengths, dim ** -0.5, None, 16)
 
 
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("some", [1, 60])
+def test_many_sequences(torch, some, bits):
+    # more than are split, with padding before and behind, beside a prompt
+    page, kv, group, dim, seqs = 16, 2, 4, 64, 700
+    new = [i % 3 if i != 400 else some for i in range(seqs)]
+    lengths = [n + 7 * i % 50 for i, n in enumerate(new)]
+    b, tables, pages = batch_of(torch, new, lengths, page, seed=5)
+    cache = spoiled(torch, dfh.KVCache(pages, kv, dim, page_size=page, bits=bits))
+    kvs = filled(torch, cache, tables, lengths, seed=5)
+    before, behind, n = 5, 9, sum(new)
+    q = torch.randn(before + n + behind, kv * group, dim, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    for hint in (2, None):
+        moved = dfh.CacheBatch(b.tables, b.lengths, b.starts + before, max_new=hint)
+        got, lse = dfh.cached_attention(q, cache, moved, return_lse=True)
+        pad = list(range(before)) + list(range(before + n, len(q)))
+        assert not got[pad].any() and bool((lse[pad] == -math.inf).all())
+        mid = slice(before, before + n)
+        check(torch, got[mid], lse[mid], q[mid], kvs, new, lengths, dim ** -0.5, None, bits)
+
+
+@pytest.mark.parametrize("hint", [1, None])
+def test_starts_that_are_out_of_order(torch, hint):
+    # nothing is said of what such a batch gives; it reads and writes within its tensors,
+    # and the next call is right
+    page, new, lengths = 16, [3, 150, 70, 40], [30, 160, 70, 90]
+    b, tables, pages = batch_of(torch, new, lengths, page)
+    cache = spoiled(torch, dfh.KVCache(pages, 1, 64, page_size=page))
+    kvs = filled(torch, cache, tables, lengths)
+    q = torch.randn(sum(new), 2, 64, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    top = (1 << 31) - 1
+    for starts in ([200, 100, 150, 20, 263], [263, 0, 263, 0, 100], [-5, 400, -top, top, 5], [top, -top, top, 0, 0]):
+        odd = dfh.CacheBatch(b.tables, b.lengths, torch.tensor(starts, dtype=torch.int32).cuda(), max_new=hint)
+        dfh.cached_attention(q, cache, odd, return_lse=True)
+        dfh.cache_read(cache, odd, len(q))
+        torch.cuda.synchronize()
+    got, lse = dfh.cached_attention(q, cache, b, return_lse=True)
+    check(torch, got, lse, q, kvs, new, lengths, 64 ** -0.5, None, 16)
+
+
 def test_a_long_sequence(torch):
     # 150000 positions: a few rows, and a chunk, sampled
     kv, group, dim, page, length = 1, 4, 64, 256, 150001
