@@ -77,38 +77,50 @@ __global__ __launch_bounds__(256) void move(const Pages c, const Sequences b, co
     if (there && mine < b.count && t >= q.first && t < q.last) token = token_at(c, b, mine, t + q.ahead);
     if (WRITE && token < 0) continue;
     const uint64_t row = token < 0 ? 0 : row_of(c, token, head);
+    uint16_t *const vec[2] = {n.k + t * n.k_token + head * n.k_head + at * 8, n.v + t * n.v_token + head * n.v_head + at * 8};
+    uint8_t *const page[2] = {c.k + row * (D * BITS / 8) + at * BITS, c.v + row * (D * BITS / 8) + at * BITS};
+    float *const scale[2] = {c.k_scales + row, c.v_scales + row};
+    // both are read before either is written: the compiler keeps that order for all it knows
+    if constexpr (WRITE) {
+      u32x4 x[2];
 #pragma unroll
-    for (int kv = 0; kv < 2; kv++) {
-      uint16_t *vec = (kv ? n.v + t * n.v_token + head * n.v_head : n.k + t * n.k_token + head * n.k_head) + at * 8;
-      uint8_t *page = (kv ? c.v : c.k) + row * (D * BITS / 8) + at * BITS;
-      float *scale = (kv ? c.v_scales : c.k_scales) + row;
-      if constexpr (WRITE) {
-        const u32x4 x = *(const u32x4 *)vec;
+      for (int kv = 0; kv < 2; kv++) x[kv] = *(const u32x4 *)vec[kv];
+#pragma unroll
+      for (int kv = 0; kv < 2; kv++) {
         if constexpr (BITS == 16) {
-          *(u32x4 *)page = x;
+          *(u32x4 *)page[kv] = x[kv];
         } else {
           Quantiser z;
-          z.init(T{}, most_of_lanes<LANES>(joined(most_bits(x, 0))));
-          *(u32x2 *)page = z.codes(T{}, x);
-          if (at == 0) *scale = z.scale;
+          z.init(T{}, most_of_lanes<LANES>(joined(most_bits(x[kv], 0))));
+          *(u32x2 *)page[kv] = z.codes(T{}, x[kv]);
+          if (at == 0) *scale[kv] = z.scale;
         }
-      } else if (there) {
-        u32x4 x = {0, 0, 0, 0};
-        if (token >= 0) {
-          if constexpr (BITS == 16) {
-            x = *(const u32x4 *)page;
-          } else {
-            const u32x2 o = *(const u32x2 *)page;
-            const float f = *scale;
+      }
+    } else if (there) {
+      u32x4 x[2] = {};
+      if (token >= 0) {
+        if constexpr (BITS == 16) {
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++) x[kv] = *(const u32x4 *)page[kv];
+        } else {
+          u32x2 o[2];
+          float f[2];
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++) {
+            o[kv] = *(const u32x2 *)page[kv];
+            f[kv] = *scale[kv];
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-              const uint32_t w = o[e / 2] >> (16 * (e & 1));
-              x[e] = pack2(T{}, (float)(int8_t)w * f, (float)(int8_t)(w >> 8) * f);
+              const uint32_t w = o[kv][e / 2] >> (16 * (e & 1));
+              x[kv][e] = pack2(T{}, (float)(int8_t)w * f[kv], (float)(int8_t)(w >> 8) * f[kv]);
             }
-          }
         }
-        *(u32x4 *)vec = x;
       }
+#pragma unroll
+      for (int kv = 0; kv < 2; kv++) *(u32x4 *)vec[kv] = x[kv];
     }
   }
 }
