@@ -151,15 +151,17 @@ struct KeyType<T, 8> {
 
 // A tile of keys or values in LDS, 16 bits a value: rows of D, 16-byte chunks exchanged
 // within a row (in the source address, where a load writes LDS linearly).  Keys are
-// read 16 bytes at one chunk of 32 rows: 8 rows in a row fall into 8 places.  Values are
-// read transposed, 64 bytes of 8 rows: neighbours fall into different ones.
+// read 16 bytes at one chunk of 32 rows, 16 rows at once: those in a row fall into 16 places of
+// 256 bytes (of heads of 256 only 8: all of a wave's loads have one exchange).  Values are read
+// transposed, 64 bytes of 8 rows: neighbours fall into different ones.
 template <int D>
 struct Rows {
   static constexpr int kBytes = D * 2, kChunks = kBytes / 16;
   static constexpr int kPer = kBytes >= 128 ? 1 : 128 / kBytes;  // rows in 128 bytes
-  static constexpr int kKeyPlaces = kChunks < 8 ? kChunks : 8;
+  static constexpr int kKeyPer = kBytes >= 256 ? 1 : 256 / kBytes;
+  static constexpr int kKeyPlaces = kChunks <= 16 ? kChunks : 8;
   static constexpr int kUnits = kChunks < 4 ? 1 : kChunks / 4 < 4 ? kChunks / 4 : 4;
-  static __device__ __forceinline__ uint32_t key_swap(uint32_t r) { return (r / kPer) & (kKeyPlaces - 1); }
+  static __device__ __forceinline__ uint32_t key_swap(uint32_t r) { return (r / kKeyPer) & (kKeyPlaces - 1); }
   static __device__ __forceinline__ uint32_t value_swap(uint32_t r) { return ((r / kPer) & (kUnits - 1)) * 4; }
 };
 
@@ -1173,7 +1175,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
     float scale = 0.f;
     // rows of a load lie in one page; the exchange is the same in all of a wave's loads
     const uint32_t in_load = lane / R::kChunks, chunk = lane % R::kChunks;
-    static_assert(kLoads >= 1 && NW * kRowsPer % (8 * R::kPer) == 0, "the exchange is the same in all of a wave's loads");
+    static_assert(kLoads >= 1 && NW * kRowsPer % (R::kKeyPlaces * R::kKeyPer) == 0 &&
+                      NW * kRowsPer % (R::kUnits * R::kPer) == 0,
+                  "the exchange is the same in all of a wave's loads");
     auto bring = [&](const uint8_t *pool, int32_t t, const Table &pages, uint64_t all, uint32_t swap, uint32_t dst) {
       const uint32_t off = in_load * R::kBytes + (chunk ^ swap) * 16;
       const uint8_t *mine = pool + (uint64_t)head * head_bytes;

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void move(const Pages c, const Sequences b, co
     uint16_t *const vec[2] = {n.k + t * n.k_token + head * n.k_head + at * 8, n.v + t * n.v_token + head * n.v_head + at * 8};
     uint8_t *const page[2] = {c.k + row * (D * BITS / 8) + at * BITS, c.v + row * (D * BITS / 8) + at * BITS};
     float *const scale[2] = {c.k_scales + row, c.v_scales + row};
-    // both are read before either is written: the compiler keeps that order for all it knows
+    // both are read before either is written, the order that the compiler keeps (write_prompts below)
     if constexpr (WRITE) {
       u32x4 x[2];
 #pragma unroll
