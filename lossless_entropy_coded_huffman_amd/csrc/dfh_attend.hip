@@ -171,21 +171,22 @@ __device__ __forceinline__ constexpr int key_of(int r) { return 8 * (r / 4) + r 
 // 16 bytes a lane from base + off (of each lane) to LDS address at + 16 lane.  The
 // compiler is not told of these loads: before a transposing read it would wait for all that it
 // knows of, the next tile's among them (4096 x 16384 x 32 heads 1038 us, unknown 967).  A load
-// of this kind writes no register; what it writes in LDS is waited for by wait_but.
+// of this kind writes no register but m0, which nothing else here uses; what it writes in LDS is
+// waited for by wait_but.
 __device__ __forceinline__ uint32_t same(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint64_t same(uint64_t v) { return (uint64_t)same((uint32_t)(v >> 32)) << 32 | same((uint32_t)v); }
 __device__ __forceinline__ void ask(const uint8_t *base, uint32_t off, uint32_t at) {
   base = (const uint8_t *)same((uint64_t)base);
   at = same(at);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void ask(const uint8_t *src, uint32_t at) {
   at = same(at);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
 __device__ __forceinline__ void ask_word(const uint8_t *src, uint32_t at) {  // 4 bytes a lane
   at = same(at);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
@@ -462,7 +463,6 @@ template <class T, int BITS, int D>
 __device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s, f32x16 &next, uint32_t lk, uint32_t lv, const float *vs,
                                            const float *next_ks, const float *next_vs) {
   typedef typename KeyType<T, BITS>::type K;
-  typedef Rows<D> R;
   constexpr int N = D / 16;  // products of the scores, and of the sums
   const uint32_t h = (threadIdx.x >> 5) & 1;
   const float ref = w.m == -__builtin_huge_valf() ? 0.f : w.m;
@@ -533,11 +533,6 @@ __device__ __forceinline__ float half_step(Wave<T, BITS, D> &w, const f32x16 &s,
 // The address of a head's row in the pool.
 __device__ __forceinline__ uint64_t pool_row(const Pages &c, uint32_t page, uint32_t head, uint32_t at) {
   return (((uint64_t)page * c.heads + head) << c.shift) + (at & ((1u << c.shift) - 1));
-}
-// What a table says of a position (of the last one, from stop on), unchecked: it is looked at
-// a tile later, when it is there.
-__device__ __forceinline__ int32_t page_at(const Pages &c, const int32_t *table, int32_t pos, int32_t stop) {
-  return table[(uint32_t)(pos < stop ? pos : stop - 1) >> c.shift];
 }
 
 // Four outputs of a row, as they are or for the join.
@@ -1021,17 +1016,18 @@ __global__ __launch_bounds__(64 * W, BITS == 8 && D < 256 ? 2 : 1) void attend_f
   }
 }
 
-// The parts of a row of few, a workgroup to a row (sequence, key head, row): D / 4 lanes
+// The parts of a row of few, a workgroup (block of blocks) to a row (sequence, key head, row): D / 4 lanes
 // hold it, and 1024 / D groups of them take the parts in turn, so that all are read at
 // once (2000 positions for a token in 16 parts: 3 us against 10 with one after the other).
 template <class T, int D>
-__global__ __launch_bounds__(256) void join_few(const Pages c, const Sequences b, const Attend a) {
+__device__ __forceinline__ void join_few(const Pages &c, const Sequences &b, const Attend &a, uint32_t block,
+                                         uint32_t blocks) {
   constexpr uint32_t kLanes = D / 4, kGroups = 256 / kLanes;
   __shared__ f32x4 vs[256];
   __shared__ float ms[kGroups], ls[kGroups];
   const uint32_t chunk = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const uint64_t all = (uint64_t)b.count * c.heads * a.cap;
-  for (uint64_t row = blockIdx.x; row < all; row += gridDim.x) {
+  for (uint64_t row = block; row < all; row += blocks) {
     const uint32_t r = (uint32_t)(row % a.cap), head = (uint32_t)(row / a.cap % c.heads), s = (uint32_t)(row / a.cap / c.heads);
     const Span sp = span_of(b, s);
     const uint32_t rows = (uint32_t)(sp.last - sp.first) * a.group;
@@ -1366,12 +1362,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile(const P
 
 // The parts of a row of tiles (token, head) added up, D / 4 lanes to a row.
 template <class T, int D>
-__global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences b, const Attend a) {
+__device__ __forceinline__ void join_tiles(const Pages &c, const Sequences &b, const Attend &a, uint32_t block,
+                                           uint32_t blocks) {
   constexpr uint32_t kLanes = D / 4;
   const uint32_t chunk = threadIdx.x % kLanes;
   // a wave's rows go together: the search below is the whole wave's
   const uint64_t rows_all = (uint64_t)b.tokens * a.heads, all = rows_all * kLanes;
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i - (threadIdx.x & 63) < all; i += (uint64_t)gridDim.x * 256) {
+  for (uint64_t i = (uint64_t)block * 256 + threadIdx.x; i - (threadIdx.x & 63) < all; i += (uint64_t)blocks * 256) {
     const bool in = i < all;
     const uint64_t row = (in ? i : all - 1) / kLanes;
     const int32_t t = (int32_t)(row / a.heads);
@@ -1408,6 +1405,17 @@ __global__ __launch_bounds__(256) void join_tiles(const Pages c, const Sequences
     }
     store4(a.out + row * D + chunk * 4, T{}, l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * (1.f / l));
     if (a.lse && chunk == 0) a.lse[row] = lse_of(m, l);
+  }
+}
+
+// All that splits leave, in one launch: the first few_blocks workgroups join rows of few, the
+// others those of tiles (19 sequences of both, FP16 in 8 bits: 43.6 us, two launches 46.8).
+template <class T, int D>
+__global__ __launch_bounds__(256) void join(const Pages c, const Sequences b, const Attend a, uint32_t few_blocks) {
+  if (blockIdx.x < few_blocks) {
+    join_few<T, D>(c, b, a, blockIdx.x, few_blocks);
+  } else {
+    join_tiles<T, D>(c, b, a, blockIdx.x - few_blocks, gridDim.x - few_blocks);
   }
 }
 
@@ -1510,9 +1518,6 @@ hipError_t few_rows(const Plan &p, const Pages &c, const Sequences &b, hipStream
   // as many workgroups as the chip holds
   hipLaunchKernelGGL((attend_few<T, BITS, D, NQ, W>), dim3(resident((const void *)attend_few<T, BITS, D, NQ, W>, 64 * W, lds)), dim3(64 * W), lds,
                      s, c, b, p.a);
-  const hipError_t st = hipGetLastError();
-  if (st != hipSuccess || p.a.few_splits == 1) return st;
-  hipLaunchKernelGGL((join_few<T, D>), dim3(grid_of((uint64_t)b.count * c.heads * p.a.cap)), dim3(256), 0, s, c, b, p.a);
   return hipGetLastError();
 }
 template <class T, int BITS, int D, int NW>
@@ -1543,12 +1548,11 @@ hipError_t attend(const Plan &p, const Pages &c, const Sequences &b, hipStream_t
     }
     if (st != hipSuccess) return st;
   }
-  if (p.a.tile_splits > 1) {
-    hipLaunchKernelGGL((join_tiles<T, D>), dim3(grid_of(((uint64_t)b.tokens * p.a.heads * (D / 4) + 255) / 256)), dim3(256), 0, s, c, b,
-                       p.a);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  const uint32_t few_blocks = p.a.few_splits > 1 ? grid_of((uint64_t)b.count * c.heads * p.a.cap) : 0;
+  const uint32_t tile_blocks = p.a.tile_splits > 1 ? grid_of(((uint64_t)b.tokens * p.a.heads * (D / 4) + 255) / 256) : 0;
+  if (few_blocks + tile_blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL((join<T, D>), dim3(few_blocks + tile_blocks), dim3(256), 0, s, c, b, p.a, few_blocks);
+  return hipGetLastError();
 }
 template <class T, int BITS>
 hipError_t attend_dim(const Plan &p, const Pages &c, const Sequences &b, hipStream_t s) {

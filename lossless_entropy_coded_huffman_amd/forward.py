@@ -322,7 +322,8 @@ class QuantizedBlocks:
                 z = None if zeros is None else torch.as_tensor(zeros).to(self.device)
                 if bits == 8 and s.shape[0] != r:
                     raise ValueError("layer %r needs %d scales, got %s" % (name, r, tuple(s.shape)))
-                ws[name] = U4Matrix(codes, s, z, cols=c, group_size=group_size) if bits == 4 else U8Matrix(codes, s, z, cols=c)
+                ws[name] = (U4Matrix(codes, s, z, cols=c, group_size=group_size) if bits == 4
+                            else U8Matrix(codes, s, z, cols=c))
             self.blocks.append(dcs)
             self.weights.append(ws)
         self._made = _Made(self.device, self.scratch
