@@ -444,7 +444,7 @@ __device__ __forceinline__ f32x4 add_planes(const float *p, uint64_t stride, uin
 // ------------------------------------------------------------------- launch
 // Raises a kernel's LDS limit where a launch needs more than 64 KiB, once per
 // kernel and device: to all that a CU has, less what the kernel declares itself.
-hipError_t allow_lds(const void *fn, uint32_t bytes, uint32_t declared = 0) {
+[[maybe_unused]] hipError_t allow_lds(const void *fn, uint32_t bytes, uint32_t declared = 0) {
   if (bytes + declared <= 65536) return hipSuccess;
   static std::mutex mu;
   static std::map<std::pair<int, const void *>, bool> raised;
@@ -545,7 +545,7 @@ struct RowCut {
   uint32_t rows;  // in the first launch
   Cut main, rest;
 };
-RowCut rows_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
+[[maybe_unused]] RowCut rows_for(uint64_t m, uint64_t n, uint64_t k, bool may_split) {
   RowCut c = {(uint32_t)m, cut_for(m, n, k, may_split), {0, 0, 0.0}};
   const uint32_t r = (uint32_t)(m % 256);
   if (m > 256 && r && r <= 64) {
